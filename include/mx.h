@@ -546,8 +546,15 @@ MX_API mx_status_t mx_gemm_dgelu_bwd(const mx_tensor_t *dy_row, const mx_tensor_
                                      const mx_tensor_t *dpre_row, const mx_tensor_t *dpre_col, float *db1,
                                      void *workspace, size_t workspace_bytes, mx_stream_t stream);
 
-/* Activation of mx_mlp_fwd_bwd. */
-typedef enum { MX_ACT_SWIGLU = 0, MX_ACT_GELU_TANH = 1 } mx_act_t;
+/* Activations.  mx_mlp_fwd_bwd takes SWIGLU and GELU_TANH, mx_linear_fwd all
+ * but SWIGLU, the activation checkpoints all but NONE. */
+typedef enum {
+  MX_ACT_SWIGLU = 0,    /* [g | u] -> g * sigmoid(g) * u */
+  MX_ACT_GELU_TANH = 1, /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  MX_ACT_NONE = 2,
+  MX_ACT_SILU = 3,      /* z * sigmoid(z) */
+  MX_ACT_RELU = 4       /* max(z, 0), slope 0 at z <= 0 */
+} mx_act_t;
 
 /*
  * Arguments of the whole MLP step.  BF16 inputs / outputs, device memory.
@@ -671,6 +678,114 @@ MX_API mx_status_t mx_mlp_pipeline_create(const mx_mlp_args_t *dev, mx_stream_t 
 MX_API mx_status_t mx_mlp_pipeline_run(mx_mlp_pipeline_t *p, const mx_mlp_host_io_t *io);
 MX_API mx_status_t mx_mlp_pipeline_sync(mx_mlp_pipeline_t *p);
 MX_API void mx_mlp_pipeline_destroy(mx_mlp_pipeline_t *p);
+
+/*
+ * BF16 layers beside the quantized ones: the products, the fused linear
+ * layer and the 8-bit activation checkpoints that the layers a recipe keeps
+ * in BF16 need.  Segments are of any length (no padding to 128 rows).
+ *
+ * Offsets here: device int32 [G], cumulative END offsets of each expert's
+ * rows, nondecreasing, any values in [0, R].  Rows in [offsets[G-1], R) are
+ * neither read nor written.  With G == 1 a NULL offsets means all R rows.  A
+ * segment that decreases or passes R is skipped on the device and reported
+ * as MX_ERR_OFFSETS by mx_get_device_status (on the host, before any
+ * launch, with MX_VALIDATE_OFFSETS=1).  G <= 1024, else
+ * MX_ERR_NOT_SUPPORTED.  K and N are multiples of 8, leading dimensions
+ * multiples of 8 elements and at least the row length; row counts have no
+ * alignment.  Non-finite values of one expert's rows reach no other
+ * expert's results.
+ *
+ * mx_ragged_gemm -- out[r, :] = A[r, :] W[g(r)]^T (MX_W_NK) or A[r, :] W[g(r)]
+ * (MX_W_KN: the input gradient dX = dY W of a layer whose W is [N, K]), fp32
+ * accumulation, one rounding to BF16.
+ *   a_bf16     device BF16 [R, K], row stride ld_a
+ *   w_bf16     device BF16 [G, N, K] (MX_W_NK) or [G, K, N] (MX_W_KN), dense
+ *   out_bf16   out, device BF16 [R, N], row stride ld_out; overlaps no input
+ * R == 0: MX_OK, nothing is written.
+ */
+enum { MX_W_NK = 0, MX_W_KN = 1 };
+MX_API mx_status_t mx_ragged_gemm(const void *a_bf16, int64_t R, int64_t K, int64_t ld_a, const void *w_bf16,
+                                  int64_t N, int32_t G, int32_t w_layout, const int32_t *offsets_dev,
+                                  void *out_bf16, int64_t ld_out, mx_stream_t stream);
+
+/*
+ * mx_ragged_gemm_wgrad -- grad[g] = dY_g^T X_g over the rows of segment g,
+ * fp32 accumulation, stored as BF16 (an empty segment stores zeros).
+ * mx_ragged_gemm_wgrad_f32 -- the same into an fp32 buffer: stored
+ * (accumulate = 0) or added to what it holds (accumulate = 1; an empty
+ * segment leaves its part unchanged).  Deterministic: the same inputs give
+ * the same bits.
+ *   dy_bf16    device BF16 [R, N], row stride ld_dy
+ *   x_bf16     device BF16 [R, K], row stride ld_x
+ *   grad       out, device [G, N, K], dense, 16-byte aligned
+ *   workspace  >= mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G) bytes (may
+ *              be NULL when that is 0); needs no preparation
+ * R == 0 stores zeros (accumulate = 1: leaves grad unchanged).
+ */
+MX_API size_t mx_ragged_gemm_wgrad_workspace_bytes(int64_t N, int64_t K, int64_t R, int32_t G);
+MX_API mx_status_t mx_ragged_gemm_wgrad(const void *dy_bf16, int64_t N, int64_t ld_dy, const void *x_bf16, int64_t K,
+                                        int64_t ld_x, int64_t R, int32_t G, const int32_t *offsets_dev,
+                                        void *grad_bf16, void *workspace, size_t workspace_bytes,
+                                        mx_stream_t stream);
+MX_API mx_status_t mx_ragged_gemm_wgrad_f32(const void *dy_bf16, int64_t N, int64_t ld_dy, const void *x_bf16,
+                                            int64_t K, int64_t ld_x, int64_t R, int32_t G,
+                                            const int32_t *offsets_dev, float *grad_f32, int32_t accumulate,
+                                            void *workspace, size_t workspace_bytes, mx_stream_t stream);
+
+/*
+ * mx_linear_fwd -- out = act(z) + res with z = X W^T + bias, all in fp32 from
+ * the accumulator, one rounding to BF16.
+ *   x_bf16     device BF16 [M, K], row stride ld_x
+ *   w_bf16     device BF16 [N, K], dense
+ *   bias_bf16  device BF16 [N] or NULL
+ *   act        MX_ACT_NONE, MX_ACT_GELU_TANH, MX_ACT_SILU or MX_ACT_RELU
+ *   res_bf16   device BF16 [M, N], row stride ld_res, or NULL; may be the
+ *              output itself (same pointer and row stride)
+ *   out_bf16   out, device BF16 [M, N], row stride ld_out
+ *   ckpt       NULL, or an E4M3 tensor [M, N] (N a multiple of 32, no
+ *              rotation) that receives z in 8 bits: the checkpoint
+ *              mx_act_ckpt_bwd reads.  Scales and codes as mx_quantize's, from
+ *              the fp32 z; scale padding is written as zero.
+ * The gradients: dz and db from mx_act_ckpt_bwd, dX = mx_ragged_gemm(dz, W,
+ * G = 1, MX_W_KN), dW = mx_ragged_gemm_wgrad(dz, X, G = 1), dres = dout.
+ * Errors as mx_ragged_gemm; MX_ERR_NOT_SUPPORTED for MX_ACT_SWIGLU.
+ */
+MX_API mx_status_t mx_linear_fwd(const void *x_bf16, int64_t M, int64_t K, int64_t ld_x, const void *w_bf16,
+                                 int64_t N, const void *bias_bf16, int32_t act, const void *res_bf16, int64_t ld_res,
+                                 void *out_bf16, int64_t ld_out, const mx_tensor_t *ckpt, mx_stream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits: a layer's pre-activation z kept for the
+ * backward pass as an E4M3 tensor with E8M0 block scales (33/64 of its BF16
+ * size), and the backward pass that reads it.
+ * mx_act_ckpt_fwd -- h = act(z) (fp32 from the BF16 z, one rounding) and the
+ * checkpoint of z, in one pass.
+ *   z_bf16   device BF16 [R, C], row stride ld_z; SWIGLU: [gate | up], C = 2F
+ *   act      any but MX_ACT_NONE
+ *   h_bf16   out, device BF16 [R, F] (SWIGLU) or [R, C], row stride ld_h
+ *   ckpt     out, E4M3 [R, C], no rotation: the bytes of mx_quantize's
+ *            rowwise output
+ * C is a multiple of 32 (SWIGLU: of 64); R has no alignment.  Columns are
+ * blocked from the start of the row; padding scales are written as zero.
+ *
+ * mx_act_ckpt_bwd -- with z^ the values the checkpoint stands for:
+ *   dz = dh * act'(z^) (SWIGLU: dg = dh u s (1 + g (1 - s)), du = dh g s),
+ *   h = act(z^) when h_bf16 is not NULL (the next product's input for its
+ *   weight gradient), db = the fp32 sum over rows of the unrounded dz when
+ *   db is not NULL (fixed order: deterministic).
+ *   dh_bf16    device BF16 [R, F] / [R, C], row stride ld_dh
+ *   dz_bf16    out, device BF16 [R, C], row stride ld_dz
+ *   h_bf16     out or NULL, row stride ld_h
+ *   db         out or NULL, device fp32 [C]
+ *   workspace  with db: >= mx_act_ckpt_workspace_bytes(R, C) bytes
+ * R == 0: nothing is written but db, which is set to zero.
+ */
+MX_API mx_status_t mx_act_ckpt_fwd(const void *z_bf16, int64_t R, int64_t C, int64_t ld_z, int32_t act, void *h_bf16,
+                                   int64_t ld_h, const mx_tensor_t *ckpt, mx_stream_t stream);
+MX_API size_t mx_act_ckpt_workspace_bytes(int64_t R, int64_t C);
+MX_API mx_status_t mx_act_ckpt_bwd(const mx_tensor_t *ckpt, int32_t act, const void *dh_bf16, int64_t ld_dh,
+                                   void *dz_bf16, int64_t ld_dz, void *h_bf16, int64_t ld_h, float *db,
+                                   void *workspace, size_t workspace_bytes, mx_stream_t stream);
 
 /*
  * mx_get_device_status -- synchronise `stream`, then report and clear the

@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libmxgb300.so")
 
 E4M3, E2M3, E2M1 = 0, 1, 2
 ROWWISE, COLWISE, HADAMARD, COLSUM = 1, 2, 4, 8
-ACT_SWIGLU, ACT_GELU_TANH = 0, 1
+ACT_SWIGLU, ACT_GELU_TANH, ACT_NONE, ACT_SILU, ACT_RELU = 0, 1, 2, 3, 4
+W_NK, W_KN = 0, 1
 
 STATUS = {
     0: "MX_OK", 1: "MX_ERR_INVALID_ARG", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGNMENT", 4: "MX_ERR_OFFSETS",
@@ -39,6 +40,8 @@ ABI_SYMBOLS = (
     "mx_moe_route_index", "mx_permute_quantize", "mx_moe_unpermute", "mx_grouped_gemm_bias", "mx_grouped_gemm_bias_2sm",
     "mx_grouped_gemm_wgrad_workspace_bytes", "mx_grouped_gemm_wgrad_ws", "mx_grouped_gemm_wgrad_f32_ws",
     "mx_mlp_workspace_layout", "mx_moe_route_rows_pad", "mx_moe_route_index_pad", "mx_grouped_gemm_2sm",
+    "mx_ragged_gemm", "mx_ragged_gemm_wgrad_workspace_bytes", "mx_ragged_gemm_wgrad", "mx_ragged_gemm_wgrad_f32",
+    "mx_linear_fwd", "mx_act_ckpt_fwd", "mx_act_ckpt_workspace_bytes", "mx_act_ckpt_bwd",
 )
 
 
@@ -136,6 +139,14 @@ def load(path=None):
         "mx_grouped_gemm_wgrad_workspace_bytes": (sz, [i64, i64, i64, i32]),
         "mx_grouped_gemm_wgrad_ws": (ctypes.c_int, [tp, tp, i32, vp, vp, vp, sz, vp]),
         "mx_grouped_gemm_wgrad_f32_ws": (ctypes.c_int, [tp, tp, i32, vp, vp, i32, vp, sz, vp]),
+        "mx_ragged_gemm": (ctypes.c_int, [vp, i64, i64, i64, vp, i64, i32, i32, vp, vp, i64, vp]),
+        "mx_ragged_gemm_wgrad_workspace_bytes": (sz, [i64, i64, i64, i32]),
+        "mx_ragged_gemm_wgrad": (ctypes.c_int, [vp, i64, i64, vp, i64, i64, i64, i32, vp, vp, vp, sz, vp]),
+        "mx_ragged_gemm_wgrad_f32": (ctypes.c_int, [vp, i64, i64, vp, i64, i64, i64, i32, vp, vp, i32, vp, sz, vp]),
+        "mx_linear_fwd": (ctypes.c_int, [vp, i64, i64, i64, vp, i64, vp, i32, vp, i64, vp, i64, tp, vp]),
+        "mx_act_ckpt_fwd": (ctypes.c_int, [vp, i64, i64, i64, i32, vp, i64, tp, vp]),
+        "mx_act_ckpt_workspace_bytes": (sz, [i64, i64]),
+        "mx_act_ckpt_bwd": (ctypes.c_int, [tp, i32, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp]),
         "mx_debug_tap": (ctypes.c_int, [vp, i64]),
         "mx_mlp_pipeline_create": (ctypes.c_int, [ctypes.POINTER(MlpArgsStruct), vp, ctypes.POINTER(vp)]),
         "mx_mlp_pipeline_run": (ctypes.c_int, [vp, ctypes.POINTER(HostIOStruct)]),
@@ -535,6 +546,142 @@ def mx_gemm_dgelu_bwd(dy_row, w2t_row, pre, dpre_row=None, dpre_col=None, db1=No
     _check(load().mx_gemm_dgelu_bwd(_s(dy_row), _s(w2t_row), _ptr(pre), _s(dpre_row), _s(dpre_col), _ptr(db1),
                                     _ptr(workspace), workspace.numel(), _stream(stream)))
     return dpre_row, dpre_col, db1
+
+
+# --------------------------------------------------------------------------
+# BF16 layers: ragged products, linear layer, 8-bit activation checkpoints
+# --------------------------------------------------------------------------
+
+def mx_ragged_gemm(a, w, offsets, layout=W_NK, out=None, stream=None):
+    """out[r] = a[r] w[g]^T (W_NK, w [G, N, K]) or a[r] w[g] (W_KN, w [G, K, N])
+    for the rows r of expert g's segment, of any length; BF16.  Rows past
+    the last segment are not written."""
+    import torch
+    assert a.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.is_contiguous() and w.dim() == 3
+    assert a.stride(1) == 1 and (offsets is None or offsets.dtype == torch.int32)
+    R, K = a.shape
+    G, N = w.shape[0], w.shape[1 if layout == W_NK else 2]
+    assert w.shape[2 if layout == W_NK else 1] == K and (offsets is None or offsets.numel() == G)
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=a.device)
+    assert out.shape == (R, N) and out.dtype == torch.bfloat16 and out.stride(1) == 1
+    _check(load().mx_ragged_gemm(a.data_ptr(), R, K, a.stride(0), w.data_ptr(), N, G, layout, _ptr(offsets),
+                                 out.data_ptr(), out.stride(0), _stream(stream)))
+    return out
+
+
+def mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G):
+    return int(load().mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G))
+
+
+def _ragged_wgrad_args(dy, x, G, offsets, workspace):
+    import torch
+    assert dy.dtype == torch.bfloat16 and x.dtype == torch.bfloat16 and dy.shape[0] == x.shape[0]
+    assert dy.stride(1) == 1 and x.stride(1) == 1
+    assert offsets is None or (offsets.dtype == torch.int32 and offsets.numel() == G)
+    R, N = dy.shape
+    K = x.shape[1]
+    if workspace is None:
+        n = mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return R, N, K, workspace, nbytes
+
+
+def mx_ragged_gemm_wgrad(dy, x, G, offsets, out=None, workspace=None, stream=None):
+    """Weight gradients [G, N, K] = dy_g^T x_g of ragged segments, BF16."""
+    import torch
+    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace)
+    if out is None:
+        out = torch.empty((G, N, K), dtype=torch.bfloat16, device=dy.device)
+    assert out.shape == (G, N, K) and out.dtype == torch.bfloat16 and out.is_contiguous()
+    _check(load().mx_ragged_gemm_wgrad(dy.data_ptr(), N, dy.stride(0), x.data_ptr(), K, x.stride(0), R, G,
+                                       _ptr(offsets), out.data_ptr(), _ptr(workspace), nbytes, _stream(stream)))
+    return out
+
+
+def mx_ragged_gemm_wgrad_f32(dy, x, G, offsets, grad, accumulate=False, workspace=None, stream=None):
+    """The weight gradients into the caller's fp32 buffer grad [G, N, K]:
+    stored (accumulate=False) or added to what it holds."""
+    import torch
+    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace)
+    assert grad.shape == (G, N, K) and grad.dtype == torch.float32 and grad.is_contiguous()
+    _check(load().mx_ragged_gemm_wgrad_f32(dy.data_ptr(), N, dy.stride(0), x.data_ptr(), K, x.stride(0), R, G,
+                                           _ptr(offsets), grad.data_ptr(), 1 if accumulate else 0, _ptr(workspace),
+                                           nbytes, _stream(stream)))
+    return grad
+
+
+def mx_linear_fwd(x, w, bias=None, act=ACT_NONE, residual=None, out=None, ckpt=None, stream=None):
+    """act(x w^T + bias) + residual in BF16 (x [M, K], w [N, K]); ckpt: an
+    E4M3 MX tensor [M, N] that receives the pre-activation in 8 bits."""
+    import torch
+    assert x.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.is_contiguous() and x.stride(1) == 1
+    M, K = x.shape
+    N = w.shape[0]
+    assert w.shape == (N, K)
+    assert bias is None or (bias.dtype == torch.bfloat16 and bias.shape == (N,) and bias.is_contiguous())
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    assert out.shape == (M, N) and out.dtype == torch.bfloat16 and out.stride(1) == 1
+    ld_res = 0
+    if residual is not None:
+        assert residual.shape == (M, N) and residual.dtype == torch.bfloat16 and residual.stride(1) == 1
+        ld_res = residual.stride(0)
+    _check(load().mx_linear_fwd(x.data_ptr(), M, K, x.stride(0), w.data_ptr(), N, _ptr(bias), act, _ptr(residual),
+                                ld_res, out.data_ptr(), out.stride(0), _s(ckpt), _stream(stream)))
+    return out
+
+
+def mx_act_ckpt_fwd(z, act, h=None, ckpt=None, stream=None):
+    """h = act(z) (SwiGLU: z [R, 2F] = [gate | up], h [R, F]) and z's 8-bit
+    checkpoint, in one pass: returns (h, MX [R, C])."""
+    import torch
+    assert z.dtype == torch.bfloat16 and z.stride(1) == 1
+    R, C = z.shape
+    if h is None:
+        h = torch.empty((R, C // 2 if act == ACT_SWIGLU else C), dtype=torch.bfloat16, device=z.device)
+    assert h.shape == (R, C // 2 if act == ACT_SWIGLU else C) and h.dtype == torch.bfloat16 and h.stride(1) == 1
+    if ckpt is None:
+        ckpt = MX(R, C, E4M3, False, z.device)
+    _check(load().mx_act_ckpt_fwd(z.data_ptr(), R, C, z.stride(0), act, h.data_ptr(), h.stride(0), _s(ckpt),
+                                  _stream(stream)))
+    return h, ckpt
+
+
+def mx_act_ckpt_workspace_bytes(R, C):
+    return int(load().mx_act_ckpt_workspace_bytes(R, C))
+
+
+def mx_act_ckpt_bwd(ckpt, act, dh, dz=None, recompute=False, h=None, colsum=False, db=None, workspace=None,
+                    stream=None):
+    """The activation's backward pass from the 8-bit checkpoint: returns
+    (dz [R, C], h or None, db or None): h = act of the checkpoint's values
+    when `recompute` or `h`, db = fp32 column sums of dz when `colsum` or `db`."""
+    import torch
+    assert dh.dtype == torch.bfloat16 and dh.stride(1) == 1
+    R, C = ckpt.rows, ckpt.cols
+    H = C // 2 if act == ACT_SWIGLU else C
+    assert dh.shape == (R, H)
+    dev = dh.device
+    if dz is None:
+        dz = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
+    assert dz.shape == (R, C) and dz.dtype == torch.bfloat16 and dz.stride(1) == 1
+    if h is None and recompute:
+        h = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
+    assert h is None or (h.shape == (R, H) and h.dtype == torch.bfloat16 and h.stride(1) == 1)
+    if db is None and colsum:
+        db = torch.empty(C, dtype=torch.float32, device=dev)
+    nbytes = 0
+    if db is not None:
+        assert db.shape == (C,) and db.dtype == torch.float32 and db.is_contiguous()
+        if workspace is None:
+            workspace = torch.empty(max(mx_act_ckpt_workspace_bytes(R, C), 16), dtype=torch.uint8, device=dev)
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(load().mx_act_ckpt_bwd(_s(ckpt), act, dh.data_ptr(), dh.stride(0), dz.data_ptr(), dz.stride(0), _ptr(h),
+                                  0 if h is None else h.stride(0), _ptr(db), _ptr(workspace), nbytes,
+                                  _stream(stream)))
+    return dz, h, db
 
 
 def mlp_args(x, w1, w2, dy, offsets, G, F, y, dx, dw1, dw2, workspace=None, act=ACT_SWIGLU, fmt=E4M3,

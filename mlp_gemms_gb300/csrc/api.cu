@@ -87,6 +87,17 @@ mx_status_t device_info(DevInfo* out) {
   return MX_OK;
 }
 
+}  // namespace
+
+mx_status_t mx::device_sms(int* sms) {
+  DevInfo d;
+  const mx_status_t st = device_info(&d);
+  *sms = d.sms;
+  return st;
+}
+
+namespace {
+
 // ---- TMA tensor maps ----------------------------------------------------
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -283,6 +294,12 @@ bool env_validate_offsets() {
   const char* v = getenv("MX_VALIDATE_OFFSETS");
   return v && v[0] == '1';
 }
+
+}  // namespace
+
+bool mx::validate_offsets_requested() { return env_validate_offsets(); }
+
+namespace {
 
 // MX_LOG=1: one line on stderr for each launch configuration the process
 // has not launched before (kernel, epilogue, tile width, shapes, grid), read
@@ -1611,16 +1628,18 @@ mx_status_t mx_mlp_fwd_bwd(const mx_mlp_args_t* a, mx_stream_t stream) { return 
 mx_status_t mx_get_device_status(mx_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-  unsigned word = 0, dense = 0, f4 = 0, quant = 0, perm = 0, pairs = 0;
+  unsigned word = 0, dense = 0, f4 = 0, quant = 0, perm = 0, pairs = 0, ragged = 0;
   if ((e = mx::read_gemm_status(&word)) != cudaSuccess || (e = mx::read_dense_status(&dense)) != cudaSuccess ||
       (e = mx::read_f4_status(&f4)) != cudaSuccess || (e = mx::read_quant_status(&quant)) != cudaSuccess ||
-      (e = mx::read_perm_status(&perm)) != cudaSuccess || (e = mx::read_pair_status(&pairs)) != cudaSuccess)
+      (e = mx::read_perm_status(&perm)) != cudaSuccess || (e = mx::read_pair_status(&pairs)) != cudaSuccess ||
+      (e = mx::read_ragged_status(&ragged)) != cudaSuccess)
     return cuda_fail(e, "reading device status");
   if ((e = mx::reset_gemm_status()) != cudaSuccess || (e = mx::reset_dense_status()) != cudaSuccess ||
       (e = mx::reset_f4_status()) != cudaSuccess || (e = mx::reset_quant_status()) != cudaSuccess ||
-      (e = mx::reset_perm_status()) != cudaSuccess || (e = mx::reset_pair_status()) != cudaSuccess)
+      (e = mx::reset_perm_status()) != cudaSuccess || (e = mx::reset_pair_status()) != cudaSuccess ||
+      (e = mx::reset_ragged_status()) != cudaSuccess)
     return cuda_fail(e, "clearing device status");
-  word |= dense | f4 | quant | perm | pairs;
+  word |= dense | f4 | quant | perm | pairs | ragged;
   if (word & 1u) return fail(MX_ERR_DEVICE_TIMEOUT, "a bounded device-side wait expired");
   if (word & 2u) return fail(MX_ERR_OFFSETS, "a kernel saw a malformed offsets segment");
   if (word & 4u) return fail(MX_ERR_INVALID_ARG, "a routing index (expert id or routed row) was out of range");

@@ -164,6 +164,70 @@ cudaError_t reset_perm_status();
 constexpr int kRouteChunk = 1024;
 cudaError_t launch_wait_selftest(uint64_t budget_ns, cudaStream_t s);
 
+// BF16 products over ragged segments (ragged.cu).
+struct RaggedEpi {           // mx_linear_fwd's epilogue; all null: plain store
+  const uint16_t* bias = nullptr;
+  int act = MX_ACT_NONE;
+  const uint16_t* res = nullptr;
+  int64_t ld_res = 0;
+  uint8_t* q = nullptr;      // E4M3 checkpoint payload [R, N]
+  uint8_t* q_scale = nullptr;
+};
+struct RaggedParams {
+  int G;
+  const int32_t* offsets;    // device [G], cumulative segment ends (null: one segment of R rows)
+  int64_t R, K, N;
+  const uint16_t* a;         // [R, K]
+  int64_t ld_a;
+  const uint16_t* w;         // [G, N, K] or (w_kn) [G, K, N]
+  int w_kn;
+  uint16_t* out;             // [R, N]
+  int64_t ld_out;
+  RaggedEpi epi;
+};
+cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t s);
+struct RaggedWgradParams {
+  int G;
+  const int32_t* offsets;
+  int64_t R, N, K;
+  const uint16_t* dy;        // [R, N]
+  int64_t ld_dy;
+  const uint16_t* x;         // [R, K]
+  int64_t ld_x;
+  uint16_t* grad;            // [G, N, K] BF16, or
+  float* grad_f32;           // fp32
+  int accumulate;
+};
+cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStream_t s);
+cudaError_t read_ragged_status(unsigned* out);
+cudaError_t reset_ragged_status();
+constexpr int MAX_RAGGED_G = 1024;  // experts the segment tables hold
+
+// 8-bit activation checkpoints (ckpt.cu).
+struct CkptParams {
+  int64_t R, C;
+  int act;
+  uint8_t* q;                // E4M3 payload [R, C]
+  uint8_t* q_scale;          // blocked E8M0 scales
+  const uint16_t* z;         // forward: input [R, C]
+  int64_t ld_z;
+  uint16_t* h;               // act output (backward: recomputed, or null)
+  int64_t ld_h;
+  const uint16_t* dh;        // backward
+  int64_t ld_dh;
+  uint16_t* dz;
+  int64_t ld_dz;
+  float* db;                 // column sums of dz, or null
+  float* partials;           // [ckpt_row_blocks(R)][C]
+};
+int64_t ckpt_row_blocks(int64_t R);
+cudaError_t launch_ckpt_fwd(const CkptParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_ckpt_bwd(const CkptParams& p, int num_sms, cudaStream_t s);
+
+// Host helpers of the ABI layer shared by its translation units (api.cu).
+mx_status_t device_sms(int* sms);   // checks the device; its SM count
+bool validate_offsets_requested();  // MX_VALIDATE_OFFSETS=1
+
 // The tensors of one MLP step that the host pipeline moves: raw inputs the
 // step reads once (X, W1, W2, dY, b1, b2) and outputs it writes (y, dX, dW1,
 // dW2, db1, db2).

@@ -1,0 +1,375 @@
+"""The BF16 ragged products and the linear layer against a plain fp64
+implementation: segment lengths from none to long, odd sizes, strides,
+non-finite neighbours, refusals on the device.
+
+Tolerances.  Products of BF16 values are exact in fp32; the kernels add K of
+them in fp32 with any order of sums.  With the sums' magnitudes S = sum |a b|
+the fp32 error is at most K * 2^-23 * S per value (2^-23: an accumulator that
+truncates), rounding to BF16 adds 2^-8 relative to the result, half a unit
+being 2^-9, doubled to keep clear of the bound itself.
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _bf16(shape, gen, std=1.0):
+    return (torch.randn(shape, generator=gen, dtype=torch.float32) * std).to(torch.bfloat16).cuda()
+
+
+def _offsets(counts):
+    return torch.tensor(np.cumsum(counts), dtype=torch.int32).cuda()
+
+
+def _check(got, ref, mag, K, rel):
+    """|got - ref| <= rel |ref| + K 2^-23 mag (+ the smallest BF16 normal)."""
+    got, ref = got.double(), ref.double()
+    bound = rel * ref.abs() + K * 2.0 ** -23 * mag.double() + 2.0 ** -126
+    bad = ~((got - ref).abs() <= bound)
+    assert not bad.any(), "%d of %d values off, worst %.3g x the bound" % (
+        int(bad.sum()), bad.numel(), float(((got - ref).abs() / bound).max()))
+
+
+def _ragged_ref(a, w, counts, kn):
+    ref = torch.zeros((a.shape[0], w.shape[2 if kn else 1]), dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(ref)
+    b = 0
+    for g, c in enumerate(counts):
+        m = w[g].double() if kn else w[g].double().T
+        ref[b:b + c] = a[b:b + c].double() @ m
+        mag[b:b + c] = a[b:b + c].double().abs() @ m.abs()
+        b += c
+    return ref, mag
+
+
+COUNTS = {
+    "one row": [1],
+    "one row of many experts": [0] * 5 + [1] + [0] * 6,
+    "eight single rows": [1, 0, 1, 1, 0, 0, 1, 1, 1, 1, 0, 1],
+    "empty ends": [0, 3, 0, 0, 129, 0],
+    "tile edges": [127, 128, 129, 255, 256, 257, 1, 31, 33],
+    "one long": [0, 0, 1500, 0],
+    "many": [(7 * i * i) % 41 for i in range(128)],
+}
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["NK", "KN"])
+@pytest.mark.parametrize("N,K", [(8, 8), (64, 72), (200, 136), (256, 64), (328, 520), (1032, 264)])
+@pytest.mark.parametrize("name", list(COUNTS))
+def test_ragged_gemm(cuda_lib, name, N, K, kn):
+    mx = cuda_lib
+    counts = COUNTS[name]
+    R, G = sum(counts), len(counts)
+    gen = torch.Generator().manual_seed(R * 7 + N + K)
+    a = _bf16((R, K), gen)
+    w = _bf16((G, K, N) if kn else (G, N, K), gen)
+    out = mx.mx_ragged_gemm(a, w, _offsets(counts), layout=mx.W_KN if kn else mx.W_NK)
+    assert mx.mx_get_device_status() == "MX_OK"
+    ref, mag = _ragged_ref(a, w, counts, kn)
+    _check(out, ref, mag, K, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["NK", "KN"])
+@pytest.mark.parametrize("R", [1, 2, 7, 8, 9, 16, 17, 31, 33, 64, 65, 100, 128, 129, 300])
+def test_ragged_gemm_row_counts(cuda_lib, R, kn):
+    """Every row count around the kernels' tile heights, one segment, no offsets."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(R)
+    N, K = 264, 1096
+    a = _bf16((R, K), gen)
+    w = _bf16((1, K, N) if kn else (1, N, K), gen)
+    out = mx.mx_ragged_gemm(a, w, None, layout=mx.W_KN if kn else mx.W_NK)
+    ref, mag = _ragged_ref(a, w, [R], kn)
+    _check(out, ref, mag, K, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("R", [5, 700])
+@pytest.mark.parametrize("kn", [False, True], ids=["NK", "KN"])
+def test_ragged_gemm_strides_and_untouched_rows(cuda_lib, kn, R):
+    """Row strides wider than the rows; rows past the last segment and the
+    columns past N of the output's rows keep what they held."""
+    mx = cuda_lib
+    counts = [R // 3, 0, R - R // 3]
+    gen = torch.Generator().manual_seed(3 + R)
+    K, N, tail = 152, 168, 9
+    abuf = _bf16((R + tail, K + 24), gen)
+    a = abuf[:, 8:8 + K]
+    w = _bf16((3, K, N) if kn else (3, N, K), gen)
+    obuf = torch.full((R + tail, N + 40), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = obuf[:, 16:16 + N]
+    mx.mx_ragged_gemm(a, w, _offsets(counts), layout=mx.W_KN if kn else mx.W_NK, out=out)
+    ref, mag = _ragged_ref(a[:R], w, counts, kn)
+    _check(out[:R], ref, mag, K, 2.0 ** -8)
+    obuf[:R, 16:16 + N] = 7.0
+    assert bool((obuf == 7.0).all())
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["NK", "KN"])
+def test_ragged_gemm_nonfinite_neighbours(cuda_lib, kn):
+    """NaN and Inf in one expert's rows, in its weights and past the last
+    segment reach no other expert's results."""
+    mx = cuda_lib
+    counts = [5, 130, 3, 260]
+    R, N, K = sum(counts), 136, 200
+    gen = torch.Generator().manual_seed(11)
+    a = _bf16((R + 4, K), gen)
+    w = _bf16((4, K, N) if kn else (4, N, K), gen)
+    a[5:135] = float("nan")
+    w[1] = float("inf")
+    a[R:] = float("nan")
+    out = mx.mx_ragged_gemm(a, w, _offsets(counts), layout=mx.W_KN if kn else mx.W_NK)
+    keep = torch.ones(R, dtype=torch.bool, device="cuda")
+    keep[5:135] = False
+    a2, w2 = a[:R].clone(), w.clone()
+    a2[5:135], w2[1] = 0, 0
+    ref, mag = _ragged_ref(a2, w2, counts, kn)
+    _check(out[:R][keep], ref[keep], mag[keep], K, 2.0 ** -8)
+    assert bool(out[5:135].isnan().all())
+
+
+def test_ragged_gemm_malformed_offsets(cuda_lib):
+    """A decreasing segment and one past R are skipped and reported; the
+    others are computed."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(2)
+    R, N, K = 40, 64, 64
+    a, w = _bf16((R, K), gen), _bf16((3, N, K), gen)
+    out = torch.full((R, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    mx.mx_ragged_gemm(a, w, torch.tensor([10, 4, 99], dtype=torch.int32, device="cuda"), out=out)
+    assert mx.mx_get_device_status() == "MX_ERR_OFFSETS"
+    assert mx.mx_get_device_status() == "MX_OK"
+    ref, mag = _ragged_ref(a[:10], w[:1], [10], False)
+    _check(out[:10], ref, mag, K, 2.0 ** -8)
+    assert bool((out[10:] == 3.0).all())
+
+
+def test_ragged_gemm_validates_on_request(cuda_lib, monkeypatch):
+    mx = cuda_lib
+    a = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((2, 64, 64), dtype=torch.bfloat16, device="cuda")
+    monkeypatch.setenv("MX_VALIDATE_OFFSETS", "1")
+    for bad in ([5, 3], [4, 9]):
+        with pytest.raises(mx.MXError, match="OFFSETS"):
+            mx.mx_ragged_gemm(a, w, torch.tensor(bad, dtype=torch.int32, device="cuda"))
+    mx.mx_ragged_gemm(a, w, torch.tensor([5, 8], dtype=torch.int32, device="cuda"))
+
+
+def test_ragged_gemm_on_another_stream_and_graph(cuda_lib):
+    """The call goes to the given stream only, and can be captured and
+    replayed with other offsets in the same buffer."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(5)
+    R, N, K, G = 333, 264, 128, 4
+    a, w = _bf16((R, K), gen), _bf16((G, N, K), gen)
+    off = _offsets([100, 0, 200, 33])
+    out = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        mx.mx_ragged_gemm(a, w, off, out=out)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.mx_ragged_gemm(a, w, off, out=out)
+    for counts in ([1, 2, 329, 1], [0, 0, 0, 333]):
+        off.copy_(_offsets(counts))
+        graph.replay()
+        ref, mag = _ragged_ref(a, w, counts, False)
+        _check(out, ref, mag, K, 2.0 ** -8)
+
+
+def test_ragged_gemm_past_two_gib_of_elements(cuda_lib):
+    """Row offsets past 2^31 elements: a strided view whose last rows lie
+    beyond them."""
+    mx = cuda_lib
+    R, K, N, ld = 300, 64, 64, 1 << 23
+    gen = torch.Generator().manual_seed(9)
+    buf = torch.empty(R * ld, dtype=torch.bfloat16, device="cuda")
+    a = buf.view(R, ld)[:, :K]
+    a.copy_(_bf16((R, K), gen))
+    w = _bf16((2, N, K), gen)
+    out = buf.view(R, ld)[:, 128:128 + N]
+    mx.mx_ragged_gemm(a, w, _offsets([17, 283]), out=out)
+    ref, mag = _ragged_ref(a, w, [17, 283], False)
+    _check(out, ref, mag, K, 2.0 ** -8)
+
+
+# ------------------------------------------------------------------ gradients
+
+@pytest.mark.parametrize("N,K", [(8, 8), (64, 136), (136, 64), (264, 200), (520, 392)])
+@pytest.mark.parametrize("name", list(COUNTS))
+@pytest.mark.parametrize("kind", ["bf16", "f32", "acc"])
+def test_ragged_wgrad(cuda_lib, name, N, K, kind):
+    mx = cuda_lib
+    counts = COUNTS[name]
+    R, G = sum(counts), len(counts)
+    gen = torch.Generator().manual_seed(R + N * 3 + K)
+    dy, x = _bf16((R, N), gen), _bf16((R, K), gen)
+    off = _offsets(counts)
+    if kind == "bf16":
+        got = mx.mx_ragged_gemm_wgrad(dy, x, G, off)
+    else:
+        got = torch.randn((G, N, K), generator=gen).cuda()
+        before = got.double()
+        mx.mx_ragged_gemm_wgrad_f32(dy, x, G, off, got, accumulate=kind == "acc")
+    assert mx.mx_get_device_status() == "MX_OK"
+    b = 0
+    for g, c in enumerate(counts):
+        d, e = dy[b:b + c].double(), x[b:b + c].double()
+        ref, mag = d.T @ e, d.abs().T @ e.abs()
+        if kind == "acc":
+            ref = ref + before[g]
+        _check(got[g], ref, mag, max(c, 1), 2.0 ** -8 if kind == "bf16" else 2.0 ** -23)
+        if c == 0:
+            assert torch.equal(got[g].double(), ref)
+        b += c
+
+
+def test_ragged_wgrad_nonfinite_neighbours_and_strides(cuda_lib):
+    """Rows of other experts and past the last segment that hold NaN and Inf,
+    read through strided views, reach no other expert's gradient."""
+    mx = cuda_lib
+    counts = [3, 70, 129, 1, 64]
+    R, N, K = sum(counts), 136, 72
+    gen = torch.Generator().manual_seed(21)
+    dy = _bf16((R + 20, N + 16), gen)[:, 8:8 + N]
+    x = _bf16((R + 20, K + 8), gen)[:, :K]
+    dy[3:73], x[3:73] = float("nan"), float("inf")
+    dy[R:], x[R:] = float("inf"), float("nan")
+    got = mx.mx_ragged_gemm_wgrad(dy, x, 5, _offsets(counts))
+    b = 0
+    for g, c in enumerate(counts):
+        if g != 1:
+            d, e = dy[b:b + c].double(), x[b:b + c].double()
+            _check(got[g], d.T @ e, d.abs().T @ e.abs(), c, 2.0 ** -8)
+        b += c
+    assert bool(got[1].isnan().all())
+
+
+def test_ragged_wgrad_is_deterministic_and_takes_no_rows(cuda_lib):
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(4)
+    counts = [2000, 0, 3, 5000]
+    R, N, K = sum(counts), 264, 520
+    dy, x = _bf16((R, N), gen), _bf16((R, K), gen)
+    first = mx.mx_ragged_gemm_wgrad(dy, x, 4, _offsets(counts))
+    for _ in range(3):
+        assert torch.equal(first, mx.mx_ragged_gemm_wgrad(dy, x, 4, _offsets(counts)))
+    none = torch.empty((0, N), dtype=torch.bfloat16, device="cuda")
+    g = mx.mx_ragged_gemm_wgrad(none, torch.empty((0, K), dtype=torch.bfloat16, device="cuda"), 2,
+                                torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert not bool(g.any())
+
+
+def test_ragged_wgrad_long_segment_fp32(cuda_lib):
+    """A long sum in fp32: 2-norm error within 2e-5 of the result's."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(8)
+    R, N, K = 65536, 64, 128
+    dy, x = _bf16((R, N), gen), _bf16((R, K), gen)
+    got = mx.mx_ragged_gemm_wgrad_f32(dy, x, 1, None, torch.empty((1, N, K), device="cuda"))[0].double()
+    ref = dy.double().T @ x.double()
+    assert float((got - ref).norm() / ref.norm()) < 2e-5
+
+
+def test_gradients_are_the_products_derivatives(cuda_lib):
+    """dX and dW of sum(out * dY) against finite differences.  out is linear
+    in a and in w, so a difference over a step h has no error of its own but
+    the rounding of the fp64 reference of out."""
+    mx = cuda_lib
+    counts = [5, 0, 12]
+    R, N, K, G = 17, 40, 24, 3
+    gen = torch.Generator().manual_seed(6)
+    a, w, dy = _bf16((R, K), gen), _bf16((G, N, K), gen), _bf16((R, N), gen)
+    off = _offsets(counts)
+    dx = mx.mx_ragged_gemm(dy, w, off, layout=mx.W_KN)
+    dw = mx.mx_ragged_gemm_wgrad(dy, a, G, off)
+
+    def value(a, w):
+        return float((_ragged_ref(a, w, counts, False)[0] * dy.double()).sum())
+
+    rng = np.random.default_rng(0)
+    for _ in range(12):
+        r, k = int(rng.integers(R)), int(rng.integers(K))
+        up, dn = a.double(), a.double()
+        up[r, k] += 0.5
+        dn[r, k] -= 0.5
+        diff = value(up, w) - value(dn, w)
+        assert abs(diff - float(dx[r, k])) <= 2.0 ** -8 * abs(diff) + 1e-3
+        g, n = int(rng.choice([0, 2])), int(rng.integers(N))
+        up, dn = w.double(), w.double()
+        up[g, n, k] += 0.5
+        dn[g, n, k] -= 0.5
+        diff = value(a, up) - value(a, dn)
+        assert abs(diff - float(dw[g, n, k])) <= 2.0 ** -8 * abs(diff) + 1e-3
+
+
+# --------------------------------------------------------------- linear layer
+
+def _act(z, act, mx):
+    if act == mx.ACT_RELU:
+        return z.clamp(min=0)
+    if act == mx.ACT_SILU:
+        return z * torch.sigmoid(z)
+    if act == mx.ACT_GELU_TANH:
+        return 0.5 * z * (1 + torch.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)))
+    return z
+
+
+@pytest.mark.parametrize("act", ["NONE", "GELU_TANH", "SILU", "RELU"])
+@pytest.mark.parametrize("bias,res", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("M,N,K", [(1, 264, 520), (3, 8, 16), (33, 136, 72), (130, 512, 256), (300, 328, 1000)])
+def test_linear(cuda_lib, act, bias, res, M, N, K):
+    mx = cuda_lib
+    act = getattr(mx, "ACT_" + act)
+    gen = torch.Generator().manual_seed(M + N + K)
+    x, w = _bf16((M, K), gen), _bf16((N, K), gen, K ** -0.5)
+    b = _bf16((N,), gen) if bias else None
+    r = _bf16((M, N), gen) if res else None
+    out = mx.mx_linear_fwd(x, w, b, act, r)
+    assert mx.mx_get_device_status() == "MX_OK"
+    z = x.double() @ w.double().T
+    mag = x.double().abs() @ w.double().abs().T
+    if bias:
+        z, mag = z + b.double(), mag + b.double().abs()
+    h = _act(z, act, mx)
+    ref = h + r.double() if res else h
+    # activations: slope at most 1.13, and 2^-18 relative for their own fp32 arithmetic
+    _check(out, ref, 1.13 * mag + h.abs() * (2.0 ** 5 / K) + (r.double().abs() / K if res else 0), K, 2.0 ** -8)
+
+
+def test_linear_residual_in_place_and_strides(cuda_lib):
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(1)
+    for M in (4, 200):
+        N, K = 136, 264
+        x, w = _bf16((M, K + 8), gen)[:, :K], _bf16((N, K), gen, 0.1)
+        buf = _bf16((M, N + 24), gen)
+        before = buf.clone()
+        out = buf[:, 8:8 + N]
+        mx.mx_linear_fwd(x, w, None, mx.ACT_NONE, out, out=out)
+        ref = x.double() @ w.double().T + before[:, 8:8 + N].double()
+        mag = x.double().abs() @ w.double().abs().T + before[:, 8:8 + N].double().abs()
+        _check(out, ref, mag, K, 2.0 ** -8)
+        buf[:, 8:8 + N] = before[:, 8:8 + N]
+        assert torch.equal(buf, before)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 32, 64), (5, 160, 136), (127, 256, 64), (129, 544, 72), (700, 1056, 128)])
+def test_linear_checkpoint_bytes(cuda_lib, M, N, K):
+    """On exact data (small integers: every sum is exact in fp32 and in BF16)
+    the checkpoint is the quantizer's rowwise output, byte for byte, scale
+    padding included."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(M)
+    x = torch.randint(-1, 2, (M, K), generator=gen).to(torch.bfloat16).cuda()
+    w = torch.randint(-1, 2, (N, K), generator=gen).to(torch.bfloat16).cuda()
+    ck = mx.MX(M, N)
+    ck.scale.fill_(0xAB)
+    out = mx.mx_linear_fwd(x, w, None, mx.ACT_RELU, ckpt=ck)
+    z = (x.float() @ w.float().T).to(torch.bfloat16)
+    ref, _, _ = mx.mx_quantize(z, mx.E4M3, True, False)
+    assert torch.equal(out, z.clamp(min=0))
+    assert torch.equal(ck.data, ref.data) and torch.equal(ck.scale, ref.scale)
