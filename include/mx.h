@@ -687,9 +687,9 @@ MX_API void mx_mlp_pipeline_destroy(mx_mlp_pipeline_t *p);
  * Offsets here: device int32 [G], cumulative END offsets of each expert's
  * rows, nondecreasing, any values in [0, R].  Rows in [offsets[G-1], R) are
  * neither read nor written.  With G == 1 a NULL offsets means all R rows.  A
- * segment that decreases or passes R is skipped on the device and reported
- * as MX_ERR_OFFSETS by mx_get_device_status (on the host, before any
- * launch, with MX_VALIDATE_OFFSETS=1).  G <= 1024, else
+ * segment that decreases, begins before an earlier one's end or passes R
+ * counts as empty and is reported as MX_ERR_OFFSETS by mx_get_device_status
+ * (on the host, before any launch, with MX_VALIDATE_OFFSETS=1).  G <= 1024, else
  * MX_ERR_NOT_SUPPORTED.  K and N are multiples of 8, leading dimensions
  * multiples of 8 elements and at least the row length; row counts have no
  * alignment.  Non-finite values of one expert's rows reach no other

@@ -241,6 +241,24 @@ mx_status_t make_tmap_bytes(CUtensorMap* m, const void* base, int64_t rows, int6
   return MX_OK;
 }
 
+}  // namespace
+
+mx_status_t mx::encode_bf16_map(CUtensorMap* m, const void* base, const TensorMapShape& s) {
+  mx_status_t st = get_encoder();
+  if (st != MX_OK) return st;
+  cuuint64_t dims[3], strides[2];
+  cuuint32_t box[3], estr[3] = {1, 1, 1};
+  for (int i = 0; i < s.rank; i++) { dims[i] = s.dims[i]; box[i] = s.box[i]; }
+  for (int i = 0; i + 1 < s.rank; i++) strides[i] = s.strides[i];
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)s.rank, const_cast<void*>(base), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MX_ERR_CUDA, "cuTensorMapEncodeTiled (BF16 operand) failed (%d)", (int)r);
+  return MX_OK;
+}
+
+namespace {
+
 // The quantizer stages E4M3 and E2M1 tiles in shared memory and stores
 // them with TMA: box 128 bytes (E4M3, 128 elements) or 64 bytes (E2M1).
 bool staged(int fmt) { return fmt == MX_E4M3 || fmt == MX_E2M1; }

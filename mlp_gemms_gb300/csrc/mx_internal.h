@@ -226,6 +226,13 @@ cudaError_t launch_ckpt_bwd(const CkptParams& p, int num_sms, cudaStream_t s);
 
 // Host helpers of the ABI layer shared by its translation units (api.cu).
 mx_status_t device_sms(int* sms);   // checks the device; its SM count
+struct TensorMapShape {              // innermost dimension first; strides (bytes) of dimensions 1, 2
+  int rank;
+  uint64_t dims[3], strides[2];
+  uint32_t box[3];
+};
+// A BF16 tensor as a TMA operand: 128-byte swizzle, out-of-range elements zero.
+mx_status_t encode_bf16_map(CUtensorMap* m, const void* base, const TensorMapShape& s);
 bool validate_offsets_requested();  // MX_VALIDATE_OFFSETS=1
 
 // The tensors of one MLP step that the host pipeline moves: raw inputs the

@@ -1,149 +1,691 @@
-// BF16 products over ragged expert segments (any length, no padding): the
-// grouped product with W [G, N, K] or [G, K, N], the weight gradient, and the
-// dense linear layer's epilogue.
+// BF16 products over ragged expert segments (any length, no padding) on the
+// 5th-generation tensor core: the grouped product with W [G, N, K] or
+// [G, K, N], the weight gradient, and the dense linear layer's epilogue.
+//
+// One kernel computes out[t, f] = sum_k Q[t, k] P[f, k].  P is the side whose
+// index runs along the output's rows in memory: the weights' features for the
+// forward product and the input gradient, X's columns for the weight
+// gradient.  P takes the MMA's M = 256 rows of a CTA pair (tcgen05
+// .cta_group::2, 128 rows per CTA), Q the N side, whose width follows the
+// segment: a tile holds up to 256 tokens and rounds them to 32.  Expert
+// segments are short and ragged (tokens) while features are long and even, so
+// the padding is at most 31 tokens per expert instead of up to 255, and a
+// decode step's few tokens cost an N = 32 MMA under a weight stream that stays
+// bound by memory.  Both operands may be K-major (rows of K) or MN-major
+// (rows of the contraction index), so no operand is transposed in memory:
+//
+//            P (M side)                    Q (N side)
+//   NK       W[g] [N, K]   K-major         A [R, K]   K-major
+//   KN       W[g] [K, N]   MN-major        A [R, K]   K-major
+//   WGRAD    X [R, K]      MN-major        dY [R, N]  MN-major
+//
+// Accumulators (128 lanes x 256 fp32 columns, two of them) live in tensor
+// memory; while the eight epilogue warps drain one, the MMA thread fills the
+// other.  A lane of the accumulator is a feature, a column a token, so the
+// epilogue reads it in 8x8 fragments (tcgen05.ld 16x256b) and turns it with
+// stmatrix.trans: rows of 32 features leave as 64-byte row pieces.
+//
+// The weight gradient contracts over a segment's rows.  Its last 64-row block
+// may hold rows of the next expert: those blocks are copied on the CTA's own
+// barrier, a helper warp zeroes the rows up to the next multiple of 16 in both
+// operands (a zero against a neighbour's Inf or NaN would be NaN) and only
+// then hands the stage to the MMA thread, which runs the 16-row steps that
+// hold rows of the segment.
+//
+// Every wait is bounded; on expiry the CTA records a device status bit and
+// unwinds.
 #include "act.cuh"
 #include "mx_internal.h"
+#include "pair_common.cuh"
 
 namespace mx {
 
 static __device__ unsigned g_ragged_status = 0;
 
-// Segment g of the offsets as [begin, end); false (and the status bit) when
-// it decreases or passes R.
-__device__ __forceinline__ bool segment(const int32_t* offsets, int g, int64_t R, int64_t* begin, int64_t* end) {
-  *begin = (offsets && g) ? (int64_t)__ldg(offsets + g - 1) : 0;
-  *end = offsets ? (int64_t)__ldg(offsets + g) : R;
-  if (*begin < 0 || *end < *begin || *end > R) {
-    atomicOr(&g_ragged_status, DEV_BAD_OFFSETS);
-    return false;
+namespace rg {
+constexpr int THREADS = 384;  // warps: 0 copies, 1 MMAs, 2 segment tails, 4..11 epilogue
+constexpr int ST = 6;         // 32 KB stages of 64 contraction steps
+constexpr int BK = 64;
+constexpr int P_BYTES = 16384, Q_BYTES = 16384;
+constexpr int OFF_Q = ST * P_BYTES;
+constexpr int STG = 2560;     // per epilogue warp: 32 rows x (64 + 16) bytes
+constexpr int OFF_STG = OFF_Q + ST * Q_BYTES;
+constexpr int OFF_SEG = OFF_STG + 8 * STG;                  // segment ends, [0] = 0
+constexpr int OFF_PREF = OFF_SEG + 4 * (MAX_RAGGED_G + 1);  // row tiles before expert g
+constexpr int OFF_BAR = (OFF_PREF + 4 * (MAX_RAGGED_G + 1) + 7) / 8 * 8;
+constexpr int NUM_BARS = 3 * ST + 5;
+constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+constexpr int SMEM = OFF_MISC + 16 + 1024;                  // + slack for 1024-byte alignment
+static_assert(SMEM <= 232448, "shared memory per CTA");
+}  // namespace rg
+
+enum RaggedMode : int { RAGGED_NK = 0, RAGGED_KN = 1, RAGGED_WGRAD = 2 };
+
+struct RaggedK {
+  int G;
+  const int32_t* offsets;
+  int64_t R;
+  int64_t N;               // output columns (the P side's extent)
+  int64_t K;               // contraction (WGRAD: the Q side's extent instead)
+  int n_f;                 // 256-column tiles of the output
+  int n_t;                 // WGRAD: 256-row tiles of an expert's output
+  void* out;
+  int64_t ld_out;          // elements; WGRAD: N
+  int accumulate;
+  RaggedEpi epi;
+};
+
+struct RaggedTile {
+  int g;
+  int64_t t0;              // first output row (WGRAD: of the expert's matrix)
+  int valid;               // rows of the tile in the output
+  int nt;                  // the MMA's N: valid rounded up to 32
+  int64_t f0;              // first output column of the pair's 256
+  int nk;                  // 64-step blocks of the contraction
+  int64_t k0;              // WGRAD: first row of the contraction
+  int rem;                 // contraction steps in the last block (1..64)
+  int part, parts;         // WGRAD into fp32: this pass over the tile, and how many it takes
+};
+
+// Rows the fp32 weight gradient sums in tensor memory before it adds the sum
+// to memory.  The tensor core's fp32 accumulation truncates, a drift towards
+// zero of about 2^-26 per 16-row step: 7.6e-5 of the result after 65536 rows
+// (measured), against the 1e-7 of fp32 sums rounded to nearest.  4096 rows
+// keep it below 5e-6 and cost one read and write of the tile per 4 MB of
+// operands.  A BF16 result (2e-3 from its own rounding) takes one pass.
+constexpr int F32_ROWS = 4096;
+
+template <int MODE, bool F32>
+__device__ __forceinline__ bool ragged_tile(const RaggedK& p, const int32_t* seg, const int32_t* pref, int64_t t,
+                                            int part, RaggedTile* T) {
+  T->part = part;
+  T->parts = 1;
+  if constexpr (MODE == RAGGED_WGRAD) {
+    const int per = p.n_f * p.n_t;
+    if (t >= (int64_t)p.G * per) return false;
+    T->g = (int)(t / per);
+    const int r = (int)(t - (int64_t)T->g * per);
+    T->t0 = (int64_t)(r / p.n_f) * 256;
+    T->f0 = (int64_t)(r % p.n_f) * 256;
+    const int64_t left = p.K - T->t0;
+    T->valid = left < 256 ? (int)left : 256;
+    T->k0 = seg[T->g];
+    int rows = pref[T->g + 1] - pref[T->g];  // rows of the segment, 0 if malformed
+    if constexpr (F32) {
+      T->parts = rows > F32_ROWS ? (rows + F32_ROWS - 1) / F32_ROWS : 1;
+      T->k0 += (int64_t)part * F32_ROWS;
+      rows -= part * F32_ROWS;
+      if (rows > F32_ROWS) rows = F32_ROWS;
+    }
+    T->nk = (rows + rg::BK - 1) / rg::BK;
+    T->rem = rows - (T->nk - 1) * rg::BK;
+  } else {
+    const int64_t mt = t / p.n_f;
+    if (mt >= pref[p.G]) return false;
+    int lo = 0, hi = p.G - 1;  // the expert with pref[g] <= mt < pref[g + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pref[mid] <= mt) lo = mid; else hi = mid - 1;
+    }
+    T->g = lo;
+    T->t0 = (int64_t)seg[lo] + 256 * (mt - pref[lo]);
+    T->f0 = (t - mt * p.n_f) * 256;
+    const int64_t left = (int64_t)seg[lo + 1] - T->t0;
+    T->valid = left < 256 ? (int)left : 256;
+    T->k0 = 0;
+    T->nk = (int)((p.K + rg::BK - 1) / rg::BK);
+    T->rem = (int)(p.K - (int64_t)(T->nk - 1) * rg::BK);
   }
+  T->nt = (T->valid + 31) & ~31;
   return true;
 }
 
-constexpr int TS = 64, TK = 16;
-
-// acc[i][j] += sum_k A(m, k) B(n, k) for a 64 x 64 tile, both read through
-// strides; 256 threads, 4 x 4 values each.
-__device__ __forceinline__ void tile_product(const uint16_t* a, int64_t sam, int64_t sak, int64_t m, const uint16_t* b,
-                                             int64_t sbn, int64_t sbk, int64_t n, int64_t k, float (&acc)[4][4]) {
-  __shared__ float sa[TK][TS + 1], sb[TK][TS + 1];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int64_t k0 = 0; k0 < k; k0 += TK) {
-    for (int i = threadIdx.x; i < TS * TK; i += 256) {
-      const int r = i / TK, c = i % TK;
-      sa[c][r] = (r < m && k0 + c < k) ? bf16_bits_to_float(a[r * sam + (k0 + c) * sak]) : 0.f;
-      sb[c][r] = (r < n && k0 + c < k) ? bf16_bits_to_float(b[r * sbn + (k0 + c) * sbk]) : 0.f;
+// The pair's passes in order: each of its tiles, and of a tile each part.
+template <int MODE, bool F32>
+struct RaggedWalk {
+  int64_t t, step;
+  int part;
+  __device__ RaggedWalk(int64_t first, int64_t step_) : t(first), step(step_), part(0) {}
+  __device__ __forceinline__ bool next(const RaggedK& p, const int32_t* seg, const int32_t* pref, RaggedTile* T) {
+    if (!ragged_tile<MODE, F32>(p, seg, pref, t, part, T)) return false;
+    if (++part >= T->parts) {
+      part = 0;
+      t += step;
     }
-    __syncthreads();
-    for (int c = 0; c < TK; c++)
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tma2_load_3d_hint(void* dst, const CUtensorMap* m, int c0, int c1, int c2,
+                                                  uint32_t bar_cl, uint64_t pol) {
+  asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+               " [%0], [%1, {%2, %3, %4}], [%5], %6;"
+               :: "r"(smem_u32(dst)), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cl), "l"(pol) : "memory");
+}
+
+__device__ __forceinline__ void tc2_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// 16 lanes x 32 columns of tensor memory as four 8-column groups: registers
+// 4j, 4j + 1 hold columns 8j + 2 (lane % 4) + {0, 1} of lane lane / 4,
+// registers 4j + 2, 4j + 3 those of lane lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&r)[16]) {
+  uint32_t u[16];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+                 "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+               : "r"(taddr));
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+  for (int i = 0; i < 16; i++) r[i] = __uint_as_float(u[i]);
+}
+
+// Four 8x8 matrices of 16-bit values, transposed on the way: lane 8m + i
+// gives the address of the row that receives column i of matrix m.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+               :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_values(float (&v)[2][16]) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = fmaf(sa[c][ty * 4 + i], sb[c][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+  for (int i = 0; i < 16; i++) {
+    v[0][i] = act_f32<ACT>(v[0][i]);
+    v[1][i] = act_f32<ACT>(v[1][i]);
   }
 }
 
-__device__ __forceinline__ float act_any(float z, int act) {
-  return act == MX_ACT_RELU ? act_f32<MX_ACT_RELU>(z)
-         : act == MX_ACT_SILU ? act_f32<MX_ACT_SILU>(z)
-         : act == MX_ACT_GELU_TANH ? act_f32<MX_ACT_GELU_TANH>(z) : z;
-}
-
-__device__ __forceinline__ uint16_t bf16_of(float v) { return (uint16_t)float2_to_bf16x2(v, 0.f); }
-
-__global__ void __launch_bounds__(256) ragged_gemm_simple(const RaggedParams p) {
-  __shared__ int64_t s_m0, s_rows;
-  __shared__ int s_g;
-  if (threadIdx.x == 0) {
-    int64_t t = blockIdx.y;
-    s_g = -1;
-    for (int g = 0; g < p.G; g++) {
-      int64_t b, e;
-      if (!segment(p.offsets, g, p.R, &b, &e)) continue;
-      const int64_t n = (e - b + TS - 1) / TS;
-      if (t < n) {
-        s_g = g; s_m0 = b + t * TS; s_rows = e - s_m0 < TS ? e - s_m0 : TS;
-        break;
+// The 8-bit checkpoint of a 32-feature x 32-token block (one scale block per
+// token).  A thread holds four features of eight tokens: the amax of a token
+// is a maximum over those and over the eight lanes that share its tokens.
+// Codes of features f and f + 8 (one thread's) travel as one 16-bit value
+// through stmatrix.trans and are separated again on the way out.
+__device__ __forceinline__ void ckpt_block(const RaggedK& p, const float (&v)[2][16], uint8_t* stg, int lane,
+                                           int64_t row0, int valid, int64_t col) {
+  const uint32_t base = smem_u32(stg);
+  uint8_t* sbytes = stg + 32 * 48;
+#pragma unroll
+  for (int jj = 0; jj < 2; jj++) {
+    uint32_t w[2][2];
+#pragma unroll
+    for (int j2 = 0; j2 < 2; j2++) {
+      const int j = 2 * jj + j2;
+      uint32_t code[2][2];  // [features' half][token]
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        float m = max_abs_nan(max_abs_nan(v[0][4 * j + e], v[0][4 * j + 2 + e]),
+                              max_abs_nan(v[1][4 * j + e], v[1][4 * j + 2 + e]));
+        m = max_abs_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+        m = max_abs_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+        m = max_abs_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+        const uint32_t sb = rceil_scale_byte_sel<E4M3>(__float_as_uint(m) & 0x7FFFFFFFu);
+        if (lane < 4) sbytes[8 * j + 2 * lane + e] = (uint8_t)sb;
+        const float s = inv_scale_from_byte(sb & 0xFFu);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          code[h][e] = sb == 0xFFu ? 0x7F7Fu : cvt_e4m3x2(v[h][4 * j + e] * s, v[h][4 * j + 2 + e] * s);
       }
-      t -= n;
+      w[j2][0] = code[0][0] | (code[0][1] << 16);
+      w[j2][1] = code[1][0] | (code[1][1] << 16);
+    }
+    // matrices: (tokens 8 (2 jj + m / 2) .., features' half m % 2)
+    stmatrix4_trans(base + (16 * jj + 8 * (lane >> 4) + (lane & 7)) * 48 + ((lane >> 3) & 1) * 16, w[0][0], w[0][1],
+                    w[1][0], w[1][1]);
+  }
+  __syncwarp();
+  if (col < p.N) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int t = 16 * i + (lane >> 1);
+      const uint4 c = *reinterpret_cast<const uint4*>(stg + t * 48 + (lane & 1) * 16);
+      if (t < valid)
+        *reinterpret_cast<uint4*>(p.epi.q + (row0 + t) * p.N + col + 16 * (lane & 1)) =
+            make_uint4(__byte_perm(c.x, c.y, 0x6420), __byte_perm(c.z, c.w, 0x6420), __byte_perm(c.x, c.y, 0x7531),
+                       __byte_perm(c.z, c.w, 0x7531));
     }
   }
-  __syncthreads();
-  if (s_g < 0) return;
-  const int64_t m0 = s_m0, rows = s_rows, n0 = (int64_t)blockIdx.x * TS;
-  const uint16_t* w = p.w + (int64_t)s_g * p.N * p.K;
-  const int64_t sbn = p.w_kn ? 1 : p.K, sbk = p.w_kn ? p.N : 1;
-  float acc[4][4] = {};
-  tile_product(p.a + m0 * p.ld_a, p.ld_a, 1, rows, w + n0 * sbn, sbn, sbk, p.N - n0, p.K, acc);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  __shared__ float sz[TS][TS + 1];
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int64_t r = ty * 4 + i, n = n0 + tx * 4 + j;
-      if (r >= rows || n >= p.N) continue;
-      float z = acc[i][j];
-      if (p.epi.bias) z += bf16_bits_to_float(p.epi.bias[n]);
-      sz[ty * 4 + i][tx * 4 + j] = z;
-      float v = act_any(z, p.epi.act);
-      if (p.epi.res) v += bf16_bits_to_float(p.epi.res[(m0 + r) * p.epi.ld_res + n]);
-      p.out[(m0 + r) * p.ld_out + n] = bf16_of(v);
-    }
-  if (p.epi.q == nullptr) return;
-  __syncthreads();
-  if (threadIdx.x < 2 * TS) {
-    const int r = threadIdx.x >> 1, c = (threadIdx.x & 1) * 32;
-    if (r < rows && n0 + c < p.N) {
-      float v[32];
-      for (int i = 0; i < 32; i++) v[i] = sz[r][c + i];
-      const uint32_t b = rceil_scale_byte<E4M3>(amax_abs_bits<32>(v));
-      uint32_t words[8];
-      quantize_block_words<E4M3>(v, b, words);
-      uint32_t* d = reinterpret_cast<uint32_t*>(p.epi.q + (m0 + r) * p.N + n0 + c);
-      for (int i = 0; i < 8; i++) d[i] = words[i];
-      p.epi.q_scale[blocked_offset(m0 + r, (n0 + c) / 32, p.N / 32)] = (uint8_t)b;
-    }
+  // scales; the padding of the blocked layout (rows to 128, columns to 4) is zero
+  const int64_t sc = p.N / 32, c = col / 32;
+  if (c < (sc + 3) / 4 * 4) {
+    if (lane < valid) p.epi.q_scale[blocked_offset(row0 + lane, c, sc)] = c < sc ? sbytes[lane] : 0;
+    const int64_t end = row0 + valid;
+    if (end == p.R && valid > 0)
+      for (int64_t r = end + lane; r < (p.R + 127) / 128 * 128; r += 32) p.epi.q_scale[blocked_offset(r, c, sc)] = 0;
   }
+  __syncwarp();
 }
 
-cudaError_t launch_ragged_gemm(const RaggedParams& p, int, cudaStream_t s) {
-  if (p.epi.q) {
-    const cudaError_t e = cudaMemsetAsync(p.epi.q_scale, 0, scale_bytes(p.R, p.N / 32), s);
-    if (e != cudaSuccess) return e;
+// One 32-feature x 32-token block of the accumulator -> BF16 rows, with the
+// linear layer's epilogue when EPI.
+template <bool EPI>
+__device__ __forceinline__ void store_block_bf16(const RaggedK& p, float (&v)[2][16], uint8_t* stg, int lane,
+                                                 const float (&bias)[4], uint16_t* out, int64_t row0, int valid,
+                                                 int64_t col) {
+  const uint32_t base = smem_u32(stg);
+  const uint32_t frag = base + (lane & 7) * 80 + (lane >> 3) * 16;
+  const int64_t mycol = col + 8 * (lane & 3);
+  if constexpr (EPI) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      v[0][i] += bias[(i >> 1) & 1];
+      v[1][i] += bias[2 + ((i >> 1) & 1)];
+    }
+    if (p.epi.q) ckpt_block(p, v, stg, lane, row0, valid, col);
+    if (p.epi.act == MX_ACT_GELU_TANH) act_values<MX_ACT_GELU_TANH>(v);
+    else if (p.epi.act == MX_ACT_SILU) act_values<MX_ACT_SILU>(v);
+    else if (p.epi.act == MX_ACT_RELU) act_values<MX_ACT_RELU>(v);
+    if (p.epi.res) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int t = 8 * i + (lane >> 2);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (t < valid && mycol < p.N)
+          x = *reinterpret_cast<const uint4*>(p.epi.res + (row0 + t) * p.epi.ld_res + mycol);
+        *reinterpret_cast<uint4*>(stg + t * 80 + (lane & 3) * 16) = x;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        uint32_t r[4];
+        ldmatrix4_trans(frag + 8 * j * 80, r);
+#pragma unroll
+        for (int m = 0; m < 4; m++) {
+          v[m >> 1][4 * j + 2 * (m & 1)] += bf16_bits_to_float(r[m] & 0xFFFFu);
+          v[m >> 1][4 * j + 2 * (m & 1) + 1] += bf16_bits_to_float(r[m] >> 16);
+        }
+      }
+    }
   }
-  const dim3 grid((unsigned)((p.N + TS - 1) / TS), (unsigned)((p.R + TS - 1) / TS + (p.offsets ? p.G : 0)));
-  ragged_gemm_simple<<<grid, 256, 0, s>>>(p);
+#pragma unroll
+  for (int j = 0; j < 4; j++)
+    stmatrix4_trans(frag + 8 * j * 80, float2_to_bf16x2(v[0][4 * j], v[0][4 * j + 1]),
+                    float2_to_bf16x2(v[0][4 * j + 2], v[0][4 * j + 3]),
+                    float2_to_bf16x2(v[1][4 * j], v[1][4 * j + 1]),
+                    float2_to_bf16x2(v[1][4 * j + 2], v[1][4 * j + 3]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int t = 8 * i + (lane >> 2);
+    const uint4 x = *reinterpret_cast<const uint4*>(stg + t * 80 + (lane & 3) * 16);
+    if (t < valid && mycol < p.N) *reinterpret_cast<uint4*>(out + (row0 + t) * p.ld_out + mycol) = x;
+  }
+  __syncwarp();
+}
+
+// The same block in fp32, stored or added: eight lanes hold eight consecutive
+// features, so each row piece is a full 32-byte sector without staging.
+__device__ __forceinline__ void store_block_f32(const RaggedK& p, float (&v)[2][16], int lane, float* out,
+                                                int64_t row0, int valid, int64_t col, bool add) {
+  float* at = out + (row0 + 2 * (lane & 3)) * p.ld_out + col + (lane >> 2);
+  const int t0 = 2 * (lane & 3);
+  if (add) {
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
+        if (t0 + t < valid && col + (lane >> 2) + f < p.N) v[h][i] += at[(int64_t)t * p.ld_out + f];
+      }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; h++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
+      if (t0 + t < valid && col + (lane >> 2) + f < p.N) at[(int64_t)t * p.ld_out + f] = v[h][i];
+    }
+}
+
+// Segment ends -> shared memory: seg[g] .. seg[g + 1] is expert g's segment,
+// pref[g] the 256-row tiles (WGRAD: the rows) of the experts before g.  A
+// segment that decreases, begins before an earlier one's end or passes R
+// counts nothing and is reported.
+template <int MODE>
+__device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, int32_t* pref, bool report) {
+  for (int g = threadIdx.x; g < p.G; g += rg::THREADS) seg[g + 1] = p.offsets ? __ldg(p.offsets + g) : (int32_t)p.R;
+  if (threadIdx.x == 0) seg[0] = 0;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  int32_t run = 0, high = 0;  // count and largest end so far
+  bool bad = false;
+  if (lane == 0) pref[0] = 0;
+  for (int b = 0; b < p.G; b += 32) {
+    const int g = b + lane;
+    const int32_t s0 = g < p.G ? seg[g] : 0, s1 = g < p.G ? seg[g + 1] : 0;
+    int32_t top = s0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, top, o);
+      if (lane >= o && u > top) top = u;
+    }
+    if (high > top) top = high;
+    high = __shfl_sync(0xFFFFFFFFu, top, 31);
+    int32_t v = 0;
+    if (g < p.G) {
+      if (s0 < top || s1 < s0 || (int64_t)s1 > p.R) bad = true;
+      else v = MODE == RAGGED_WGRAD ? s1 - s0 : (int32_t)(((int64_t)s1 - s0 + 255) / 256);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (g < p.G) pref[g + 1] = run + v;
+    run += __shfl_sync(0xFFFFFFFFu, v, 31);
+  }
+  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && report) atomicOr(&g_ragged_status, DEV_BAD_OFFSETS);
+}
+
+// tmP: the P operand, 3-D (inner, outer, expert).  tmQ: the Q operand's
+// 128-row boxes (WGRAD: 64 x 64 boxes); tmQ16: its 16-row boxes.
+template <int MODE, bool EPI, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(rg::THREADS, 1)
+ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+              const __grid_constant__ CUtensorMap tmQ16, const RaggedK p) {
+  using namespace rg;
+  constexpr bool P_MN = MODE != RAGGED_NK, Q_MN = MODE == RAGGED_WGRAD;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // leader's: the stage is in both CTAs' shared memory
+  uint64_t* empty = full + ST;      // both CTAs: the stage's MMAs are done
+  uint64_t* tail = empty + ST;      // each CTA's own: a segment's last block has landed
+  uint64_t* acc_full = tail + ST;   // both CTAs: the tile's MMAs are done
+  uint64_t* acc_empty = acc_full + 2;  // leader's: both CTAs' epilogue warps have read the accumulator
+  uint64_t* final_bar = acc_empty + 2;
+  int32_t* seg = reinterpret_cast<int32_t*>(smem + OFF_SEG);
+  int32_t* pref = reinterpret_cast<int32_t*>(smem + OFF_PREF);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmP); prefetch_tensormap(&tmQ); prefetch_tensormap(&tmQ16);
+    for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); mbar_init(&tail[s], 1); }
+    for (int a = 0; a < 2; a++) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 16); }
+    mbar_init(final_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  ragged_tables<MODE>(p, seg, pref, blockIdx.x == 0);
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers are initialised before any remote arrive or copy; the tables are built
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  RaggedTile T;
+  RaggedWalk<MODE, F32> walk(first, step);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies (both CTAs)
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      int armed[ST], armed_tail[ST];
+      uint32_t tail_phase = 0;
+      for (int s = 0; s < ST; s++) armed[s] = armed_tail[s] = -1;
+      bool ok = true;
+      while (ok && walk.next(p, seg, pref, &T)) {
+        const int half = T.nt >> 1;                       // Q rows of this CTA
+        const int nq = Q_MN ? (half + 63) / 64 : half / 16;
+        const uint32_t bytes = P_BYTES + (Q_MN ? nq * 8192u : nq * 2048u);
+        const int f = (int)(T.f0 + 128 * rank), q0 = (int)(T.t0 + half * rank);
+        for (int kb = 0; kb < T.nk; kb++) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, WAIT_BUDGET_NS)) { ok = false; break; }
+          uint8_t* sp = smem + stage * P_BYTES;
+          uint8_t* sq = smem + OFF_Q + stage * Q_BYTES;
+          const int k = (int)T.k0 + kb * BK;
+          armed[stage] = (int)phase;
+          if (MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0) {
+            mbar_arrive_expect_tx(&tail[stage], bytes);
+            armed_tail[stage] = (int)((tail_phase >> stage) & 1u);
+            tail_phase ^= 1u << stage;
+#pragma unroll
+            for (int j = 0; j < 2; j++) tma_load_2d(sp + j * 8192, &tmP, f + 64 * j, k, &tail[stage], pol);
+            for (int j = 0; j < nq; j++) tma_load_2d(sq + j * 8192, &tmQ, q0 + 64 * j, k, &tail[stage], pol);
+          } else {
+            const uint32_t fb = leader_addr(&full[stage]);
+            if (leader) {
+              mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+              mbar_arrive(&full[stage]);
+            }
+            if constexpr (MODE == RAGGED_NK) {
+              tma2_load_3d_hint(sp, &tmP, k, f, T.g, fb, pol);
+            } else if constexpr (MODE == RAGGED_KN) {
+#pragma unroll
+              for (int j = 0; j < 2; j++) tma2_load_3d_hint(sp + j * 8192, &tmP, f + 64 * j, k, T.g, fb, pol);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; j++) tma2_load_2d(sp + j * 8192, &tmP, f + 64 * j, k, fb, pol);
+            }
+            if constexpr (Q_MN) {
+              for (int j = 0; j < nq; j++) tma2_load_2d(sq + j * 8192, &tmQ, q0 + 64 * j, k, fb, pol);
+            } else if (half == 128) {
+              tma2_load_2d(sq, &tmQ, k, q0, fb, pol);
+            } else {
+              for (int j = 0; j < nq; j++) tma2_load_2d(sq + j * 2048, &tmQ16, k, q0 + 16 * j, fb, pol);
+            }
+          }
+          if (++stage == ST) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // Every copy has landed before the CTA leaves (the drain ignores the abort flag).
+      volatile int no_abort = 0;
+      for (int s = 0; s < ST; s++) {
+        if (leader && armed[s] >= 0) mbar_wait_bounded(&full[s], (uint32_t)armed[s], &no_abort, WAIT_BUDGET_NS);
+        if (armed_tail[s] >= 0) mbar_wait_bounded(&tail[s], (uint32_t)armed_tail[s], &no_abort, WAIT_BUDGET_NS);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs (leader)
+    if (lane == 0 && leader) {
+      // K-major: 8-row groups 1024 bytes apart, a 16-step 32 bytes on.
+      // MN-major: 64-wide column blocks 8192 bytes apart, groups of 8 steps
+      // 1024 bytes apart, a 16-step 2048 bytes on.
+      const uint64_t pd0 = smem_desc(smem_u32(smem), P_MN ? 8192 : 16, 1024, 2);
+      const uint64_t qd0 = smem_desc(smem_u32(smem + OFF_Q), Q_MN ? 8192 : 16, 1024, 2);
+      constexpr uint64_t p_step = P_MN ? 128 : 2, q_step = Q_MN ? 128 : 2;
+      // fp32 accumulator, BF16 operands, M = 256
+      constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((P_MN ? 1u : 0u) << 15) |
+                                  ((Q_MN ? 1u : 0u) << 16) | (16u << 24);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      while (ok && walk.next(p, seg, pref, &T)) {
+        if (T.nk == 0) continue;
+        if (!mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t idesc = idesc0 | ((uint32_t)(T.nt >> 3) << 17);
+        const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+        for (int kb = 0; kb < T.nk; kb++) {
+          if (!mbar_wait_cluster(&full[stage], phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t pd = pd0 + (uint64_t)((stage * P_BYTES) >> 4), qd = qd0 + (uint64_t)((stage * Q_BYTES) >> 4);
+          const int steps = kb == T.nk - 1 ? (T.rem + 15) >> 4 : 4;
+          for (int j = 0; j < steps; j++)
+            tc2_mma_bf16(d, pd + p_step * j, qd + q_step * j, idesc, (kb | j) != 0 ? 1u : 0u);
+          tc2_commit_both(&empty[stage]);
+          if (++stage == ST) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc2_commit_both(&acc_full[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!ok) *abort_flag = 1;
+      // No MMA may still be writing either CTA's tensor memory when it is freed.
+      volatile int no_abort = 0;
+      tc2_commit_local(final_bar);
+      mbar_wait_bounded(final_bar, 0, &no_abort, WAIT_BUDGET_NS);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ segment tails (both CTAs)
+    if constexpr (MODE == RAGGED_WGRAD) {
+      int64_t blocks = 0;  // contraction blocks of this pair so far
+      uint32_t tail_phase = 0;
+      while (walk.next(p, seg, pref, &T)) {
+        blocks += T.nk;
+        if (T.nk == 0 || (T.rem & 15) == 0) continue;
+        const int stage = (int)((blocks - 1) % ST);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tail[stage], (tail_phase >> stage) & 1u, abort_flag,
+                                                       WAIT_BUDGET_NS)))
+          break;
+        tail_phase ^= 1u << stage;
+        const int r0 = T.rem, rows = ((T.rem + 15) & ~15) - r0;  // 1..15 rows of 128 bytes per box
+        const int boxes = 2 + ((T.nt >> 1) + 63) / 64;
+        for (int i = lane; i < boxes * rows * 8; i += 32) {
+          const int box = i / (rows * 8), at = (r0 + (i % (rows * 8)) / 8) * 128 + (i & 7) * 16;
+          uint8_t* b = box < 2 ? smem + stage * P_BYTES + box * 8192 : smem + OFF_Q + stage * Q_BYTES + (box - 2) * 8192;
+          *reinterpret_cast<uint4*>(b + at) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_on_leader(leader_addr(&full[stage]));
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3, h = (warp - 4) >> 2;  // lane quarter (32 features), parity of the 32-token blocks
+    uint8_t* stg = smem + OFF_STG + (warp - 4) * STG;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    while (walk.next(p, seg, pref, &T)) {
+      const int64_t col = T.f0 + 128 * rank + 32 * q;
+      float bias[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (EPI) {
+        if (p.epi.bias) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int64_t f = col + (lane >> 2) + 8 * i;
+            if (f < p.N) bias[i] = bf16_bits_to_float(__ldg(p.epi.bias + f));
+          }
+        }
+      }
+      if (T.nk > 0) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag, WAIT_BUDGET_NS))) break;
+        tc_fence_after();
+      }
+      const int nb = T.nt >> 5;
+      const uint32_t tb = tmem_base + (uint32_t)(acc * 256) + ((uint32_t)(q * 32) << 16);
+      const uint32_t hand_back = leader_addr(&acc_empty[acc]);
+      if (T.nk > 0 && h >= nb && lane == 0) arrive_on_leader(hand_back);
+      for (int b = h; b < nb; b += 2) {
+        float v[2][16];
+        if (T.nk > 0) {
+          tmem_ld_16x32(tb + 32 * b, v[0]);
+          tmem_ld_16x32(tb + 32 * b + (16u << 16), v[1]);
+          tmem_wait_ld();
+          if (b + 2 >= nb) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_on_leader(hand_back);
+          }
+        } else {  // an expert without rows: zeros
+#pragma unroll
+          for (int i = 0; i < 16; i++) v[0][i] = v[1][i] = 0.f;
+        }
+        const int64_t row0 = T.t0 + 32 * b;
+        const int valid = T.valid - 32 * b < 32 ? T.valid - 32 * b : 32;
+        const int64_t base = MODE == RAGGED_WGRAD ? (int64_t)T.g * p.K * p.ld_out : 0;
+        if constexpr (F32)
+          store_block_f32(p, v, lane, static_cast<float*>(p.out) + base, row0, valid, col,
+                          p.accumulate || T.part > 0);
+        else
+          store_block_bf16<EPI>(p, v, stg, lane, bias, static_cast<uint16_t*>(p.out) + base, row0, valid, col);
+      }
+      if (T.nk > 0) {
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(&g_ragged_status, DEV_TIMEOUT);
+  cluster_sync_all();  // neither CTA frees tensor memory or exits while the other still uses the pair
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem_base) : "memory");
+  cluster_sync_all();
+}
+
+template <int MODE, bool EPI, bool F32>
+static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const CUtensorMap& tq,
+                                 const CUtensorMap& tq16, int64_t tiles, int num_sms, cudaStream_t s) {
+  const cudaError_t e = ensure_smem_attr<ragged_kernel<MODE, EPI, F32>>(rg::SMEM);
+  if (e != cudaSuccess) return e;
+  int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+  if (pairs < 1) pairs = 1;
+  ragged_kernel<MODE, EPI, F32><<<(unsigned)(2 * pairs), rg::THREADS, rg::SMEM, s>>>(tp, tq, tq16, p);
   return cudaGetLastError();
 }
 
-__global__ void __launch_bounds__(256) ragged_wgrad_simple(const RaggedWgradParams p) {
-  const int g = blockIdx.z;
-  int64_t b, e;
-  if (!segment(p.offsets, g, p.R, &b, &e)) e = b;
-  const int64_t n0 = (int64_t)blockIdx.y * TS, k0 = (int64_t)blockIdx.x * TS;
-  float acc[4][4] = {};
-  if (e > b)
-    tile_product(p.dy + b * p.ld_dy + n0, 1, p.ld_dy, p.N - n0, p.x + b * p.ld_x + k0, 1, p.ld_x, p.K - k0, e - b,
-                 acc);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int64_t n = n0 + ty * 4 + i, k = k0 + tx * 4 + j;
-      if (n >= p.N || k >= p.K) continue;
-      const int64_t at = ((int64_t)g * p.N + n) * p.K + k;
-      if (p.grad) p.grad[at] = bf16_of(acc[i][j]);
-      else p.grad_f32[at] = p.accumulate ? p.grad_f32[at] + acc[i][j] : acc[i][j];
-    }
+// BF16 matrix [outer, inner] (row stride ld elements), optionally a stack of
+// `batch` of them, as 128-byte swizzled boxes of 64 x box_rows.
+static bool bf16_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int64_t batch,
+                     int box_rows) {
+  TensorMapShape s{};
+  s.rank = batch > 0 ? 3 : 2;
+  s.dims[0] = (uint64_t)inner; s.dims[1] = (uint64_t)outer; s.dims[2] = (uint64_t)batch;
+  s.strides[0] = (uint64_t)ld * 2; s.strides[1] = (uint64_t)outer * (uint64_t)ld * 2;
+  s.box[0] = 64; s.box[1] = (uint32_t)box_rows; s.box[2] = 1;
+  return encode_bf16_map(m, base, s) == MX_OK;
 }
 
-cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.K + TS - 1) / TS), (unsigned)((p.N + TS - 1) / TS), (unsigned)p.G);
-  ragged_wgrad_simple<<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t s) {
+  RaggedK k{};
+  k.G = p.G; k.offsets = p.offsets;
+  k.R = p.R; k.N = p.N; k.K = p.K;
+  k.n_f = (int)((p.N + 255) / 256);
+  k.out = p.out; k.ld_out = p.ld_out;
+  k.epi = p.epi;
+  CUtensorMap tp, tq, tq16;
+  if (!(p.w_kn ? bf16_map(&tp, p.w, p.N, p.K, p.N, p.G, 64) : bf16_map(&tp, p.w, p.K, p.N, p.K, p.G, 128)) ||
+      !bf16_map(&tq, p.a, p.K, p.R, p.ld_a, 0, 128) || !bf16_map(&tq16, p.a, p.K, p.R, p.ld_a, 0, 16))
+    return cudaErrorInvalidValue;
+  // each segment ends in one tile of its own at most
+  const int64_t own = p.offsets ? (p.G < p.R ? p.G : p.R) : 1;
+  const int64_t tiles = (p.R / 256 + own) * k.n_f;
+  const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res || p.epi.q;
+  if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tq16, tiles, num_sms, s);
+  return epi ? launch_ragged<RAGGED_NK, true, false>(k, tp, tq, tq16, tiles, num_sms, s)
+             : launch_ragged<RAGGED_NK, false, false>(k, tp, tq, tq16, tiles, num_sms, s);
+}
+
+cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStream_t s) {
+  RaggedK k{};
+  k.G = p.G; k.offsets = p.offsets;
+  k.R = p.R;
+  k.N = p.K;  // the output's columns
+  k.K = p.N;  // its rows
+  k.n_f = (int)((p.K + 255) / 256);
+  k.n_t = (int)((p.N + 255) / 256);
+  k.out = p.grad ? static_cast<void*>(p.grad) : p.grad_f32;
+  k.ld_out = p.K;
+  k.accumulate = p.accumulate;
+  CUtensorMap tp, tq;
+  if (!bf16_map(&tp, p.x, p.K, p.R, p.ld_x, 0, 64) || !bf16_map(&tq, p.dy, p.N, p.R, p.ld_dy, 0, 64))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)p.G * k.n_f * k.n_t;
+  return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tq, tiles, num_sms, s)
+                : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tq, tiles, num_sms, s);
 }
 
 cudaError_t read_ragged_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_ragged_status, sizeof(unsigned)); }

@@ -373,3 +373,24 @@ def test_linear_checkpoint_bytes(cuda_lib, M, N, K):
     ref, _, _ = mx.mx_quantize(z, mx.E4M3, True, False)
     assert torch.equal(out, z.clamp(min=0))
     assert torch.equal(ck.data, ref.data) and torch.equal(ck.scale, ref.scale)
+
+
+def test_ragged_wgrad_stage_reuse_ends_promptly(cuda_lib):
+    """Segments whose last blocks (zeroed past their end) and whole blocks
+    alternate in every stage of the ring, ending on either kind: the launch
+    ends by itself, far below the bound of a wait (2 s)."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(12)
+    N, K = 264, 264
+    for tail in range(1, 14):
+        counts = [64 * (i % 5) + (3 if (i + tail) % 2 else 0) for i in range(tail)] + [64 * tail + 5, 64]
+        R = sum(counts)
+        dy, x = _bf16((R, N), gen), _bf16((R, K), gen)
+        off = _offsets(counts)
+        mx.mx_ragged_gemm_wgrad(dy, x, len(counts), off)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        mx.mx_ragged_gemm_wgrad(dy, x, len(counts), off)
+        b.record()
+        assert mx.mx_get_device_status() == "MX_OK"
+        assert a.elapsed_time(b) < 500.0
