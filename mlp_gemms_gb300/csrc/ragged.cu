@@ -43,7 +43,7 @@ namespace mx {
 static __device__ unsigned g_ragged_status = 0;
 
 namespace rg {
-constexpr int THREADS = 384;  // warps: 0 copies, 1 MMAs, 2 segment tails, 4..11 epilogue
+constexpr int THREADS = 384;  // warps: 0 and 3 copies, 1 MMAs, 2 segment tails, 4..11 epilogue
 constexpr int ST = 6;         // 32 KB stages of 64 contraction steps
 constexpr int BK = 64;
 constexpr int P_BYTES = 16384, Q_BYTES = 16384;
@@ -80,9 +80,9 @@ struct RaggedTile {
   int64_t t0;              // first output row (WGRAD: of the expert's matrix)
   int valid;               // rows of the tile in the output
   int nt;                  // the MMA's N: valid rounded up to 32
-  int64_t f0;              // first output column of the pair's 256
+  int f0;                  // first output column of the pair's 256
   int nk;                  // 64-step blocks of the contraction
-  int64_t k0;              // WGRAD: first row of the contraction
+  int k0;                  // WGRAD: first row of the contraction
   int rem;                 // contraction steps in the last block (1..64)
   int part, parts;         // WGRAD into fp32: this pass over the tile, and how many it takes
 };
@@ -95,59 +95,56 @@ struct RaggedTile {
 // operands.  A BF16 result (2e-3 from its own rounding) takes one pass.
 constexpr int F32_ROWS = 4096;
 
-template <int MODE, bool F32>
-__device__ __forceinline__ bool ragged_tile(const RaggedK& p, const int32_t* seg, const int32_t* pref, int64_t t,
-                                            int part, RaggedTile* T) {
-  T->part = part;
-  T->parts = 1;
-  if constexpr (MODE == RAGGED_WGRAD) {
-    const int per = p.n_f * p.n_t;
-    if (t >= (int64_t)p.G * per) return false;
-    T->g = (int)(t / per);
-    const int r = (int)(t - (int64_t)T->g * per);
-    T->t0 = (int64_t)(r / p.n_f) * 256;
-    T->f0 = (int64_t)(r % p.n_f) * 256;
-    const int64_t left = p.K - T->t0;
-    T->valid = left < 256 ? (int)left : 256;
-    T->k0 = seg[T->g];
-    int rows = pref[T->g + 1] - pref[T->g];  // rows of the segment, 0 if malformed
-    if constexpr (F32) {
-      T->parts = rows > F32_ROWS ? (rows + F32_ROWS - 1) / F32_ROWS : 1;
-      T->k0 += (int64_t)part * F32_ROWS;
-      rows -= part * F32_ROWS;
-      if (rows > F32_ROWS) rows = F32_ROWS;
-    }
-    T->nk = (rows + rg::BK - 1) / rg::BK;
-    T->rem = rows - (T->nk - 1) * rg::BK;
-  } else {
-    const int64_t mt = t / p.n_f;
-    if (mt >= pref[p.G]) return false;
-    int lo = 0, hi = p.G - 1;  // the expert with pref[g] <= mt < pref[g + 1]
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pref[mid] <= mt) lo = mid; else hi = mid - 1;
-    }
-    T->g = lo;
-    T->t0 = (int64_t)seg[lo] + 256 * (mt - pref[lo]);
-    T->f0 = (t - mt * p.n_f) * 256;
-    const int64_t left = (int64_t)seg[lo + 1] - T->t0;
-    T->valid = left < 256 ? (int)left : 256;
-    T->k0 = 0;
-    T->nk = (int)((p.K + rg::BK - 1) / rg::BK);
-    T->rem = (int)(p.K - (int64_t)(T->nk - 1) * rg::BK);
-  }
-  T->nt = (T->valid + 31) & ~31;
-  return true;
-}
-
-// The pair's passes in order: each of its tiles, and of a tile each part.
+// The pair's passes in order: each of its tiles (every step-th one), and of a
+// tile each part.  Tile indices only grow, so the expert is found by walking
+// on from the last one: every role walks for itself, the MMA thread between
+// two tiles included, and a division or a search there is time without MMAs.
 template <int MODE, bool F32>
 struct RaggedWalk {
-  int64_t t, step;
-  int part;
-  __device__ RaggedWalk(int64_t first, int64_t step_) : t(first), step(step_), part(0) {}
+  uint32_t t, step;
+  uint32_t base;  // first tile of expert g
+  int g, part;
+  __device__ RaggedWalk(uint32_t first, uint32_t step_) : t(first), step(step_), base(0), g(0), part(0) {}
   __device__ __forceinline__ bool next(const RaggedK& p, const int32_t* seg, const int32_t* pref, RaggedTile* T) {
-    if (!ragged_tile<MODE, F32>(p, seg, pref, t, part, T)) return false;
+    const uint32_t n_f = (uint32_t)p.n_f;
+    int32_t seg0;
+    uint32_t mt;
+    while (true) {
+      if (g >= p.G) return false;
+      const uint32_t count = MODE == RAGGED_WGRAD ? n_f * (uint32_t)p.n_t : (uint32_t)(pref[g + 1] - pref[g]) * n_f;
+      if (t - base < count) break;
+      base += count;
+      g++;
+    }
+    mt = (t - base) / n_f;
+    seg0 = seg[g];
+    T->g = g;
+    T->f0 = (int)(t - base - mt * n_f) * 256;
+    T->parts = 1;
+    int64_t left;
+    if constexpr (MODE == RAGGED_WGRAD) {
+      T->t0 = (int64_t)mt * 256;
+      left = p.K - T->t0;
+      int rows = pref[g + 1] - pref[g];  // rows of the segment, 0 if malformed
+      T->k0 = seg0;
+      if constexpr (F32) {
+        T->parts = rows > F32_ROWS ? (rows + F32_ROWS - 1) / F32_ROWS : 1;
+        T->k0 += part * F32_ROWS;
+        rows -= part * F32_ROWS;
+        if (rows > F32_ROWS) rows = F32_ROWS;
+      }
+      T->nk = (rows + rg::BK - 1) / rg::BK;
+      T->rem = rows - (T->nk - 1) * rg::BK;
+    } else {
+      T->t0 = (int64_t)seg0 + 256 * (int64_t)mt;
+      left = (int64_t)seg[g + 1] - T->t0;
+      T->k0 = 0;
+      T->nk = (int)((p.K + rg::BK - 1) / rg::BK);
+      T->rem = (int)p.K - (T->nk - 1) * rg::BK;
+    }
+    T->valid = left < 256 ? (int)left : 256;
+    T->nt = (T->valid + 31) & ~31;
+    T->part = part;
     if (++part >= T->parts) {
       part = 0;
       t += step;
@@ -384,12 +381,89 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
   if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && report) atomicOr(&g_ragged_status, DEV_BAD_OFFSETS);
 }
 
-// tmP: the P operand, 3-D (inner, outer, expert).  tmQ: the Q operand's
-// 128-row boxes (WGRAD: 64 x 64 boxes); tmQ16: its 16-row boxes.
+// The Q operand's maps: boxes of 128, 64, 32 and 16 rows (a CTA's half of a
+// tile is a multiple of 16 tokens); WGRAD: box[0] only, 64 x 64.
+struct RaggedMapsQ {
+  CUtensorMap box[4];
+};
+
+// One operand's copies into the stage ring of this CTA (one thread).  Warp 0
+// copies P, warp 3 Q: one thread issuing both was the limit where a stage
+// takes four copies (weight gradient, G = 128: 397 -> 367 us).
+template <int MODE, bool F32, bool IS_P>
+__device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const RaggedMapsQ& tmQ, const RaggedK& p,
+                                              uint8_t* smem, const int32_t* seg, const int32_t* pref,
+                                              uint32_t rank) {
+  using namespace rg;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* empty = full + ST;
+  uint64_t* tail = empty + ST;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  const uint64_t pol = l2_policy_evict_normal();
+  uint8_t* const ring = smem + (IS_P ? 0 : OFF_Q);
+  const bool leader = rank == 0;
+  RaggedTile T;
+  RaggedWalk<MODE, F32> walk(blockIdx.x >> 1, gridDim.x >> 1);
+  int stage = 0;
+  uint32_t phase = 0, tail_phase = 0, armed = 0, armed_phase = 0, armed_tail = 0;
+  bool ok = true;
+  while (ok && walk.next(p, seg, pref, &T)) {
+    const int half = T.nt >> 1;                       // Q rows of this CTA
+    const int boxes = IS_P ? 2 : (half + 63) >> 6;    // MN-major boxes of 64
+    const uint32_t bytes = IS_P ? P_BYTES : (MODE == RAGGED_WGRAD ? boxes * 8192u : half * 128u);
+    const int x = IS_P ? T.f0 + 128 * (int)rank : (int)T.t0 + half * (int)rank;
+    for (int kb = 0; kb < T.nk; kb++) {
+      if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, WAIT_BUDGET_NS)) { ok = false; break; }
+      uint8_t* dst = ring + stage * P_BYTES;
+      const int k = T.k0 + kb * BK;
+      armed |= 1u << stage;
+      armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+      if (MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0) {
+        mbar_arrive_expect_tx(&tail[stage], bytes);
+        armed_tail |= 1u << stage;
+        tail_phase ^= 1u << stage;
+        for (int j = 0; j < boxes; j++)
+          tma_load_2d(dst + j * 8192, IS_P ? &tmP : &tmQ.box[0], x + 64 * j, k, &tail[stage], pol);
+      } else {
+        const uint32_t fb = leader_addr(&full[stage]);
+        if (leader) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+        if constexpr (MODE == RAGGED_WGRAD) {
+          for (int j = 0; j < boxes; j++)
+            tma2_load_2d(dst + j * 8192, IS_P ? &tmP : &tmQ.box[0], x + 64 * j, k, fb, pol);
+        } else if constexpr (IS_P && MODE == RAGGED_NK) {
+          tma2_load_3d_hint(dst, &tmP, k, x, T.g, fb, pol);
+        } else if constexpr (IS_P) {
+#pragma unroll
+          for (int j = 0; j < 2; j++) tma2_load_3d_hint(dst + j * 8192, &tmP, x + 64 * j, k, T.g, fb, pol);
+        } else if (half == 128) {
+          tma2_load_2d(dst, &tmQ.box[0], k, x, fb, pol);
+        } else {
+          int row = 0;
+#pragma unroll
+          for (int j = 1; j < 4; j++) {
+            if (half & (128 >> j)) {
+              tma2_load_2d(dst + row * 128, &tmQ.box[j], k, x + row, fb, pol);
+              row += 128 >> j;
+            }
+          }
+        }
+      }
+      if (++stage == ST) { stage = 0; phase ^= 1u; }
+    }
+  }
+  // Every copy has landed before the CTA leaves (the drain ignores the abort flag).
+  volatile int no_abort = 0;
+  for (int s = 0; s < ST; s++) {
+    if (leader && (armed >> s & 1u)) mbar_wait_bounded(&full[s], armed_phase >> s & 1u, &no_abort, WAIT_BUDGET_NS);
+    if (armed_tail >> s & 1u)
+      mbar_wait_bounded(&tail[s], (tail_phase >> s & 1u) ^ 1u, &no_abort, WAIT_BUDGET_NS);
+  }
+}
+
+// tmP: the P operand, 3-D (inner, outer, expert; WGRAD: 2-D).
 template <int MODE, bool EPI, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(rg::THREADS, 1)
-ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-              const __grid_constant__ CUtensorMap tmQ16, const RaggedK p) {
+ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ RaggedMapsQ tmQ, const RaggedK p) {
   using namespace rg;
   constexpr bool P_MN = MODE != RAGGED_NK, Q_MN = MODE == RAGGED_WGRAD;
   extern __shared__ uint8_t smem_raw[];
@@ -409,8 +483,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    prefetch_tensormap(&tmP); prefetch_tensormap(&tmQ); prefetch_tensormap(&tmQ16);
-    for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); mbar_init(&tail[s], 1); }
+    prefetch_tensormap(&tmP);
+    for (int j = 0; j < (Q_MN ? 1 : 4); j++) prefetch_tensormap(&tmQ.box[j]);
+    for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); mbar_init(&tail[s], 2); }
     for (int a = 0; a < 2; a++) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 16); }
     mbar_init(final_bar, 1);
     *abort_flag = 0;
@@ -427,71 +502,13 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
   cluster_sync_all();  // both CTAs' barriers are initialised before any remote arrive or copy; the tables are built
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
   RaggedTile T;
-  RaggedWalk<MODE, F32> walk(first, step);
+  RaggedWalk<MODE, F32> walk(blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ copies (both CTAs)
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      int armed[ST], armed_tail[ST];
-      uint32_t tail_phase = 0;
-      for (int s = 0; s < ST; s++) armed[s] = armed_tail[s] = -1;
-      bool ok = true;
-      while (ok && walk.next(p, seg, pref, &T)) {
-        const int half = T.nt >> 1;                       // Q rows of this CTA
-        const int nq = Q_MN ? (half + 63) / 64 : half / 16;
-        const uint32_t bytes = P_BYTES + (Q_MN ? nq * 8192u : nq * 2048u);
-        const int f = (int)(T.f0 + 128 * rank), q0 = (int)(T.t0 + half * rank);
-        for (int kb = 0; kb < T.nk; kb++) {
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, WAIT_BUDGET_NS)) { ok = false; break; }
-          uint8_t* sp = smem + stage * P_BYTES;
-          uint8_t* sq = smem + OFF_Q + stage * Q_BYTES;
-          const int k = (int)T.k0 + kb * BK;
-          armed[stage] = (int)phase;
-          if (MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0) {
-            mbar_arrive_expect_tx(&tail[stage], bytes);
-            armed_tail[stage] = (int)((tail_phase >> stage) & 1u);
-            tail_phase ^= 1u << stage;
-#pragma unroll
-            for (int j = 0; j < 2; j++) tma_load_2d(sp + j * 8192, &tmP, f + 64 * j, k, &tail[stage], pol);
-            for (int j = 0; j < nq; j++) tma_load_2d(sq + j * 8192, &tmQ, q0 + 64 * j, k, &tail[stage], pol);
-          } else {
-            const uint32_t fb = leader_addr(&full[stage]);
-            if (leader) {
-              mbar_arrive_expect_tx(&full[stage], 2u * bytes);
-              mbar_arrive(&full[stage]);
-            }
-            if constexpr (MODE == RAGGED_NK) {
-              tma2_load_3d_hint(sp, &tmP, k, f, T.g, fb, pol);
-            } else if constexpr (MODE == RAGGED_KN) {
-#pragma unroll
-              for (int j = 0; j < 2; j++) tma2_load_3d_hint(sp + j * 8192, &tmP, f + 64 * j, k, T.g, fb, pol);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 2; j++) tma2_load_2d(sp + j * 8192, &tmP, f + 64 * j, k, fb, pol);
-            }
-            if constexpr (Q_MN) {
-              for (int j = 0; j < nq; j++) tma2_load_2d(sq + j * 8192, &tmQ, q0 + 64 * j, k, fb, pol);
-            } else if (half == 128) {
-              tma2_load_2d(sq, &tmQ, k, q0, fb, pol);
-            } else {
-              for (int j = 0; j < nq; j++) tma2_load_2d(sq + j * 2048, &tmQ16, k, q0 + 16 * j, fb, pol);
-            }
-          }
-          if (++stage == ST) { stage = 0; phase ^= 1u; }
-        }
-      }
-      // Every copy has landed before the CTA leaves (the drain ignores the abort flag).
-      volatile int no_abort = 0;
-      for (int s = 0; s < ST; s++) {
-        if (leader && armed[s] >= 0) mbar_wait_bounded(&full[s], (uint32_t)armed[s], &no_abort, WAIT_BUDGET_NS);
-        if (armed_tail[s] >= 0) mbar_wait_bounded(&tail[s], (uint32_t)armed_tail[s], &no_abort, WAIT_BUDGET_NS);
-      }
-    }
+    if (lane == 0) ragged_copies<MODE, F32, true>(tmP, tmQ, p, smem, seg, pref, rank);
+  } else if (warp == 3) {
+    if (lane == 0) ragged_copies<MODE, F32, false>(tmP, tmQ, p, smem, seg, pref, rank);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader)
     if (lane == 0 && leader) {
@@ -537,22 +554,21 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
   } else if (warp == 2) {
     // ------------------------------------------------------------ segment tails (both CTAs)
     if constexpr (MODE == RAGGED_WGRAD) {
-      int64_t blocks = 0;  // contraction blocks of this pair so far
+      uint32_t blocks = 0;  // contraction blocks of this pair so far, modulo the stages
       uint32_t tail_phase = 0;
       while (walk.next(p, seg, pref, &T)) {
-        blocks += T.nk;
+        blocks = (blocks + T.nk) % ST;
         if (T.nk == 0 || (T.rem & 15) == 0) continue;
-        const int stage = (int)((blocks - 1) % ST);
+        const int stage = blocks == 0 ? ST - 1 : (int)blocks - 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tail[stage], (tail_phase >> stage) & 1u, abort_flag,
                                                        WAIT_BUDGET_NS)))
           break;
         tail_phase ^= 1u << stage;
-        const int r0 = T.rem, rows = ((T.rem + 15) & ~15) - r0;  // 1..15 rows of 128 bytes per box
-        const int boxes = 2 + ((T.nt >> 1) + 63) / 64;
-        for (int i = lane; i < boxes * rows * 8; i += 32) {
-          const int box = i / (rows * 8), at = (r0 + (i % (rows * 8)) / 8) * 128 + (i & 7) * 16;
-          uint8_t* b = box < 2 ? smem + stage * P_BYTES + box * 8192 : smem + OFF_Q + stage * Q_BYTES + (box - 2) * 8192;
-          *reinterpret_cast<uint4*>(b + at) = make_uint4(0, 0, 0, 0);
+        // up to 15 rows of each 128-byte wide box: two of P, up to two of Q
+        const int box = lane >> 3;
+        if (box < 2 + ((T.nt + 127) >> 7)) {
+          uint8_t* b = smem + stage * P_BYTES + (box < 2 ? box * 8192 : OFF_Q + (box - 2) * 8192) + (lane & 7) * 16;
+          for (int r = T.rem; r & 15; r++) *reinterpret_cast<uint4*>(b + r * 128) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -627,13 +643,14 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ C
 }
 
 template <int MODE, bool EPI, bool F32>
-static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const CUtensorMap& tq,
-                                 const CUtensorMap& tq16, int64_t tiles, int num_sms, cudaStream_t s) {
+static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const RaggedMapsQ& tq, int64_t tiles,
+                                 int num_sms, cudaStream_t s) {
+  if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem_attr<ragged_kernel<MODE, EPI, F32>>(rg::SMEM);
   if (e != cudaSuccess) return e;
   int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
   if (pairs < 1) pairs = 1;
-  ragged_kernel<MODE, EPI, F32><<<(unsigned)(2 * pairs), rg::THREADS, rg::SMEM, s>>>(tp, tq, tq16, p);
+  ragged_kernel<MODE, EPI, F32><<<(unsigned)(2 * pairs), rg::THREADS, rg::SMEM, s>>>(tp, tq, p);
   return cudaGetLastError();
 }
 
@@ -656,17 +673,20 @@ cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t 
   k.n_f = (int)((p.N + 255) / 256);
   k.out = p.out; k.ld_out = p.ld_out;
   k.epi = p.epi;
-  CUtensorMap tp, tq, tq16;
+  CUtensorMap tp;
+  RaggedMapsQ tq;
   if (!(p.w_kn ? bf16_map(&tp, p.w, p.N, p.K, p.N, p.G, 64) : bf16_map(&tp, p.w, p.K, p.N, p.K, p.G, 128)) ||
-      !bf16_map(&tq, p.a, p.K, p.R, p.ld_a, 0, 128) || !bf16_map(&tq16, p.a, p.K, p.R, p.ld_a, 0, 16))
+      !bf16_map(&tq.box[0], p.a, p.K, p.R, p.ld_a, 0, 128))
     return cudaErrorInvalidValue;
+  for (int j = 1; j < 4; j++)
+    if (!bf16_map(&tq.box[j], p.a, p.K, p.R, p.ld_a, 0, 128 >> j)) return cudaErrorInvalidValue;
   // each segment ends in one tile of its own at most
   const int64_t own = p.offsets ? (p.G < p.R ? p.G : p.R) : 1;
   const int64_t tiles = (p.R / 256 + own) * k.n_f;
   const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res || p.epi.q;
-  if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tq16, tiles, num_sms, s);
-  return epi ? launch_ragged<RAGGED_NK, true, false>(k, tp, tq, tq16, tiles, num_sms, s)
-             : launch_ragged<RAGGED_NK, false, false>(k, tp, tq, tq16, tiles, num_sms, s);
+  if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tiles, num_sms, s);
+  return epi ? launch_ragged<RAGGED_NK, true, false>(k, tp, tq, tiles, num_sms, s)
+             : launch_ragged<RAGGED_NK, false, false>(k, tp, tq, tiles, num_sms, s);
 }
 
 cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStream_t s) {
@@ -680,12 +700,13 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   k.out = p.grad ? static_cast<void*>(p.grad) : p.grad_f32;
   k.ld_out = p.K;
   k.accumulate = p.accumulate;
-  CUtensorMap tp, tq;
-  if (!bf16_map(&tp, p.x, p.K, p.R, p.ld_x, 0, 64) || !bf16_map(&tq, p.dy, p.N, p.R, p.ld_dy, 0, 64))
+  CUtensorMap tp;
+  RaggedMapsQ tq;
+  if (!bf16_map(&tp, p.x, p.K, p.R, p.ld_x, 0, 64) || !bf16_map(&tq.box[0], p.dy, p.N, p.R, p.ld_dy, 0, 64))
     return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)p.G * k.n_f * k.n_t;
-  return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tq, tiles, num_sms, s)
-                : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tq, tiles, num_sms, s);
+  return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tiles, num_sms, s)
+                : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, num_sms, s);
 }
 
 cudaError_t read_ragged_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_ragged_status, sizeof(unsigned)); }
