@@ -167,9 +167,10 @@ def _check(status):
 
 
 def _stream(stream=None):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    from torch import _C
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
 
 
 def _ptr(t):
@@ -194,8 +195,8 @@ class MX:
     def __init__(self, rows, cols, fmt=E4M3, hadamard=False, device="cuda", data=None, scale=None):
         import torch
         self.rows, self.cols, self.fmt, self.hadamard = int(rows), int(cols), int(fmt), bool(hadamard)
-        rb = payload_bytes(1, cols, fmt)
-        self.data = data if data is not None else torch.empty((rows, rb), dtype=torch.uint8, device=device)
+        self.data = data if data is not None else torch.empty((rows, payload_bytes(1, cols, fmt)),
+                                                              dtype=torch.uint8, device=device)
         self.scale = scale if scale is not None else torch.empty(scale_bytes(rows, cols), dtype=torch.uint8,
                                                                  device=device)
 

@@ -244,12 +244,12 @@ mx_status_t mx_act_ckpt_fwd(const void* z_bf16, int64_t R, int64_t C, int64_t ld
   p.q = static_cast<uint8_t*>(ckpt->data); p.q_scale = ckpt->scale;
   p.z = static_cast<const uint16_t*>(z_bf16); p.ld_z = ld_z;
   p.h = static_cast<uint16_t*>(h_bf16); p.ld_h = ld_h;
-  return cuda_result(mx::launch_ckpt_fwd(p, sms, reinterpret_cast<cudaStream_t>(stream)), "checkpoint launch");
+  return cuda_result(mx::launch_ckpt_fwd(p, reinterpret_cast<cudaStream_t>(stream)), "checkpoint launch");
 }
 
 size_t mx_act_ckpt_workspace_bytes(int64_t R, int64_t C) {
   if (R <= 0 || C <= 0) return 0;
-  return (size_t)(mx::ckpt_row_blocks(R) * C) * sizeof(float);
+  return (size_t)(mx::ckpt_row_blocks(R, C) * C) * sizeof(float);
 }
 
 mx_status_t mx_act_ckpt_bwd(const mx_tensor_t* ckpt, int32_t act, const void* dh_bf16, int64_t ld_dh, void* dz_bf16,
@@ -285,7 +285,7 @@ mx_status_t mx_act_ckpt_bwd(const mx_tensor_t* ckpt, int32_t act, const void* dh
   p.h = static_cast<uint16_t*>(h_bf16); p.ld_h = ld_h;
   p.db = db;
   p.partials = static_cast<float*>(workspace);
-  return cuda_result(mx::launch_ckpt_bwd(p, sms, s), "checkpoint backward launch");
+  return cuda_result(mx::launch_ckpt_bwd(p, s), "checkpoint backward launch");
 }
 
 }  // extern "C"

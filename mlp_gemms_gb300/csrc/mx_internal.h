@@ -218,11 +218,11 @@ struct CkptParams {
   uint16_t* dz;
   int64_t ld_dz;
   float* db;                 // column sums of dz, or null
-  float* partials;           // [ckpt_row_blocks(R)][C]
+  float* partials;           // [ckpt_row_blocks(R, C)][C]
 };
-int64_t ckpt_row_blocks(int64_t R);
-cudaError_t launch_ckpt_fwd(const CkptParams& p, int num_sms, cudaStream_t s);
-cudaError_t launch_ckpt_bwd(const CkptParams& p, int num_sms, cudaStream_t s);
+int64_t ckpt_row_blocks(int64_t R, int64_t C);
+cudaError_t launch_ckpt_fwd(const CkptParams& p, cudaStream_t s);
+cudaError_t launch_ckpt_bwd(const CkptParams& p, cudaStream_t s);
 
 // Host helpers of the ABI layer shared by its translation units (api.cu).
 mx_status_t device_sms(int* sms);   // checks the device; its SM count

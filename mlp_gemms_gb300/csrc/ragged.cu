@@ -320,23 +320,30 @@ __device__ __forceinline__ void store_block_bf16(const RaggedK& p, float (&v)[2]
 // features, so each row piece is a full 32-byte sector without staging.
 __device__ __forceinline__ void store_block_f32(const RaggedK& p, float (&v)[2][16], int lane, float* out,
                                                 int64_t row0, int valid, int64_t col, bool add) {
-  float* at = out + (row0 + 2 * (lane & 3)) * p.ld_out + col + (lane >> 2);
   const int t0 = 2 * (lane & 3);
-  if (add) {
+  const int64_t c0 = col + (lane >> 2);
+  float* at = out + (row0 + t0) * p.ld_out + c0;
+  const int left = p.N - c0 > 32 ? 32 : (int)(p.N - c0);  // columns from this lane's first one on
+  if (add) {  // all loads before the first use
+    float old[2][16];
 #pragma unroll
     for (int h = 0; h < 2; h++)
 #pragma unroll
       for (int i = 0; i < 16; i++) {
         const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
-        if (t0 + t < valid && col + (lane >> 2) + f < p.N) v[h][i] += at[(int64_t)t * p.ld_out + f];
+        old[h][i] = t0 + t < valid && f < left ? __ldcg(at + (int64_t)t * p.ld_out + f) : 0.f;
       }
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int i = 0; i < 16; i++) v[h][i] += old[h][i];
   }
 #pragma unroll
   for (int h = 0; h < 2; h++)
 #pragma unroll
     for (int i = 0; i < 16; i++) {
       const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
-      if (t0 + t < valid && col + (lane >> 2) + f < p.N) at[(int64_t)t * p.ld_out + f] = v[h][i];
+      if (t0 + t < valid && f < left) at[(int64_t)t * p.ld_out + f] = v[h][i];
     }
 }
 
