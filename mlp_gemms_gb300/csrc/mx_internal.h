@@ -199,6 +199,9 @@ struct RaggedWgradParams {
   int accumulate;
 };
 cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s);  // skinny.cu: few rows, MX_W_NK
+cudaError_t read_skinny_status(unsigned* out);
+cudaError_t reset_skinny_status();
 cudaError_t read_ragged_status(unsigned* out);
 cudaError_t reset_ragged_status();
 constexpr int MAX_RAGGED_G = 1024;  // experts the segment tables hold

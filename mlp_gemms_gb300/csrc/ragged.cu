@@ -394,7 +394,32 @@ struct RaggedMapsQ {
   CUtensorMap box[4];
 };
 
-// One operand's copies into the stage ring of this CTA (one thread).  Warp 0
+// Bounded wait of a whole warp for a phase of a barrier (CLUSTER: with
+// arrivals of the other CTA's).  The roles run as whole warps and elect one
+// lane for what a single thread issues: in a branch on the lane's number every
+// operand of a copy or an MMA goes through a register move that the loop waits
+// for (measured: 97 cycles per MMA issued, 200 per wait, 720 a stage).
+template <bool CLUSTER>
+__device__ __forceinline__ bool ragged_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; n++) {
+    uint32_t ok;
+    if constexpr (CLUSTER)
+      asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                   "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, ok != 0)) return true;
+    if ((n & 63u) == 0u) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > WAIT_BUDGET_NS) *abort_flag = 1;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) return false;
+    }
+  }
+}
+
+// One operand's copies into the stage ring of this CTA (one warp).  Warp 0
 // copies P, warp 3 Q: one thread issuing both was the limit where a stage
 // takes four copies (weight gradient, G = 128: 397 -> 367 us).
 template <int MODE, bool F32, bool IS_P>
@@ -420,15 +445,19 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
     const uint32_t bytes = IS_P ? P_BYTES : (MODE == RAGGED_WGRAD ? boxes * 8192u : half * 128u);
     const int x = IS_P ? T.f0 + 128 * (int)rank : (int)T.t0 + half * (int)rank;
     for (int kb = 0; kb < T.nk; kb++) {
-      if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, WAIT_BUDGET_NS)) { ok = false; break; }
+      if (!ragged_wait<false>(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
       uint8_t* dst = ring + stage * P_BYTES;
       const int k = T.k0 + kb * BK;
       armed |= 1u << stage;
       armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-      if (MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0) {
-        mbar_arrive_expect_tx(&tail[stage], bytes);
+      const bool last = MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0;
+      if (last) {
         armed_tail |= 1u << stage;
         tail_phase ^= 1u << stage;
+      }
+      if (!elect_one_lane()) {
+      } else if (last) {
+        mbar_arrive_expect_tx(&tail[stage], bytes);
         for (int j = 0; j < boxes; j++)
           tma_load_2d(dst + j * 8192, IS_P ? &tmP : &tmQ.box[0], x + 64 * j, k, &tail[stage], pol);
       } else {
@@ -461,9 +490,9 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
   // Every copy has landed before the CTA leaves (the drain ignores the abort flag).
   volatile int no_abort = 0;
   for (int s = 0; s < ST; s++) {
-    if (leader && (armed >> s & 1u)) mbar_wait_bounded(&full[s], armed_phase >> s & 1u, &no_abort, WAIT_BUDGET_NS);
+    if (leader && (armed >> s & 1u)) ragged_wait<false>(&full[s], armed_phase >> s & 1u, &no_abort);
     if (armed_tail >> s & 1u)
-      mbar_wait_bounded(&tail[s], (tail_phase >> s & 1u) ^ 1u, &no_abort, WAIT_BUDGET_NS);
+      ragged_wait<false>(&tail[s], (tail_phase >> s & 1u) ^ 1u, &no_abort);
   }
 }
 
@@ -513,12 +542,12 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   RaggedWalk<MODE, F32> walk(blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
-    if (lane == 0) ragged_copies<MODE, F32, true>(tmP, tmQ, p, smem, seg, pref, rank);
+    ragged_copies<MODE, F32, true>(tmP, tmQ, p, smem, seg, pref, rank);
   } else if (warp == 3) {
-    if (lane == 0) ragged_copies<MODE, F32, false>(tmP, tmQ, p, smem, seg, pref, rank);
+    ragged_copies<MODE, F32, false>(tmP, tmQ, p, smem, seg, pref, rank);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader)
-    if (lane == 0 && leader) {
+    if (leader) {
       // K-major: 8-row groups 1024 bytes apart, a 16-step 32 bytes on.
       // MN-major: 64-wide column blocks 8192 bytes apart, groups of 8 steps
       // 1024 bytes apart, a 16-step 2048 bytes on.
@@ -533,30 +562,43 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
       bool ok = true;
       while (ok && walk.next(p, seg, pref, &T)) {
         if (T.nk == 0) continue;
-        if (!mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (!ragged_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t idesc = idesc0 | ((uint32_t)(T.nt >> 3) << 17);
         const uint32_t d = tmem_base + (uint32_t)(acc * 256);
+        const int last_steps = (T.rem + 15) >> 4;
         for (int kb = 0; kb < T.nk; kb++) {
-          if (!mbar_wait_cluster(&full[stage], phase, abort_flag)) { ok = false; break; }
+          const bool last = kb == T.nk - 1;
+          // a segment's last block is handed over by the helper warps of both CTAs
+          if (!(MODE == RAGGED_WGRAD && last ? ragged_wait<true>(&full[stage], phase, abort_flag)
+                                             : ragged_wait<false>(&full[stage], phase, abort_flag))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint64_t pd = pd0 + (uint64_t)((stage * P_BYTES) >> 4), qd = qd0 + (uint64_t)((stage * Q_BYTES) >> 4);
-          const int steps = kb == T.nk - 1 ? (T.rem + 15) >> 4 : 4;
-          for (int j = 0; j < steps; j++)
-            tc2_mma_bf16(d, pd + p_step * j, qd + q_step * j, idesc, (kb | j) != 0 ? 1u : 0u);
-          tc2_commit_both(&empty[stage]);
+          if (elect_one_lane()) {
+            const int steps = last ? last_steps : 4;
+            tc2_mma_bf16(d, pd, qd, idesc, kb != 0 ? 1u : 0u);
+            if (steps > 1) tc2_mma_bf16(d, pd + p_step, qd + q_step, idesc, 1u);
+            if (steps > 2) tc2_mma_bf16(d, pd + 2 * p_step, qd + 2 * q_step, idesc, 1u);
+            if (steps > 3) tc2_mma_bf16(d, pd + 3 * p_step, qd + 3 * q_step, idesc, 1u);
+            tc2_commit_both(&empty[stage]);
+            if (last) tc2_commit_both(&acc_full[acc]);
+          }
+          __syncwarp();
           if (++stage == ST) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        tc2_commit_both(&acc_full[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
       if (!ok) *abort_flag = 1;
       // No MMA may still be writing either CTA's tensor memory when it is freed.
       volatile int no_abort = 0;
-      tc2_commit_local(final_bar);
-      mbar_wait_bounded(final_bar, 0, &no_abort, WAIT_BUDGET_NS);
+      if (elect_one_lane()) tc2_commit_local(final_bar);
+      __syncwarp();
+      ragged_wait<false>(final_bar, 0, &no_abort);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ segment tails (both CTAs)
@@ -567,9 +609,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
         blocks = (blocks + T.nk) % ST;
         if (T.nk == 0 || (T.rem & 15) == 0) continue;
         const int stage = blocks == 0 ? ST - 1 : (int)blocks - 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&tail[stage], (tail_phase >> stage) & 1u, abort_flag,
-                                                       WAIT_BUDGET_NS)))
-          break;
+        if (!ragged_wait<false>(&tail[stage], (tail_phase >> stage) & 1u, abort_flag)) break;
         tail_phase ^= 1u << stage;
         // up to 15 rows of each 128-byte wide box: two of P, up to two of Q
         const int box = lane >> 3;
@@ -601,7 +641,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
         }
       }
       if (T.nk > 0) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag, WAIT_BUDGET_NS))) break;
+        if (!ragged_wait<false>(&acc_full[acc], acc_phase, abort_flag)) break;
         tc_fence_after();
       }
       const int nb = T.nt >> 5;
@@ -674,6 +714,7 @@ static bool bf16_map(CUtensorMap* m, const void* base, int64_t inner, int64_t ou
 }
 
 cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t s) {
+  if (!p.w_kn && (p.R <= 8 || (p.offsets && 2 * p.R <= p.G))) return launch_skinny(p, s);
   RaggedK k{};
   k.G = p.G; k.offsets = p.offsets;
   k.R = p.R; k.N = p.N; k.K = p.K;

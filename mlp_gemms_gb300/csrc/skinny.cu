@@ -1,0 +1,192 @@
+// The ragged product and the linear layer for a few rows (decode steps): every
+// weight is read once and meets at most a handful of tokens, so the time is
+// the weights' way through HBM plus the launch.  A CTA takes 16 (32 with a
+// checkpoint) features of one expert and all of K, split over its eight warps
+// in turns of 32: 64 consecutive bytes of a row per warp, 512 per CTA.  The
+// weights go from global memory straight into the registers of mma.sync's A
+// operand: the sum over k may be taken in any order as long as both operands
+// use the same one, so a lane's 16-byte load (8 consecutive k) serves as two
+// fragments without a shuffle, and so does the tokens' load on the B side.
+// No shared-memory ring, no barriers before the first load: a tcgen05 tile
+// costs its prologue (tensor-memory allocation, cluster barrier, descriptor
+// fetch) before any weight arrives, and with one row of 48 tiles it reaches
+// 96 of the 152 SMs.  Measured on 8 rows of 8 of 128 experts, 2048 -> 1536:
+// SKINNY_FIG.
+#include "act.cuh"
+#include "mx_internal.h"
+
+namespace mx {
+
+static __device__ unsigned g_skinny_status = 0;
+
+constexpr int SK_WARPS = 8;
+constexpr int SK_BATCH = 4;  // 32-k chunks a warp loads before it uses the first
+constexpr int SK_TOK = 8;    // tokens of a pass; more go over the weights again, from L2
+
+__device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
+  uint4 q;
+  asm("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(p));
+  return q;
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The want-th expert with rows, by one warp; false when there are fewer.
+__device__ __forceinline__ bool find_expert(const RaggedParams& p, int want, int lane, int* g_out, int64_t* r0,
+                                            int64_t* r1, bool report) {
+  if (p.offsets == nullptr) {
+    *g_out = 0; *r0 = 0; *r1 = p.R;
+    return want == 0;
+  }
+  int64_t high = 0;
+  int seen = 0;
+  bool bad = false, found = false;
+  for (int b = 0; b < p.G; b += 32) {
+    const int g = b + lane;
+    const int64_t s0 = g < p.G && g ? (int64_t)__ldg(p.offsets + g - 1) : 0;
+    const int64_t s1 = g < p.G ? (int64_t)__ldg(p.offsets + g) : 0;
+    int64_t top = s0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, top, o);
+      if (lane >= o && u > top) top = u;
+    }
+    if (high > top) top = high;
+    high = __shfl_sync(0xFFFFFFFFu, top, 31);
+    const bool ok = s0 >= top && s1 >= s0 && s1 <= p.R;
+    if (g < p.G && !ok) bad = true;
+    const unsigned has = __ballot_sync(0xFFFFFFFFu, g < p.G && ok && s1 > s0);
+    const int n = __popc(has);
+    if (!found && want < seen + n) {
+      const int src = __fns(has, 0, want - seen + 1);
+      *g_out = b + src;
+      *r0 = __shfl_sync(0xFFFFFFFFu, s0, src);
+      *r1 = __shfl_sync(0xFFFFFFFFu, s1, src);
+      found = true;
+      if (!report) return true;
+    }
+    seen += n;
+  }
+  if (report && __any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(&g_skinny_status, DEV_BAD_OFFSETS);
+  return found;
+}
+
+// Three CTAs an SM with 4 chunks in flight (two with 32 features): measured
+// on one token of 4096 -> 16384 against 2 x 8, 4 x 4, 4 x 2 and 5 x 2 chunks
+// 23.9 us against 24.0, 29.0, 24.4, 35.1, and on 8 experts' rows 12.8 against
+// 14.0, 16.5, 13.9, 17.8 (more CTAs spill).
+template <int MT, bool EPI>
+__global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(const RaggedParams p) {
+  constexpr int ROWS = 16 * MT, TOK = SK_TOK;
+  __shared__ float red[SK_WARPS][TOK][ROWS + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
+  int g = 0;
+  int64_t r0, r1;
+  if (!find_expert(p, (int)blockIdx.y, lane, &g, &r0, &r1, blockIdx.x == 0 && blockIdx.y == 0 && warp == 0)) return;
+  const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+  const uint16_t* w[2 * MT];
+  bool win[2 * MT];
+#pragma unroll
+  for (int i = 0; i < 2 * MT; i++) {
+    win[i] = n0 + g4 + 8 * i < p.N;
+    w[i] = p.w + ((int64_t)g * p.N + (win[i] ? n0 + g4 + 8 * i : 0)) * p.K + 8 * t4;
+  }
+  const int chunks = (int)((p.K + 31) / 32);
+  for (int64_t m0 = r0; m0 < r1; m0 += TOK) {
+    float acc[MT][4] = {};
+    const bool xin = m0 + g4 < r1;
+    const uint16_t* x = p.a + (xin ? m0 + g4 : m0) * p.ld_a + 8 * t4;
+    for (int c0 = warp; c0 < chunks; c0 += SK_WARPS * SK_BATCH) {
+      uint4 qw[SK_BATCH][2 * MT], qx[SK_BATCH];
+#pragma unroll
+      for (int b = 0; b < SK_BATCH; b++) {
+        const int k = (c0 + b * SK_WARPS) * 32;
+        const bool kin = k + 8 * t4 < p.K;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; i++) qw[b][i] = kin && win[i] ? ld_stream(w[i] + k) : make_uint4(0, 0, 0, 0);
+        qx[b] = kin && xin ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int b = 0; b < SK_BATCH; b++)
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+          const uint4 &u = qw[b][2 * m], &v = qw[b][2 * m + 1];
+          mma_16816(acc[m], u.x, v.x, u.y, v.y, qx[b].x, qx[b].y);
+          mma_16816(acc[m], u.z, v.z, u.w, v.w, qx[b].z, qx[b].w);
+        }
+    }
+    if (m0 != r0) __syncthreads();  // the last group's sums have been read
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) red[warp][2 * t4 + (i & 1)][16 * m + g4 + 8 * (i >> 1)] = acc[m][i];
+    __syncthreads();
+    // the warps' sums in warp order; consecutive threads hold consecutive features
+    const int count = r1 - m0 < TOK ? (int)(r1 - m0) : TOK;
+    for (int i = threadIdx.x; i < TOK * ROWS; i += 32 * SK_WARPS) {
+      const int t = i / ROWS, f = i % ROWS;
+      float z = 0.f;
+#pragma unroll
+      for (int s = 0; s < SK_WARPS; s++) z += red[s][t][f];
+      const int64_t row = m0 + t, col = n0 + f;
+      const bool in = t < count && col < p.N;
+      float v = z;
+      if constexpr (EPI) {
+        if (p.epi.bias && in) z += bf16_bits_to_float(__ldg(p.epi.bias + col));
+        if (MT == 2 && p.epi.q) {  // a warp's 32 lanes are one scale block
+          float m = z;
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) m = max_abs_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          const uint32_t b = rceil_scale_byte_sel<E4M3>(__float_as_uint(m) & 0x7FFFFFFFu);
+          const int64_t sc = p.N >> 5;
+          if (in) {
+            p.epi.q[row * p.N + col] =
+                b == 0xFFu ? 0x7Fu : (uint8_t)cvt_e4m3x2(z * inv_scale_from_byte(b & 0xFFu), 0.f);
+            if (f == 0) p.epi.q_scale[blocked_offset(row, col >> 5, sc)] = (uint8_t)b;
+          }
+        }
+        v = p.epi.act == MX_ACT_GELU_TANH ? act_f32<MX_ACT_GELU_TANH>(z)
+            : p.epi.act == MX_ACT_SILU    ? act_f32<MX_ACT_SILU>(z)
+            : p.epi.act == MX_ACT_RELU    ? act_f32<MX_ACT_RELU>(z)
+                                          : z;
+        if (p.epi.res && in) v += bf16_bits_to_float(p.epi.res[row * p.epi.ld_res + col]);
+      }
+      if (in) p.out[row * p.ld_out + col] = (uint16_t)float2_to_bf16x2(v, 0.f);
+    }
+  }
+  if constexpr (EPI && MT == 2) {  // zero padding of the scale layout: rows to 128, columns to 4
+    if (p.epi.q && n0 < p.N) {
+      const int64_t sc = p.N >> 5, top = (p.R + 127) / 128 * 128;
+      for (int64_t c = n0 >> 5; c < ((n0 >> 5) + 1 == sc ? (sc + 3) / 4 * 4 : (n0 >> 5) + 1); c++)
+        for (int64_t r = (c < sc ? p.R : 0) + threadIdx.x; r < top; r += blockDim.x)
+          p.epi.q_scale[blocked_offset(r, c, sc)] = 0;
+    }
+  }
+}
+
+template <int MT, bool EPI>
+static cudaError_t launch(const RaggedParams& p, cudaStream_t s) {
+  const dim3 grid((unsigned)((p.N + 16 * MT - 1) / (16 * MT)), (unsigned)(p.offsets ? (p.G < p.R ? p.G : p.R) : 1));
+  skinny_kernel<MT, EPI><<<grid, 32 * SK_WARPS, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s) {
+  if (p.epi.q) return launch<2, true>(p, s);
+  const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res;
+  return epi ? launch<1, true>(p, s) : launch<1, false>(p, s);
+}
+
+cudaError_t read_skinny_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_skinny_status, sizeof(unsigned)); }
+cudaError_t reset_skinny_status() {
+  const unsigned zero = 0;
+  return cudaMemcpyToSymbol(g_skinny_status, &zero, sizeof(unsigned));
+}
+
+}  // namespace mx
