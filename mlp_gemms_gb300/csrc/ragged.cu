@@ -27,10 +27,12 @@
 //
 // The weight gradient contracts over a segment's rows.  Its last 64-row block
 // may hold rows of the next expert: those blocks are copied on the CTA's own
-// barrier, a helper warp zeroes the rows up to the next multiple of 16 in both
-// operands (a zero against a neighbour's Inf or NaN would be NaN) and only
-// then hands the stage to the MMA thread, which runs the 16-row steps that
-// hold rows of the segment.
+// barrier, then a helper warp has the rows up to the next multiple of 16
+// zeroed in both operands (a zero against a neighbour's Inf or NaN would be
+// NaN) by copies that start beyond the tensor and read as zeros, counted on
+// the stage's barrier; the MMA thread runs the 16-row steps that hold rows of
+// the segment.  (Zeroing with stores needs a proxy fence and a cluster-scope
+// release from the peer, 1100 cycles measured.)
 //
 // Every wait is bounded; on expiry the CTA records a device status bit and
 // unwinds.
@@ -389,9 +391,10 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
 }
 
 // The Q operand's maps: boxes of 128, 64, 32 and 16 rows (a CTA's half of a
-// tile is a multiple of 16 tokens); WGRAD: box[0] only, 64 x 64.
+// tile is a multiple of 16 tokens); WGRAD: box[0] 64 x 64, box[1..4] 8, 4, 2
+// and 1 rows of 64 columns, unswizzled, for the zeros.
 struct RaggedMapsQ {
-  CUtensorMap box[4];
+  CUtensorMap box[5];
 };
 
 // Bounded wait of a whole warp for a phase of a barrier (CLUSTER: with
@@ -419,6 +422,14 @@ __device__ __forceinline__ bool ragged_wait(uint64_t* bar, uint32_t parity, vola
   }
 }
 
+// Hand an accumulator back: an arrival on a barrier of the leader CTA that
+// orders no memory.  What it announces, this warp's tensor-memory loads, is
+// complete (tcgen05.wait::ld); a release at cluster scope would also wait for
+// the warp's stores to global memory, about 1100 cycles a tile.
+__device__ __forceinline__ void arrive_on_leader_relaxed(uint32_t bar_cl) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cl) : "memory");
+}
+
 // One operand's copies into the stage ring of this CTA (one warp).  Warp 0
 // copies P, warp 3 Q: one thread issuing both was the limit where a stage
 // takes four copies (weight gradient, G = 128: 397 -> 367 us).
@@ -431,7 +442,9 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
   uint64_t* empty = full + ST;
   uint64_t* tail = empty + ST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-  const uint64_t pol = l2_policy_evict_normal();
+  // The weight gradient's outputs (as large as its inputs) would push operands
+  // out of L2 that other tiles still need.
+  const uint64_t pol = MODE == RAGGED_WGRAD ? l2_policy_evict_last() : l2_policy_evict_normal();
   uint8_t* const ring = smem + (IS_P ? 0 : OFF_Q);
   const bool leader = rank == 0;
   RaggedTile T;
@@ -506,7 +519,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // leader's: the stage is in both CTAs' shared memory
   uint64_t* empty = full + ST;      // both CTAs: the stage's MMAs are done
-  uint64_t* tail = empty + ST;      // each CTA's own: a segment's last block has landed
+  uint64_t* tail = empty + ST;      // each CTA's own: a segment's last block has landed, its end not yet zeroed
   uint64_t* acc_full = tail + ST;   // both CTAs: the tile's MMAs are done
   uint64_t* acc_empty = acc_full + 2;  // leader's: both CTAs' epilogue warps have read the accumulator
   uint64_t* final_bar = acc_empty + 2;
@@ -520,7 +533,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
 
   if (threadIdx.x == 0) {
     prefetch_tensormap(&tmP);
-    for (int j = 0; j < (Q_MN ? 1 : 4); j++) prefetch_tensormap(&tmQ.box[j]);
+    for (int j = 0; j < (Q_MN ? 5 : 4); j++) prefetch_tensormap(&tmQ.box[j]);
     for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); mbar_init(&tail[s], 2); }
     for (int a = 0; a < 2; a++) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 16); }
     mbar_init(final_bar, 1);
@@ -569,12 +582,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
         const int last_steps = (T.rem + 15) >> 4;
         for (int kb = 0; kb < T.nk; kb++) {
           const bool last = kb == T.nk - 1;
-          // a segment's last block is handed over by the helper warps of both CTAs
-          if (!(MODE == RAGGED_WGRAD && last ? ragged_wait<true>(&full[stage], phase, abort_flag)
-                                             : ragged_wait<false>(&full[stage], phase, abort_flag))) {
-            ok = false;
-            break;
-          }
+          if (!ragged_wait<false>(&full[stage], phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint64_t pd = pd0 + (uint64_t)((stage * P_BYTES) >> 4), qd = qd0 + (uint64_t)((stage * Q_BYTES) >> 4);
           if (elect_one_lane()) {
@@ -603,6 +611,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   } else if (warp == 2) {
     // ------------------------------------------------------------ segment tails (both CTAs)
     if constexpr (MODE == RAGGED_WGRAD) {
+      const uint64_t pol = l2_policy_evict_normal();
       uint32_t blocks = 0;  // contraction blocks of this pair so far, modulo the stages
       uint32_t tail_phase = 0;
       while (walk.next(p, seg, pref, &T)) {
@@ -611,15 +620,28 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
         const int stage = blocks == 0 ? ST - 1 : (int)blocks - 1;
         if (!ragged_wait<false>(&tail[stage], (tail_phase >> stage) & 1u, abort_flag)) break;
         tail_phase ^= 1u << stage;
-        // up to 15 rows of each 128-byte wide box: two of P, up to two of Q
-        const int box = lane >> 3;
-        if (box < 2 + ((T.nt + 127) >> 7)) {
-          uint8_t* b = smem + stage * P_BYTES + (box < 2 ? box * 8192 : OFF_Q + (box - 2) * 8192) + (lane & 7) * 16;
-          for (int r = T.rem; r & 15; r++) *reinterpret_cast<uint4*>(b + r * 128) = make_uint4(0, 0, 0, 0);
+        // The rows from the segment's end to the next multiple of 16, of each
+        // 128-byte wide box (two of P, up to two of Q), become zero by copies
+        // from beyond the tensor: 1 to 15 rows as 8 + 4 + 2 + 1.
+        const int boxes = 2 + ((T.nt + 127) >> 7), zrows = 16 - (T.rem & 15);
+        if (elect_one_lane()) {
+          const uint32_t fb = leader_addr(&full[stage]);
+          if (leader) {
+            mbar_arrive_expect_tx(&full[stage], 2u * (uint32_t)(boxes * zrows * 128));
+            mbar_arrive(&full[stage]);
+          }
+          for (int j = 0; j < boxes; j++) {
+            uint8_t* dst = smem + stage * P_BYTES + (j < 2 ? j * 8192 : OFF_Q + (j - 2) * 8192) + T.rem * 128;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              if (zrows & (8 >> i)) {
+                tma2_load_2d(dst, &tmQ.box[1 + i], 0, (int)p.R, fb, pol);
+                dst += (8 >> i) * 128;
+              }
+            }
+          }
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_on_leader(leader_addr(&full[stage]));
       }
     }
   } else if (warp >= 4) {
@@ -647,7 +669,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
       const int nb = T.nt >> 5;
       const uint32_t tb = tmem_base + (uint32_t)(acc * 256) + ((uint32_t)(q * 32) << 16);
       const uint32_t hand_back = leader_addr(&acc_empty[acc]);
-      if (T.nk > 0 && h >= nb && lane == 0) arrive_on_leader(hand_back);
+      if (T.nk > 0 && h >= nb && lane == 0) arrive_on_leader_relaxed(hand_back);
       for (int b = h; b < nb; b += 2) {
         float v[2][16];
         if (T.nk > 0) {
@@ -657,7 +679,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
           if (b + 2 >= nb) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_on_leader(hand_back);
+            if (lane == 0) arrive_on_leader_relaxed(hand_back);
           }
         } else {  // an expert without rows: zeros
 #pragma unroll
@@ -704,12 +726,13 @@ static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const 
 // BF16 matrix [outer, inner] (row stride ld elements), optionally a stack of
 // `batch` of them, as 128-byte swizzled boxes of 64 x box_rows.
 static bool bf16_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int64_t batch,
-                     int box_rows) {
+                     int box_rows, bool swizzle = true) {
   TensorMapShape s{};
   s.rank = batch > 0 ? 3 : 2;
   s.dims[0] = (uint64_t)inner; s.dims[1] = (uint64_t)outer; s.dims[2] = (uint64_t)batch;
   s.strides[0] = (uint64_t)ld * 2; s.strides[1] = (uint64_t)outer * (uint64_t)ld * 2;
   s.box[0] = 64; s.box[1] = (uint32_t)box_rows; s.box[2] = 1;
+  s.swizzle = swizzle;
   return encode_bf16_map(m, base, s) == MX_OK;
 }
 
@@ -752,6 +775,8 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   RaggedMapsQ tq;
   if (!bf16_map(&tp, p.x, p.K, p.R, p.ld_x, 0, 64) || !bf16_map(&tq.box[0], p.dy, p.N, p.R, p.ld_dy, 0, 64))
     return cudaErrorInvalidValue;
+  for (int j = 0; j < 4; j++)
+    if (!bf16_map(&tq.box[1 + j], p.dy, p.N, p.R, p.ld_dy, 0, 8 >> j, false)) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)p.G * k.n_f * k.n_t;
   return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tiles, num_sms, s)
                 : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, num_sms, s);
