@@ -50,7 +50,7 @@ constexpr int ST = 6;         // 32 KB stages of 64 contraction steps
 constexpr int BK = 64;
 constexpr int P_BYTES = 16384, Q_BYTES = 16384;
 constexpr int OFF_Q = ST * P_BYTES;
-constexpr int STG = 2560;     // per epilogue warp: 32 rows x (64 + 16) bytes
+constexpr int STG = 2304;     // per epilogue warp; two share 32 rows x (128 + 16) bytes
 constexpr int OFF_STG = OFF_Q + ST * Q_BYTES;
 constexpr int OFF_SEG = OFF_STG + 8 * STG;                  // segment ends, [0] = 0
 constexpr int OFF_PREF = OFF_SEG + 4 * (MAX_RAGGED_G + 1);  // row tiles before expert g
@@ -261,39 +261,48 @@ __device__ __forceinline__ void ckpt_block(const RaggedK& p, const float (&v)[2]
   __syncwarp();
 }
 
+// The residual's part of a block, 16 bytes of 8 rows a load: fetched a block
+// ahead, so that its latency is not the epilogue's.
+__device__ __forceinline__ void load_residual(const RaggedK& p, uint4 (&x)[4], int lane, int64_t row0, int valid,
+                                              int64_t col) {
+  const int64_t c = col + 8 * (lane & 3);
+  const uint16_t* at = p.epi.res + (row0 + (lane >> 2)) * p.epi.ld_res + c;
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    x[i] = 8 * i + (lane >> 2) < valid && c < p.N ? *reinterpret_cast<const uint4*>(at + 8 * i * p.epi.ld_res)
+                                                  : make_uint4(0, 0, 0, 0);
+}
+
 // One 32-feature x 32-token block of the accumulator -> BF16 rows, with the
-// linear layer's epilogue when EPI.
+// linear layer's epilogue when EPI.  Two warps whose features are neighbours
+// share a staging buffer (32 rows of 128 + 16 bytes; stg, this warp's features
+// 64 bytes into it or not) and store whole 128-byte lines of 16 rows each.
 template <bool EPI>
 __device__ __forceinline__ void store_block_bf16(const RaggedK& p, float (&v)[2][16], uint8_t* stg, int lane,
-                                                 const float (&bias)[4], uint16_t* out, int64_t row0, int valid,
-                                                 int64_t col) {
+                                                 int odd, int bar, const float (&bias)[4], const uint4 (&res)[4],
+                                                 uint16_t* out, int64_t row0, int valid, int64_t col) {
   const uint32_t base = smem_u32(stg);
-  const uint32_t frag = base + (lane & 7) * 80 + (lane >> 3) * 16;
-  const int64_t mycol = col + 8 * (lane & 3);
+  const uint32_t frag = base + (lane & 7) * 144 + (lane >> 3) * 16 + odd * 64;
   if constexpr (EPI) {
 #pragma unroll
     for (int i = 0; i < 16; i++) {
       v[0][i] += bias[(i >> 1) & 1];
       v[1][i] += bias[2 + ((i >> 1) & 1)];
     }
-    if (p.epi.q) ckpt_block(p, v, stg, lane, row0, valid, col);
+    if (p.epi.q) ckpt_block(p, v, stg + odd * 2304, lane, row0, valid, col);
+    if (p.epi.q) named_bar(bar, 64);
     if (p.epi.act == MX_ACT_GELU_TANH) act_values<MX_ACT_GELU_TANH>(v);
     else if (p.epi.act == MX_ACT_SILU) act_values<MX_ACT_SILU>(v);
     else if (p.epi.act == MX_ACT_RELU) act_values<MX_ACT_RELU>(v);
     if (p.epi.res) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int t = 8 * i + (lane >> 2);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (t < valid && mycol < p.N)
-          x = *reinterpret_cast<const uint4*>(p.epi.res + (row0 + t) * p.epi.ld_res + mycol);
-        *reinterpret_cast<uint4*>(stg + t * 80 + (lane & 3) * 16) = x;
-      }
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<uint4*>(stg + (8 * i + (lane >> 2)) * 144 + (lane & 3) * 16 + odd * 64) = res[i];
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         uint32_t r[4];
-        ldmatrix4_trans(frag + 8 * j * 80, r);
+        ldmatrix4_trans(frag + 8 * j * 144, r);
 #pragma unroll
         for (int m = 0; m < 4; m++) {
           v[m >> 1][4 * j + 2 * (m & 1)] += bf16_bits_to_float(r[m] & 0xFFFFu);
@@ -304,18 +313,30 @@ __device__ __forceinline__ void store_block_bf16(const RaggedK& p, float (&v)[2]
   }
 #pragma unroll
   for (int j = 0; j < 4; j++)
-    stmatrix4_trans(frag + 8 * j * 80, float2_to_bf16x2(v[0][4 * j], v[0][4 * j + 1]),
+    stmatrix4_trans(frag + 8 * j * 144, float2_to_bf16x2(v[0][4 * j], v[0][4 * j + 1]),
                     float2_to_bf16x2(v[0][4 * j + 2], v[0][4 * j + 3]),
                     float2_to_bf16x2(v[1][4 * j], v[1][4 * j + 1]),
                     float2_to_bf16x2(v[1][4 * j + 2], v[1][4 * j + 3]));
-  __syncwarp();
+  named_bar(bar, 64);
+  const int64_t c = col - 32 * odd + 8 * (lane & 7);
+  const int t0 = 16 * odd + (lane >> 3);
+  uint16_t* at = out + (row0 + t0) * p.ld_out + c;
+  uint4 x[4];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int t = 8 * i + (lane >> 2);
-    const uint4 x = *reinterpret_cast<const uint4*>(stg + t * 80 + (lane & 3) * 16);
-    if (t < valid && mycol < p.N) *reinterpret_cast<uint4*>(out + (row0 + t) * p.ld_out + mycol) = x;
-  }
-  __syncwarp();
+  for (int i = 0; i < 4; i++) x[i] = *reinterpret_cast<const uint4*>(stg + (t0 + 4 * i) * 144 + (lane & 7) * 16);
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    if (t0 + 4 * i < valid && c < p.N) *reinterpret_cast<uint4*>(at + 4 * i * p.ld_out) = x[i];
+  named_bar(bar, 64);  // the buffer is free
+}
+
+// Whether both of a pair's warps have `ok`; both always come here, so neither
+// waits at a later barrier for one that gave up.
+__device__ __forceinline__ bool both_ok(bool ok, int bar) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, 64, p;\n\t"
+               "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)ok), "r"(bar) : "memory");
+  return r != 0;
 }
 
 // The same block in fp32, stored or added: eight lanes hold eight consecutive
@@ -647,7 +668,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, h = (warp - 4) >> 2;  // lane quarter (32 features), parity of the 32-token blocks
-    uint8_t* stg = smem + OFF_STG + (warp - 4) * STG;
+    const int odd = warp & 1, bar = 1 + ((warp - 4) >> 1);  // the warp's place in its pair, the pair's barrier
+    uint8_t* stg = smem + OFF_STG + ((warp - 4) & ~1) * STG;
     int acc = 0;
     uint32_t acc_phase = 0;
     while (walk.next(p, seg, pref, &T)) {
@@ -662,11 +684,13 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
           }
         }
       }
+      const int nb = T.nt >> 5;
+      uint4 res[4];
+      if (EPI && p.epi.res && h < nb) load_residual(p, res, lane, T.t0 + 32 * h, T.valid - 32 * h, col);
       if (T.nk > 0) {
-        if (!ragged_wait<false>(&acc_full[acc], acc_phase, abort_flag)) break;
+        if (!both_ok(ragged_wait<false>(&acc_full[acc], acc_phase, abort_flag), bar)) break;
         tc_fence_after();
       }
-      const int nb = T.nt >> 5;
       const uint32_t tb = tmem_base + (uint32_t)(acc * 256) + ((uint32_t)(q * 32) << 16);
       const uint32_t hand_back = leader_addr(&acc_empty[acc]);
       if (T.nk > 0 && h >= nb && lane == 0) arrive_on_leader_relaxed(hand_back);
@@ -688,11 +712,18 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
         const int64_t row0 = T.t0 + 32 * b;
         const int valid = T.valid - 32 * b < 32 ? T.valid - 32 * b : 32;
         const int64_t base = MODE == RAGGED_WGRAD ? (int64_t)T.g * p.K * p.ld_out : 0;
+        uint4 next[4];
+        if (EPI && p.epi.res && b + 2 < nb) load_residual(p, next, lane, row0 + 64, T.valid - 32 * b - 64, col);
         if constexpr (F32)
           store_block_f32(p, v, lane, static_cast<float*>(p.out) + base, row0, valid, col,
                           p.accumulate || T.part > 0);
         else
-          store_block_bf16<EPI>(p, v, stg, lane, bias, static_cast<uint16_t*>(p.out) + base, row0, valid, col);
+          store_block_bf16<EPI>(p, v, stg, lane, odd, bar, bias, res, static_cast<uint16_t*>(p.out) + base, row0,
+                                valid, col);
+        if (EPI && p.epi.res) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) res[i] = next[i];
+        }
       }
       if (T.nk > 0) {
         acc ^= 1;
