@@ -1,9 +1,16 @@
-// Activations of the BF16 layers and their slopes, in fp32.
+// Device helpers of the BF16 layers: activations and their slopes in fp32,
+// programmatic launches.
 #pragma once
 #include "../../include/mx.h"
 #include "mx_common.cuh"
 
 namespace mx {
+
+// Programmatic launches: everything the stream's earlier kernels wrote is
+// visible after pdl_wait(); pdl_trigger() lets the stream's next kernel start
+// as far as its own pdl_wait().
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // 1 / (1 + exp(-x)): exp by the hardware's 2^x and one approximate
 // reciprocal (relative error a few 2^-23, against the 2^-9 of the BF16 the

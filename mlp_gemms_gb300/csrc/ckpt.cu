@@ -109,6 +109,8 @@ template <int ACT>
 __global__ void __launch_bounds__(256) ckpt_fwd_kernel(const CkptParams p, uint32_t per) {
   constexpr bool GLU = ACT == MX_ACT_SWIGLU;
   const int64_t F = GLU ? p.C / 2 : p.C;
+  pdl_trigger();
+  pdl_wait();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.R * per; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i < (1ll << 32) ? (uint32_t)i / per : i / per;
     const int c = (int)(i - r * per) * 32;
@@ -132,18 +134,20 @@ __global__ void __launch_bounds__(256) ckpt_fwd_kernel(const CkptParams p, uint3
   if (blockIdx.x == 0) zero_scale_padding(p);
 }
 
-// Row blocks of both passes: enough for eight blocks on every SM (GB300:
-// 152), each with a row for each of its warps.
+// Row blocks of the backward pass: one wave of two blocks on every SM (GB300:
+// 152) where the columns alone do not give it, each with a row for each of its
+// warps.  col_blocks counts SWIGLU's columns twice: its blocks do two halves'
+// work.
 int64_t ckpt_row_blocks(int64_t R, int64_t C) {
   const int64_t col_blocks = (C + COLS - 1) / COLS;
-  int64_t want = (152 * 8 + col_blocks - 1) / col_blocks;
+  int64_t want = 152 * 4 / col_blocks;
   const int64_t most = (R + WARPS - 1) / WARPS;
   if (want > most) want = most;
   return want < 1 ? 1 : want;
 }
 
 template <int ACT, bool H, bool DB>
-__global__ void __launch_bounds__(32 * WARPS) ckpt_bwd_kernel(const CkptParams p, int64_t rows_per_block) {
+__global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParams p, int64_t rows_per_block) {
   constexpr bool GLU = ACT == MX_ACT_SWIGLU;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t F = ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C;
@@ -152,6 +156,8 @@ __global__ void __launch_bounds__(32 * WARPS) ckpt_bwd_kernel(const CkptParams p
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
   const int64_t r1 = r0 + rows_per_block < p.R ? r0 + rows_per_block : p.R;
   float sum[8] = {}, sum_u[8] = {};
+  pdl_trigger();
+  pdl_wait();
   for (int64_t rb = r0 + warp; in && rb < r1; rb += WARPS * BATCH) {
     uint2 qz[BATCH], qu[BATCH];
     uint32_t bz[BATCH], bu[BATCH];
@@ -227,6 +233,8 @@ __global__ void __launch_bounds__(256) ckpt_colsum_kernel(const float* __restric
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // C is a multiple of 32
   float t = 0.f;
+  pdl_trigger();
+  pdl_wait();
 #pragma unroll 4
   for (int64_t b = w; b < blocks; b += 8) t += part[b * C + c];
   s[w][lane] = t;
@@ -246,42 +254,42 @@ static dim3 ckpt_grid(const CkptParams& p, int64_t* rows) {
 }
 
 template <int ACT>
-static void launch_fwd(const CkptParams& p, cudaStream_t s) {
+static cudaError_t launch_fwd(const CkptParams& p, cudaStream_t s) {
   const int64_t per = (ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C) / 32, blocks = (p.R * per + 255) / 256;
-  ckpt_fwd_kernel<ACT><<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, s>>>(p, (uint32_t)per);
+  return launch_pdl(ckpt_fwd_kernel<ACT>, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), 256, 0, s, p,
+                    (uint32_t)per);
 }
 
 cudaError_t launch_ckpt_fwd(const CkptParams& p, cudaStream_t s) {
   switch (p.act) {
-    case MX_ACT_SWIGLU: launch_fwd<MX_ACT_SWIGLU>(p, s); break;
-    case MX_ACT_GELU_TANH: launch_fwd<MX_ACT_GELU_TANH>(p, s); break;
-    case MX_ACT_SILU: launch_fwd<MX_ACT_SILU>(p, s); break;
-    default: launch_fwd<MX_ACT_RELU>(p, s); break;
+    case MX_ACT_SWIGLU: return launch_fwd<MX_ACT_SWIGLU>(p, s);
+    case MX_ACT_GELU_TANH: return launch_fwd<MX_ACT_GELU_TANH>(p, s);
+    case MX_ACT_SILU: return launch_fwd<MX_ACT_SILU>(p, s);
+    default: return launch_fwd<MX_ACT_RELU>(p, s);
   }
-  return cudaGetLastError();
 }
 
 template <int ACT>
-static void launch_bwd(const CkptParams& p, dim3 grid, int64_t rows, cudaStream_t s) {
-  if (p.h && p.db) ckpt_bwd_kernel<ACT, true, true><<<grid, 32 * WARPS, 0, s>>>(p, rows);
-  else if (p.h) ckpt_bwd_kernel<ACT, true, false><<<grid, 32 * WARPS, 0, s>>>(p, rows);
-  else if (p.db) ckpt_bwd_kernel<ACT, false, true><<<grid, 32 * WARPS, 0, s>>>(p, rows);
-  else ckpt_bwd_kernel<ACT, false, false><<<grid, 32 * WARPS, 0, s>>>(p, rows);
+static cudaError_t launch_bwd(const CkptParams& p, dim3 grid, int64_t rows, cudaStream_t s) {
+  constexpr unsigned T = 32 * WARPS;
+  if (p.h && p.db) return launch_pdl(ckpt_bwd_kernel<ACT, true, true>, grid, T, 0, s, p, rows);
+  if (p.h) return launch_pdl(ckpt_bwd_kernel<ACT, true, false>, grid, T, 0, s, p, rows);
+  if (p.db) return launch_pdl(ckpt_bwd_kernel<ACT, false, true>, grid, T, 0, s, p, rows);
+  return launch_pdl(ckpt_bwd_kernel<ACT, false, false>, grid, T, 0, s, p, rows);
 }
 
 cudaError_t launch_ckpt_bwd(const CkptParams& p, cudaStream_t s) {
   int64_t rows;
   const dim3 grid = ckpt_grid(p, &rows);
+  cudaError_t e;
   switch (p.act) {
-    case MX_ACT_SWIGLU: launch_bwd<MX_ACT_SWIGLU>(p, grid, rows, s); break;
-    case MX_ACT_GELU_TANH: launch_bwd<MX_ACT_GELU_TANH>(p, grid, rows, s); break;
-    case MX_ACT_SILU: launch_bwd<MX_ACT_SILU>(p, grid, rows, s); break;
-    default: launch_bwd<MX_ACT_RELU>(p, grid, rows, s); break;
+    case MX_ACT_SWIGLU: e = launch_bwd<MX_ACT_SWIGLU>(p, grid, rows, s); break;
+    case MX_ACT_GELU_TANH: e = launch_bwd<MX_ACT_GELU_TANH>(p, grid, rows, s); break;
+    case MX_ACT_SILU: e = launch_bwd<MX_ACT_SILU>(p, grid, rows, s); break;
+    default: e = launch_bwd<MX_ACT_RELU>(p, grid, rows, s); break;
   }
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.db == nullptr) return e;
-  ckpt_colsum_kernel<<<(unsigned)(p.C / 32), 256, 0, s>>>(p.partials, (int64_t)grid.y, p.C, p.db);
-  return cudaGetLastError();
+  return launch_pdl(ckpt_colsum_kernel, dim3((unsigned)(p.C / 32)), 256, 0, s, p.partials, (int64_t)grid.y, p.C, p.db);
 }
 
 }  // namespace mx

@@ -164,6 +164,24 @@ cudaError_t reset_perm_status();
 constexpr int kRouteChunk = 1024;
 cudaError_t launch_wait_selftest(uint64_t budget_ns, cudaStream_t s);
 
+// Launch with programmatic stream serialization: the kernel may start while
+// the stream's previous kernel drains, and must run pdl_wait() before it
+// touches global memory (pdl_trigger() lets the next such kernel start).
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // BF16 products over ragged segments (ragged.cu).
 struct RaggedEpi {           // mx_linear_fwd's epilogue; all null: plain store
   const uint16_t* bias = nullptr;

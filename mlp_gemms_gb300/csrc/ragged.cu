@@ -70,7 +70,8 @@ struct RaggedK {
   int64_t N;               // output columns (the P side's extent)
   int64_t K;               // contraction (WGRAD: the Q side's extent instead)
   int n_f;                 // 256-column tiles of the output
-  int n_t;                 // WGRAD: 256-row tiles of an expert's output
+  int n_t;                 // WGRAD: row tiles of an expert's output
+  int tw;                  // rows of a tile, a multiple of 32 up to 256
   void* out;
   int64_t ld_out;          // elements; WGRAD: N
   int accumulate;
@@ -125,7 +126,7 @@ struct RaggedWalk {
     T->parts = 1;
     int64_t left;
     if constexpr (MODE == RAGGED_WGRAD) {
-      T->t0 = (int64_t)mt * 256;
+      T->t0 = (int64_t)mt * p.tw;
       left = p.K - T->t0;
       int rows = pref[g + 1] - pref[g];  // rows of the segment, 0 if malformed
       T->k0 = seg0;
@@ -138,13 +139,13 @@ struct RaggedWalk {
       T->nk = (rows + rg::BK - 1) / rg::BK;
       T->rem = rows - (T->nk - 1) * rg::BK;
     } else {
-      T->t0 = (int64_t)seg0 + 256 * (int64_t)mt;
+      T->t0 = (int64_t)seg0 + p.tw * (int64_t)mt;
       left = (int64_t)seg[g + 1] - T->t0;
       T->k0 = 0;
       T->nk = (int)((p.K + rg::BK - 1) / rg::BK);
       T->rem = (int)p.K - (T->nk - 1) * rg::BK;
     }
-    T->valid = left < 256 ? (int)left : 256;
+    T->valid = left < p.tw ? (int)left : p.tw;
     T->nt = (T->valid + 31) & ~31;
     T->part = part;
     if (++part >= T->parts) {
@@ -340,38 +341,39 @@ __device__ __forceinline__ bool both_ok(bool ok, int bar) {
 }
 
 // The same block in fp32, stored or added: eight lanes hold eight consecutive
-// features, so each row piece is a full 32-byte sector without staging.
-__device__ __forceinline__ void store_block_f32(const RaggedK& p, float (&v)[2][16], int lane, float* out,
-                                                int64_t row0, int valid, int64_t col, bool add) {
-  const int t0 = 2 * (lane & 3);
-  const int64_t c0 = col + (lane >> 2);
-  float* at = out + (row0 + t0) * p.ld_out + c0;
-  const int left = p.N - c0 > 32 ? 32 : (int)(p.N - c0);  // columns from this lane's first one on
-  if (add) {  // all loads before the first use
-    float old[2][16];
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-      for (int i = 0; i < 16; i++) {
-        const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
-        old[h][i] = t0 + t < valid && f < left ? __ldcg(at + (int64_t)t * p.ld_out + f) : 0.f;
-      }
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-      for (int i = 0; i < 16; i++) v[h][i] += old[h][i];
-  }
+// features, so each row piece is a full 32-byte sector without staging.  What
+// it is added to is loaded a block ahead.
+struct F32Block {
+  float* at;    // this lane's first value
+  int rows, cols;  // valid ones from there on
+};
+__device__ __forceinline__ F32Block f32_block(const RaggedK& p, float* out, int lane, int64_t row0, int valid,
+                                              int64_t col) {
+  const int64_t c = col + (lane >> 2);
+  return F32Block{out + (row0 + 2 * (lane & 3)) * p.ld_out + c, valid - 2 * (lane & 3),
+                  p.N - c > 32 ? 32 : (int)(p.N - c)};
+}
+__device__ __forceinline__ void load_block_f32(const RaggedK& p, const F32Block& b, float (&old)[2][16]) {
 #pragma unroll
   for (int h = 0; h < 2; h++)
 #pragma unroll
     for (int i = 0; i < 16; i++) {
       const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
-      if (t0 + t < valid && f < left) at[(int64_t)t * p.ld_out + f] = v[h][i];
+      old[h][i] = t < b.rows && f < b.cols ? __ldcg(b.at + (int64_t)t * p.ld_out + f) : 0.f;
+    }
+}
+__device__ __forceinline__ void store_block_f32(const RaggedK& p, const F32Block& b, const float (&v)[2][16]) {
+#pragma unroll
+  for (int h = 0; h < 2; h++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
+      if (t < b.rows && f < b.cols) b.at[(int64_t)t * p.ld_out + f] = v[h][i];
     }
 }
 
 // Segment ends -> shared memory: seg[g] .. seg[g + 1] is expert g's segment,
-// pref[g] the 256-row tiles (WGRAD: the rows) of the experts before g.  A
+// pref[g] the row tiles (WGRAD: the rows) of the experts before g.  A
 // segment that decreases, begins before an earlier one's end or passes R
 // counts nothing and is reported.
 template <int MODE>
@@ -398,7 +400,7 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
     int32_t v = 0;
     if (g < p.G) {
       if (s0 < top || s1 < s0 || (int64_t)s1 > p.R) bad = true;
-      else v = MODE == RAGGED_WGRAD ? s1 - s0 : (int32_t)(((int64_t)s1 - s0 + 255) / 256);
+      else v = MODE == RAGGED_WGRAD ? s1 - s0 : (int32_t)(((uint32_t)(s1 - s0) + (uint32_t)p.tw - 1) / (uint32_t)p.tw);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -417,6 +419,14 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
 struct RaggedMapsQ {
   CUtensorMap box[5];
 };
+
+// One poll that does not suspend the thread.
+__device__ __forceinline__ uint32_t mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok;
+}
 
 // Bounded wait of a whole warp for a phase of a barrier (CLUSTER: with
 // arrivals of the other CTA's).  The roles run as whole warps and elect one
@@ -566,6 +576,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  pdl_trigger();
+  pdl_wait();
   ragged_tables<MODE>(p, seg, pref, blockIdx.x == 0);
   __syncwarp();
   tc_fence_before();
@@ -593,30 +605,37 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
                                   ((Q_MN ? 1u : 0u) << 16) | (16u << 24);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
+      bool ok = true, ready = false;  // the next stage has already been seen to be full
       while (ok && walk.next(p, seg, pref, &T)) {
         if (T.nk == 0) continue;
         if (!ragged_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t idesc = idesc0 | ((uint32_t)(T.nt >> 3) << 17);
         const uint32_t d = tmem_base + (uint32_t)(acc * 256);
-        const int last_steps = (T.rem + 15) >> 4;
         for (int kb = 0; kb < T.nk; kb++) {
           const bool last = kb == T.nk - 1;
-          if (!ragged_wait<false>(&full[stage], phase, abort_flag)) { ok = false; break; }
+          if (!ready && !ragged_wait<false>(&full[stage], phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint64_t pd = pd0 + (uint64_t)((stage * P_BYTES) >> 4), qd = qd0 + (uint64_t)((stage * Q_BYTES) >> 4);
-          if (elect_one_lane()) {
-            const int steps = last ? last_steps : 4;
-            tc2_mma_bf16(d, pd, qd, idesc, kb != 0 ? 1u : 0u);
-            if (steps > 1) tc2_mma_bf16(d, pd + p_step, qd + q_step, idesc, 1u);
-            if (steps > 2) tc2_mma_bf16(d, pd + 2 * p_step, qd + 2 * q_step, idesc, 1u);
-            if (steps > 3) tc2_mma_bf16(d, pd + 3 * p_step, qd + 3 * q_step, idesc, 1u);
-            tc2_commit_both(&empty[stage]);
-            if (last) tc2_commit_both(&acc_full[acc]);
-          }
-          __syncwarp();
+          uint64_t* const done = &empty[stage];
           if (++stage == ST) { stage = 0; phase ^= 1u; }
+          const uint32_t next = mbar_try(&full[stage], phase);  // polled while this stage's MMAs are issued
+          if (elect_one_lane()) {
+            tc2_mma_bf16(d, pd, qd, idesc, kb != 0 ? 1u : 0u);
+            if (!last) {
+              tc2_mma_bf16(d, pd + p_step, qd + q_step, idesc, 1u);
+              tc2_mma_bf16(d, pd + 2 * p_step, qd + 2 * q_step, idesc, 1u);
+              tc2_mma_bf16(d, pd + 3 * p_step, qd + 3 * q_step, idesc, 1u);
+              tc2_commit_both(done);
+            } else {
+              if (T.rem > 16) tc2_mma_bf16(d, pd + p_step, qd + q_step, idesc, 1u);
+              if (T.rem > 32) tc2_mma_bf16(d, pd + 2 * p_step, qd + 2 * q_step, idesc, 1u);
+              if (T.rem > 48) tc2_mma_bf16(d, pd + 3 * p_step, qd + 3 * q_step, idesc, 1u);
+              tc2_commit_both(done);
+              tc2_commit_both(&acc_full[acc]);
+            }
+          }
+          ready = __all_sync(0xFFFFFFFFu, next != 0);
         }
         if (!ok) break;
         acc ^= 1;
@@ -686,6 +705,12 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
       }
       const int nb = T.nt >> 5;
       uint4 res[4];
+      const auto valid_of = [&](int b) { return T.valid - 32 * b < 32 ? T.valid - 32 * b : 32; };
+      const int64_t base = MODE == RAGGED_WGRAD ? (int64_t)T.g * p.K * p.ld_out : 0;
+      const bool add = F32 && (p.accumulate || T.part > 0);
+      float old[2][16];
+      if (F32 && add && h < nb)
+        load_block_f32(p, f32_block(p, static_cast<float*>(p.out) + base, lane, T.t0 + 32 * h, valid_of(h), col), old);
       if (EPI && p.epi.res && h < nb) load_residual(p, res, lane, T.t0 + 32 * h, T.valid - 32 * h, col);
       if (T.nk > 0) {
         if (!both_ok(ragged_wait<false>(&acc_full[acc], acc_phase, abort_flag), bar)) break;
@@ -710,14 +735,22 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
           for (int i = 0; i < 16; i++) v[0][i] = v[1][i] = 0.f;
         }
         const int64_t row0 = T.t0 + 32 * b;
-        const int valid = T.valid - 32 * b < 32 ? T.valid - 32 * b : 32;
-        const int64_t base = MODE == RAGGED_WGRAD ? (int64_t)T.g * p.K * p.ld_out : 0;
+        const int valid = valid_of(b);
         uint4 next[4];
         if (EPI && p.epi.res && b + 2 < nb) load_residual(p, next, lane, row0 + 64, T.valid - 32 * b - 64, col);
-        if constexpr (F32)
-          store_block_f32(p, v, lane, static_cast<float*>(p.out) + base, row0, valid, col,
-                          p.accumulate || T.part > 0);
-        else
+        if constexpr (F32) {
+          if (add) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+              v[0][i] += old[0][i];
+              v[1][i] += old[1][i];
+            }
+            if (b + 2 < nb)
+              load_block_f32(p, f32_block(p, static_cast<float*>(p.out) + base, lane, row0 + 64, valid_of(b + 2), col),
+                             old);
+          }
+          store_block_f32(p, f32_block(p, static_cast<float*>(p.out) + base, lane, row0, valid, col), v);
+        } else
           store_block_bf16<EPI>(p, v, stg, lane, odd, bar, bias, res, static_cast<uint16_t*>(p.out) + base, row0,
                                 valid, col);
         if (EPI && p.epi.res) {
@@ -742,6 +775,26 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   cluster_sync_all();
 }
 
+// The tile width for `rows` output rows in `segments` pieces under n_f column
+// tiles: the one with the least waves x (width + 64).  A tile costs its width
+// in MMA time and about 64 columns' worth besides; narrow tiles pay where wide
+// ones leave pairs idle (777 rows x 2048 columns: 32 tiles of 256 on 76 pairs,
+// 31 us; 72 of 96, TW_FIG us).  Past four waves the width is 256: fewer bytes
+// to load per product.
+static int tile_width(int64_t rows, int64_t segments, int64_t n_f, int pairs) {
+  int best = 256;
+  int64_t cost = -1;
+  for (int w = 256; w >= 32; w -= 32) {
+    const int64_t tiles = (rows + (int64_t)segments * w - 1) / w * n_f, waves = (tiles + pairs - 1) / pairs;
+    if (w == 256 && waves > 4) break;
+    if (cost < 0 || waves * (w + 64) < cost) {
+      cost = waves * (w + 64);
+      best = w;
+    }
+  }
+  return best;
+}
+
 template <int MODE, bool EPI, bool F32>
 static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const RaggedMapsQ& tq, int64_t tiles,
                                  int num_sms, cudaStream_t s) {
@@ -750,8 +803,7 @@ static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const 
   if (e != cudaSuccess) return e;
   int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
   if (pairs < 1) pairs = 1;
-  ragged_kernel<MODE, EPI, F32><<<(unsigned)(2 * pairs), rg::THREADS, rg::SMEM, s>>>(tp, tq, p);
-  return cudaGetLastError();
+  return launch_pdl(ragged_kernel<MODE, EPI, F32>, dim3((unsigned)(2 * pairs)), rg::THREADS, rg::SMEM, s, tp, tq, p);
 }
 
 // BF16 matrix [outer, inner] (row stride ld elements), optionally a stack of
@@ -784,7 +836,8 @@ cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t 
     if (!bf16_map(&tq.box[j], p.a, p.K, p.R, p.ld_a, 0, 128 >> j)) return cudaErrorInvalidValue;
   // each segment ends in one tile of its own at most
   const int64_t own = p.offsets ? (p.G < p.R ? p.G : p.R) : 1;
-  const int64_t tiles = (p.R / 256 + own) * k.n_f;
+  k.tw = tile_width(p.R, own, k.n_f, num_sms / 2);
+  const int64_t tiles = (p.R / k.tw + own) * k.n_f;
   const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res || p.epi.q;
   if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tiles, num_sms, s);
   return epi ? launch_ragged<RAGGED_NK, true, false>(k, tp, tq, tiles, num_sms, s)
@@ -798,7 +851,8 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   k.N = p.K;  // the output's columns
   k.K = p.N;  // its rows
   k.n_f = (int)((p.K + 255) / 256);
-  k.n_t = (int)((p.N + 255) / 256);
+  k.tw = tile_width(p.N, 1, k.n_f * (int64_t)p.G, num_sms / 2);
+  k.n_t = (int)((p.N + k.tw - 1) / k.tw);
   k.out = p.grad ? static_cast<void*>(p.grad) : p.grad_f32;
   k.ld_out = p.K;
   k.accumulate = p.accumulate;

@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
   constexpr int ROWS = 16 * MT, TOK = SK_TOK;
   __shared__ float red[SK_WARPS][TOK][ROWS + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
+  pdl_trigger();
+  pdl_wait();
   int g = 0;
   int64_t r0, r1;
   if (!find_expert(p, (int)blockIdx.y, lane, &g, &r0, &r1, blockIdx.x == 0 && blockIdx.y == 0 && warp == 0)) return;
@@ -173,8 +175,7 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
 template <int MT, bool EPI>
 static cudaError_t launch(const RaggedParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.N + 16 * MT - 1) / (16 * MT)), (unsigned)(p.offsets ? (p.G < p.R ? p.G : p.R) : 1));
-  skinny_kernel<MT, EPI><<<grid, 32 * SK_WARPS, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(skinny_kernel<MT, EPI>, grid, 32 * SK_WARPS, 0, s, p);
 }
 
 cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s) {
