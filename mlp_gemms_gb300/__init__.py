@@ -166,15 +166,21 @@ def _check(status):
         raise MXError(status, load().mx_last_error().decode())
 
 
+_current = None  # torch's raw-stream and current-device queries
+
+
 def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
-    from torch import _C
-    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    global _current
+    if _current is None:
+        from torch import _C
+        _current = (_C._cuda_getCurrentRawStream, _C._cuda_getDevice)
+    return _current[0](_current[1]())
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # --------------------------------------------------------------------------

@@ -54,8 +54,11 @@ constexpr int STG = 2304;     // per epilogue warp; two share 32 rows x (128 + 1
 constexpr int OFF_STG = OFF_Q + ST * Q_BYTES;
 constexpr int OFF_SEG = OFF_STG + 8 * STG;                  // segment ends, [0] = 0
 constexpr int OFF_PREF = OFF_SEG + 4 * (MAX_RAGGED_G + 1);  // row tiles before expert g
-constexpr int OFF_BAR = (OFF_PREF + 4 * (MAX_RAGGED_G + 1) + 7) / 8 * 8;
-constexpr int NUM_BARS = 3 * ST + 5;
+constexpr int OFF_ORD = OFF_PREF + 4 * (MAX_RAGGED_G + 1);  // experts by falling row count (uint16)
+constexpr int SLOTS = 4;      // tile indices on their way to the roles
+constexpr int OFF_NEXT = (OFF_ORD + 2 * MAX_RAGGED_G + 15) / 16 * 16;
+constexpr int OFF_BAR = OFF_NEXT + 16 * (SLOTS + 1);
+constexpr int NUM_BARS = 3 * ST + 5 + 2 * SLOTS + 1;
 constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;                  // + slack for 1024-byte alignment
 static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -98,29 +101,122 @@ struct RaggedTile {
 // operands.  A BF16 result (2e-3 from its own rounding) takes one pass.
 constexpr int F32_ROWS = 4096;
 
-// The pair's passes in order: each of its tiles (every step-th one), and of a
-// tile each part.  Tile indices only grow, so the expert is found by walking
-// on from the last one: every role walks for itself, the MMA thread between
-// two tiles included, and a division or a search there is time without MMAs.
+// One poll that does not suspend the thread.
+__device__ __forceinline__ uint32_t mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok;
+}
+
+// Bounded wait of a whole warp for a phase of a barrier (CLUSTER: with
+// arrivals of the other CTA's).  The roles run as whole warps and elect one
+// lane for what a single thread issues: in a branch on the lane's number every
+// operand of a copy or an MMA goes through a register move that the loop waits
+// for (measured: 97 cycles per MMA issued, 200 per wait, 720 a stage).
+template <bool CLUSTER>
+__device__ __forceinline__ bool ragged_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; n++) {
+    uint32_t ok;
+    if constexpr (CLUSTER)
+      asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                   "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, ok != 0)) return true;
+    if ((n & 63u) == 0u) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > WAIT_BUDGET_NS) *abort_flag = 1;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) return false;
+    }
+  }
+}
+
+// Hand an accumulator back: an arrival on a barrier of the leader CTA that
+// orders no memory.  What it announces, this warp's tensor-memory loads, is
+// complete (tcgen05.wait::ld); a release at cluster scope would also wait for
+// the warp's stores to global memory, about 1100 cycles a tile.
+__device__ __forceinline__ void arrive_on_leader_relaxed(uint32_t bar_cl) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cl) : "memory");
+}
+
+// Tiles are handed out by the hardware: the grid has a cluster for every tile,
+// and a running pair takes over the next cluster that has not started yet
+// (clusterlaunchcontrol.try_cancel), so pairs stay busy whatever the segments'
+// lengths.  Experts come by falling row count, the long ones first.  The
+// leader's copy warp asks for the next tile while the pair works on the last
+// one; the answer arrives in both CTAs, and every role reads it for itself.
+struct RaggedSched {
+  uint4* next;         // SLOTS answers, and one for the drain
+  uint64_t* full;      // each CTA's: the answer is there
+  uint64_t* empty;     // leader's: every role of both CTAs has read it
+};
+
+__device__ __forceinline__ RaggedSched ragged_sched(uint8_t* smem) {
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + rg::OFF_BAR) + 3 * rg::ST + 5;
+  return RaggedSched{reinterpret_cast<uint4*>(smem + rg::OFF_NEXT), bars, bars + rg::SLOTS};
+}
+
+// The first CTA of the cluster taken over, or false when none was left.
+__device__ __forceinline__ bool taken_cta(const uint4* answer, uint32_t* cta) {
+  uint32_t ok, x = 0;
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+               "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+               "mov.u32 %1, 0;\n\t"
+               "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+               : "=r"(ok), "=r"(x) : "r"(smem_u32(answer)) : "memory");
+  *cta = x;
+  return ok != 0;
+}
+
+// One role's way through the pair's passes: each of its tiles, and of a tile
+// each part.  Tile indices only grow, so the expert is found by walking on
+// from the last one.
 template <int MODE, bool F32>
 struct RaggedWalk {
-  uint32_t t, step;
-  uint32_t base;  // first tile of expert g
-  int g, part;
-  __device__ RaggedWalk(uint32_t first, uint32_t step_) : t(first), step(step_), base(0), g(0), part(0) {}
-  __device__ __forceinline__ bool next(const RaggedK& p, const int32_t* seg, const int32_t* pref, RaggedTile* T) {
+  const RaggedK& p;
+  const int32_t *seg, *pref;
+  const uint16_t* ord;
+  RaggedSched sched;
+  volatile int* abort_flag;
+  uint32_t t, base;  // current tile; first tile of the expert at place `at`
+  int at, part, slot;
+  uint32_t phase;
+  bool fetch;        // the next pass is another tile's
+  bool asked;        // the asking warp's: an answer is on its way
+  bool more;         // a cluster was taken over for the last tile asked for (else none is left)
+  __device__ RaggedWalk(const RaggedK& p_, uint8_t* smem)
+      : p(p_), seg(reinterpret_cast<int32_t*>(smem + rg::OFF_SEG)), pref(reinterpret_cast<int32_t*>(smem + rg::OFF_PREF)),
+        ord(reinterpret_cast<uint16_t*>(smem + rg::OFF_ORD)), sched(ragged_sched(smem)),
+        abort_flag(reinterpret_cast<volatile int*>(smem + rg::OFF_MISC + 4)), t(blockIdx.x >> 1), base(0), at(0),
+        part(0), slot(0), phase(0), fetch(false), asked(false), more(true) {}
+  __device__ bool next(RaggedTile* T) {
+    if (fetch) {
+      if (!ragged_wait<false>(&sched.full[slot], phase, abort_flag)) return false;
+      uint32_t cta;
+      more = taken_cta(&sched.next[slot], &cta);
+      asked = false;
+      if (!more) return false;
+      t = cta >> 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (elect_one_lane()) arrive_on_leader_relaxed(leader_addr(&sched.empty[slot]));
+      if (++slot == rg::SLOTS) { slot = 0; phase ^= 1u; }
+    }
     const uint32_t n_f = (uint32_t)p.n_f;
-    int32_t seg0;
-    uint32_t mt;
+    int g;
     while (true) {
-      if (g >= p.G) return false;
+      if (at >= p.G) return false;
+      g = ord[at];
       const uint32_t count = MODE == RAGGED_WGRAD ? n_f * (uint32_t)p.n_t : (uint32_t)(pref[g + 1] - pref[g]) * n_f;
       if (t - base < count) break;
       base += count;
-      g++;
+      at++;
     }
-    mt = (t - base) / n_f;
-    seg0 = seg[g];
+    const uint32_t mt = (t - base) / n_f;
+    const int32_t seg0 = seg[g];
     T->g = g;
     T->f0 = (int)(t - base - mt * n_f) * 256;
     T->parts = 1;
@@ -148,10 +244,8 @@ struct RaggedWalk {
     T->valid = left < p.tw ? (int)left : p.tw;
     T->nt = (T->valid + 31) & ~31;
     T->part = part;
-    if (++part >= T->parts) {
-      part = 0;
-      t += step;
-    }
+    fetch = ++part >= T->parts;
+    if (fetch) part = 0;
     return true;
   }
 };
@@ -377,10 +471,20 @@ __device__ __forceinline__ void store_block_f32(const RaggedK& p, const F32Block
 // segment that decreases, begins before an earlier one's end or passes R
 // counts nothing and is reported.
 template <int MODE>
-__device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, int32_t* pref, bool report) {
+__device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, int32_t* pref, uint16_t* ord, bool report) {
   for (int g = threadIdx.x; g < p.G; g += rg::THREADS) seg[g + 1] = p.offsets ? __ldg(p.offsets + g) : (int32_t)p.R;
   if (threadIdx.x == 0) seg[0] = 0;
   __syncthreads();
+  // the place of expert g: how many segments are longer (or as long and earlier)
+  for (int g = threadIdx.x; g < p.G; g += rg::THREADS) {
+    const int32_t mine = seg[g + 1] - seg[g];
+    int place = 0;
+    for (int j = 0; j < p.G; j++) {
+      const int32_t other = seg[j + 1] - seg[j];
+      place += other > mine || (other == mine && j < g);
+    }
+    ord[place] = (uint16_t)g;
+  }
   if (threadIdx.x >= 32) return;
   const int lane = threadIdx.x;
   int32_t run = 0, high = 0;  // count and largest end so far
@@ -420,54 +524,12 @@ struct RaggedMapsQ {
   CUtensorMap box[5];
 };
 
-// One poll that does not suspend the thread.
-__device__ __forceinline__ uint32_t mbar_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return ok;
-}
-
-// Bounded wait of a whole warp for a phase of a barrier (CLUSTER: with
-// arrivals of the other CTA's).  The roles run as whole warps and elect one
-// lane for what a single thread issues: in a branch on the lane's number every
-// operand of a copy or an MMA goes through a register move that the loop waits
-// for (measured: 97 cycles per MMA issued, 200 per wait, 720 a stage).
-template <bool CLUSTER>
-__device__ __forceinline__ bool ragged_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  uint64_t t0 = 0;
-  for (uint32_t n = 1;; n++) {
-    uint32_t ok;
-    if constexpr (CLUSTER)
-      asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                   "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    else
-      ok = mbar_try_wait(bar, parity);
-    if (__all_sync(0xFFFFFFFFu, ok != 0)) return true;
-    if ((n & 63u) == 0u) {
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > WAIT_BUDGET_NS) *abort_flag = 1;
-      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) return false;
-    }
-  }
-}
-
-// Hand an accumulator back: an arrival on a barrier of the leader CTA that
-// orders no memory.  What it announces, this warp's tensor-memory loads, is
-// complete (tcgen05.wait::ld); a release at cluster scope would also wait for
-// the warp's stores to global memory, about 1100 cycles a tile.
-__device__ __forceinline__ void arrive_on_leader_relaxed(uint32_t bar_cl) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cl) : "memory");
-}
-
 // One operand's copies into the stage ring of this CTA (one warp).  Warp 0
 // copies P, warp 3 Q: one thread issuing both was the limit where a stage
 // takes four copies (weight gradient, G = 128: 397 -> 367 us).
 template <int MODE, bool F32, bool IS_P>
 __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const RaggedMapsQ& tmQ, const RaggedK& p,
-                                              uint8_t* smem, const int32_t* seg, const int32_t* pref,
-                                              uint32_t rank) {
+                                              uint8_t* smem, uint32_t rank) {
   using namespace rg;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint64_t* empty = full + ST;
@@ -479,11 +541,28 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
   uint8_t* const ring = smem + (IS_P ? 0 : OFF_Q);
   const bool leader = rank == 0;
   RaggedTile T;
-  RaggedWalk<MODE, F32> walk(blockIdx.x >> 1, gridDim.x >> 1);
+  RaggedWalk<MODE, F32> walk(p, smem);
+  const RaggedSched sched = walk.sched;
+  uint32_t ask_phase = 1;  // parity of sched.empty the next request waits for
+  int ask = 0;
   int stage = 0;
   uint32_t phase = 0, tail_phase = 0, armed = 0, armed_phase = 0, armed_tail = 0;
   bool ok = true;
-  while (ok && walk.next(p, seg, pref, &T)) {
+  while (ok && walk.next(&T)) {
+    if (IS_P && leader && walk.fetch) {  // ask for the tile after this one
+      if (!ragged_wait<true>(&sched.empty[ask], ask_phase, abort_flag)) { ok = false; break; }
+      if (elect_one_lane()) {
+        mbar_arrive_expect_tx(&sched.full[ask], 16);
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 16;"
+                     :: "r"(peer_addr(&sched.full[ask])) : "memory");
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+                     ".multicast::cluster::all.b128 [%0], [%1];"
+                     :: "r"(smem_u32(&sched.next[ask])), "r"(smem_u32(&sched.full[ask])) : "memory");
+      }
+      __syncwarp();
+      walk.asked = true;
+      if (++ask == SLOTS) { ask = 0; ask_phase ^= 1u; }
+    }
     const int half = T.nt >> 1;                       // Q rows of this CTA
     const int boxes = IS_P ? 2 : (half + 63) >> 6;    // MN-major boxes of 64
     const uint32_t bytes = IS_P ? P_BYTES : (MODE == RAGGED_WGRAD ? boxes * 8192u : half * 128u);
@@ -531,8 +610,28 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
       if (++stage == ST) { stage = 0; phase ^= 1u; }
     }
   }
-  // Every copy has landed before the CTA leaves (the drain ignores the abort flag).
   volatile int no_abort = 0;
+  if (IS_P && leader && walk.asked) {  // given up while an answer is on its way: it lands first
+    ragged_wait<false>(&sched.full[walk.slot], walk.phase, &no_abort);
+  } else if (IS_P && leader && ok && walk.more) {
+    // The tile taken over last lies past the end: the grid counts a tile more
+    // than there may be for every segment.  Take over the rest as well, so
+    // that they do not start only to find nothing to do.
+    uint64_t* bar = sched.empty + SLOTS;
+    for (uint32_t parity = 0;; parity ^= 1u) {
+      if (elect_one_lane()) {
+        mbar_arrive_expect_tx(bar, 16);
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                     :: "r"(smem_u32(&sched.next[SLOTS])), "r"(smem_u32(bar)) : "memory");
+      }
+      __syncwarp();
+      uint32_t cta;
+      if (!ragged_wait<false>(bar, parity, &no_abort) || !taken_cta(&sched.next[SLOTS], &cta)) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+  }
+  // Every copy has landed before the CTA leaves (the drain ignores the abort flag).
   for (int s = 0; s < ST; s++) {
     if (leader && (armed >> s & 1u)) ragged_wait<false>(&full[s], armed_phase >> s & 1u, &no_abort);
     if (armed_tail >> s & 1u)
@@ -568,6 +667,10 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
     for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); mbar_init(&tail[s], 2); }
     for (int a = 0; a < 2; a++) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 16); }
     mbar_init(final_bar, 1);
+    // readers of a slot: both CTAs' copy and epilogue warps (and tail warps), the leader's MMA warp
+    const RaggedSched sched = ragged_sched(smem);
+    for (int i = 0; i < SLOTS; i++) { mbar_init(&sched.full[i], 1); mbar_init(&sched.empty[i], Q_MN ? 23 : 21); }
+    mbar_init(sched.empty + SLOTS, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -578,19 +681,19 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   }
   pdl_trigger();
   pdl_wait();
-  ragged_tables<MODE>(p, seg, pref, blockIdx.x == 0);
+  ragged_tables<MODE>(p, seg, pref, reinterpret_cast<uint16_t*>(smem + OFF_ORD), blockIdx.x == 0);
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();  // both CTAs' barriers are initialised before any remote arrive or copy; the tables are built
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   RaggedTile T;
-  RaggedWalk<MODE, F32> walk(blockIdx.x >> 1, gridDim.x >> 1);
+  RaggedWalk<MODE, F32> walk(p, smem);
 
   if (warp == 0) {
-    ragged_copies<MODE, F32, true>(tmP, tmQ, p, smem, seg, pref, rank);
+    ragged_copies<MODE, F32, true>(tmP, tmQ, p, smem, rank);
   } else if (warp == 3) {
-    ragged_copies<MODE, F32, false>(tmP, tmQ, p, smem, seg, pref, rank);
+    ragged_copies<MODE, F32, false>(tmP, tmQ, p, smem, rank);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader)
     if (leader) {
@@ -606,7 +709,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, ready = false;  // the next stage has already been seen to be full
-      while (ok && walk.next(p, seg, pref, &T)) {
+      while (ok && walk.next(&T)) {
         if (T.nk == 0) continue;
         if (!ragged_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -654,7 +757,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
       const uint64_t pol = l2_policy_evict_normal();
       uint32_t blocks = 0;  // contraction blocks of this pair so far, modulo the stages
       uint32_t tail_phase = 0;
-      while (walk.next(p, seg, pref, &T)) {
+      while (walk.next(&T)) {
         blocks = (blocks + T.nk) % ST;
         if (T.nk == 0 || (T.rem & 15) == 0) continue;
         const int stage = blocks == 0 ? ST - 1 : (int)blocks - 1;
@@ -691,7 +794,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
     uint8_t* stg = smem + OFF_STG + ((warp - 4) & ~1) * STG;
     int acc = 0;
     uint32_t acc_phase = 0;
-    while (walk.next(p, seg, pref, &T)) {
+    while (walk.next(&T)) {
       const int64_t col = T.f0 + 128 * rank + 32 * q;
       float bias[4] = {0.f, 0.f, 0.f, 0.f};
       if constexpr (EPI) {
@@ -797,13 +900,11 @@ static int tile_width(int64_t rows, int64_t segments, int64_t n_f, int pairs) {
 
 template <int MODE, bool EPI, bool F32>
 static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const RaggedMapsQ& tq, int64_t tiles,
-                                 int num_sms, cudaStream_t s) {
-  if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+                                 cudaStream_t s) {
+  if (tiles >= (1ll << 30)) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem_attr<ragged_kernel<MODE, EPI, F32>>(rg::SMEM);
   if (e != cudaSuccess) return e;
-  int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
-  if (pairs < 1) pairs = 1;
-  return launch_pdl(ragged_kernel<MODE, EPI, F32>, dim3((unsigned)(2 * pairs)), rg::THREADS, rg::SMEM, s, tp, tq, p);
+  return launch_pdl(ragged_kernel<MODE, EPI, F32>, dim3((unsigned)(2 * tiles)), rg::THREADS, rg::SMEM, s, tp, tq, p);
 }
 
 // BF16 matrix [outer, inner] (row stride ld elements), optionally a stack of
@@ -839,9 +940,9 @@ cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t 
   k.tw = tile_width(p.R, own, k.n_f, num_sms / 2);
   const int64_t tiles = (p.R / k.tw + own) * k.n_f;
   const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res || p.epi.q;
-  if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tiles, num_sms, s);
-  return epi ? launch_ragged<RAGGED_NK, true, false>(k, tp, tq, tiles, num_sms, s)
-             : launch_ragged<RAGGED_NK, false, false>(k, tp, tq, tiles, num_sms, s);
+  if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tiles, s);
+  return epi ? launch_ragged<RAGGED_NK, true, false>(k, tp, tq, tiles, s)
+             : launch_ragged<RAGGED_NK, false, false>(k, tp, tq, tiles, s);
 }
 
 cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStream_t s) {
@@ -863,8 +964,8 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   for (int j = 0; j < 4; j++)
     if (!bf16_map(&tq.box[1 + j], p.dy, p.N, p.R, p.ld_dy, 0, 8 >> j, false)) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)p.G * k.n_f * k.n_t;
-  return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tiles, num_sms, s)
-                : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, num_sms, s);
+  return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tiles, s)
+                : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, s);
 }
 
 cudaError_t read_ragged_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_ragged_status, sizeof(unsigned)); }
