@@ -251,8 +251,7 @@ mx_status_t mx::encode_bf16_map(CUtensorMap* m, const void* base, const TensorMa
   for (int i = 0; i < s.rank; i++) { dims[i] = s.dims[i]; box[i] = s.box[i]; }
   for (int i = 0; i + 1 < s.rank; i++) strides[i] = s.strides[i];
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)s.rank, const_cast<void*>(base), dims, strides,
-                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        s.swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MX_ERR_CUDA, "cuTensorMapEncodeTiled (BF16 operand) failed (%d)", (int)r);
   return MX_OK;

@@ -251,9 +251,8 @@ struct TensorMapShape {              // innermost dimension first; strides (byte
   int rank;
   uint64_t dims[3], strides[2];
   uint32_t box[3];
-  bool swizzle;                      // 128-byte
 };
-// A BF16 tensor as a TMA operand, out-of-range elements zero.
+// A BF16 tensor as a TMA operand: 128-byte swizzle, out-of-range elements zero.
 mx_status_t encode_bf16_map(CUtensorMap* m, const void* base, const TensorMapShape& s);
 bool validate_offsets_requested();  // MX_VALIDATE_OFFSETS=1
 

@@ -26,13 +26,13 @@
 // stmatrix.trans: rows of 32 features leave as 64-byte row pieces.
 //
 // The weight gradient contracts over a segment's rows.  Its last 64-row block
-// may hold rows of the next expert: those blocks are copied on the CTA's own
-// barrier, then a helper warp has the rows up to the next multiple of 16
-// zeroed in both operands (a zero against a neighbour's Inf or NaN would be
-// NaN) by copies that start beyond the tensor and read as zeros, counted on
-// the stage's barrier; the MMA thread runs the 16-row steps that hold rows of
-// the segment.  (Zeroing with stores needs a proxy fence and a cluster-scope
-// release from the peer, 1100 cycles measured.)
+// would hold rows of the next expert, whose Inf or NaN times a zero is NaN: it
+// is copied in pieces of 32, 16, 8, 4, 2 and 1 rows that end with the segment,
+// and filled up to a multiple of 16 by pieces that start beyond the tensor and
+// read as zeros.  The pieces start on any 128-byte row: the swizzle goes by
+// the shared-memory address.  (Zeroing the foreign rows after the copy, by
+// stores or by copies, delayed the MMAs by 1500 to 3300 cycles a tile; adding
+// those rows in the epilogue with mma.sync cost 100 us of 314.)
 //
 // Every wait is bounded; on expiry the CTA records a device status bit and
 // unwinds.
@@ -45,7 +45,7 @@ namespace mx {
 static __device__ unsigned g_ragged_status = 0;
 
 namespace rg {
-constexpr int THREADS = 384;  // warps: 0 and 3 copies, 1 MMAs, 2 segment tails, 4..11 epilogue
+constexpr int THREADS = 384;  // warps: 0 and 3 copies, 1 MMAs, 4..11 epilogue (2 makes their quarters even)
 constexpr int ST = 6;         // 32 KB stages of 64 contraction steps
 constexpr int BK = 64;
 constexpr int P_BYTES = 16384, Q_BYTES = 16384;
@@ -58,7 +58,7 @@ constexpr int OFF_ORD = OFF_PREF + 4 * (MAX_RAGGED_G + 1);  // experts by fallin
 constexpr int SLOTS = 4;      // tile indices on their way to the roles
 constexpr int OFF_NEXT = (OFF_ORD + 2 * MAX_RAGGED_G + 15) / 16 * 16;
 constexpr int OFF_BAR = OFF_NEXT + 16 * (SLOTS + 1);
-constexpr int NUM_BARS = 3 * ST + 5 + 2 * SLOTS + 1;
+constexpr int NUM_BARS = 2 * ST + 5 + 2 * SLOTS + 1;
 constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;                  // + slack for 1024-byte alignment
 static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -155,7 +155,7 @@ struct RaggedSched {
 };
 
 __device__ __forceinline__ RaggedSched ragged_sched(uint8_t* smem) {
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + rg::OFF_BAR) + 3 * rg::ST + 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + rg::OFF_BAR) + 2 * rg::ST + 5;
   return RaggedSched{reinterpret_cast<uint4*>(smem + rg::OFF_NEXT), bars, bars + rg::SLOTS};
 }
 
@@ -471,22 +471,51 @@ __device__ __forceinline__ void store_block_f32(const RaggedK& p, const F32Block
 // segment that decreases, begins before an earlier one's end or passes R
 // counts nothing and is reported.
 template <int MODE>
-__device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, int32_t* pref, uint16_t* ord, bool report) {
-  for (int g = threadIdx.x; g < p.G; g += rg::THREADS) seg[g + 1] = p.offsets ? __ldg(p.offsets + g) : (int32_t)p.R;
+__device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, int32_t* pref, uint16_t* ord, int32_t* count,
+                                              bool report) {
+  if (p.offsets == nullptr) {  // one segment
+    if (threadIdx.x == 0) {
+      seg[0] = pref[0] = 0;
+      seg[1] = (int32_t)p.R;
+      pref[1] = MODE == RAGGED_WGRAD ? (int32_t)p.R : (int32_t)((p.R + p.tw - 1) / p.tw);
+      ord[0] = 0;
+    }
+    return;
+  }
+  pdl_wait();
+  for (int g = threadIdx.x; g < p.G; g += rg::THREADS) seg[g + 1] = __ldg(p.offsets + g);
   if (threadIdx.x == 0) seg[0] = 0;
   __syncthreads();
-  // the place of expert g: how many segments are longer (or as long and earlier)
-  for (int g = threadIdx.x; g < p.G; g += rg::THREADS) {
-    const int32_t mine = seg[g + 1] - seg[g];
-    int place = 0;
-    for (int j = 0; j < p.G; j++) {
-      const int32_t other = seg[j + 1] - seg[j];
-      place += other > mine || (other == mine && j < g);
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x >> 5 == 2) {  // the order, beside warp 0's scan and warp 1's allocation
+    // A counting sort by the number of bits of the row count, long segments
+    // first: within a factor of two is enough for the balance at the end.
+    count[lane] = 0;
+    __syncwarp();
+    for (int g = lane; g < p.G; g += 32) atomicAdd(&count[__clz(max(seg[g + 1] - seg[g], 1))], 1);
+    __syncwarp();
+    int32_t upto = count[lane];  // class `lane`: 32 - lane bits
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += u;
     }
-    ord[place] = (uint16_t)g;
+    count[lane] = upto - count[lane];  // place of the class's next expert
+    __syncwarp();
+    for (int b = 0; b < p.G; b += 32) {
+      const int g = b + lane;
+      const int key = g < p.G ? __clz(max(seg[g + 1] - seg[g], 1)) : 32;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, key), below = same & ((1u << lane) - 1u);
+      const int first = g < p.G ? count[key] : 0;
+      __syncwarp();
+      if (g < p.G) {
+        ord[first + __popc(below)] = (uint16_t)g;
+        if (below == 0) count[key] = first + __popc(same);
+      }
+      __syncwarp();
+    }
   }
   if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
   int32_t run = 0, high = 0;  // count and largest end so far
   bool bad = false;
   if (lane == 0) pref[0] = 0;
@@ -517,23 +546,23 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
   if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && report) atomicOr(&g_ragged_status, DEV_BAD_OFFSETS);
 }
 
-// The Q operand's maps: boxes of 128, 64, 32 and 16 rows (a CTA's half of a
-// tile is a multiple of 16 tokens); WGRAD: box[0] 64 x 64, box[1..4] 8, 4, 2
-// and 1 rows of 64 columns, unswizzled, for the zeros.
-struct RaggedMapsQ {
-  CUtensorMap box[5];
+// The operands' maps.  P: NK and KN use box[0] only, 3-D (inner, outer,
+// expert).  Q: boxes of half a tile's rows, and of 64, 32 and 16 for the
+// narrower ones (a CTA's half is a multiple of 16 tokens).  WGRAD, both: boxes
+// of 64, 32, 16, 8, 4, 2 and 1 rows of 64 columns.
+struct RaggedMaps {
+  CUtensorMap box[7];
 };
 
 // One operand's copies into the stage ring of this CTA (one warp).  Warp 0
 // copies P, warp 3 Q: one thread issuing both was the limit where a stage
 // takes four copies (weight gradient, G = 128: 397 -> 367 us).
 template <int MODE, bool F32, bool IS_P>
-__device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const RaggedMapsQ& tmQ, const RaggedK& p,
+__device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const RaggedK& p,
                                               uint8_t* smem, uint32_t rank) {
   using namespace rg;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint64_t* empty = full + ST;
-  uint64_t* tail = empty + ST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   // The weight gradient's outputs (as large as its inputs) would push operands
   // out of L2 that other tiles still need.
@@ -546,7 +575,9 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
   uint32_t ask_phase = 1;  // parity of sched.empty the next request waits for
   int ask = 0;
   int stage = 0;
-  uint32_t phase = 0, tail_phase = 0, armed = 0, armed_phase = 0, armed_tail = 0;
+  uint32_t phase = 0, used = 0;  // stages copied into
+  bool ready = false;  // the next stage has already been seen to be free
+  const uint32_t full0 = leader_addr(&full[0]);
   bool ok = true;
   while (ok && walk.next(&T)) {
     if (IS_P && leader && walk.fetch) {  // ask for the tile after this one
@@ -567,47 +598,63 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
     const int boxes = IS_P ? 2 : (half + 63) >> 6;    // MN-major boxes of 64
     const uint32_t bytes = IS_P ? P_BYTES : (MODE == RAGGED_WGRAD ? boxes * 8192u : half * 128u);
     const int x = IS_P ? T.f0 + 128 * (int)rank : (int)T.t0 + half * (int)rank;
-    for (int kb = 0; kb < T.nk; kb++) {
-      if (!ragged_wait<false>(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-      uint8_t* dst = ring + stage * P_BYTES;
-      const int k = T.k0 + kb * BK;
-      armed |= 1u << stage;
-      armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-      const bool last = MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0;
-      if (last) {
-        armed_tail |= 1u << stage;
-        tail_phase ^= 1u << stage;
-      }
-      if (!elect_one_lane()) {
-      } else if (last) {
-        mbar_arrive_expect_tx(&tail[stage], bytes);
-        for (int j = 0; j < boxes; j++)
-          tma_load_2d(dst + j * 8192, IS_P ? &tmP : &tmQ.box[0], x + 64 * j, k, &tail[stage], pol);
-      } else {
-        const uint32_t fb = leader_addr(&full[stage]);
-        if (leader) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+    int k = T.k0;
+    for (int kb = 0; kb < T.nk; kb++, k += BK) {
+      if (!ready && !ragged_wait<false>(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+      uint8_t* const dst = ring + stage * P_BYTES;
+      const int here = stage;
+      used |= 1u << here;
+      if (++stage == ST) { stage = 0; phase ^= 1u; }
+      const uint32_t free_next = mbar_try(&empty[stage], phase ^ 1u);  // polled while this stage's copies are issued
+      if (elect_one_lane()) {
+        const uint32_t fb = full0 + 8u * here;
+        const bool pieces = MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0;
+        if (leader) mbar_arrive_expect_tx(&full[here], pieces ? (uint32_t)(boxes * 256 * ((T.rem + 15) & ~15)) : 2u * bytes);
         if constexpr (MODE == RAGGED_WGRAD) {
-          for (int j = 0; j < boxes; j++)
-            tma2_load_2d(dst + j * 8192, IS_P ? &tmP : &tmQ.box[0], x + 64 * j, k, fb, pol);
-        } else if constexpr (IS_P && MODE == RAGGED_NK) {
-          tma2_load_3d_hint(dst, &tmP, k, x, T.g, fb, pol);
-        } else if constexpr (IS_P) {
+          if (!pieces) {
+            tma2_load_2d(dst, &tm.box[0], x, k, fb, pol);
+            if (boxes > 1) tma2_load_2d(dst + 8192, &tm.box[0], x + 64, k, fb, pol);
+          } else {
+            const int zeros = 16 - (T.rem & 15);
+            for (int j = 0; j < boxes; j++) {
+              uint8_t* at = dst + j * 8192;
+              int row = k;
 #pragma unroll
-          for (int j = 0; j < 2; j++) tma2_load_3d_hint(dst + j * 8192, &tmP, x + 64 * j, k, T.g, fb, pol);
-        } else if (half == 128) {
-          tma2_load_2d(dst, &tmQ.box[0], k, x, fb, pol);
+              for (int i = 1; i < 7; i++) {
+                if (T.rem & (64 >> i)) {
+                  tma2_load_2d(at, &tm.box[i], x + 64 * j, row, fb, pol);
+                  row += 64 >> i;
+                  at += (64 >> i) * 128;
+                }
+              }
+#pragma unroll
+              for (int i = 3; i < 7; i++) {
+                if (zeros & (64 >> i)) {
+                  tma2_load_2d(at, &tm.box[i], 0, (int)p.R, fb, pol);
+                  at += (64 >> i) * 128;
+                }
+              }
+            }
+          }
+        } else if constexpr (IS_P && MODE == RAGGED_NK) {
+          tma2_load_3d_hint(dst, &tm.box[0], k, x, T.g, fb, pol);
+        } else if constexpr (IS_P) {
+          tma2_load_3d_hint(dst, &tm.box[0], x, k, T.g, fb, pol);
+          tma2_load_3d_hint(dst + 8192, &tm.box[0], x + 64, k, T.g, fb, pol);
+        } else if (2 * half == p.tw) {
+          tma2_load_2d(dst, &tm.box[0], k, x, fb, pol);
         } else {
           int row = 0;
 #pragma unroll
           for (int j = 1; j < 4; j++) {
             if (half & (128 >> j)) {
-              tma2_load_2d(dst + row * 128, &tmQ.box[j], k, x + row, fb, pol);
+              tma2_load_2d(dst + row * 128, &tm.box[j], k, x + row, fb, pol);
               row += 128 >> j;
             }
           }
         }
       }
-      if (++stage == ST) { stage = 0; phase ^= 1u; }
+      ready = __all_sync(0xFFFFFFFFu, free_next != 0);
     }
   }
   volatile int no_abort = 0;
@@ -631,26 +678,23 @@ __device__ __forceinline__ void ragged_copies(const CUtensorMap& tmP, const Ragg
       __syncwarp();
     }
   }
-  // Every copy has landed before the CTA leaves (the drain ignores the abort flag).
-  for (int s = 0; s < ST; s++) {
-    if (leader && (armed >> s & 1u)) ragged_wait<false>(&full[s], armed_phase >> s & 1u, &no_abort);
-    if (armed_tail >> s & 1u)
-      ragged_wait<false>(&tail[s], (tail_phase >> s & 1u) ^ 1u, &no_abort);
-  }
+  // Every copy has landed before the CTA leaves (the drain ignores the abort
+  // flag).  Stages before the current one were last filled in this round of
+  // the ring, the others in the one before.
+  for (int s = 0; s < ST; s++)
+    if (leader && (used >> s & 1u)) ragged_wait<false>(&full[s], s < stage ? phase : phase ^ 1u, &no_abort);
 }
 
-// tmP: the P operand, 3-D (inner, outer, expert; WGRAD: 2-D).
 template <int MODE, bool EPI, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(rg::THREADS, 1)
-ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ RaggedMapsQ tmQ, const RaggedK p) {
+ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ RaggedMaps tmQ, const RaggedK p) {
   using namespace rg;
   constexpr bool P_MN = MODE != RAGGED_NK, Q_MN = MODE == RAGGED_WGRAD;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // leader's: the stage is in both CTAs' shared memory
   uint64_t* empty = full + ST;      // both CTAs: the stage's MMAs are done
-  uint64_t* tail = empty + ST;      // each CTA's own: a segment's last block has landed, its end not yet zeroed
-  uint64_t* acc_full = tail + ST;   // both CTAs: the tile's MMAs are done
+  uint64_t* acc_full = empty + ST;  // both CTAs: the tile's MMAs are done
   uint64_t* acc_empty = acc_full + 2;  // leader's: both CTAs' epilogue warps have read the accumulator
   uint64_t* final_bar = acc_empty + 2;
   int32_t* seg = reinterpret_cast<int32_t*>(smem + OFF_SEG);
@@ -662,38 +706,39 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    prefetch_tensormap(&tmP);
-    for (int j = 0; j < (Q_MN ? 5 : 4); j++) prefetch_tensormap(&tmQ.box[j]);
-    for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); mbar_init(&tail[s], 2); }
+    for (int j = 0; j < (Q_MN ? 7 : 1); j++) prefetch_tensormap(&tmP.box[j]);
+    for (int j = 0; j < (Q_MN ? 7 : 4); j++) prefetch_tensormap(&tmQ.box[j]);
+    for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); }
     for (int a = 0; a < 2; a++) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 16); }
     mbar_init(final_bar, 1);
-    // readers of a slot: both CTAs' copy and epilogue warps (and tail warps), the leader's MMA warp
+    // readers of a slot: both CTAs' copy and epilogue warps, the leader's MMA warp
     const RaggedSched sched = ragged_sched(smem);
-    for (int i = 0; i < SLOTS; i++) { mbar_init(&sched.full[i], 1); mbar_init(&sched.empty[i], Q_MN ? 23 : 21); }
+    for (int i = 0; i < SLOTS; i++) { mbar_init(&sched.full[i], 1); mbar_init(&sched.empty[i], 21); }
     mbar_init(sched.empty + SLOTS, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
+  pdl_trigger();
+  ragged_tables<MODE>(p, seg, pref, reinterpret_cast<uint16_t*>(smem + OFF_ORD),
+                      reinterpret_cast<int32_t*>(smem + OFF_STG), blockIdx.x == 0);
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(tmem_slot))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  pdl_trigger();
-  pdl_wait();
-  ragged_tables<MODE>(p, seg, pref, reinterpret_cast<uint16_t*>(smem + OFF_ORD), blockIdx.x == 0);
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();  // both CTAs' barriers are initialised before any remote arrive or copy; the tables are built
   tc_fence_after();
+  pdl_wait();
   const uint32_t tmem_base = *tmem_slot;
   RaggedTile T;
   RaggedWalk<MODE, F32> walk(p, smem);
 
   if (warp == 0) {
-    ragged_copies<MODE, F32, true>(tmP, tmQ, p, smem, rank);
+    ragged_copies<MODE, F32, true>(tmP, p, smem, rank);
   } else if (warp == 3) {
-    ragged_copies<MODE, F32, false>(tmP, tmQ, p, smem, rank);
+    ragged_copies<MODE, F32, false>(tmQ, p, smem, rank);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader)
     if (leader) {
@@ -750,42 +795,6 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
       if (elect_one_lane()) tc2_commit_local(final_bar);
       __syncwarp();
       ragged_wait<false>(final_bar, 0, &no_abort);
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ segment tails (both CTAs)
-    if constexpr (MODE == RAGGED_WGRAD) {
-      const uint64_t pol = l2_policy_evict_normal();
-      uint32_t blocks = 0;  // contraction blocks of this pair so far, modulo the stages
-      uint32_t tail_phase = 0;
-      while (walk.next(&T)) {
-        blocks = (blocks + T.nk) % ST;
-        if (T.nk == 0 || (T.rem & 15) == 0) continue;
-        const int stage = blocks == 0 ? ST - 1 : (int)blocks - 1;
-        if (!ragged_wait<false>(&tail[stage], (tail_phase >> stage) & 1u, abort_flag)) break;
-        tail_phase ^= 1u << stage;
-        // The rows from the segment's end to the next multiple of 16, of each
-        // 128-byte wide box (two of P, up to two of Q), become zero by copies
-        // from beyond the tensor: 1 to 15 rows as 8 + 4 + 2 + 1.
-        const int boxes = 2 + ((T.nt + 127) >> 7), zrows = 16 - (T.rem & 15);
-        if (elect_one_lane()) {
-          const uint32_t fb = leader_addr(&full[stage]);
-          if (leader) {
-            mbar_arrive_expect_tx(&full[stage], 2u * (uint32_t)(boxes * zrows * 128));
-            mbar_arrive(&full[stage]);
-          }
-          for (int j = 0; j < boxes; j++) {
-            uint8_t* dst = smem + stage * P_BYTES + (j < 2 ? j * 8192 : OFF_Q + (j - 2) * 8192) + T.rem * 128;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              if (zrows & (8 >> i)) {
-                tma2_load_2d(dst, &tmQ.box[1 + i], 0, (int)p.R, fb, pol);
-                dst += (8 >> i) * 128;
-              }
-            }
-          }
-        }
-        __syncwarp();
-      }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
@@ -875,7 +884,6 @@ ragged_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ R
   tc_fence_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem_base) : "memory");
-  cluster_sync_all();
 }
 
 // The tile width for `rows` output rows in `segments` pieces under n_f column
@@ -899,7 +907,7 @@ static int tile_width(int64_t rows, int64_t segments, int64_t n_f, int pairs) {
 }
 
 template <int MODE, bool EPI, bool F32>
-static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const RaggedMapsQ& tq, int64_t tiles,
+static cudaError_t launch_ragged(const RaggedK& p, const RaggedMaps& tp, const RaggedMaps& tq, int64_t tiles,
                                  cudaStream_t s) {
   if (tiles >= (1ll << 30)) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem_attr<ragged_kernel<MODE, EPI, F32>>(rg::SMEM);
@@ -910,13 +918,12 @@ static cudaError_t launch_ragged(const RaggedK& p, const CUtensorMap& tp, const 
 // BF16 matrix [outer, inner] (row stride ld elements), optionally a stack of
 // `batch` of them, as 128-byte swizzled boxes of 64 x box_rows.
 static bool bf16_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int64_t batch,
-                     int box_rows, bool swizzle = true) {
+                     int box_rows) {
   TensorMapShape s{};
   s.rank = batch > 0 ? 3 : 2;
   s.dims[0] = (uint64_t)inner; s.dims[1] = (uint64_t)outer; s.dims[2] = (uint64_t)batch;
   s.strides[0] = (uint64_t)ld * 2; s.strides[1] = (uint64_t)outer * (uint64_t)ld * 2;
   s.box[0] = 64; s.box[1] = (uint32_t)box_rows; s.box[2] = 1;
-  s.swizzle = swizzle;
   return encode_bf16_map(m, base, s) == MX_OK;
 }
 
@@ -928,16 +935,16 @@ cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t 
   k.n_f = (int)((p.N + 255) / 256);
   k.out = p.out; k.ld_out = p.ld_out;
   k.epi = p.epi;
-  CUtensorMap tp;
-  RaggedMapsQ tq;
-  if (!(p.w_kn ? bf16_map(&tp, p.w, p.N, p.K, p.N, p.G, 64) : bf16_map(&tp, p.w, p.K, p.N, p.K, p.G, 128)) ||
-      !bf16_map(&tq.box[0], p.a, p.K, p.R, p.ld_a, 0, 128))
-    return cudaErrorInvalidValue;
-  for (int j = 1; j < 4; j++)
-    if (!bf16_map(&tq.box[j], p.a, p.K, p.R, p.ld_a, 0, 128 >> j)) return cudaErrorInvalidValue;
   // each segment ends in one tile of its own at most
   const int64_t own = p.offsets ? (p.G < p.R ? p.G : p.R) : 1;
   k.tw = tile_width(p.R, own, k.n_f, num_sms / 2);
+  RaggedMaps tp, tq;
+  if (!(p.w_kn ? bf16_map(&tp.box[0], p.w, p.N, p.K, p.N, p.G, 64)
+               : bf16_map(&tp.box[0], p.w, p.K, p.N, p.K, p.G, 128)) ||
+      !bf16_map(&tq.box[0], p.a, p.K, p.R, p.ld_a, 0, k.tw / 2))
+    return cudaErrorInvalidValue;
+  for (int j = 1; j < 4; j++)
+    if (!bf16_map(&tq.box[j], p.a, p.K, p.R, p.ld_a, 0, 128 >> j)) return cudaErrorInvalidValue;
   const int64_t tiles = (p.R / k.tw + own) * k.n_f;
   const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res || p.epi.q;
   if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tiles, s);
@@ -957,12 +964,11 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   k.out = p.grad ? static_cast<void*>(p.grad) : p.grad_f32;
   k.ld_out = p.K;
   k.accumulate = p.accumulate;
-  CUtensorMap tp;
-  RaggedMapsQ tq;
-  if (!bf16_map(&tp, p.x, p.K, p.R, p.ld_x, 0, 64) || !bf16_map(&tq.box[0], p.dy, p.N, p.R, p.ld_dy, 0, 64))
-    return cudaErrorInvalidValue;
-  for (int j = 0; j < 4; j++)
-    if (!bf16_map(&tq.box[1 + j], p.dy, p.N, p.R, p.ld_dy, 0, 8 >> j, false)) return cudaErrorInvalidValue;
+  RaggedMaps tp, tq;
+  for (int j = 0; j < 7; j++)
+    if (!bf16_map(&tp.box[j], p.x, p.K, p.R, p.ld_x, 0, 64 >> j) ||
+        !bf16_map(&tq.box[j], p.dy, p.N, p.R, p.ld_dy, 0, 64 >> j))
+      return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)p.G * k.n_f * k.n_t;
   return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tiles, s)
                 : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, s);
