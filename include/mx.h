@@ -777,7 +777,8 @@ MX_API mx_status_t mx_linear_fwd(const void *x_bf16, int64_t M, int64_t K, int64
  *   dz_bf16    out, device BF16 [R, C], row stride ld_dz
  *   h_bf16     out or NULL, row stride ld_h
  *   db         out or NULL, device fp32 [C]
- *   workspace  with db: >= mx_act_ckpt_workspace_bytes(R, C) bytes
+ *   workspace  with db: >= mx_act_ckpt_workspace_bytes(R, C) bytes (may be NULL
+ *              when that is 0)
  * R == 0: nothing is written but db, which is set to zero.
  */
 MX_API mx_status_t mx_act_ckpt_fwd(const void *z_bf16, int64_t R, int64_t C, int64_t ld_z, int32_t act, void *h_bf16,

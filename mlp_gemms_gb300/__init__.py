@@ -683,8 +683,9 @@ def mx_act_ckpt_bwd(ckpt, act, dh, dz=None, recompute=False, h=None, colsum=Fals
     if db is not None:
         assert db.shape == (C,) and db.dtype == torch.float32 and db.is_contiguous()
         if workspace is None:
-            workspace = torch.empty(max(mx_act_ckpt_workspace_bytes(R, C), 16), dtype=torch.uint8, device=dev)
-        nbytes = workspace.numel() * workspace.element_size()
+            n = mx_act_ckpt_workspace_bytes(R, C)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().mx_act_ckpt_bwd(_s(ckpt), act, dh.data_ptr(), dh.stride(0), dz.data_ptr(), dz.stride(0), _ptr(h),
                                   0 if h is None else h.stride(0), _ptr(db), _ptr(workspace), nbytes,
                                   _stream(stream)))

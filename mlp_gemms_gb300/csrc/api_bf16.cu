@@ -249,7 +249,7 @@ mx_status_t mx_act_ckpt_fwd(const void* z_bf16, int64_t R, int64_t C, int64_t ld
 
 size_t mx_act_ckpt_workspace_bytes(int64_t R, int64_t C) {
   if (R <= 0 || C <= 0) return 0;
-  return (size_t)(mx::ckpt_row_blocks(R, C) * C) * sizeof(float);
+  return (size_t)mx::ckpt_partials(R, C) * sizeof(float);
 }
 
 mx_status_t mx_act_ckpt_bwd(const mx_tensor_t* ckpt, int32_t act, const void* dh_bf16, int64_t ld_dh, void* dz_bf16,
@@ -284,7 +284,7 @@ mx_status_t mx_act_ckpt_bwd(const mx_tensor_t* ckpt, int32_t act, const void* dh
   p.dz = static_cast<uint16_t*>(dz_bf16); p.ld_dz = ld_dz;
   p.h = static_cast<uint16_t*>(h_bf16); p.ld_h = ld_h;
   p.db = db;
-  p.partials = static_cast<float*>(workspace);
+  p.partials = need ? static_cast<float*>(workspace) : nullptr;
   return cuda_result(mx::launch_ckpt_bwd(p, s), "checkpoint backward launch");
 }
 

@@ -2,6 +2,7 @@
 // its input, and the backward pass that reads the copy.
 #include "act.cuh"
 #include "mx_internal.h"
+#include "pair_common.cuh"
 
 namespace mx {
 
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(256) ckpt_fwd_kernel(const CkptParams p, uint3
 // 152) where the columns alone do not give it, each with a row for each of its
 // warps.  col_blocks counts SWIGLU's columns twice: its blocks do two halves'
 // work.
-int64_t ckpt_row_blocks(int64_t R, int64_t C) {
+static int64_t ckpt_row_blocks(int64_t R, int64_t C) {
   const int64_t col_blocks = (C + COLS - 1) / COLS;
   int64_t want = 152 * 4 / col_blocks;
   const int64_t most = (R + WARPS - 1) / WARPS;
@@ -146,7 +147,15 @@ int64_t ckpt_row_blocks(int64_t R, int64_t C) {
   return want < 1 ? 1 : want;
 }
 
-template <int ACT, bool H, bool DB>
+// Column sums of up to CLUSTER_ROWS rows: a cluster of blocks holds all rows of
+// its columns and adds its blocks' sums through shared memory, with no
+// partials in memory and no second launch (measured on [333, 8192]: CLUSTER_FIG).
+// More rows want more row blocks than a cluster has.
+constexpr int CLUSTER = 8, CLUSTER_ROWS = 512;
+int64_t ckpt_partials(int64_t R, int64_t C) { return R <= CLUSTER_ROWS ? 0 : ckpt_row_blocks(R, C) * C; }
+
+// DB: 0 no column sums, 1 partials per row block, 2 summed in the cluster.
+template <int ACT, bool H, int DB>
 __global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParams p, int64_t rows_per_block) {
   constexpr bool GLU = ACT == MX_ACT_SWIGLU;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParam
           h[j] = a * u[j];
           z[j] = d[j] * u[j] * s;
           u[j] = d[j] * a;
-          if (DB) sum_u[j] += u[j];
+          if (DB != 0) sum_u[j] += u[j];
         }
         *reinterpret_cast<uint4*>(p.dz + r * p.ld_dz + F + c) = pack8(u);
       } else {
@@ -203,13 +212,14 @@ __global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParam
       }
 #pragma unroll
       for (int j = 0; j < 8; j++)
-        if (DB) sum[j] += z[j];
+        if (DB != 0) sum[j] += z[j];
       *reinterpret_cast<uint4*>(p.dz + r * p.ld_dz + c) = pack8(z);
       if (H) *reinterpret_cast<uint4*>(p.h + r * p.ld_h + c) = pack8(h);
     }
   }
-  if constexpr (DB) {  // the warps' sums in warp order, then one row of partials per block
+  if constexpr (DB != 0) {  // the warps' sums in warp order, then the blocks'
     __shared__ float part[WARPS][COLS];
+    __shared__ float block_sum[GLU ? 2 : 1][COLS];
 #pragma unroll
     for (int half = 0; half < (GLU ? 2 : 1); half++) {
       if (half) __syncthreads();
@@ -219,8 +229,32 @@ __global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParam
       float t = 0.f;
 #pragma unroll
       for (int w = 0; w < WARPS; w++) t += part[w][threadIdx.x];
+      if constexpr (DB == 2) {
+        block_sum[half][threadIdx.x] = t;
+      } else {
+        const int64_t col = (int64_t)blockIdx.x * COLS + threadIdx.x;
+        if (col < F) p.partials[(int64_t)blockIdx.y * p.C + half * F + col] = t;
+      }
+    }
+    if constexpr (DB == 2) {
+      cluster_sync_all();
       const int64_t col = (int64_t)blockIdx.x * COLS + threadIdx.x;
-      if (col < F) p.partials[(int64_t)blockIdx.y * p.C + half * F + col] = t;
+      const unsigned rank = blockIdx.y, blocks = gridDim.y;  // the cluster is the grid's whole y extent
+      if (threadIdx.x % blocks == rank && col < F) {
+#pragma unroll
+        for (int half = 0; half < (GLU ? 2 : 1); half++) {
+          float t = 0.f;
+          for (unsigned b = 0; b < blocks; b++) {
+            uint32_t at;
+            float v;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&block_sum[half][threadIdx.x])), "r"(b));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+            t += v;
+          }
+          p.db[half * F + col] = t;
+        }
+      }
+      cluster_sync_all();  // no block leaves while another reads its sums
     }
   }
 }
@@ -247,16 +281,10 @@ __global__ void __launch_bounds__(256) ckpt_colsum_kernel(const float* __restric
   }
 }
 
-static dim3 ckpt_grid(const CkptParams& p, int64_t* rows) {
-  const int64_t F = p.act == MX_ACT_SWIGLU ? p.C / 2 : p.C, blocks = ckpt_row_blocks(p.R, p.C);
-  *rows = (p.R + blocks - 1) / blocks;
-  return dim3((unsigned)((F + COLS - 1) / COLS), (unsigned)blocks);
-}
-
 template <int ACT>
 static cudaError_t launch_fwd(const CkptParams& p, cudaStream_t s) {
   const int64_t per = (ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C) / 32, blocks = (p.R * per + 255) / 256;
-  return launch_pdl(ckpt_fwd_kernel<ACT>, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), 256, 0, s, p,
+  return launch_pdl(ckpt_fwd_kernel<ACT>, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), 256, 0, s, 1, p,
                     (uint32_t)per);
 }
 
@@ -270,26 +298,34 @@ cudaError_t launch_ckpt_fwd(const CkptParams& p, cudaStream_t s) {
 }
 
 template <int ACT>
-static cudaError_t launch_bwd(const CkptParams& p, dim3 grid, int64_t rows, cudaStream_t s) {
+static cudaError_t launch_bwd(const CkptParams& p, cudaStream_t s) {
   constexpr unsigned T = 32 * WARPS;
-  if (p.h && p.db) return launch_pdl(ckpt_bwd_kernel<ACT, true, true>, grid, T, 0, s, p, rows);
-  if (p.h) return launch_pdl(ckpt_bwd_kernel<ACT, true, false>, grid, T, 0, s, p, rows);
-  if (p.db) return launch_pdl(ckpt_bwd_kernel<ACT, false, true>, grid, T, 0, s, p, rows);
-  return launch_pdl(ckpt_bwd_kernel<ACT, false, false>, grid, T, 0, s, p, rows);
+  const int64_t F = ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C;
+  const bool cluster = p.db && p.partials == nullptr;
+  const int64_t most = (p.R + WARPS - 1) / WARPS;
+  const int64_t blocks = cluster ? (most < CLUSTER ? most : CLUSTER) : ckpt_row_blocks(p.R, p.C);
+  const int64_t rows = (p.R + blocks - 1) / blocks;
+  const dim3 grid((unsigned)((F + COLS - 1) / COLS), (unsigned)blocks);
+  const unsigned cy = (unsigned)blocks;
+  if (cluster)
+    return p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 2>, grid, T, 0, s, cy, p, rows)
+               : launch_pdl(ckpt_bwd_kernel<ACT, false, 2>, grid, T, 0, s, cy, p, rows);
+  if (p.db == nullptr)
+    return p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 0>, grid, T, 0, s, 1, p, rows)
+               : launch_pdl(ckpt_bwd_kernel<ACT, false, 0>, grid, T, 0, s, 1, p, rows);
+  const cudaError_t e = p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 1>, grid, T, 0, s, 1, p, rows)
+                            : launch_pdl(ckpt_bwd_kernel<ACT, false, 1>, grid, T, 0, s, 1, p, rows);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(ckpt_colsum_kernel, dim3((unsigned)(p.C / 32)), 256, 0, s, 1, p.partials, blocks, p.C, p.db);
 }
 
 cudaError_t launch_ckpt_bwd(const CkptParams& p, cudaStream_t s) {
-  int64_t rows;
-  const dim3 grid = ckpt_grid(p, &rows);
-  cudaError_t e;
   switch (p.act) {
-    case MX_ACT_SWIGLU: e = launch_bwd<MX_ACT_SWIGLU>(p, grid, rows, s); break;
-    case MX_ACT_GELU_TANH: e = launch_bwd<MX_ACT_GELU_TANH>(p, grid, rows, s); break;
-    case MX_ACT_SILU: e = launch_bwd<MX_ACT_SILU>(p, grid, rows, s); break;
-    default: e = launch_bwd<MX_ACT_RELU>(p, grid, rows, s); break;
+    case MX_ACT_SWIGLU: return launch_bwd<MX_ACT_SWIGLU>(p, s);
+    case MX_ACT_GELU_TANH: return launch_bwd<MX_ACT_GELU_TANH>(p, s);
+    case MX_ACT_SILU: return launch_bwd<MX_ACT_SILU>(p, s);
+    default: return launch_bwd<MX_ACT_RELU>(p, s);
   }
-  if (e != cudaSuccess || p.db == nullptr) return e;
-  return launch_pdl(ckpt_colsum_kernel, dim3((unsigned)(p.C / 32)), 256, 0, s, p.partials, (int64_t)grid.y, p.C, p.db);
 }
 
 }  // namespace mx

@@ -167,18 +167,24 @@ cudaError_t launch_wait_selftest(uint64_t budget_ns, cudaStream_t s);
 // Launch with programmatic stream serialization: the kernel may start while
 // the stream's previous kernel drains, and must run pdl_wait() before it
 // touches global memory (pdl_trigger() lets the next such kernel start).
+// cluster_y > 1: clusters of that many blocks along y.
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, A&&... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, unsigned cluster_y,
+                       A&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = cluster_y;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster_y > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
@@ -239,9 +245,9 @@ struct CkptParams {
   uint16_t* dz;
   int64_t ld_dz;
   float* db;                 // column sums of dz, or null
-  float* partials;           // [ckpt_row_blocks(R, C)][C]
+  float* partials;           // column sums' row blocks, ckpt_partials(R, C) values
 };
-int64_t ckpt_row_blocks(int64_t R, int64_t C);
+int64_t ckpt_partials(int64_t R, int64_t C);  // 0: none needed
 cudaError_t launch_ckpt_fwd(const CkptParams& p, cudaStream_t s);
 cudaError_t launch_ckpt_bwd(const CkptParams& p, cudaStream_t s);
 

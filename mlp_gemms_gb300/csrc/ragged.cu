@@ -912,7 +912,7 @@ static cudaError_t launch_ragged(const RaggedK& p, const RaggedMaps& tp, const R
   if (tiles >= (1ll << 30)) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem_attr<ragged_kernel<MODE, EPI, F32>>(rg::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ragged_kernel<MODE, EPI, F32>, dim3((unsigned)(2 * tiles)), rg::THREADS, rg::SMEM, s, tp, tq, p);
+  return launch_pdl(ragged_kernel<MODE, EPI, F32>, dim3((unsigned)(2 * tiles)), rg::THREADS, rg::SMEM, s, 1, tp, tq, p);
 }
 
 // BF16 matrix [outer, inner] (row stride ld elements), optionally a stack of

@@ -10,8 +10,11 @@
 // No shared-memory ring, no barriers before the first load: a tcgen05 tile
 // costs its prologue (tensor-memory allocation, cluster barrier, descriptor
 // fetch) before any weight arrives, and with one row of 48 tiles it reaches
-// 96 of the 152 SMs.  Measured on 8 rows of 8 of 128 experts, 2048 -> 1536:
-// SKINNY_FIG.
+// 96 of the 152 SMs.  Measured: 8 rows of 8 of 128 experts, 2048 -> 1536, 12.5
+// us (4.0 TB/s) against 25 on the tensor-core tiles; one row, 4096 -> 16384,
+// 23.6 us (5.7 TB/s) against 30.  The rows staged in shared memory by bulk
+// copies instead: 11.9 and 23.7 us, but 28 for 8 rows, 4096 -> 16384 (24.5
+// here), where the tokens' loads wait behind the barrier.
 #include "act.cuh"
 #include "mx_internal.h"
 
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
 template <int MT, bool EPI>
 static cudaError_t launch(const RaggedParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.N + 16 * MT - 1) / (16 * MT)), (unsigned)(p.offsets ? (p.G < p.R ? p.G : p.R) : 1));
-  return launch_pdl(skinny_kernel<MT, EPI>, grid, 32 * SK_WARPS, 0, s, p);
+  return launch_pdl(skinny_kernel<MT, EPI>, grid, 32 * SK_WARPS, 0, s, 1, p);
 }
 
 cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s) {

@@ -64,7 +64,7 @@ def _values(mx, ck):
                                               O.E4M3)).cuda()
 
 
-SHAPES = [(1, 64), (3, 128), (31, 192), (129, 64), (256, 512), (300, 1536), (1000, 2240)]
+SHAPES = [(1, 64), (3, 128), (31, 192), (129, 64), (256, 512), (300, 1536), (512, 1088), (513, 1088), (1000, 2240)]
 
 
 @pytest.mark.parametrize("act", ACTS)

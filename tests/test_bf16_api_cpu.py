@@ -172,7 +172,7 @@ def test_save_refusals(mx, kw, status, word):
     (dict(act=2), "MX_ERR_NOT_SUPPORTED", "identity"),
     (dict(ckpt=_t(10, 32), act=0), "MX_ERR_SHAPE", "C ="),
     (dict(ckpt=_t(10, 64, data=ODD)), "MX_ERR_ALIGNMENT", "ckpt data"),
-    (dict(db=FAKE), "MX_ERR_WORKSPACE", "workspace"),
+    (dict(ckpt=_t(5000, 64), db=FAKE), "MX_ERR_WORKSPACE", "workspace"),
     (dict(db=FAKE, ws=ODD, nb=1 << 30), "MX_ERR_ALIGNMENT", "workspace"),
     (dict(db=ODD, ws=FAKE, nb=1 << 30), "MX_ERR_ALIGNMENT", "db"),
 ], ids=lambda v: str(v)[:40])
