@@ -10,7 +10,8 @@ namespace mx {
 // (16 bytes of BF16, 8 of payload) of a row, so every access of a warp covers
 // one contiguous piece of a row, and a block 256 columns (SWIGLU: of each
 // half) and a run of rows, each warp every eighth of them: the column sums
-// stay in registers.
+// stay in registers.  [65536, 1536] SWIGLU with h: 82.6 us = 6.1 TB/s, 91 % of
+// the copy rate (a thread per 32-column block, as in the forward pass: 137).
 constexpr int COLS = 256, WARPS = 8;
 
 __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
@@ -28,13 +29,13 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // Streaming loads: nothing here is read twice.
 __device__ __forceinline__ uint4 load_once(const void* p) {
   uint4 q;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
       : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(p));
   return q;
 }
 __device__ __forceinline__ uint2 load_once8(const void* p) {
   uint2 q;
-  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(p));
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(p));
   return q;
 }
 
@@ -69,66 +70,99 @@ __device__ __forceinline__ void zero_scale_padding(const CkptParams& p) {
     *reinterpret_cast<uint32_t*>(p.q_scale + blocked_offset(p.R + i / chunks, i % chunks * 4, sc)) = 0u;
 }
 
-// 32 BF16 columns of a row in one thread (four 16-byte accesses; the warp's
-// four accesses cover 2 KB of consecutive lines between them).
-__device__ __forceinline__ void load32(const uint16_t* p, float (&v)[32]) {
+// 32 BF16 columns of a row in one thread.  WIDE: 32-byte accesses, so that a
+// lane reads and writes whole sectors (needs rows that start on 32 bytes);
+// otherwise 16-byte ones.
+template <bool WIDE>
+__device__ __forceinline__ void load32(const uint16_t* p, uint32_t (&w)[16]) {
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    for (int i = 0; i < 2; i++)
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          : "=r"(w[8 * i]), "=r"(w[8 * i + 1]), "=r"(w[8 * i + 2]), "=r"(w[8 * i + 3]), "=r"(w[8 * i + 4]),
+            "=r"(w[8 * i + 5]), "=r"(w[8 * i + 6]), "=r"(w[8 * i + 7]) : "l"(p + 16 * i));
+  } else {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      v[8 * i + 2 * j] = bf16_bits_to_float(w[j] & 0xFFFFu);
-      v[8 * i + 2 * j + 1] = bf16_bits_to_float(w[j] >> 16);
+    for (int i = 0; i < 4; i++) {
+      const uint4 q = *(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
     }
   }
 }
-__device__ __forceinline__ void store32(uint16_t* p, const float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-    reinterpret_cast<uint4*>(p)[i] =
-        make_uint4(float2_to_bf16x2(v[8 * i], v[8 * i + 1]), float2_to_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                   float2_to_bf16x2(v[8 * i + 4], v[8 * i + 5]), float2_to_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+template <bool WIDE>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {  // 8 words
+  if constexpr (WIDE) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
+__device__ __forceinline__ void unpack32(const uint32_t (&w)[16], float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 16; j++) {
+    v[2 * j] = bf16_bits_to_float(w[j] & 0xFFFFu);
+    v[2 * j + 1] = bf16_bits_to_float(w[j] >> 16);
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store32(uint16_t* p, const float (&v)[32]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; j++) w[j] = float2_to_bf16x2(v[2 * j], v[2 * j + 1]);
+  store_words<WIDE>(p, w);
+  store_words<WIDE>(p + 16, w + 8);
+}
+template <bool WIDE>
 __device__ __forceinline__ void save32(const CkptParams& p, int64_t r, int c, float (&v)[32]) {
   const uint32_t b = rceil_scale_byte_sel<E4M3>(amax_abs_bits<32>(v));
   uint32_t w[8];
   quantize_block_words<E4M3>(v, b, w);
-  uint4* d = reinterpret_cast<uint4*>(p.q + r * p.C + c);
-  d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  store_words<WIDE>(p.q + r * p.C + c, w);
   p.q_scale[blocked_offset(r, c >> 5, p.C >> 5)] = (uint8_t)b;
 }
 
 // Forward: a thread owns one 32-column block of a row (SWIGLU: the gate's and
-// the up half's), so the block's amax needs no exchange.  Measured against
-// the backward kernel's mapping (8 columns a lane, four lanes a block,
-// amax by shuffles): 69 against 96 us on [65536, 1536] SWIGLU, 5.8 TB/s; the
-// exchange and its address arithmetic cost more issue slots than the
-// coalescing saves.
-template <int ACT>
+// the up half's), so the block's amax needs no exchange.  [65536, 1536] SWIGLU:
+// 62.6 us = 6.5 TB/s, 97 % of the copy rate (with 16-byte accesses, which
+// touch each sector twice, 68.5; with 8 columns a lane and the amax by
+// shuffles, 72.8: issue slots).  [16384, 8192]: ReLU 103 us = 98 %, GELU 110 us
+// = 91 % (its activation's issue slots).
+template <int ACT, bool WIDE>
 __global__ void __launch_bounds__(256) ckpt_fwd_kernel(const CkptParams p, uint32_t per) {
   constexpr bool GLU = ACT == MX_ACT_SWIGLU;
   const int64_t F = GLU ? p.C / 2 : p.C;
   pdl_trigger();
   pdl_wait();
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.R * per; i += (int64_t)gridDim.x * 256) {
+  const int64_t items = p.R * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i < (1ll << 32) ? (uint32_t)i / per : i / per;
     const int c = (int)(i - r * per) * 32;
+    uint32_t wz[16], wu[16];
+    load32<WIDE>(p.z + r * p.ld_z + c, wz);
+    if constexpr (GLU) load32<WIDE>(p.z + r * p.ld_z + F + c, wu);
     float z[32], h[32];
-    load32(p.z + r * p.ld_z + c, z);
+    unpack32(wz, z);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      h[j] = z[j];
+      h[j + 1] = z[j + 1];
+      act2<GLU ? MX_ACT_SILU : ACT>(&h[j], &h[j + 1]);
+    }
+    save32<WIDE>(p, r, c, z);
     if constexpr (GLU) {
       float u[32];
-      load32(p.z + r * p.ld_z + F + c, u);
+      unpack32(wu, u);
 #pragma unroll
-      for (int j = 0; j < 32; j++) h[j] = act_f32<MX_ACT_SILU>(z[j]) * u[j];
-      save32(p, r, (int)F + c, u);
+      for (int j = 0; j < 32; j += 2)
+        unpack2(mul2(pack2(h[j], h[j + 1]), pack2(u[j], u[j + 1])), &h[j], &h[j + 1]);
+      store32<WIDE>(p.h + r * p.ld_h + c, h);
+      save32<WIDE>(p, r, (int)F + c, u);
     } else {
-#pragma unroll
-      for (int j = 0; j < 32; j++) h[j] = act_f32<ACT>(z[j]);
+      store32<WIDE>(p.h + r * p.ld_h + c, h);
     }
-    store32(p.h + r * p.ld_h + c, h);
-    save32(p, r, c, z);
     if (c == 0)  // column padding behind the last block
       for (int64_t sc = p.C >> 5, k = sc; k & 3; k++) p.q_scale[blocked_offset(r, k, sc)] = 0;
   }
@@ -149,7 +183,8 @@ static int64_t ckpt_row_blocks(int64_t R, int64_t C) {
 
 // Column sums of up to CLUSTER_ROWS rows: a cluster of blocks holds all rows of
 // its columns and adds its blocks' sums through shared memory, with no
-// partials in memory and no second launch (measured on [333, 8192]: CLUSTER_FIG).
+// partials in memory and no second launch (measured on [333, 8192] GELU: 6.9 us
+// against 7.8, and no workspace to allocate).
 // More rows want more row blocks than a cluster has.
 constexpr int CLUSTER = 8, CLUSTER_ROWS = 512;
 int64_t ckpt_partials(int64_t R, int64_t C) { return R <= CLUSTER_ROWS ? 0 : ckpt_row_blocks(R, C) * C; }
@@ -175,10 +210,10 @@ __global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParam
     for (int i = 0; i < BATCH; i++) {
       const int64_t r = rb + i * WARPS < r1 ? rb + i * WARPS : r1 - 1;
       qz[i] = load_once8(p.q + r * p.C + c);
-      bz[i] = __ldg(p.q_scale + blocked_offset(r, c >> 5, sc));
+      bz[i] = *(p.q_scale + blocked_offset(r, c >> 5, sc));
       if (GLU) {
         qu[i] = load_once8(p.q + r * p.C + F + c);
-        bu[i] = __ldg(p.q_scale + blocked_offset(r, (F + c) >> 5, sc));
+        bu[i] = *(p.q_scale + blocked_offset(r, (F + c) >> 5, sc));
       }
       qd[i] = load_once(p.dh + r * p.ld_dh + c);
     }
@@ -193,21 +228,26 @@ __global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParam
         float u[8];
         read8(qu[i], bu[i], u);
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          float a, s;
-          act_slope_f32<MX_ACT_SILU>(z[j], &a, &s);
-          h[j] = a * u[j];
-          z[j] = d[j] * u[j] * s;
-          u[j] = d[j] * a;
-          if (DB != 0) sum_u[j] += u[j];
+        for (int j = 0; j < 8; j += 2) {
+          uint64_t a, s;
+          act_slope2<MX_ACT_SILU>(pack2(z[j], z[j + 1]), &a, &s);
+          const uint64_t uu = pack2(u[j], u[j + 1]), dd = pack2(d[j], d[j + 1]);
+          unpack2(mul2(a, uu), &h[j], &h[j + 1]);
+          unpack2(mul2(mul2(dd, uu), s), &z[j], &z[j + 1]);
+          unpack2(mul2(dd, a), &u[j], &u[j + 1]);
+          if (DB != 0) {
+            sum_u[j] += u[j];
+            sum_u[j + 1] += u[j + 1];
+          }
         }
         *reinterpret_cast<uint4*>(p.dz + r * p.ld_dz + F + c) = pack8(u);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          float s;
-          act_slope_f32<ACT>(z[j], &h[j], &s);
-          z[j] = d[j] * s;
+        for (int j = 0; j < 8; j += 2) {
+          uint64_t a, s;
+          act_slope2<ACT>(pack2(z[j], z[j + 1]), &a, &s);
+          unpack2(a, &h[j], &h[j + 1]);
+          unpack2(mul2(pack2(d[j], d[j + 1]), s), &z[j], &z[j + 1]);
         }
       }
 #pragma unroll
@@ -284,8 +324,11 @@ __global__ void __launch_bounds__(256) ckpt_colsum_kernel(const float* __restric
 template <int ACT>
 static cudaError_t launch_fwd(const CkptParams& p, cudaStream_t s) {
   const int64_t per = (ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C) / 32, blocks = (p.R * per + 255) / 256;
-  return launch_pdl(ckpt_fwd_kernel<ACT>, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)), 256, 0, s, 1, p,
-                    (uint32_t)per);
+  const dim3 grid((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8));
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.z) | reinterpret_cast<uintptr_t>(p.h) |
+                       reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.ld_z * 2) | (uintptr_t)(p.ld_h * 2);
+  return (at & 31) == 0 ? launch_pdl(ckpt_fwd_kernel<ACT, true>, grid, 256, 0, s, 1, p, (uint32_t)per)
+                        : launch_pdl(ckpt_fwd_kernel<ACT, false>, grid, 256, 0, s, 1, p, (uint32_t)per);
 }
 
 cudaError_t launch_ckpt_fwd(const CkptParams& p, cudaStream_t s) {

@@ -206,9 +206,10 @@ struct RaggedWalk {
       if (++slot == rg::SLOTS) { slot = 0; phase ^= 1u; }
     }
     const uint32_t n_f = (uint32_t)p.n_f;
+    // past the end: told from the total, not by walking through every expert
+    if (t >= (MODE == RAGGED_WGRAD ? (uint32_t)p.G * n_f * (uint32_t)p.n_t : (uint32_t)pref[p.G] * n_f)) return false;
     int g;
     while (true) {
-      if (at >= p.G) return false;
       g = ord[at];
       const uint32_t count = MODE == RAGGED_WGRAD ? n_f * (uint32_t)p.n_t : (uint32_t)(pref[g + 1] - pref[g]) * n_f;
       if (t - base < count) break;
@@ -290,9 +291,9 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
 template <int ACT>
 __device__ __forceinline__ void act_values(float (&v)[2][16]) {
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
-    v[0][i] = act_f32<ACT>(v[0][i]);
-    v[1][i] = act_f32<ACT>(v[1][i]);
+  for (int i = 0; i < 16; i += 2) {
+    act2<ACT>(&v[0][i], &v[0][i + 1]);
+    act2<ACT>(&v[1][i], &v[1][i + 1]);
   }
 }
 
@@ -483,9 +484,14 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
     return;
   }
   pdl_wait();
-  for (int g = threadIdx.x; g < p.G; g += rg::THREADS) seg[g + 1] = __ldg(p.offsets + g);
+  bool wrong = false;
+  for (int g = threadIdx.x; g < p.G; g += rg::THREADS) {
+    const int32_t s0 = g ? *(p.offsets + g - 1) : 0, s1 = *(p.offsets + g);
+    seg[g + 1] = s1;
+    wrong |= s0 < 0 || s1 < s0 || (int64_t)s1 > p.R;
+  }
   if (threadIdx.x == 0) seg[0] = 0;
-  __syncthreads();
+  wrong = __syncthreads_or(wrong) != 0;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x >> 5 == 2) {  // the order, beside warp 0's scan and warp 1's allocation
     // A counting sort by the number of bits of the row count, long segments
@@ -522,14 +528,16 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
   for (int b = 0; b < p.G; b += 32) {
     const int g = b + lane;
     const int32_t s0 = g < p.G ? seg[g] : 0, s1 = g < p.G ? seg[g + 1] : 0;
-    int32_t top = s0;
+    int32_t top = s0;  // the largest end before segment g
+    if (wrong) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, top, o);
-      if (lane >= o && u > top) top = u;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xFFFFFFFFu, top, o);
+        if (lane >= o && u > top) top = u;
+      }
+      if (high > top) top = high;
+      high = __shfl_sync(0xFFFFFFFFu, top, 31);
     }
-    if (high > top) top = high;
-    high = __shfl_sync(0xFFFFFFFFu, top, 31);
     int32_t v = 0;
     if (g < p.G) {
       if (s0 < top || s1 < s0 || (int64_t)s1 > p.R) bad = true;
@@ -543,7 +551,7 @@ __device__ __forceinline__ void ragged_tables(const RaggedK& p, int32_t* seg, in
     if (g < p.G) pref[g + 1] = run + v;
     run += __shfl_sync(0xFFFFFFFFu, v, 31);
   }
-  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && report) atomicOr(&g_ragged_status, DEV_BAD_OFFSETS);
+  if (wrong && __any_sync(0xFFFFFFFFu, bad) && lane == 0 && report) atomicOr(&g_ragged_status, DEV_BAD_OFFSETS);
 }
 
 // The operands' maps.  P: NK and KN use box[0] only, 3-D (inner, outer,
@@ -811,7 +819,7 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int64_t f = col + (lane >> 2) + 8 * i;
-            if (f < p.N) bias[i] = bf16_bits_to_float(__ldg(p.epi.bias + f));
+            if (f < p.N) bias[i] = bf16_bits_to_float(*(p.epi.bias + f));
           }
         }
       }

@@ -28,7 +28,7 @@ constexpr int SK_TOK = 8;    // tokens of a pass; more go over the weights again
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   uint4 q;
-  asm("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
       : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(p));
   return q;
 }
@@ -52,8 +52,8 @@ __device__ __forceinline__ bool find_expert(const RaggedParams& p, int want, int
   bool bad = false, found = false;
   for (int b = 0; b < p.G; b += 32) {
     const int g = b + lane;
-    const int64_t s0 = g < p.G && g ? (int64_t)__ldg(p.offsets + g - 1) : 0;
-    const int64_t s1 = g < p.G ? (int64_t)__ldg(p.offsets + g) : 0;
+    const int64_t s0 = g < p.G && g ? (int64_t)*(p.offsets + g - 1) : 0;
+    const int64_t s1 = g < p.G ? (int64_t)*(p.offsets + g) : 0;
     int64_t top = s0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
         const bool kin = k + 8 * t4 < p.K;
 #pragma unroll
         for (int i = 0; i < 2 * MT; i++) qw[b][i] = kin && win[i] ? ld_stream(w[i] + k) : make_uint4(0, 0, 0, 0);
-        qx[b] = kin && xin ? __ldg(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
+        qx[b] = kin && xin ? *(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int b = 0; b < SK_BATCH; b++)
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
       const bool in = t < count && col < p.N;
       float v = z;
       if constexpr (EPI) {
-        if (p.epi.bias && in) z += bf16_bits_to_float(__ldg(p.epi.bias + col));
+        if (p.epi.bias && in) z += bf16_bits_to_float(*(p.epi.bias + col));
         if (MT == 2 && p.epi.q) {  // a warp's 32 lanes are one scale block
           float m = z;
 #pragma unroll
@@ -156,10 +156,11 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
             if (f == 0) p.epi.q_scale[blocked_offset(row, col >> 5, sc)] = (uint8_t)b;
           }
         }
-        v = p.epi.act == MX_ACT_GELU_TANH ? act_f32<MX_ACT_GELU_TANH>(z)
-            : p.epi.act == MX_ACT_SILU    ? act_f32<MX_ACT_SILU>(z)
-            : p.epi.act == MX_ACT_RELU    ? act_f32<MX_ACT_RELU>(z)
-                                          : z;
+        float idle = 0.f;
+        v = z;
+        if (p.epi.act == MX_ACT_GELU_TANH) act2<MX_ACT_GELU_TANH>(&v, &idle);
+        else if (p.epi.act == MX_ACT_SILU) act2<MX_ACT_SILU>(&v, &idle);
+        else if (p.epi.act == MX_ACT_RELU) act2<MX_ACT_RELU>(&v, &idle);
         if (p.epi.res && in) v += bf16_bits_to_float(p.epi.res[row * p.epi.ld_res + col]);
       }
       if (in) p.out[row * p.ld_out + col] = (uint16_t)float2_to_bf16x2(v, 0.f);
