@@ -394,3 +394,85 @@ def test_ragged_wgrad_stage_reuse_ends_promptly(cuda_lib):
         b.record()
         assert mx.mx_get_device_status() == "MX_OK"
         assert a.elapsed_time(b) < 500.0
+
+
+# More tiles than CTA pairs: every pair takes over tiles of other experts, of
+# other widths and of another number of contraction steps.
+
+@pytest.mark.parametrize("kn", [False, True], ids=["NK", "KN"])
+@pytest.mark.parametrize("N,K", [(1024, 136), (512, 200), (768, 72), (2048, 328)])
+def test_ragged_gemm_many_tiles(cuda_lib, N, K, kn):
+    mx = cuda_lib
+    counts = [(37 * i * i) % 331 for i in range(160)]
+    counts[5] = counts[77] = 0
+    counts[40] = 1500
+    R, G = sum(counts), len(counts)
+    gen = torch.Generator().manual_seed(N + K)
+    a = _bf16((R + 3, K), gen)
+    a[R:] = float("nan")
+    w = _bf16((G, K, N) if kn else (G, N, K), gen)
+    out = torch.full((R + 3, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        mx.mx_ragged_gemm(a, w, _offsets(counts), layout=mx.W_KN if kn else mx.W_NK, out=out)
+    assert mx.mx_get_device_status() == "MX_OK"
+    ref, mag = _ragged_ref(a[:R], w, counts, kn)
+    _check(out[:R], ref, mag, K, 2.0 ** -8)
+    assert bool((out[R:] == 9.0).all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "acc"])
+@pytest.mark.parametrize("N,K", [(264, 512), (40, 1024), (520, 1000), (136, 2048)])
+def test_ragged_wgrad_many_tiles(cuda_lib, N, K, kind):
+    mx = cuda_lib
+    counts = [(13 * i * i) % 97 for i in range(170)]
+    counts[3] = counts[4] = 0
+    counts[9] = 4500
+    R, G = sum(counts), len(counts)
+    gen = torch.Generator().manual_seed(N + K)
+    dy, x = _bf16((R + 7, N), gen), _bf16((R + 7, K), gen)
+    dy[R:], x[R:] = float("inf"), float("nan")
+    off = _offsets(counts)
+    if kind == "bf16":
+        got = mx.mx_ragged_gemm_wgrad(dy, x, G, off)
+        assert torch.equal(got, mx.mx_ragged_gemm_wgrad(dy, x, G, off))
+    else:
+        got = torch.randn((G, N, K), generator=gen).cuda()
+        before = got.clone()
+        mx.mx_ragged_gemm_wgrad_f32(dy, x, G, off, got, accumulate=kind == "acc")
+    assert mx.mx_get_device_status() == "MX_OK"
+    b = 0
+    for g, c in enumerate(counts):
+        d, e = dy[b:b + c].double(), x[b:b + c].double()
+        ref, mag = d.T @ e, d.abs().T @ e.abs()
+        if kind == "acc":
+            ref = ref + before[g].double()
+        _check(got[g], ref, mag, max(c, 1), 2.0 ** -8 if kind == "bf16" else 2.0 ** -23)
+        b += c
+
+
+@pytest.mark.parametrize("M,N,K", [(20011, 1024, 72), (9000, 2560, 136)])
+def test_linear_many_tiles(cuda_lib, M, N, K):
+    """Bias, activation, residual and checkpoint together."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(M)
+    x, w, b, r = _bf16((M, K), gen), _bf16((N, K), gen, K ** -0.5), _bf16((N,), gen), _bf16((M, N), gen)
+    ck = mx.MX(M, N)
+    out = mx.mx_linear_fwd(x, w, b, mx.ACT_GELU_TANH, r, ckpt=ck)
+    assert mx.mx_get_device_status() == "MX_OK"
+    z = x.double() @ w.double().T + b.double()
+    mag = x.double().abs() @ w.double().abs().T + b.double().abs()
+    h = _act(z, mx.ACT_GELU_TANH, mx)
+    _check(out, h + r.double(), 1.13 * mag + h.abs() * (2.0 ** 5 / K) + r.double().abs() / K, K, 2.0 ** -8)
+    # the checkpoint's values: half a unit of 4 significant bits, or of the block's subnormals
+    q, s = ck.data.view(torch.float8_e4m3fn), ck.scale
+    rows = torch.arange(M, device="cuda").unsqueeze(1)
+    cols = torch.arange(N // 32, device="cuda").unsqueeze(0)
+    at = (rows // 128 * (N // 128) + cols // 4) * 512 + rows % 32 * 16 + rows % 128 // 32 * 4 + cols % 4
+    scale = torch.exp2(s[at].double() - 127).repeat_interleave(32, 1)
+    assert bool(((q.double() * scale - z).abs() <= 2.0 ** -4 * z.abs() + 2.0 ** -10 * scale).all())
+    blocks = z.abs().view(M, N // 32, 32).amax(-1)
+    assert bool((blocks <= 448 * (1 + 1e-5) * scale[:, ::32]).all())
+    assert bool((blocks * (1 + 1e-5) > 224 * scale[:, ::32]).all())
+    pad = torch.arange(M, (M + 127) // 128 * 128, device="cuda").unsqueeze(1)
+    at = (pad // 128 * (N // 128) + cols // 4) * 512 + pad % 32 * 16 + pad % 128 // 32 * 4 + cols % 4
+    assert not bool(s[at].any())
