@@ -719,7 +719,9 @@ MX_API mx_status_t mx_ragged_gemm(const void *a_bf16, int64_t R, int64_t K, int6
  *   x_bf16     device BF16 [R, K], row stride ld_x
  *   grad       out, device [G, N, K], dense, 16-byte aligned
  *   workspace  >= mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G) bytes (may
- *              be NULL when that is 0); needs no preparation
+ *              be NULL when that is 0); needs no preparation.  Used where the
+ *              output is small and the segments long: the segments are cut
+ *              into parts that are summed in order by a second launch.
  * R == 0 stores zeros (accumulate = 1: leaves grad unchanged).
  */
 MX_API size_t mx_ragged_gemm_wgrad_workspace_bytes(int64_t N, int64_t K, int64_t R, int32_t G);

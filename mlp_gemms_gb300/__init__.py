@@ -666,26 +666,29 @@ def mx_act_ckpt_bwd(ckpt, act, dh, dz=None, recompute=False, h=None, colsum=Fals
     (dz [R, C], h or None, db or None): h = act of the checkpoint's values
     when `recompute` or `h`, db = fp32 column sums of dz when `colsum` or `db`."""
     import torch
-    assert dh.dtype == torch.bfloat16 and dh.stride(1) == 1
     R, C = ckpt.rows, ckpt.cols
     H = C // 2 if act == ACT_SWIGLU else C
-    assert dh.shape == (R, H)
-    dev = dh.device
+    dev, bf16 = dh.device, torch.bfloat16
+    assert dh.dtype == bf16 and dh.shape == (R, H) and dh.stride(1) == 1
     if dz is None:
-        dz = torch.empty((R, C), dtype=torch.bfloat16, device=dev)
-    assert dz.shape == (R, C) and dz.dtype == torch.bfloat16 and dz.stride(1) == 1
-    if h is None and recompute:
-        h = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    assert h is None or (h.shape == (R, H) and h.dtype == torch.bfloat16 and h.stride(1) == 1)
-    if db is None and colsum:
+        dz = torch.empty((R, C), dtype=bf16, device=dev)
+    else:
+        assert dz.shape == (R, C) and dz.dtype == bf16 and dz.stride(1) == 1
+    if h is not None:
+        assert h.shape == (R, H) and h.dtype == bf16 and h.stride(1) == 1
+    elif recompute:
+        h = torch.empty((R, H), dtype=bf16, device=dev)
+    if db is not None:
+        assert db.shape == (C,) and db.dtype == torch.float32 and db.is_contiguous()
+    elif colsum:
         db = torch.empty(C, dtype=torch.float32, device=dev)
     nbytes = 0
     if db is not None:
-        assert db.shape == (C,) and db.dtype == torch.float32 and db.is_contiguous()
         if workspace is None:
             n = mx_act_ckpt_workspace_bytes(R, C)
             workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        if workspace is not None:
+            nbytes = workspace.numel() * workspace.element_size()
     _check(load().mx_act_ckpt_bwd(_s(ckpt), act, dh.data_ptr(), dh.stride(0), dz.data_ptr(), dz.stride(0), _ptr(h),
                                   0 if h is None else h.stride(0), _ptr(db), _ptr(workspace), nbytes,
                                   _stream(stream)))

@@ -155,8 +155,8 @@ mx_status_t mx_linear_fwd(const void* x_bf16, int64_t M, int64_t K, int64_t ld_x
 }
 
 size_t mx_ragged_gemm_wgrad_workspace_bytes(int64_t N, int64_t K, int64_t R, int32_t G) {
-  (void)N; (void)K; (void)R; (void)G;
-  return 0;
+  if (N <= 0 || K <= 0 || R <= 0 || G <= 0) return 0;
+  return mx::ragged_wgrad_workspace(N, K, R, G);
 }
 
 }  // extern "C"
@@ -190,6 +190,7 @@ mx_status_t wgrad(const void* dy, int64_t N, int64_t ld_dy, const void* x, int64
   p.grad = f32 ? nullptr : static_cast<uint16_t*>(grad);
   p.grad_f32 = f32 ? static_cast<float*>(grad) : nullptr;
   p.accumulate = accumulate;
+  p.workspace = workspace;
   return cuda_result(mx::launch_ragged_wgrad(p, sms, s), "ragged weight-gradient launch");
 }
 

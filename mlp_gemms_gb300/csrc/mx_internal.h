@@ -221,7 +221,9 @@ struct RaggedWgradParams {
   uint16_t* grad;            // [G, N, K] BF16, or
   float* grad_f32;           // fp32
   int accumulate;
+  void* workspace;           // ragged_wgrad_workspace(N, K, R, G) bytes
 };
+size_t ragged_wgrad_workspace(int64_t N, int64_t K, int64_t R, int G);
 cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s);  // skinny.cu: few rows, MX_W_NK
 cudaError_t read_skinny_status(unsigned* out);

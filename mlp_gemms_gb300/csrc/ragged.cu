@@ -75,6 +75,7 @@ struct RaggedK {
   int n_f;                 // 256-column tiles of the output
   int n_t;                 // WGRAD: row tiles of an expert's output
   int tw;                  // rows of a tile, a multiple of 32 up to 256
+  int splits;              // WGRAD: parts of every segment, each with an output [G, ...] of its own
   void* out;
   int64_t ld_out;          // elements; WGRAD: N
   int accumulate;
@@ -92,6 +93,7 @@ struct RaggedTile {
   int k0;                  // WGRAD: first row of the contraction
   int rem;                 // contraction steps in the last block (1..64)
   int part, parts;         // WGRAD into fp32: this pass over the tile, and how many it takes
+  int split;               // WGRAD: which part of the segment
 };
 
 // Rows the fp32 weight gradient sums in tensor memory before it adds the sum
@@ -183,7 +185,7 @@ struct RaggedWalk {
   RaggedSched sched;
   volatile int* abort_flag;
   uint32_t t, base;  // current tile; first tile of the expert at place `at`
-  int at, part, slot;
+  int at, part, slot, split;
   uint32_t phase;
   bool fetch;        // the next pass is another tile's
   bool asked;        // the asking warp's: an answer is on its way
@@ -192,7 +194,7 @@ struct RaggedWalk {
       : p(p_), seg(reinterpret_cast<int32_t*>(smem + rg::OFF_SEG)), pref(reinterpret_cast<int32_t*>(smem + rg::OFF_PREF)),
         ord(reinterpret_cast<uint16_t*>(smem + rg::OFF_ORD)), sched(ragged_sched(smem)),
         abort_flag(reinterpret_cast<volatile int*>(smem + rg::OFF_MISC + 4)), t(blockIdx.x >> 1), base(0), at(0),
-        part(0), slot(0), phase(0), fetch(false), asked(false), more(true) {}
+        part(0), slot(0), split(0), phase(0), fetch(false), asked(false), more(true) {}
   __device__ bool next(RaggedTile* T) {
     if (fetch) {
       if (!ragged_wait<false>(&sched.full[slot], phase, abort_flag)) return false;
@@ -208,19 +210,32 @@ struct RaggedWalk {
     }
     const uint32_t n_f = (uint32_t)p.n_f;
     // past the end: told from the total, not by walking through every expert
-    if (t >= (MODE == RAGGED_WGRAD ? (uint32_t)p.G * n_f * (uint32_t)p.n_t : (uint32_t)pref[p.G] * n_f)) return false;
+    const uint32_t all = MODE == RAGGED_WGRAD ? (uint32_t)p.G * n_f * (uint32_t)p.n_t : (uint32_t)pref[p.G] * n_f;
+    if (t >= (MODE == RAGGED_WGRAD ? all * (uint32_t)p.splits : all)) return false;
+    uint32_t u = t;  // the tile within its part of the segments
+    if (MODE == RAGGED_WGRAD && p.splits > 1) {
+      T->split = (int)(t / all);
+      u = t - (uint32_t)T->split * all;
+      if (T->split != split) {
+        split = T->split;
+        at = 0;
+        base = 0;
+      }
+    } else {
+      T->split = 0;
+    }
     int g;
     while (true) {
       g = ord[at];
       const uint32_t count = MODE == RAGGED_WGRAD ? n_f * (uint32_t)p.n_t : (uint32_t)(pref[g + 1] - pref[g]) * n_f;
-      if (t - base < count) break;
+      if (u - base < count) break;
       base += count;
       at++;
     }
-    const uint32_t mt = (t - base) / n_f;
+    const uint32_t mt = (u - base) / n_f;
     const int32_t seg0 = seg[g];
     T->g = g;
-    T->f0 = (int)(t - base - mt * n_f) * 256;
+    T->f0 = (int)(u - base - mt * n_f) * 256;
     T->parts = 1;
     int64_t left;
     if constexpr (MODE == RAGGED_WGRAD) {
@@ -228,6 +243,11 @@ struct RaggedWalk {
       left = p.K - T->t0;
       int rows = pref[g + 1] - pref[g];  // rows of the segment, 0 if malformed
       T->k0 = seg0;
+      if (p.splits > 1) {
+        const int per = ((rows + p.splits - 1) / p.splits + rg::BK - 1) / rg::BK * rg::BK, from = per * T->split;
+        T->k0 += from < rows ? from : 0;
+        rows = from < rows ? (rows - from < per ? rows - from : per) : 0;
+      }
       if constexpr (F32) {
         T->parts = rows > F32_ROWS ? (rows + F32_ROWS - 1) / F32_ROWS : 1;
         T->k0 += part * F32_ROWS;
@@ -829,7 +849,7 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
       const int nb = T.nt >> 5;
       uint4 res[4];
       const auto valid_of = [&](int b) { return T.valid - 32 * b < 32 ? T.valid - 32 * b : 32; };
-      const int64_t base = MODE == RAGGED_WGRAD ? (int64_t)T.g * p.K * p.ld_out : 0;
+      const int64_t base = MODE == RAGGED_WGRAD ? ((int64_t)T.split * p.G + T.g) * p.K * p.ld_out : 0;
       const bool add = F32 && (p.accumulate || T.part > 0);
       float old[2][16];
       if (F32 && add && h < nb)
@@ -901,7 +921,7 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
 // tiles: the one with the least waves x (width + 64).  A tile costs its width
 // in MMA time and about 64 columns' worth besides; narrow tiles pay where wide
 // ones leave pairs idle (777 rows x 2048 columns: 32 tiles of 256 on 76 pairs,
-// 31 us; 72 of 96, TW_FIG us).  Past four waves the width is 256: fewer bytes
+// 31 us; 72 of 96, 22 us).  Past four waves the width is 256: fewer bytes
 // to load per product.
 static int tile_width(int64_t rows, int64_t segments, int64_t n_f, int pairs) {
   int best = 256;
@@ -964,6 +984,53 @@ cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t 
              : launch_ragged<RAGGED_NK, false, false>(k, tp, tq, tiles, s);
 }
 
+// Parts that every segment is cut into when an output has few tiles: a single
+// [512, 512] gradient is 4 tiles on 76 pairs, each summing all rows.  Every
+// part sums its rows into an fp32 gradient of its own in the workspace, and a
+// second launch adds them in order.  Worth it where it takes 2048 rows or more
+// off a pair's sums (whole against split, us: [512, 512] from 65536 rows 210,
+// 38; from 4096 rows 17.1, 12.6; two halves of 2048 rows 11.2, 12.1; 8
+// gradients of [512, 512] from 16384 rows 14.9, 17.6).
+constexpr int PAIRS = 76;  // GB300: 152 SMs
+static int wgrad_splits(int64_t N, int64_t K, int64_t R, int64_t G) {
+  const int64_t tiles = G * ((K + 255) / 256) * ((N + 255) / 256);
+  int64_t s = PAIRS / tiles;
+  if (s > R / (G * 1024)) s = R / (G * 1024);
+  return s < 2 || R / G * (s - 1) / s < 2048 ? 1 : (int)s;
+}
+
+size_t ragged_wgrad_workspace(int64_t N, int64_t K, int64_t R, int G) {
+  const int s = wgrad_splits(N, K, R, G);
+  return s > 1 ? (size_t)s * (size_t)G * (size_t)N * (size_t)K * sizeof(float) : 0;
+}
+
+// grad (+)= the parts' sums, in order; n is a multiple of 4.
+template <bool F32>
+__global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* parts, int splits, int64_t n, void* grad,
+                                                        int accumulate) {
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+    float4 t = *reinterpret_cast<const float4*>(parts + i);
+#pragma unroll 4
+    for (int s = 1; s < splits; s++) {
+      const float4 v = *reinterpret_cast<const float4*>(parts + s * n + i);
+      t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+    }
+    if constexpr (F32) {
+      float4* g = reinterpret_cast<float4*>(static_cast<float*>(grad) + i);
+      if (accumulate) {
+        const float4 v = *g;
+        t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+      }
+      *g = t;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(grad) + i) =
+          make_uint2(float2_to_bf16x2(t.x, t.y), float2_to_bf16x2(t.z, t.w));
+    }
+  }
+}
+
 cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStream_t s) {
   RaggedK k{};
   k.G = p.G; k.offsets = p.offsets;
@@ -971,19 +1038,29 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   k.N = p.K;  // the output's columns
   k.K = p.N;  // its rows
   k.n_f = (int)((p.K + 255) / 256);
-  k.tw = tile_width(p.N, 1, k.n_f * (int64_t)p.G, num_sms / 2);
+  k.splits = wgrad_splits(p.N, p.K, p.R, p.G);
+  k.tw = k.splits > 1 ? 256 : tile_width(p.N, 1, k.n_f * (int64_t)p.G, num_sms / 2);
   k.n_t = (int)((p.N + k.tw - 1) / k.tw);
-  k.out = p.grad ? static_cast<void*>(p.grad) : p.grad_f32;
+  k.out = k.splits > 1 ? p.workspace : p.grad ? static_cast<void*>(p.grad) : p.grad_f32;
   k.ld_out = p.K;
-  k.accumulate = p.accumulate;
+  k.accumulate = k.splits > 1 ? 0 : p.accumulate;
   RaggedMaps tp, tq;
   for (int j = 0; j < 7; j++)
     if (!bf16_map(&tp.box[j], p.x, p.K, p.R, p.ld_x, 0, 64 >> j) ||
         !bf16_map(&tq.box[j], p.dy, p.N, p.R, p.ld_dy, 0, 64 >> j))
       return cudaErrorInvalidValue;
-  const int64_t tiles = (int64_t)p.G * k.n_f * k.n_t;
-  return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tiles, s)
-                : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, s);
+  const int64_t tiles = (int64_t)p.G * k.n_f * k.n_t * k.splits;
+  if (k.splits == 1)
+    return p.grad ? launch_ragged<RAGGED_WGRAD, false, false>(k, tp, tq, tiles, s)
+                  : launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, s);
+  const cudaError_t e = launch_ragged<RAGGED_WGRAD, false, true>(k, tp, tq, tiles, s);
+  if (e != cudaSuccess) return e;
+  const int64_t n = (int64_t)p.G * p.N * p.K, blocks = (n / 4 + 255) / 256;
+  const dim3 grid((unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8));
+  const float* parts = static_cast<const float*>(p.workspace);
+  return p.grad ? launch_pdl(wgrad_sum_kernel<false>, grid, 256, 0, s, 1, parts, k.splits, n, (void*)p.grad, 0)
+                : launch_pdl(wgrad_sum_kernel<true>, grid, 256, 0, s, 1, parts, k.splits, n, (void*)p.grad_f32,
+                             p.accumulate);
 }
 
 cudaError_t read_ragged_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_ragged_status, sizeof(unsigned)); }

@@ -476,3 +476,43 @@ def test_linear_many_tiles(cuda_lib, M, N, K):
     pad = torch.arange(M, (M + 127) // 128 * 128, device="cuda").unsqueeze(1)
     at = (pad // 128 * (N // 128) + cols // 4) * 512 + pad % 32 * 16 + pad % 128 // 32 * 4 + cols % 4
     assert not bool(s[at].any())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "acc"])
+@pytest.mark.parametrize("counts,N,K", [([9001], 64, 72), ([5000, 0, 17000, 3], 136, 264), ([5000] * 8, 40, 8),
+                                        ([30011], 520, 200)])
+def test_ragged_wgrad_few_tiles(cuda_lib, counts, N, K, kind):
+    """Few output tiles and long segments: the parts of a segment are summed
+    apart and added in order."""
+    mx = cuda_lib
+    R, G = sum(counts), len(counts)
+    assert mx.mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G) > 0
+    gen = torch.Generator().manual_seed(R + N)
+    dy, x = _bf16((R + 70, N), gen), _bf16((R + 70, K), gen)
+    dy[R:], x[R:] = float("nan"), float("inf")
+    off = _offsets(counts)
+    if kind == "bf16":
+        got = mx.mx_ragged_gemm_wgrad(dy, x, G, off)
+        assert torch.equal(got, mx.mx_ragged_gemm_wgrad(dy, x, G, off))
+    else:
+        got = torch.randn((G, N, K), generator=gen).cuda()
+        before = got.clone()
+        mx.mx_ragged_gemm_wgrad_f32(dy, x, G, off, got, accumulate=kind == "acc")
+    assert mx.mx_get_device_status() == "MX_OK"
+    b = 0
+    for g, c in enumerate(counts):
+        d, e = dy[b:b + c].double(), x[b:b + c].double()
+        ref, mag = d.T @ e, d.abs().T @ e.abs()
+        if kind == "acc":
+            ref = ref + before[g].double()
+        _check(got[g], ref, mag, max(c, 1), 2.0 ** -8 if kind == "bf16" else 2.0 ** -22)
+        b += c
+
+
+def test_ragged_wgrad_workspace_refused(cuda_lib):
+    mx = cuda_lib
+    R, N, K = 20000, 64, 64
+    dy = torch.zeros((R, N), dtype=torch.bfloat16, device="cuda")
+    n = mx.mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, 1)
+    with pytest.raises(mx.MXError, match="WORKSPACE"):
+        mx.mx_ragged_gemm_wgrad(dy, dy, 1, None, workspace=torch.empty(n - 4, dtype=torch.uint8, device="cuda"))
