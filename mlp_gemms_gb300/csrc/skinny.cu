@@ -47,34 +47,46 @@ __device__ __forceinline__ bool find_expert(const RaggedParams& p, int want, int
     *g_out = 0; *r0 = 0; *r1 = p.R;
     return want == 0;
   }
-  int64_t high = 0;
+  int32_t high = 0;
   int seen = 0;
   bool bad = false, found = false;
-  for (int b = 0; b < p.G; b += 32) {
-    const int g = b + lane;
-    const int64_t s0 = g < p.G && g ? (int64_t)*(p.offsets + g - 1) : 0;
-    const int64_t s1 = g < p.G ? (int64_t)*(p.offsets + g) : 0;
-    int64_t top = s0;
+  for (int b0 = 0; b0 < p.G; b0 += 128) {
+    int32_t end[4], start[4];  // 128 experts' loads in flight at a time
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, top, o);
-      if (lane >= o && u > top) top = u;
+    for (int i = 0; i < 4; i++) {
+      const int g = b0 + 32 * i + lane;
+      end[i] = g < p.G ? *(p.offsets + g) : 0;
+      start[i] = g < p.G && g ? *(p.offsets + g - 1) : 0;
     }
-    if (high > top) top = high;
-    high = __shfl_sync(0xFFFFFFFFu, top, 31);
-    const bool ok = s0 >= top && s1 >= s0 && s1 <= p.R;
-    if (g < p.G && !ok) bad = true;
-    const unsigned has = __ballot_sync(0xFFFFFFFFu, g < p.G && ok && s1 > s0);
-    const int n = __popc(has);
-    if (!found && want < seen + n) {
-      const int src = __fns(has, 0, want - seen + 1);
-      *g_out = b + src;
-      *r0 = __shfl_sync(0xFFFFFFFFu, s0, src);
-      *r1 = __shfl_sync(0xFFFFFFFFu, s1, src);
-      found = true;
-      if (!report) return true;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int g = b0 + 32 * i + lane;
+      const int32_t s0 = start[i], s1 = end[i];
+      int32_t top = s0;
+      if (__any_sync(0xFFFFFFFFu, g < p.G && (s0 < high || s1 < s0))) {  // a decreasing end: the largest so far counts
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int32_t u = __shfl_up_sync(0xFFFFFFFFu, top, o);
+          if (lane >= o && u > top) top = u;
+        }
+        if (high > top) top = high;
+      }
+      const bool ok = s0 >= top && s1 >= s0 && (int64_t)s1 <= p.R;
+      high = max(high, __shfl_sync(0xFFFFFFFFu, top, 31));
+      if (g < p.G && !ok) bad = true;
+      const unsigned has = __ballot_sync(0xFFFFFFFFu, g < p.G && ok && s1 > s0);
+      const int n = __popc(has);
+      if (!found && want < seen + n) {
+        const bool it = (has >> lane & 1u) && __popc(has & ((1u << lane) - 1u)) == want - seen;
+        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, it)) - 1;
+        *g_out = b0 + 32 * i + src;
+        *r0 = __shfl_sync(0xFFFFFFFFu, s0, src);
+        *r1 = __shfl_sync(0xFFFFFFFFu, s1, src);
+        found = true;
+        if (!report) return true;
+      }
+      seen += n;
     }
-    seen += n;
   }
   if (report && __any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(&g_skinny_status, DEV_BAD_OFFSETS);
   return found;

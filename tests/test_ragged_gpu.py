@@ -145,6 +145,26 @@ def test_ragged_gemm_malformed_offsets(cuda_lib):
     assert bool((out[10:] == 3.0).all())
 
 
+@pytest.mark.parametrize("ends,good", [([3, 1, 3, 9], [(0, 0, 3)]), ([2, 2, 5, 4, 7, 8], [(0, 0, 2), (2, 2, 5), (5, 7, 8)]),
+                                       ([-4, 2, 6], [(2, 2, 6)]), ([0, 0, 8], [(2, 0, 8)])])
+def test_ragged_gemm_malformed_offsets_few_rows(cuda_lib, ends, good):
+    """The same for a few rows: (expert, begin, end) of the segments that count."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(2)
+    R, N, K, G = 8, 72, 64, len(ends)
+    a, w = _bf16((R, K), gen), _bf16((G, N, K), gen)
+    out = torch.full((R, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    mx.mx_ragged_gemm(a, w, torch.tensor(ends, dtype=torch.int32, device="cuda"), out=out)
+    bad = any(e < s or e > R or s < max([0] + ends[:g]) for g, (s, e) in enumerate(zip([0] + ends, ends)))
+    assert mx.mx_get_device_status() == ("MX_ERR_OFFSETS" if bad else "MX_OK")
+    rest = torch.ones(R, dtype=torch.bool, device="cuda")
+    for g, b, e in good:
+        ref, mag = _ragged_ref(a[b:e], w[g:g + 1], [e - b], False)
+        _check(out[b:e], ref, mag, K, 2.0 ** -8)
+        rest[b:e] = False
+    assert bool((out[rest] == 3.0).all())
+
+
 def test_ragged_gemm_validates_on_request(cuda_lib, monkeypatch):
     mx = cuda_lib
     a = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
