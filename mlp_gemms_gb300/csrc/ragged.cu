@@ -91,6 +91,7 @@ struct RaggedK {
   void* out;
   int64_t ld_out;          // elements; WGRAD: N
   int accumulate;
+  int fetch_old;           // bring what a tile is added to into L2 first
   int w_once;              // the weights are read by about one tile each
   RaggedEpi epi;
 };
@@ -453,9 +454,14 @@ __device__ __forceinline__ void store_block_bf16(const RaggedK& p, float (&v)[2]
   uint4 x[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) x[i] = *reinterpret_cast<const uint4*>(stg + (t0 + 4 * i) * 144 + (lane & 7) * 16);
+  if (valid >= 32 && col - 32 * odd + 64 <= p.N) {
 #pragma unroll
-  for (int i = 0; i < 4; i++)
-    if (t0 + 4 * i < valid && c < p.N) *reinterpret_cast<uint4*>(at + 4 * i * p.ld_out) = x[i];
+    for (int i = 0; i < 4; i++) *reinterpret_cast<uint4*>(at + 4 * i * p.ld_out) = x[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (t0 + 4 * i < valid && c < p.N) *reinterpret_cast<uint4*>(at + 4 * i * p.ld_out) = x[i];
+  }
   named_bar(bar, 64);  // the buffer is free
 }
 
@@ -468,36 +474,45 @@ __device__ __forceinline__ bool both_ok(bool ok, int bar) {
   return r != 0;
 }
 
-// The same block in fp32, stored or added: eight lanes hold eight consecutive
-// features, so each row piece is a full 32-byte sector without staging.  What
-// it is added to is loaded a block ahead.
+// The same block in fp32, stored or added.  A lane holds a feature's 32 tokens
+// (tcgen05.ld 32x32b), so each token's row piece is a whole 128-byte line
+// without staging.  Loads and whole blocks' stores have no conditions: under a
+// condition of its own each became a branch of its own and waited for the one
+// before (128 experts, 805 MB added to: 895 us, without 702).
 struct F32Block {
-  float* at;    // this lane's first value
-  int rows, cols;  // valid ones from there on
+  float* at;  // this lane's first value
+  int rows;   // valid ones from there on, at least one
+  bool in;    // the lane's feature is one
 };
 __device__ __forceinline__ F32Block f32_block(const RaggedK& p, float* out, int lane, int64_t row0, int valid,
                                               int64_t col) {
-  const int64_t c = col + (lane >> 2);
-  return F32Block{out + (row0 + 2 * (lane & 3)) * p.ld_out + c, valid - 2 * (lane & 3),
-                  p.N - c > 32 ? 32 : (int)(p.N - c)};
+  return F32Block{out + row0 * p.ld_out + col + lane, valid, col + lane < p.N};
 }
-__device__ __forceinline__ void load_block_f32(const RaggedK& p, const F32Block& b, float (&old)[2][16]) {
+__device__ __forceinline__ void load_block_f32(const RaggedK& p, const F32Block& b, float (&old)[32]) {
+  if (!b.in) return;
+  if (b.rows >= 32) {
 #pragma unroll
-  for (int h = 0; h < 2; h++)
+    for (int t = 0; t < 32; t++) old[t] = __ldcg(b.at + t * p.ld_out);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
-      old[h][i] = t < b.rows && f < b.cols ? __ldcg(b.at + (int64_t)t * p.ld_out + f) : 0.f;
-    }
+    for (int t = 0; t < 32; t++) old[t] = __ldcg(b.at + (t < b.rows ? t : 0) * p.ld_out);
+  }
 }
-__device__ __forceinline__ void store_block_f32(const RaggedK& p, const F32Block& b, const float (&v)[2][16]) {
+__device__ __forceinline__ void store_block_f32(const RaggedK& p, const F32Block& b, const float (&v)[32]) {
+  if (!b.in) return;
+  if (b.rows >= 32) {
 #pragma unroll
-  for (int h = 0; h < 2; h++)
+    for (int t = 0; t < 32; t++) b.at[t * p.ld_out] = v[t];
+  } else {
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const int t = 8 * (i >> 2) + (i & 1), f = 16 * h + 8 * ((i >> 1) & 1);
-      if (t < b.rows && f < b.cols) b.at[(int64_t)t * p.ld_out + f] = v[h][i];
-    }
+    for (int t = 0; t < 32; t++)
+      if (t < b.rows) b.at[t * p.ld_out] = v[t];
+  }
+}
+
+// Ask for bytes [a, a + n) in L2; a and n are multiples of 16.
+__device__ __forceinline__ void prefetch_l2(const void* a, uint32_t n) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(a), "r"(n) : "memory");
 }
 
 // Segment ends -> shared memory: seg[g] .. seg[g + 1] is expert g's segment,
@@ -863,7 +878,8 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
       const auto valid_of = [&](int b) { return T.valid - 32 * b < 32 ? T.valid - 32 * b : 32; };
       const int64_t base = MODE == RAGGED_WGRAD ? ((int64_t)T.split * p.G + T.g) * p.K * p.ld_out : 0;
       const bool add = F32 && (p.accumulate || T.part > 0);
-      float old[2][16];
+      if (add && T.nk == 0) continue;  // nothing to add
+      float old[32] = {};
       if (F32 && add && h < nb)
         load_block_f32(p, f32_block(p, static_cast<float*>(p.out) + base, lane, T.t0 + 32 * h, valid_of(h), col), old);
       if (EPI && p.epi.res && h < nb) load_residual(p, res, lane, T.t0 + 32 * h, T.valid - 32 * h, col);
@@ -871,15 +887,30 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
         if (!both_ok(ragged_wait<false>(&acc_full[acc], acc_phase, abort_flag), bar)) break;
         tc_fence_after();
       }
+      if (F32 && p.fetch_old && add && T.part == 0) {
+        const int row = 64 + (warp - 4) * 32 + lane;
+        const int64_t f = T.f0 + 128 * rank;
+        if (row < T.valid && f < p.N)
+          prefetch_l2(static_cast<const float*>(p.out) + base + (T.t0 + row) * p.ld_out + f,
+                      (uint32_t)(p.N - f < 128 ? p.N - f : 128) * 4u);
+      }
       const uint32_t tb = tmem_base + (uint32_t)(acc * 256) + ((uint32_t)(q * 32) << 16);
       const uint32_t hand_back = leader_addr(&acc_empty[acc]);
       if (T.nk > 0 && h >= nb && lane == 0) arrive_on_leader_relaxed(hand_back);
       for (int b = h; b < nb; b += 2) {
-        float v[2][16];
+        float v[2][16], w[32];  // of one block, w in fp32 outputs' order
         if (T.nk > 0) {
-          tmem_ld_16x32(tb + 32 * b, v[0]);
-          tmem_ld_16x32(tb + 32 * b + (16u << 16), v[1]);
-          tmem_wait_ld();
+          if constexpr (F32) {
+            uint32_t u[32];
+            tmem_ld32(tb + 32 * b, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i++) w[i] = __uint_as_float(u[i]);
+          } else {
+            tmem_ld_16x32(tb + 32 * b, v[0]);
+            tmem_ld_16x32(tb + 32 * b + (16u << 16), v[1]);
+            tmem_wait_ld();
+          }
           if (b + 2 >= nb) {
             tc_fence_before();
             __syncwarp();
@@ -887,7 +918,7 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
           }
         } else {  // an expert without rows: zeros
 #pragma unroll
-          for (int i = 0; i < 16; i++) v[0][i] = v[1][i] = 0.f;
+          for (int i = 0; i < 16; i++) v[0][i] = v[1][i] = w[i] = w[16 + i] = 0.f;
         }
         const int64_t row0 = T.t0 + 32 * b;
         const int valid = valid_of(b);
@@ -896,15 +927,12 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
         if constexpr (F32) {
           if (add) {
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-              v[0][i] += old[0][i];
-              v[1][i] += old[1][i];
-            }
+            for (int i = 0; i < 32; i++) w[i] += old[i];
             if (b + 2 < nb)
               load_block_f32(p, f32_block(p, static_cast<float*>(p.out) + base, lane, row0 + 64, valid_of(b + 2), col),
                              old);
           }
-          store_block_f32(p, f32_block(p, static_cast<float*>(p.out) + base, lane, row0, valid, col), v);
+          store_block_f32(p, f32_block(p, static_cast<float*>(p.out) + base, lane, row0, valid, col), w);
         } else
           store_block_bf16<EPI>(p, v, stg, lane, odd, bar, bias, res, static_cast<uint16_t*>(p.out) + base, row0,
                                 valid, col);
@@ -1056,6 +1084,12 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   k.out = k.splits > 1 ? p.workspace : p.grad ? static_cast<void*>(p.grad) : p.grad_f32;
   k.ld_out = p.K;
   k.accumulate = k.splits > 1 ? 0 : p.accumulate;
+  // What a tile is added to is asked for in one go, in pieces of 512 bytes,
+  // once its sums are ready (not before, when its operands are on their way).
+  // Pays where pairs go through several tiles (us without and with: 128
+  // experts of [1536, 2048], 702, 605; 64 of [1024, 1024] with few rows, 103,
+  // 84); in one or two narrower tiles it does not (8 of [1000, 520]: 16.2, 17.7).
+  k.fetch_old = k.accumulate && k.tw == 256;
   RaggedMaps tp, tq;
   for (int j = 0; j < 7; j++)
     if (!bf16_map(&tp.box[j], p.x, p.K, p.R, p.ld_x, 0, 64 >> j) ||

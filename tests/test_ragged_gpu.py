@@ -470,6 +470,23 @@ def test_ragged_wgrad_many_tiles(cuda_lib, N, K, kind):
         b += c
 
 
+@pytest.mark.parametrize("G", [3, 170])
+def test_ragged_wgrad_accumulate_leaves_empty_experts_alone(cuda_lib, G):
+    """Bit for bit: negative zeros, subnormals and NaN payloads stay."""
+    mx = cuda_lib
+    N, K = 264, 520
+    counts = [0 if g % 3 else 5 for g in range(G)]
+    gen = torch.Generator().manual_seed(G)
+    dy, x = _bf16((sum(counts), N), gen), _bf16((sum(counts), K), gen)
+    before = torch.randint(-2 ** 31, 2 ** 31 - 1, (G, N, K), generator=gen, dtype=torch.int32).cuda()
+    before[1, :, ::3] = -2 ** 31
+    got = before.clone().view(torch.float32)
+    mx.mx_ragged_gemm_wgrad_f32(dy, x, G, _offsets(counts), got, accumulate=True)
+    assert mx.mx_get_device_status() == "MX_OK"
+    for g, c in enumerate(counts):
+        assert torch.equal(got[g].view(torch.int32), before[g]) == (c == 0)
+
+
 @pytest.mark.parametrize("M,N,K", [(20011, 1024, 72), (9000, 2560, 136)])
 def test_linear_many_tiles(cuda_lib, M, N, K):
     """Bias, activation, residual and checkpoint together."""
