@@ -188,8 +188,9 @@ __device__ __forceinline__ bool taken_cta(const uint4* answer, uint32_t* cta) {
 }
 
 // One role's way through the pair's passes: each of its tiles, and of a tile
-// each part.  Tile indices only grow, so the expert is found by walking on
-// from the last one.
+// each part.  Tile indices only grow, so the expert is searched for from the
+// last one on, 32 at a time (one by one the 38 short experts between a pair's
+// tiles took 8000 cycles: 8113 rows of 128 experts, 104 -> 64, 14.0 us, now 8.3).
 template <int MODE, bool F32>
 struct RaggedWalk {
   const RaggedK& p;
@@ -198,7 +199,7 @@ struct RaggedWalk {
   RaggedSched sched;
   volatile int* abort_flag;
   uint32_t t, base;  // current tile; first tile of the expert at place `at`
-  int at, part, slot, split;
+  int at, part, slot;
   uint32_t phase;
   bool fetch;        // the next pass is another tile's
   bool asked;        // the asking warp's: an answer is on its way
@@ -207,7 +208,7 @@ struct RaggedWalk {
       : p(p_), seg(reinterpret_cast<int32_t*>(smem + rg::OFF_SEG)), pref(reinterpret_cast<int32_t*>(smem + rg::OFF_PREF)),
         ord(reinterpret_cast<uint16_t*>(smem + rg::OFF_ORD)), sched(ragged_sched(smem)),
         abort_flag(reinterpret_cast<volatile int*>(smem + rg::OFF_MISC + 4)), t(blockIdx.x >> 1), base(0), at(0),
-        part(0), slot(0), split(0), phase(0), fetch(false), asked(false), more(true) {}
+        part(0), slot(0), phase(0), fetch(false), asked(false), more(true) {}
   __device__ bool next(RaggedTile* T) {
     if (fetch) {
       if (!ragged_wait<false>(&sched.full[slot], phase, abort_flag)) return false;
@@ -229,22 +230,40 @@ struct RaggedWalk {
     if (MODE == RAGGED_WGRAD && p.splits > 1) {
       T->split = (int)(t / all);
       u = t - (uint32_t)T->split * all;
-      if (T->split != split) {
-        split = T->split;
-        at = 0;
-        base = 0;
-      }
     } else {
       T->split = 0;
     }
-    int g;
-    while (true) {
-      g = ord[at];
-      const uint32_t count = MODE == RAGGED_WGRAD ? n_f * (uint32_t)p.n_t : (uint32_t)(pref[g + 1] - pref[g]) * n_f;
-      if (u - base < count) break;
-      base += count;
-      at++;
+    if constexpr (MODE == RAGGED_WGRAD) {
+      at = (int)(u / (n_f * (uint32_t)p.n_t));
+      base = (uint32_t)at * n_f * (uint32_t)p.n_t;
+    } else {
+      const int lane = threadIdx.x & 31;
+      const auto tiles_of = [&](int place) {
+        const int e = ord[place];
+        return (uint32_t)(pref[e + 1] - pref[e]) * n_f;
+      };
+      uint32_t count = tiles_of(at);
+      if (u - base >= count) {
+        for (base += count, at++;; at += 32) {
+          count = at + lane < p.G ? tiles_of(at + lane) : 0;
+          uint32_t upto = count;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+          }
+          const unsigned there = __ballot_sync(0xFFFFFFFFu, u - base < upto);
+          if (there) {
+            const int l = __ffs(there) - 1;
+            base += __shfl_sync(0xFFFFFFFFu, upto - count, l);
+            at += l;
+            break;
+          }
+          base += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        }
+      }
     }
+    const int g = ord[at];
     const uint32_t mt = (u - base) / n_f;
     const int32_t seg0 = seg[g];
     T->g = g;
