@@ -327,8 +327,8 @@ static cudaError_t launch_fwd(const CkptParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8));
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.z) | reinterpret_cast<uintptr_t>(p.h) |
                        reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.ld_z * 2) | (uintptr_t)(p.ld_h * 2);
-  return (at & 31) == 0 ? launch_pdl(ckpt_fwd_kernel<ACT, true>, grid, 256, 0, s, 1, p, (uint32_t)per)
-                        : launch_pdl(ckpt_fwd_kernel<ACT, false>, grid, 256, 0, s, 1, p, (uint32_t)per);
+  return (at & 31) == 0 ? launch_pdl(ckpt_fwd_kernel<ACT, true>, grid, 256, 0, s, dim3(1), p, (uint32_t)per)
+                        : launch_pdl(ckpt_fwd_kernel<ACT, false>, grid, 256, 0, s, dim3(1), p, (uint32_t)per);
 }
 
 cudaError_t launch_ckpt_fwd(const CkptParams& p, cudaStream_t s) {
@@ -351,15 +351,15 @@ static cudaError_t launch_bwd(const CkptParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)((F + COLS - 1) / COLS), (unsigned)blocks);
   const unsigned cy = (unsigned)blocks;
   if (cluster)
-    return p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 2>, grid, T, 0, s, cy, p, rows)
-               : launch_pdl(ckpt_bwd_kernel<ACT, false, 2>, grid, T, 0, s, cy, p, rows);
+    return p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 2>, grid, T, 0, s, dim3(1, cy), p, rows)
+               : launch_pdl(ckpt_bwd_kernel<ACT, false, 2>, grid, T, 0, s, dim3(1, cy), p, rows);
   if (p.db == nullptr)
-    return p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 0>, grid, T, 0, s, 1, p, rows)
-               : launch_pdl(ckpt_bwd_kernel<ACT, false, 0>, grid, T, 0, s, 1, p, rows);
-  const cudaError_t e = p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 1>, grid, T, 0, s, 1, p, rows)
-                            : launch_pdl(ckpt_bwd_kernel<ACT, false, 1>, grid, T, 0, s, 1, p, rows);
+    return p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 0>, grid, T, 0, s, dim3(1), p, rows)
+               : launch_pdl(ckpt_bwd_kernel<ACT, false, 0>, grid, T, 0, s, dim3(1), p, rows);
+  const cudaError_t e = p.h ? launch_pdl(ckpt_bwd_kernel<ACT, true, 1>, grid, T, 0, s, dim3(1), p, rows)
+                            : launch_pdl(ckpt_bwd_kernel<ACT, false, 1>, grid, T, 0, s, dim3(1), p, rows);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ckpt_colsum_kernel, dim3((unsigned)(p.C / 32)), 256, 0, s, 1, p.partials, blocks, p.C, p.db);
+  return launch_pdl(ckpt_colsum_kernel, dim3((unsigned)(p.C / 32)), 256, 0, s, dim3(1), p.partials, blocks, p.C, p.db);
 }
 
 cudaError_t launch_ckpt_bwd(const CkptParams& p, cudaStream_t s) {

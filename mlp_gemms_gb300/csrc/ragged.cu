@@ -52,6 +52,8 @@
 #include "mx_internal.h"
 #include "pair_common.cuh"
 
+#include <atomic>
+
 namespace mx {
 
 static __device__ unsigned g_ragged_status = 0;
@@ -87,7 +89,7 @@ struct RaggedK {
   int n_f;                 // 256-column tiles of the output
   int n_t;                 // WGRAD: row tiles of an expert's output
   int tw;                  // rows of a tile, a multiple of 32 up to 256
-  int splits;              // WGRAD: parts of every segment, each with an output [G, ...] of its own
+  int splits;              // NK, KN: pairs that share a tile; WGRAD: parts of a segment, each with an output [G, ...]
   void* out;
   int64_t ld_out;          // elements; WGRAD: N
   int accumulate;
@@ -150,6 +152,18 @@ __device__ __forceinline__ bool ragged_wait(uint64_t* bar, uint32_t parity, vola
   }
 }
 
+// The shared::cluster address of a local shared address in another CTA of the
+// cluster, and the commit to both CTAs of the pair that starts at CTA `first`.
+__device__ __forceinline__ uint32_t cta_addr(const void* p, uint32_t cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(cta));
+  return r;
+}
+__device__ __forceinline__ void tc2_commit_pair(uint64_t* bar, uint32_t first) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(smem_u32(bar)), "h"((uint16_t)(3u << first)) : "memory");
+}
+
 // Hand an accumulator back: an arrival on a barrier of the leader CTA that
 // orders no memory.  What it announces, this warp's tensor-memory loads, is
 // complete (tcgen05.wait::ld); a release at cluster scope would also wait for
@@ -191,7 +205,7 @@ __device__ __forceinline__ bool taken_cta(const uint4* answer, uint32_t* cta) {
 // each part.  Tile indices only grow, so the expert is searched for from the
 // last one on, 32 at a time (one by one the 38 short experts between a pair's
 // tiles took 8000 cycles: 8113 rows of 128 experts, 104 -> 64, 14.0 us, now 8.3).
-template <int MODE, bool F32>
+template <int MODE, bool F32, bool SPLIT>
 struct RaggedWalk {
   const RaggedK& p;
   const int32_t *seg, *pref;
@@ -207,10 +221,12 @@ struct RaggedWalk {
   __device__ RaggedWalk(const RaggedK& p_, uint8_t* smem)
       : p(p_), seg(reinterpret_cast<int32_t*>(smem + rg::OFF_SEG)), pref(reinterpret_cast<int32_t*>(smem + rg::OFF_PREF)),
         ord(reinterpret_cast<uint16_t*>(smem + rg::OFF_ORD)), sched(ragged_sched(smem)),
-        abort_flag(reinterpret_cast<volatile int*>(smem + rg::OFF_MISC + 4)), t(blockIdx.x >> 1), base(0), at(0),
+        abort_flag(reinterpret_cast<volatile int*>(smem + rg::OFF_MISC + 4)),
+        t(SPLIT ? blockIdx.x / (2 * p_.splits) : blockIdx.x >> 1), base(0), at(0),
         part(0), slot(0), phase(0), fetch(false), asked(false), more(true) {}
   __device__ bool next(RaggedTile* T) {
-    if (fetch) {
+    if (SPLIT && fetch) return false;  // a cluster's only tile
+    if (!SPLIT && fetch) {
       if (!ragged_wait<false>(&sched.full[slot], phase, abort_flag)) return false;
       uint32_t cta;
       more = taken_cta(&sched.next[slot], &cta);
@@ -294,6 +310,12 @@ struct RaggedWalk {
       T->k0 = 0;
       T->nk = (int)((p.K + rg::BK - 1) / rg::BK);
       T->rem = (int)p.K - (T->nk - 1) * rg::BK;
+      if constexpr (SPLIT) {  // this pair's blocks of the contraction
+        const int pair = (int)(cluster_rank() >> 1), from = T->nk * pair / p.splits, to = T->nk * (pair + 1) / p.splits;
+        T->k0 = from * rg::BK;
+        if (to < T->nk) T->rem = rg::BK;
+        T->nk = to - from;
+      }
     }
     T->valid = left < p.tw ? (int)left : p.tw;
     T->nt = (T->valid + 31) & ~31;
@@ -632,9 +654,9 @@ struct RaggedMaps {
 // One operand's copies into the stage ring of this CTA (one warp).  Warp 0
 // copies P, warp 3 Q: one thread issuing both was the limit where a stage
 // takes four copies (weight gradient, G = 128: 397 -> 367 us).
-template <int MODE, bool F32, bool IS_P>
+template <int MODE, bool F32, bool IS_P, bool SPLIT>
 __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const RaggedK& p,
-                                              uint8_t* smem, uint32_t rank) {
+                                              uint8_t* smem, uint32_t rank, uint32_t first) {
   using namespace rg;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint64_t* empty = full + ST;
@@ -647,17 +669,17 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
   uint8_t* const ring = smem + (IS_P ? 0 : OFF_Q);
   const bool leader = rank == 0;
   RaggedTile T;
-  RaggedWalk<MODE, F32> walk(p, smem);
+  RaggedWalk<MODE, F32, SPLIT> walk(p, smem);
   const RaggedSched sched = walk.sched;
   uint32_t ask_phase = 1;  // parity of sched.empty the next request waits for
   int ask = 0;
   int stage = 0;
   uint32_t phase = 0, used = 0;  // stages copied into
   bool ready = false;  // the next stage has already been seen to be free
-  const uint32_t full0 = leader_addr(&full[0]);
+  const uint32_t full0 = SPLIT ? cta_addr(&full[0], first) : leader_addr(&full[0]);
   bool ok = true;
   while (ok && walk.next(&T)) {
-    if (IS_P && leader && walk.fetch) {  // ask for the tile after this one
+    if (!SPLIT && IS_P && leader && walk.fetch) {  // ask for the tile after this one
       if (!ragged_wait<true>(&sched.empty[ask], ask_phase, abort_flag)) { ok = false; break; }
       if (elect_one_lane()) {
         mbar_arrive_expect_tx(&sched.full[ask], 16);
@@ -735,7 +757,8 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
     }
   }
   volatile int no_abort = 0;
-  if (IS_P && leader && walk.asked) {  // given up while an answer is on its way: it lands first
+  if (SPLIT) {
+  } else if (IS_P && leader && walk.asked) {  // given up while an answer is on its way: it lands first
     ragged_wait<false>(&sched.full[walk.slot], walk.phase, &no_abort);
   } else if (IS_P && leader && ok && walk.more) {
     // The tile taken over last lies past the end: the grid counts a tile more
@@ -762,9 +785,84 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
     if (leader && (used >> s & 1u)) ragged_wait<false>(&full[s], s < stage ? phase : phase ^ 1u, &no_abort);
 }
 
-template <int MODE, bool EPI, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(rg::THREADS, 1)
-ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ RaggedMaps tmQ, const RaggedK p) {
+// The end of a tile whose contraction `splits` pairs of a cluster have shared:
+// 32-token block b is one pair's to finish; the others hand it their sums
+// through its shared memory (the stage ring: every pair's loads and MMAs are
+// done), and it adds them in the pairs' order.  All threads of the cluster
+// come here, also those that have given up or have no tile.
+template <bool EPI>
+__device__ __forceinline__ void ragged_join(const RaggedK& p, const RaggedTile& T, uint8_t* smem, uint32_t tmem_base,
+                                            int warp, int lane, uint32_t rank, uint32_t first, bool mine) {
+  using namespace rg;
+  const int S = p.splits, pair = (int)(first >> 1), nb = mine ? T.nt >> 5 : 0;
+  const int q = warp & 3, h = warp < 8 ? 0 : 1;  // nb is 0 for the other warps
+  // both parities of blocks go to each pair where there are enough
+  const bool twos = nb >= 2 * S;
+  const auto owner = [&](int b) { return (twos ? b >> 1 : b) % S; };
+  const auto slot = [&](int b, int from, int to) {  // 16 KB each: 4 warps x 32 lanes x 32 sums
+    const int place = twos ? (b >> 1) / S * 2 + (b & 1) : b / S;
+    return (place * (S - 1) + (from < to ? from : from - 1)) * 16384 + q * 4096 + lane * 16;
+  };
+  const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+  __syncwarp();
+  cluster_sync_all();  // every pair's sums are ready
+  tc_fence_after();
+  for (int b = h; b < nb; b += 2) {
+    const int to = owner(b);
+    if (to == pair) continue;
+    float v[2][16];
+    tmem_ld_16x32(tb + 32 * b, v[0]);
+    tmem_ld_16x32(tb + 32 * b + (16u << 16), v[1]);
+    tmem_wait_ld();
+    const uint32_t dst = cta_addr(smem + slot(b, pair, to), 2u * (uint32_t)to + rank);
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                   :: "r"(dst + 512u * j), "f"(v[j >> 2][4 * (j & 3)]), "f"(v[j >> 2][4 * (j & 3) + 1]),
+                      "f"(v[j >> 2][4 * (j & 3) + 2]), "f"(v[j >> 2][4 * (j & 3) + 3]) : "memory");
+  }
+  __syncwarp();
+  cluster_sync_all();  // every block's sums are with its owner
+  const int64_t col = T.f0 + 128 * rank + 32 * q;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (EPI) {
+    if (mine && p.epi.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int64_t f = col + (lane >> 2) + 8 * i;
+        if (f < p.N) bias[i] = bf16_bits_to_float(*(p.epi.bias + f));
+      }
+    }
+  }
+  for (int b = h; b < nb; b += 2) {
+    if (owner(b) != pair) continue;
+    const int64_t row0 = T.t0 + 32 * b;
+    const int valid = T.valid - 32 * b < 32 ? T.valid - 32 * b : 32;
+    uint4 res[4];
+    if (EPI && p.epi.res) load_residual(p, res, lane, row0, T.valid - 32 * b, col);
+    float v[2][16];
+    tmem_ld_16x32(tb + 32 * b, v[0]);
+    tmem_ld_16x32(tb + 32 * b + (16u << 16), v[1]);
+    tmem_wait_ld();
+    for (int from = 0; from < S; from++) {
+      if (from == pair) continue;
+      const float4* src = reinterpret_cast<const float4*>(smem + slot(b, from, pair));
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float4 x = src[32 * j];
+        v[j >> 2][4 * (j & 3)] += x.x;
+        v[j >> 2][4 * (j & 3) + 1] += x.y;
+        v[j >> 2][4 * (j & 3) + 2] += x.z;
+        v[j >> 2][4 * (j & 3) + 3] += x.w;
+      }
+    }
+    store_block_bf16<EPI>(p, v, smem + OFF_STG + ((warp - 4) & ~1) * STG, lane, warp & 1, 1 + ((warp - 4) >> 1), bias,
+                          res, static_cast<uint16_t*>(p.out), row0, valid, col);
+  }
+}
+
+template <int MODE, bool EPI, bool F32, bool SPLIT>
+__device__ __forceinline__ void ragged_body(const RaggedMaps& tmP, const RaggedMaps& tmQ, const RaggedK& p) {
   using namespace rg;
   constexpr bool P_MN = MODE != RAGGED_NK, Q_MN = MODE == RAGGED_WGRAD;
   extern __shared__ uint8_t smem_raw[];
@@ -778,7 +876,8 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
   int32_t* pref = reinterpret_cast<int32_t*>(smem + OFF_PREF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = SPLIT ? cluster_rank() & 1u : cluster_rank();  // in the pair
+  const uint32_t first = SPLIT ? cluster_rank() & ~1u : 0;             // the pair's leader
   const bool leader = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -810,12 +909,13 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
   pdl_wait();
   const uint32_t tmem_base = *tmem_slot;
   RaggedTile T;
-  RaggedWalk<MODE, F32> walk(p, smem);
+  RaggedWalk<MODE, F32, SPLIT> walk(p, smem);
+  bool mine = false;  // SPLIT, epilogue warps: the pair's sums are there
 
   if (warp == 0) {
-    ragged_copies<MODE, F32, true>(tmP, p, smem, rank);
+    ragged_copies<MODE, F32, true, SPLIT>(tmP, p, smem, rank, first);
   } else if (warp == 3) {
-    ragged_copies<MODE, F32, false>(tmQ, p, smem, rank);
+    ragged_copies<MODE, F32, false, SPLIT>(tmQ, p, smem, rank, first);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader)
     if (leader) {
@@ -851,13 +951,13 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
               tc2_mma_bf16(d, pd + p_step, qd + q_step, idesc, 1u);
               tc2_mma_bf16(d, pd + 2 * p_step, qd + 2 * q_step, idesc, 1u);
               tc2_mma_bf16(d, pd + 3 * p_step, qd + 3 * q_step, idesc, 1u);
-              tc2_commit_both(done);
+              tc2_commit_pair(done, first);
             } else {
               if (T.rem > 16) tc2_mma_bf16(d, pd + p_step, qd + q_step, idesc, 1u);
               if (T.rem > 32) tc2_mma_bf16(d, pd + 2 * p_step, qd + 2 * q_step, idesc, 1u);
               if (T.rem > 48) tc2_mma_bf16(d, pd + 3 * p_step, qd + 3 * q_step, idesc, 1u);
-              tc2_commit_both(done);
-              tc2_commit_both(&acc_full[acc]);
+              tc2_commit_pair(done, first);
+              tc2_commit_pair(&acc_full[acc], first);
             }
           }
           ready = __all_sync(0xFFFFFFFFu, next != 0);
@@ -873,6 +973,8 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
       __syncwarp();
       ragged_wait<false>(final_bar, 0, &no_abort);
     }
+  } else if (SPLIT && warp >= 4) {
+    if (walk.next(&T)) mine = both_ok(ragged_wait<false>(&acc_full[0], 0, abort_flag), 1 + ((warp - 4) >> 1));
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, h = (warp - 4) >> 2;  // lane quarter (32 features), parity of the 32-token blocks
@@ -966,6 +1068,7 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
       }
     }
   }
+  if constexpr (SPLIT) ragged_join<EPI>(p, T, smem, tmem_base, warp, lane, rank, first, mine);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -974,6 +1077,17 @@ ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ Ra
   tc_fence_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem_base) : "memory");
+}
+
+template <int MODE, bool EPI, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(rg::THREADS, 1)
+ragged_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ RaggedMaps tmQ, const RaggedK p) {
+  ragged_body<MODE, EPI, F32, false>(tmP, tmQ, p);
+}
+template <int MODE, bool EPI>
+__global__ void __launch_bounds__(rg::THREADS, 1)
+ragged_split_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constant__ RaggedMaps tmQ, const RaggedK p) {
+  ragged_body<MODE, EPI, false, true>(tmP, tmQ, p);
 }
 
 // The tile width for `rows` output rows in `segments` pieces under n_f column
@@ -996,13 +1110,80 @@ static int tile_width(int64_t rows, int64_t segments, int64_t n_f, int pairs) {
   return best;
 }
 
+// Row tiles of width w for `rows` rows in up to `segments` pieces (0: one
+// piece), at most.
+static int64_t row_tiles(int64_t rows, int64_t segments, int64_t w) {
+  return segments ? rows / w + segments : (rows + w - 1) / w;
+}
+
+// Clusters of 2 x splits CTAs that run at the same time.
+constexpr int MAX_SPLITS = 4;
+static cudaError_t resident_clusters(int splits, int* n) {
+  static std::atomic<int> known[MAX_SPLITS + 1];
+  if ((*n = known[splits].load(std::memory_order_relaxed)) != 0) return cudaSuccess;
+  cudaError_t e = ensure_smem_attr<ragged_split_kernel<RAGGED_NK, true>>(rg::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2u * (unsigned)splits;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2u * (unsigned)splits);
+  cfg.blockDim = dim3(rg::THREADS);
+  cfg.dynamicSmemBytes = rg::SMEM;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, ragged_split_kernel<RAGGED_NK, true>, &cfg);
+  if (e == cudaSuccess) known[splits].store(*n, std::memory_order_relaxed);
+  return e;
+}
+
+// A tile's width and the pairs that share its contraction.  Where the tiles
+// leave pairs idle, clusters of 2, 3 or 4 pairs take a tile each, a part of
+// the contraction per pair, and join their sums through shared memory.  The
+// cost in units of 0.4 ns, from sweeps of widths and splits: a 64-step block
+// w + 450 (how long its loads are on their way), joining 4000 + 15 w splits,
+// and all clusters must run at once (36, 23 and 15 of them).  Whole against
+// split, us: 16 rows, 16384 -> 4096, 54.1, 29.5 (three pairs a tile); 128 rows,
+// 5120 -> 2048, 19.2, 12.8; 777 rows, 21.2, 19.7; 600 rows, 8192 -> 1024, 29.1,
+// 17.6; 53 rows, 2944 -> 128, 10.9, 7.7; 64 rows, 512 -> 256, 4.7, 6.0.
+struct TileShape { int width, splits; };
+static cudaError_t tile_shape(int64_t rows, int64_t segments, int64_t n_f, int64_t nk, int pairs, TileShape* best) {
+  *best = TileShape{tile_width(rows, segments ? segments : 1, n_f, pairs), 1};
+  const int64_t whole = row_tiles(rows, segments, best->width) * n_f;
+  if (whole > pairs) return cudaSuccess;
+  int64_t least = nk * (best->width + 450) * 19 / 20;
+  for (int s = 2; s <= MAX_SPLITS && 2 * s <= nk; s++) {
+    int clusters;
+    const cudaError_t e = resident_clusters(s, &clusters);
+    if (e != cudaSuccess) return e;
+    for (int w = 32; w <= 256; w += 32) {
+      const int64_t cost = (nk + s - 1) / s * (w + 450) + 4000 + 15 * w * s;
+      if (row_tiles(rows, segments, w) * n_f <= clusters && cost < least) {
+        least = cost;
+        *best = TileShape{w, s};
+      }
+    }
+  }
+  return cudaSuccess;
+}
+
 template <int MODE, bool EPI, bool F32>
 static cudaError_t launch_ragged(const RaggedK& p, const RaggedMaps& tp, const RaggedMaps& tq, int64_t tiles,
                                  cudaStream_t s) {
   if (tiles >= (1ll << 30)) return cudaErrorInvalidValue;
   const cudaError_t e = ensure_smem_attr<ragged_kernel<MODE, EPI, F32>>(rg::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ragged_kernel<MODE, EPI, F32>, dim3((unsigned)(2 * tiles)), rg::THREADS, rg::SMEM, s, 1, tp, tq, p);
+  return launch_pdl(ragged_kernel<MODE, EPI, F32>, dim3((unsigned)(2 * tiles)), rg::THREADS, rg::SMEM, s, dim3(1), tp, tq, p);
+}
+template <int MODE, bool EPI>
+static cudaError_t launch_split(const RaggedK& p, const RaggedMaps& tp, const RaggedMaps& tq, int64_t tiles,
+                                cudaStream_t s) {
+  const cudaError_t e = ensure_smem_attr<ragged_split_kernel<MODE, EPI>>(rg::SMEM);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = 2u * (unsigned)p.splits;
+  return launch_pdl(ragged_split_kernel<MODE, EPI>, dim3((unsigned)tiles * ctas), rg::THREADS, rg::SMEM, s, dim3(ctas), tp,
+                    tq, p);
 }
 
 // BF16 matrix [outer, inner] (row stride ld elements), optionally a stack of
@@ -1027,7 +1208,11 @@ cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t 
   k.epi = p.epi;
   // each segment ends in one tile of its own at most
   const int64_t own = p.offsets ? (p.G < p.R ? p.G : p.R) : 1;
-  k.tw = tile_width(p.R, own, k.n_f, num_sms / 2);
+  TileShape shape;
+  const cudaError_t e = tile_shape(p.R, p.offsets ? own : 0, k.n_f, (p.K + rg::BK - 1) / rg::BK, num_sms / 2, &shape);
+  if (e != cudaSuccess) return e;
+  k.tw = shape.width;
+  k.splits = shape.splits;
   k.w_once = p.R <= 32 * (p.offsets ? (int64_t)p.G : 1);
   RaggedMaps tp, tq;
   if (!(p.w_kn ? bf16_map(&tp.box[0], p.w, p.N, p.K, p.N, p.G, 64)
@@ -1036,8 +1221,12 @@ cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t 
     return cudaErrorInvalidValue;
   for (int j = 1; j < 4; j++)
     if (!bf16_map(&tq.box[j], p.a, p.K, p.R, p.ld_a, 0, 128 >> j)) return cudaErrorInvalidValue;
-  const int64_t tiles = (p.R / k.tw + own) * k.n_f;
+  const int64_t tiles = row_tiles(p.R, p.offsets ? own : 0, k.tw) * k.n_f;
   const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res || p.epi.q;
+  if (k.splits > 1)
+    return p.w_kn ? launch_split<RAGGED_KN, false>(k, tp, tq, tiles, s)
+           : epi  ? launch_split<RAGGED_NK, true>(k, tp, tq, tiles, s)
+                  : launch_split<RAGGED_NK, false>(k, tp, tq, tiles, s);
   if (p.w_kn) return launch_ragged<RAGGED_KN, false, false>(k, tp, tq, tiles, s);
   return epi ? launch_ragged<RAGGED_NK, true, false>(k, tp, tq, tiles, s)
              : launch_ragged<RAGGED_NK, false, false>(k, tp, tq, tiles, s);
@@ -1123,8 +1312,8 @@ cudaError_t launch_ragged_wgrad(const RaggedWgradParams& p, int num_sms, cudaStr
   const int64_t n = (int64_t)p.G * p.N * p.K, blocks = (n / 4 + 255) / 256;
   const dim3 grid((unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8));
   const float* parts = static_cast<const float*>(p.workspace);
-  return p.grad ? launch_pdl(wgrad_sum_kernel<false>, grid, 256, 0, s, 1, parts, k.splits, n, (void*)p.grad, 0)
-                : launch_pdl(wgrad_sum_kernel<true>, grid, 256, 0, s, 1, parts, k.splits, n, (void*)p.grad_f32,
+  return p.grad ? launch_pdl(wgrad_sum_kernel<false>, grid, 256, 0, s, dim3(1), parts, k.splits, n, (void*)p.grad, 0)
+                : launch_pdl(wgrad_sum_kernel<true>, grid, 256, 0, s, dim3(1), parts, k.splits, n, (void*)p.grad_f32,
                              p.accumulate);
 }
 

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
 template <int MT, bool EPI>
 static cudaError_t launch(const RaggedParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.N + 16 * MT - 1) / (16 * MT)), (unsigned)(p.offsets ? (p.G < p.R ? p.G : p.R) : 1));
-  return launch_pdl(skinny_kernel<MT, EPI>, grid, 32 * SK_WARPS, 0, s, 1, p);
+  return launch_pdl(skinny_kernel<MT, EPI>, grid, 32 * SK_WARPS, 0, s, dim3(1), p);
 }
 
 cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s) {

@@ -553,3 +553,76 @@ def test_ragged_wgrad_workspace_refused(cuda_lib):
     n = mx.mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, 1)
     with pytest.raises(mx.MXError, match="WORKSPACE"):
         mx.mx_ragged_gemm_wgrad(dy, dy, 1, None, workspace=torch.empty(n - 4, dtype=torch.uint8, device="cuda"))
+
+
+# --------------------------------------------- few tiles, long contractions
+
+@pytest.mark.parametrize("act,bias,res,ckpt", [("NONE", False, False, False), ("SILU", True, False, False),
+                                               ("GELU_TANH", True, True, True), ("RELU", False, True, False)])
+@pytest.mark.parametrize("M,N,K", [(9, 128, 2944), (16, 2048, 1032), (53, 128, 4104), (77, 1056, 1992),
+                                   (300, 2048, 1288), (600, 1024, 2056), (777, 2048, 1536), (130, 264, 16384)])
+def test_linear_long_contraction(cuda_lib, M, N, K, act, bias, res, ckpt):
+    """Tiles whose contraction several pairs share, among them ones with a
+    last block of 8 and of 40 steps, and fewer blocks than tokens' blocks."""
+    mx = cuda_lib
+    act = getattr(mx, "ACT_" + act)
+    ckpt = ckpt and N % 32 == 0
+    gen = torch.Generator().manual_seed(M + N + K)
+    x, w = _bf16((M, K + 8), gen)[:, :K], _bf16((N, K), gen, K ** -0.5)
+    b = _bf16((N,), gen) if bias else None
+    r = _bf16((M, N), gen) if res else None
+    ck = mx.MX(M, N) if ckpt else None
+    out = mx.mx_linear_fwd(x, w, b, act, r, ckpt=ck)
+    assert mx.mx_get_device_status() == "MX_OK"
+    z = x.double() @ w.double().T
+    mag = x.double().abs() @ w.double().abs().T
+    if bias:
+        z, mag = z + b.double(), mag + b.double().abs()
+    h = _act(z, act, mx)
+    ref = h + r.double() if res else h
+    _check(out, ref, 1.13 * mag + h.abs() * (2.0 ** 5 / K) + (r.double().abs() / K if res else 0), K, 2.0 ** -8)
+    assert torch.equal(out, mx.mx_linear_fwd(x, w, b, act, r))
+    if ckpt:
+        rows = torch.arange(M, device="cuda").unsqueeze(1)
+        cols = torch.arange(N // 32, device="cuda").unsqueeze(0)
+        at = (rows // 128 * ((N + 127) // 128) + cols // 4) * 512 + rows % 32 * 16 + rows % 128 // 32 * 4 + cols % 4
+        scale = torch.exp2(ck.scale[at].double() - 127).repeat_interleave(32, 1)
+        # half a unit of the code, and the sums' own error
+        off = (ck.data.view(torch.float8_e4m3fn).double() * scale - z).abs()
+        assert bool((off <= 2.0 ** -4 * z.abs() + 2.0 ** -10 * scale + K * 2.0 ** -22 * mag).all())
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["NK", "KN"])
+@pytest.mark.parametrize("counts,N,K", [([33], 520, 2056), ([0, 7, 0, 50], 264, 3144), ([200, 1, 129], 136, 1544),
+                                        ([16, 16], 2048, 1024), ([700], 1024, 4104)])
+def test_ragged_gemm_long_contraction(cuda_lib, counts, N, K, kn):
+    """The same for the ragged product, with NaN and Inf in another expert's
+    rows and past the last one."""
+    mx = cuda_lib
+    R, G = sum(counts), len(counts)
+    gen = torch.Generator().manual_seed(R + N + K)
+    a = _bf16((R + 40, K), gen)
+    w = _bf16((G, K, N) if kn else (G, N, K), gen, K ** -0.5)
+    out = torch.full((R + 40, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    a[R:] = float("nan")
+    if G > 1:
+        a[:counts[0]] = float("inf")
+    mx.mx_ragged_gemm(a, w, _offsets(counts), layout=mx.W_KN if kn else mx.W_NK, out=out)
+    assert mx.mx_get_device_status() == "MX_OK"
+    first = counts[0] if G > 1 else 0
+    ref, mag = _ragged_ref(a[:R], w, counts, kn)
+    _check(out[first:R], ref[first:], mag[first:], K, 2.0 ** -8)
+    assert bool((out[R:] == 9.0).all())
+
+
+def test_ragged_gemm_long_contraction_malformed_offsets(cuda_lib):
+    """Segments past the rows count nothing and are reported; no cluster waits."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(5)
+    a, w = _bf16((48, 2056), gen), _bf16((3, 264, 2056), gen)
+    out = torch.full((48, 264), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.mx_ragged_gemm(a, w, torch.tensor([20, 10, 48], dtype=torch.int32).cuda(), out=out)
+    assert mx.mx_get_device_status() == "MX_ERR_OFFSETS"
+    ref, mag = _ragged_ref(a[:20], w, [20], False)
+    _check(out[:20], ref, mag, 2056, 2.0 ** -8)
+    assert bool((out[20:] == 9.0).all())
