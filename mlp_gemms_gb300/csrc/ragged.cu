@@ -705,36 +705,26 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
       used |= 1u << here;
       if (++stage == ST) { stage = 0; phase ^= 1u; }
       const uint32_t free_next = mbar_try(&empty[stage], phase ^ 1u);  // polled while this stage's copies are issued
-      if (elect_one_lane()) {
-        const uint32_t fb = full0 + 8u * here;
-        const bool pieces = MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0;
-        if (leader) mbar_arrive_expect_tx(&full[here], pieces ? (uint32_t)(boxes * 256 * ((T.rem + 15) & ~15)) : 2u * bytes);
+      const uint32_t fb = full0 + 8u * here;
+      const bool pieces = MODE == RAGGED_WGRAD && kb == T.nk - 1 && (T.rem & 15) != 0;
+      if (MODE == RAGGED_WGRAD && pieces) {
+        // A lane per piece: the segment's last rows by the bits of their number
+        // (lanes 0..5 of a box's 16: 32, 16, .. 1 rows), then the zeros (6..9: 8, 4, 2, 1).
+        // (One lane issuing them in turn took 3000 cycles a tile.)
+        const int lane = threadIdx.x & 31, i = lane & 15, zeros = 16 - (T.rem & 15);
+        if (leader && elect_one_lane()) mbar_arrive_expect_tx(&full[here], (uint32_t)(boxes * 256 * ((T.rem + 15) & ~15)));
+        __syncwarp();
+        const int rows = i < 6 ? 32 >> i : 8 >> (i - 6);  // of this lane's piece
+        const int of = i < 6 ? T.rem : zeros, before = of & -(2 * rows);
+        if (i < 10 && (of & rows) && lane >> 4 < boxes)
+          tma2_load_2d(dst + (lane >> 4) * 8192 + (before + (i < 6 ? 0 : T.rem)) * 128, &tm.box[i < 6 ? i + 1 : i - 3],
+                       i < 6 ? x + 64 * (lane >> 4) : 0, i < 6 ? k + before : (int)p.R, fb, pol);
+        __syncwarp();
+      } else if (elect_one_lane()) {
+        if (leader) mbar_arrive_expect_tx(&full[here], 2u * bytes);
         if constexpr (MODE == RAGGED_WGRAD) {
-          if (!pieces) {
-            tma2_load_2d(dst, &tm.box[0], x, k, fb, pol);
-            if (boxes > 1) tma2_load_2d(dst + 8192, &tm.box[0], x + 64, k, fb, pol);
-          } else {
-            const int zeros = 16 - (T.rem & 15);
-            for (int j = 0; j < boxes; j++) {
-              uint8_t* at = dst + j * 8192;
-              int row = k;
-#pragma unroll
-              for (int i = 1; i < 7; i++) {
-                if (T.rem & (64 >> i)) {
-                  tma2_load_2d(at, &tm.box[i], x + 64 * j, row, fb, pol);
-                  row += 64 >> i;
-                  at += (64 >> i) * 128;
-                }
-              }
-#pragma unroll
-              for (int i = 3; i < 7; i++) {
-                if (zeros & (64 >> i)) {
-                  tma2_load_2d(at, &tm.box[i], 0, (int)p.R, fb, pol);
-                  at += (64 >> i) * 128;
-                }
-              }
-            }
-          }
+          tma2_load_2d(dst, &tm.box[0], x, k, fb, pol);
+          if (boxes > 1) tma2_load_2d(dst + 8192, &tm.box[0], x + 64, k, fb, pol);
         } else if constexpr (IS_P && MODE == RAGGED_NK) {
           tma2_load_3d_hint(dst, &tm.box[0], k, x, T.g, fb, pol);
         } else if constexpr (IS_P) {
