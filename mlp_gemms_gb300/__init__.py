@@ -10,6 +10,7 @@ There is no fallback: if the shared library is missing or fails to load,
 ``load()`` raises and nothing runs.
 """
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -187,10 +188,12 @@ def _ptr(t):
 # Quantized tensors
 # --------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=256)
 def payload_bytes(rows, cols, fmt):
     return int(load().mx_payload_bytes(rows, cols, fmt))
 
 
+@functools.lru_cache(maxsize=256)
 def scale_bytes(rows, cols):
     return int(load().mx_scale_bytes(rows, cols))
 
@@ -656,6 +659,7 @@ def mx_act_ckpt_fwd(z, act, h=None, ckpt=None, stream=None):
     return h, ckpt
 
 
+@functools.lru_cache(maxsize=256)
 def mx_act_ckpt_workspace_bytes(R, C):
     return int(load().mx_act_ckpt_workspace_bytes(R, C))
 

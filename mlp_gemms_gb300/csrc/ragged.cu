@@ -28,11 +28,11 @@
 //
 // What bounds it (us at 8192 tokens x 8 choices, 128 experts, skewed, K = 2048,
 // N = 1536; floor 209 at the measured BF16 rate, 189 at the copy rate): forward
-// 281, input gradient 281, weight gradient 310, back to back from a cold chip;
-// 309 / 309 / 340 over seconds, when the power limit holds the clock down.
+// 277, input gradient 279, weight gradient 305, back to back from a cold chip;
+// 315 / 317 / 347 over seconds, when the power limit holds the clock down.
 // Without MMAs the forward product takes 238: the 64 KB that a 256 x 256 x 64
 // block of the output brings from L2, at 15 TB/s; the MMAs alone about 190.
-// Dense [16384, 2048] x [8192, 2048]: 280 us = 1.96 PFLOP/s.  Two pairs sharing
+// Dense [16384, 2048] x [8192, 2048], GELU and checkpoint: 305 us = 1.80 PFLOP/s.  Two pairs sharing
 // the token operand by multicast (clusters of four: 144 of 152 SMs) moved a
 // quarter fewer bytes and were 0 to 3 % slower; an L2 prefetch of the next
 // tile's operands was 6 to 30 % slower.
@@ -1188,8 +1188,26 @@ static bool bf16_map(CUtensorMap* m, const void* base, int64_t inner, int64_t ou
   return encode_bf16_map(m, base, s) == MX_OK;
 }
 
+// Whether the kernel for few rows is the faster one (us there, on tiles).
+static bool few_rows(const RaggedParams& p, int pairs) {
+  if (p.R <= 8) return true;
+  const int64_t n_f = (p.N + 255) / 256, weights = 2 * p.N * p.K;
+  if (p.offsets) {
+    // Mostly empty experts (16 rows of 128 experts, 2048 -> 1536: 19.5, 25.0; 64
+    // rows 58.0, 57.6), or few tiles of which each meets a handful of rows (16 rows
+    // of 8 experts 10.8, 12.9; 32 rows 12.0, 13.7; 64 rows 15.3, 13.8; 64 rows of
+    // 64 experts, 512 -> 768, 13.4, 11.3).
+    return 2 * p.R <= p.G || (p.R <= 4 * (int64_t)p.G && (p.G < p.R ? p.G : p.R) * n_f <= pairs);
+  }
+  // 16 rows, 2048 -> 2048: 4.9, 8.4; 16384 -> 4096: 26.1, 29.6; 4096 -> 16384, where
+  // the tiles fill the pairs: 28.4, 25.2.  32 rows, 2048 -> 2048: 6.9, 8.4; 512 ->
+  // 512: 2.4, 4.7; 5120 -> 2048: 13.0, 11.1.
+  if (p.R <= 16) return weights <= 64000000 || 3 * n_f < 2 * pairs;
+  return p.R <= 32 && weights <= 12000000;
+}
+
 cudaError_t launch_ragged_gemm(const RaggedParams& p, int num_sms, cudaStream_t s) {
-  if (!p.w_kn && (p.R <= 8 || (p.offsets && 2 * p.R <= p.G))) return launch_skinny(p, s);
+  if (!p.w_kn && few_rows(p, num_sms / 2)) return launch_skinny(p, s);
   RaggedK k{};
   k.G = p.G; k.offsets = p.offsets;
   k.R = p.R; k.N = p.N; k.K = p.K;

@@ -1,5 +1,5 @@
 // The ragged product and the linear layer for a few rows (decode steps): every
-// weight is read once and meets at most a handful of tokens, so the time is
+// weight is read once and meets at most a few tokens, so the time is
 // the weights' way through HBM plus the launch.  A CTA takes 16 (32 with a
 // checkpoint) features of one expert and all of K, split over its eight warps
 // in turns of 32: 64 consecutive bytes of a row per warp, 512 per CTA.  The
@@ -10,9 +10,10 @@
 // No shared-memory ring, no barriers before the first load: a tcgen05 tile
 // costs its prologue (tensor-memory allocation, cluster barrier, descriptor
 // fetch) before any weight arrives, and with one row of 48 tiles it reaches
-// 96 of the 152 SMs.  Measured: 8 rows of 8 of 128 experts, 2048 -> 1536, 12.5
-// us (4.0 TB/s) against 25 on the tensor-core tiles; one row, 4096 -> 16384,
-// 23.6 us (5.7 TB/s) against 30.  The rows staged in shared memory by bulk
+// 96 of the 152 SMs.  Measured: 8 rows of 8 of 128 experts, 2048 -> 1536, 11.4
+// us (4.4 TB/s) against 14.5 on the tensor-core tiles; one row, 4096 -> 16384,
+// 23.5 us (5.7 TB/s) against 25.7; 2048 -> 2048, 4.5 against 8.3.  Up to 32 rows
+// meet a weight at once, eight to an MMA (16 rows, 2048 -> 2048: 4.9 us).  The rows staged in shared memory by bulk
 // copies instead: 11.9 and 23.7 us, but 28 for 8 rows, 4096 -> 16384 (24.5
 // here), where the tokens' loads wait behind the barrier.
 #include "act.cuh"
@@ -23,8 +24,10 @@ namespace mx {
 static __device__ unsigned g_skinny_status = 0;
 
 constexpr int SK_WARPS = 8;
-constexpr int SK_BATCH = 4;  // 32-k chunks a warp loads before it uses the first
-constexpr int SK_TOK = 8;    // tokens of a pass; more go over the weights again, from L2
+
+// 32-k chunks a warp loads before it uses the first, with MT x 16 features and
+// NT x 8 tokens of a pass (more tokens go over the weights again, from L2).
+constexpr int sk_batch(int mt, int nt) { return mt * nt <= 2 ? 4 : 2; }
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   uint4 q;
@@ -92,13 +95,14 @@ __device__ __forceinline__ bool find_expert(const RaggedParams& p, int want, int
   return found;
 }
 
-// Three CTAs an SM with 4 chunks in flight (two with 32 features): measured
+// Three CTAs an SM with 4 chunks in flight (two with 32 features or more
+// tokens): measured
 // on one token of 4096 -> 16384 against 2 x 8, 4 x 4, 4 x 2 and 5 x 2 chunks
 // 23.9 us against 24.0, 29.0, 24.4, 35.1, and on 8 experts' rows 12.8 against
 // 14.0, 16.5, 13.9, 17.8 (more CTAs spill).
-template <int MT, bool EPI>
-__global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(const RaggedParams p) {
-  constexpr int ROWS = 16 * MT, TOK = SK_TOK;
+template <int MT, int NT, bool EPI>
+__global__ void __launch_bounds__(32 * SK_WARPS, MT * NT == 1 ? 3 : 2) skinny_kernel(const RaggedParams p) {
+  constexpr int ROWS = 16 * MT, TOK = 8 * NT, SK_BATCH = sk_batch(MT, NT);
   __shared__ float red[SK_WARPS][TOK][ROWS + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
   pdl_trigger();
@@ -116,33 +120,46 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
   }
   const int chunks = (int)((p.K + 31) / 32);
   for (int64_t m0 = r0; m0 < r1; m0 += TOK) {
-    float acc[MT][4] = {};
-    const bool xin = m0 + g4 < r1;
-    const uint16_t* x = p.a + (xin ? m0 + g4 : m0) * p.ld_a + 8 * t4;
+    float acc[MT][NT][4] = {};
+    bool xin[NT];
+    const uint16_t* x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      xin[n] = m0 + 8 * n + g4 < r1;
+      x[n] = p.a + (xin[n] ? m0 + 8 * n + g4 : m0) * p.ld_a + 8 * t4;
+    }
     for (int c0 = warp; c0 < chunks; c0 += SK_WARPS * SK_BATCH) {
-      uint4 qw[SK_BATCH][2 * MT], qx[SK_BATCH];
+      uint4 qw[SK_BATCH][2 * MT], qx[SK_BATCH][NT];
 #pragma unroll
       for (int b = 0; b < SK_BATCH; b++) {
         const int k = (c0 + b * SK_WARPS) * 32;
         const bool kin = k + 8 * t4 < p.K;
 #pragma unroll
         for (int i = 0; i < 2 * MT; i++) qw[b][i] = kin && win[i] ? ld_stream(w[i] + k) : make_uint4(0, 0, 0, 0);
-        qx[b] = kin && xin ? *(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+          qx[b][n] = kin && xin[n] ? *(reinterpret_cast<const uint4*>(x[n] + k)) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int b = 0; b < SK_BATCH; b++)
 #pragma unroll
         for (int m = 0; m < MT; m++) {
           const uint4 &u = qw[b][2 * m], &v = qw[b][2 * m + 1];
-          mma_16816(acc[m], u.x, v.x, u.y, v.y, qx[b].x, qx[b].y);
-          mma_16816(acc[m], u.z, v.z, u.w, v.w, qx[b].z, qx[b].w);
+#pragma unroll
+          for (int n = 0; n < NT; n++) {
+            mma_16816(acc[m][n], u.x, v.x, u.y, v.y, qx[b][n].x, qx[b][n].y);
+            mma_16816(acc[m][n], u.z, v.z, u.w, v.w, qx[b][n].z, qx[b][n].w);
+          }
         }
     }
     if (m0 != r0) __syncthreads();  // the last group's sums have been read
 #pragma unroll
     for (int m = 0; m < MT; m++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) red[warp][2 * t4 + (i & 1)][16 * m + g4 + 8 * (i >> 1)] = acc[m][i];
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          red[warp][8 * n + 2 * t4 + (i & 1)][16 * m + g4 + 8 * (i >> 1)] = acc[m][n][i];
     __syncthreads();
     // the warps' sums in warp order; consecutive threads hold consecutive features
     const int count = r1 - m0 < TOK ? (int)(r1 - m0) : TOK;
@@ -188,16 +205,23 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT == 1 ? 3 : 2) skinny_kernel(
   }
 }
 
-template <int MT, bool EPI>
+template <int MT, int NT, bool EPI>
 static cudaError_t launch(const RaggedParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.N + 16 * MT - 1) / (16 * MT)), (unsigned)(p.offsets ? (p.G < p.R ? p.G : p.R) : 1));
-  return launch_pdl(skinny_kernel<MT, EPI>, grid, 32 * SK_WARPS, 0, s, dim3(1), p);
+  return launch_pdl(skinny_kernel<MT, NT, EPI>, grid, 32 * SK_WARPS, 0, s, dim3(1), p);
 }
 
-cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s) {
-  if (p.epi.q) return launch<2, true>(p, s);
+template <int NT>
+static cudaError_t launch_tokens(const RaggedParams& p, cudaStream_t s) {
+  if (p.epi.q) return launch<2, NT, true>(p, s);
   const bool epi = p.epi.bias || p.epi.act != MX_ACT_NONE || p.epi.res;
-  return epi ? launch<1, true>(p, s) : launch<1, false>(p, s);
+  return epi ? launch<1, NT, true>(p, s) : launch<1, NT, false>(p, s);
+}
+
+// Experts' segments are short here: 8 rows at a time.
+cudaError_t launch_skinny(const RaggedParams& p, cudaStream_t s) {
+  if (p.offsets != nullptr || p.R <= 8) return launch_tokens<1>(p, s);
+  return p.R <= 16 ? launch_tokens<2>(p, s) : launch_tokens<4>(p, s);
 }
 
 cudaError_t read_skinny_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_skinny_status, sizeof(unsigned)); }

@@ -626,3 +626,49 @@ def test_ragged_gemm_long_contraction_malformed_offsets(cuda_lib):
     ref, mag = _ragged_ref(a[:20], w, [20], False)
     _check(out[:20], ref, mag, 2056, 2.0 ** -8)
     assert bool((out[20:] == 9.0).all())
+
+
+@pytest.mark.parametrize("act,bias,res,ckpt", [("NONE", False, False, False), ("SILU", True, True, False),
+                                               ("GELU_TANH", True, False, True)])
+@pytest.mark.parametrize("N,K", [(8, 8), (136, 1000), (544, 328), (96, 4104)])
+@pytest.mark.parametrize("M", [7, 8, 9, 15, 16, 17, 23, 24, 31, 32, 33])
+def test_linear_few_rows(cuda_lib, M, N, K, act, bias, res, ckpt):
+    mx = cuda_lib
+    act = getattr(mx, "ACT_" + act)
+    gen = torch.Generator().manual_seed(M + N + K)
+    buf = _bf16((M + 2, K + 8), gen)
+    buf[M:] = float("nan")
+    x, w = buf[:M, :K], _bf16((N, K), gen, K ** -0.5)
+    b = _bf16((N,), gen) if bias else None
+    r = _bf16((M, N), gen) if res else None
+    ck = mx.MX(M, N) if ckpt and N % 32 == 0 else None
+    out = torch.full((M + 2, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.mx_linear_fwd(x, w, b, act, r, out=out[:M], ckpt=ck)
+    assert mx.mx_get_device_status() == "MX_OK"
+    z = x.double() @ w.double().T
+    mag = x.double().abs() @ w.double().abs().T
+    if bias:
+        z, mag = z + b.double(), mag + b.double().abs()
+    h = _act(z, act, mx)
+    ref = h + r.double() if res else h
+    _check(out[:M], ref, 1.13 * mag + h.abs() * (2.0 ** 5 / K) + (r.double().abs() / K if res else 0), K, 2.0 ** -8)
+    assert bool((out[M:] == 9.0).all())
+    if ck is not None:
+        rows = torch.arange(M, device="cuda").unsqueeze(1)
+        cols = torch.arange(N // 32, device="cuda").unsqueeze(0)
+        at = (rows // 128 * ((N + 127) // 128) + cols // 4) * 512 + rows % 32 * 16 + rows % 128 // 32 * 4 + cols % 4
+        scale = torch.exp2(ck.scale[at].double() - 127).repeat_interleave(32, 1)
+        off = (ck.data.view(torch.float8_e4m3fn).double() * scale - z).abs()
+        assert bool((off <= 2.0 ** -4 * z.abs() + 2.0 ** -10 * scale + K * 2.0 ** -22 * mag).all())
+
+
+@pytest.mark.parametrize("counts", [[9, 0, 3, 1], [1] * 8, [0, 17, 0, 0, 0, 0, 0, 3], [4, 4, 4, 4]])
+def test_ragged_gemm_few_rows_of_few_experts(cuda_lib, counts):
+    mx = cuda_lib
+    R, G, N, K = sum(counts), len(counts), 200, 1160
+    gen = torch.Generator().manual_seed(R + G)
+    a, w = _bf16((R, K), gen), _bf16((G, N, K), gen, K ** -0.5)
+    out = mx.mx_ragged_gemm(a, w, _offsets(counts))
+    assert mx.mx_get_device_status() == "MX_OK"
+    ref, mag = _ragged_ref(a, w, counts, False)
+    _check(out, ref, mag, K, 2.0 ** -8)
