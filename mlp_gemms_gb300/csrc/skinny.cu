@@ -1,6 +1,6 @@
 // The ragged product and the linear layer for a few rows (decode steps): every
-// weight is read once and meets at most a few tokens, so the time is
-// the weights' way through HBM plus the launch.  A CTA takes 16 (32 with a
+// weight is read once and meets at most a few tokens, so the time is the
+// weights' way through HBM plus the launch.  A CTA takes 16 (32 with a
 // checkpoint) features of one expert and all of K, split over its eight warps
 // in turns of 32: 64 consecutive bytes of a row per warp, 512 per CTA.  The
 // weights go from global memory straight into the registers of mma.sync's A
@@ -9,13 +9,13 @@
 // fragments without a shuffle, and so does the tokens' load on the B side.
 // No shared-memory ring, no barriers before the first load: a tcgen05 tile
 // costs its prologue (tensor-memory allocation, cluster barrier, descriptor
-// fetch) before any weight arrives, and with one row of 48 tiles it reaches
-// 96 of the 152 SMs.  Measured: 8 rows of 8 of 128 experts, 2048 -> 1536, 11.4
-// us (4.4 TB/s) against 14.5 on the tensor-core tiles; one row, 4096 -> 16384,
-// 23.5 us (5.7 TB/s) against 25.7; 2048 -> 2048, 4.5 against 8.3.  Up to 32 rows
-// meet a weight at once, eight to an MMA (16 rows, 2048 -> 2048: 4.9 us).  The rows staged in shared memory by bulk
-// copies instead: 11.9 and 23.7 us, but 28 for 8 rows, 4096 -> 16384 (24.5
-// here), where the tokens' loads wait behind the barrier.
+// fetch) before any weight arrives.  Measured: 8 rows of 8 of 128 experts,
+// 2048 -> 1536, 11.4 us (4.4 TB/s) against 14.5 on the tensor-core tiles; one
+// row, 4096 -> 16384, 23.5 us (5.7 TB/s) against 25.7; 2048 -> 2048, 4.5 against
+// 8.3.  Up to 32 rows meet a weight at once, eight to an MMA (16 rows, 2048 ->
+// 2048: 4.9 us).  The rows staged in shared memory by bulk copies instead: 11.9
+// and 23.7 us, but 28 for 8 rows, 4096 -> 16384 (24.5 here), where the tokens'
+// loads wait behind the barrier.
 #include "act.cuh"
 #include "mx_internal.h"
 
