@@ -28,14 +28,14 @@
 //
 // What bounds it (us at 8192 tokens x 8 choices, 128 experts, skewed, K = 2048,
 // N = 1536; floor 209 at the measured BF16 rate, 189 at the copy rate): forward
-// 277, input gradient 279, weight gradient 305, back to back from a cold chip;
+// 275, input gradient 274, weight gradient 287, back to back from a cold chip;
 // 315 / 317 / 347 over seconds, when the power limit holds the clock down.
 // Without MMAs the forward product takes 238: the 64 KB that a 256 x 256 x 64
 // block of the output brings from L2, at 15 TB/s; the MMAs alone about 190.
-// Dense [16384, 2048] x [8192, 2048], GELU and checkpoint: 305 us = 1.80 PFLOP/s.  Two pairs sharing
-// the token operand by multicast (clusters of four: 144 of 152 SMs) moved a
-// quarter fewer bytes and were 0 to 3 % slower; an L2 prefetch of the next
-// tile's operands was 6 to 30 % slower.
+// Dense [16384, 2048] x [8192, 2048], GELU and checkpoint: 296 us = 1.86
+// PFLOP/s.  Two pairs sharing the token operand by multicast (clusters of four:
+// 144 of 152 SMs) moved a quarter fewer bytes and were 0 to 3 % slower; an L2
+// prefetch of the next tile's operands was 6 to 30 % slower.
 //
 // The weight gradient contracts over a segment's rows.  Its last 64-row block
 // would hold rows of the next expert, whose Inf or NaN times a zero is NaN: it
@@ -53,13 +53,14 @@
 #include "pair_common.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace mx {
 
 static __device__ unsigned g_ragged_status = 0;
 
 namespace rg {
-constexpr int THREADS = 384;  // warps: 0 and 3 copies, 1 MMAs, 4..11 epilogue (2 makes their quarters even)
+constexpr int THREADS = 384;  // warps: 0 and 3 copies, 1 MMAs, 2 hands out tiles, 4..11 epilogue
 constexpr int ST = 6;         // 32 KB stages of 64 contraction steps
 constexpr int BK = 64;
 constexpr int P_BYTES = 16384, Q_BYTES = 16384;
@@ -69,10 +70,17 @@ constexpr int OFF_STG = OFF_Q + ST * Q_BYTES;
 constexpr int OFF_SEG = OFF_STG + 8 * STG;                  // segment ends, [0] = 0
 constexpr int OFF_PREF = OFF_SEG + 4 * (MAX_RAGGED_G + 1);  // row tiles before expert g
 constexpr int OFF_ORD = OFF_PREF + 4 * (MAX_RAGGED_G + 1);  // experts by falling row count (uint16)
-constexpr int SLOTS = 4;      // tile indices on their way to the roles
+constexpr int SLOTS = 2;      // tile indices on their way from the hardware
+constexpr int TILES = 4;      // tiles on their way to the roles
+// Blocks of a tile still to be copied when the next tile is asked for: the answer
+// comes in time, and a pair takes on no tile long before it is free for it
+// (us with 8, and asked for at a tile's begin: weight gradient, skewed, 286, 293;
+// 16384 rows, 512 -> 8192, 84.5, 95).
+constexpr int AHEAD = 8;
 constexpr int OFF_NEXT = (OFF_ORD + 2 * MAX_RAGGED_G + 15) / 16 * 16;
-constexpr int OFF_BAR = OFF_NEXT + 16 * (SLOTS + 1);
-constexpr int NUM_BARS = 2 * ST + 5 + 2 * SLOTS + 1;
+constexpr int OFF_TILES = OFF_NEXT + 16 * (SLOTS + 1);
+constexpr int OFF_BAR = OFF_TILES + 48 * TILES;
+constexpr int NUM_BARS = 2 * ST + 5 + 2 * SLOTS + 1 + 3 * TILES;
 constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
 constexpr int SMEM = OFF_MISC + 16 + 1024;                  // + slack for 1024-byte alignment
 static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -98,18 +106,19 @@ struct RaggedK {
   RaggedEpi epi;
 };
 
-struct RaggedTile {
-  int g;
+struct alignas(16) RaggedTile {
   int64_t t0;              // first output row (WGRAD: of the expert's matrix)
+  int g;
   int valid;               // rows of the tile in the output
   int nt;                  // the MMA's N: valid rounded up to 32
   int f0;                  // first output column of the pair's 256
-  int nk;                  // 64-step blocks of the contraction
-  int k0;                  // WGRAD: first row of the contraction
+  int nk;                  // 64-step blocks of the contraction; -1: no tile, the last one was before
+  int k0;                  // first step of the contraction
   int rem;                 // contraction steps in the last block (1..64)
   int part, parts;         // WGRAD into fp32: this pass over the tile, and how many it takes
   int split;               // WGRAD: which part of the segment
 };
+static_assert(sizeof(RaggedTile) == 48, "RaggedTile");
 
 // Rows the fp32 weight gradient sums in tensor memory before it adds the sum
 // to memory.  The tensor core's fp32 accumulation truncates, a drift towards
@@ -175,13 +184,17 @@ __device__ __forceinline__ void arrive_on_leader_relaxed(uint32_t bar_cl) {
 // Tiles are handed out by the hardware: the grid has a cluster for every tile,
 // and a running pair takes over the next cluster that has not started yet
 // (clusterlaunchcontrol.try_cancel), so pairs stay busy whatever the segments'
-// lengths.  Experts come by falling row count, the long ones first.  The
-// leader's copy warp asks for the next tile while the pair works on the last
-// one; the answer arrives in both CTAs, and every role reads it for itself.
+// lengths.  Experts come by falling row count, the long ones first.  A warp of
+// each CTA does nothing else: the leader's asks for a tile once the last one's
+// copies come to their end, the answer arrives in both CTAs, and each finds the expert and
+// hands the finished description to its roles.  (Every role finding its
+// tiles for itself held the copies up by 3000 cycles a tile, the lookups queueing
+// behind the warp's own copies: 64 rows of each of 128 experts, weight gradient of
+// [1536, 2048], 151 us, now 134; skewed training segments 301, now 287.)
 struct RaggedSched {
   uint4* next;         // SLOTS answers, and one for the drain
   uint64_t* full;      // each CTA's: the answer is there
-  uint64_t* empty;     // leader's: every role of both CTAs has read it
+  uint64_t* empty;     // leader's: both CTAs have read it
 };
 
 __device__ __forceinline__ RaggedSched ragged_sched(uint8_t* smem) {
@@ -201,8 +214,7 @@ __device__ __forceinline__ bool taken_cta(const uint4* answer, uint32_t* cta) {
   return ok != 0;
 }
 
-// One role's way through the pair's passes: each of its tiles, and of a tile
-// each part.  Tile indices only grow, so the expert is searched for from the
+// The way through the pair's passes: each of its tiles, and of a tile each part.  Tile indices only grow, so the expert is searched for from the
 // last one on, 32 at a time (one by one the 38 short experts between a pair's
 // tiles took 8000 cycles: 8113 rows of 128 experts, 104 -> 64, 14.0 us, now 8.3).
 template <int MODE, bool F32, bool SPLIT>
@@ -216,7 +228,7 @@ struct RaggedWalk {
   int at, part, slot;
   uint32_t phase;
   bool fetch;        // the next pass is another tile's
-  bool asked;        // the asking warp's: an answer is on its way
+  bool asked;        // an answer is on its way
   bool more;         // a cluster was taken over for the last tile asked for (else none is left)
   __device__ RaggedWalk(const RaggedK& p_, uint8_t* smem)
       : p(p_), seg(reinterpret_cast<int32_t*>(smem + rg::OFF_SEG)), pref(reinterpret_cast<int32_t*>(smem + rg::OFF_PREF)),
@@ -325,6 +337,101 @@ struct RaggedWalk {
     return true;
   }
 };
+
+// A role's view of the tiles handed to it (a whole warp).
+struct RaggedFeed {
+  const RaggedTile* tiles;
+  uint64_t *full, *empty, *ending;  // the tile is there; all roles have read it; its copies come to their end
+  volatile int* abort_flag;
+  int slot;
+  uint32_t phase;
+  __device__ RaggedFeed(const RaggedK&, uint8_t* smem)
+      : tiles(reinterpret_cast<const RaggedTile*>(smem + rg::OFF_TILES)),
+        full(reinterpret_cast<uint64_t*>(smem + rg::OFF_BAR) + 2 * rg::ST + 5 + 2 * rg::SLOTS + 1),
+        empty(full + rg::TILES), ending(empty + rg::TILES),
+        abort_flag(reinterpret_cast<volatile int*>(smem + rg::OFF_MISC + 4)), slot(0), phase(0) {}
+  __device__ bool next(RaggedTile* T) {
+    if (!ragged_wait<false>(&full[slot], phase, abort_flag)) return false;
+    *T = tiles[slot];
+    __syncwarp();
+    if (elect_one_lane()) mbar_arrive(&empty[slot]);
+    if (++slot == rg::TILES) { slot = 0; phase ^= 1u; }
+    return T->nk >= 0;
+  }
+  // The copying warp's word that the next tile may be asked for.
+  __device__ void near_end() {
+    if (elect_one_lane()) mbar_arrive(&ending[slot == 0 ? rg::TILES - 1 : slot - 1]);
+  }
+};
+template <int MODE, bool F32, bool SPLIT>  // a cluster's only tile: every role works it out for itself
+using RaggedSource = std::conditional_t<SPLIT, RaggedWalk<MODE, F32, SPLIT>, RaggedFeed>;
+
+// The warp that hands out the tiles.
+template <int MODE, bool F32>
+__device__ __forceinline__ void ragged_tiles(const RaggedK& p, uint8_t* smem, bool leader) {
+  using namespace rg;
+  RaggedWalk<MODE, F32, false> walk(p, smem);
+  RaggedFeed feed(p, smem);
+  const RaggedSched sched = walk.sched;
+  volatile int* abort_flag = walk.abort_flag;
+  RaggedTile* const tiles = reinterpret_cast<RaggedTile*>(smem + OFF_TILES);
+  const int lane = threadIdx.x & 31;
+  int ask = 0, at = 0;                      // slots of the next request and of the tile that ends next
+  uint32_t ask_phase = 1, at_phase = 0;
+  bool ok = true;
+  while (true) {
+    RaggedTile T;
+    const bool more = walk.next(&T);
+    if (!more) T.nk = -1;
+    if (!ragged_wait<false>(&feed.empty[feed.slot], feed.phase ^ 1u, abort_flag)) { ok = false; break; }
+    if (lane == 0) tiles[feed.slot] = T;
+    __syncwarp();
+    if (elect_one_lane()) mbar_arrive(&feed.full[feed.slot]);
+    if (++feed.slot == TILES) { feed.slot = 0; feed.phase ^= 1u; }
+    if (!more) break;
+    if (leader) {
+      if (!ragged_wait<false>(&feed.ending[at], at_phase, abort_flag)) { ok = false; break; }
+      if (++at == TILES) { at = 0; at_phase ^= 1u; }
+    }
+    if (walk.fetch) {  // ask for the tile after this one
+      if (leader) {
+        if (!ragged_wait<true>(&sched.empty[ask], ask_phase, abort_flag)) { ok = false; break; }
+        if (elect_one_lane()) {
+          mbar_arrive_expect_tx(&sched.full[ask], 16);
+          asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 16;"
+                       :: "r"(peer_addr(&sched.full[ask])) : "memory");
+          asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+                       ".multicast::cluster::all.b128 [%0], [%1];"
+                       :: "r"(smem_u32(&sched.next[ask])), "r"(smem_u32(&sched.full[ask])) : "memory");
+        }
+        __syncwarp();
+        if (++ask == SLOTS) { ask = 0; ask_phase ^= 1u; }
+      }
+      walk.asked = true;
+    }
+  }
+  volatile int no_abort = 0;
+  if (walk.asked) {  // given up while an answer is on its way: it lands first
+    ragged_wait<false>(&sched.full[walk.slot], walk.phase, &no_abort);
+  } else if (leader && ok && walk.more) {
+    // The tile taken over last lies past the end: the grid counts a tile more
+    // than there may be for every segment.  Take over the rest as well, so
+    // that they do not start only to find nothing to do.
+    uint64_t* bar = sched.empty + SLOTS;
+    for (uint32_t parity = 0;; parity ^= 1u) {
+      if (elect_one_lane()) {
+        mbar_arrive_expect_tx(bar, 16);
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                     :: "r"(smem_u32(&sched.next[SLOTS])), "r"(smem_u32(bar)) : "memory");
+      }
+      __syncwarp();
+      uint32_t cta;
+      if (!ragged_wait<false>(bar, parity, &no_abort) || !taken_cta(&sched.next[SLOTS], &cta)) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+  }
+}
 
 __device__ __forceinline__ void tma2_load_3d_hint(void* dst, const CUtensorMap* m, int c0, int c1, int c2,
                                                   uint32_t bar_cl, uint64_t pol) {
@@ -669,36 +776,26 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
   uint8_t* const ring = smem + (IS_P ? 0 : OFF_Q);
   const bool leader = rank == 0;
   RaggedTile T;
-  RaggedWalk<MODE, F32, SPLIT> walk(p, smem);
-  const RaggedSched sched = walk.sched;
-  uint32_t ask_phase = 1;  // parity of sched.empty the next request waits for
-  int ask = 0;
+  RaggedSource<MODE, F32, SPLIT> feed(p, smem);
   int stage = 0;
   uint32_t phase = 0, used = 0;  // stages copied into
   bool ready = false;  // the next stage has already been seen to be free
   const uint32_t full0 = SPLIT ? cta_addr(&full[0], first) : leader_addr(&full[0]);
   bool ok = true;
-  while (ok && walk.next(&T)) {
-    if (!SPLIT && IS_P && leader && walk.fetch) {  // ask for the tile after this one
-      if (!ragged_wait<true>(&sched.empty[ask], ask_phase, abort_flag)) { ok = false; break; }
-      if (elect_one_lane()) {
-        mbar_arrive_expect_tx(&sched.full[ask], 16);
-        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 16;"
-                     :: "r"(peer_addr(&sched.full[ask])) : "memory");
-        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
-                     ".multicast::cluster::all.b128 [%0], [%1];"
-                     :: "r"(smem_u32(&sched.next[ask])), "r"(smem_u32(&sched.full[ask])) : "memory");
-      }
-      __syncwarp();
-      walk.asked = true;
-      if (++ask == SLOTS) { ask = 0; ask_phase ^= 1u; }
-    }
+  while (ok && feed.next(&T)) {
     const int half = T.nt >> 1;                       // Q rows of this CTA
     const int boxes = IS_P ? 2 : (half + 63) >> 6;    // MN-major boxes of 64
     const uint32_t bytes = IS_P ? P_BYTES : (MODE == RAGGED_WGRAD ? boxes * 8192u : half * 128u);
     const int x = IS_P ? T.f0 + 128 * (int)rank : (int)T.t0 + half * (int)rank;
     int k = T.k0;
+    const int tell = T.nk > AHEAD ? T.nk - AHEAD : 0;
+    if constexpr (IS_P && !SPLIT) {
+      if (T.nk == 0) feed.near_end();
+    }
     for (int kb = 0; kb < T.nk; kb++, k += BK) {
+      if constexpr (IS_P && !SPLIT) {
+        if (kb == tell) feed.near_end();
+      }
       if (!ready && !ragged_wait<false>(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
       uint8_t* const dst = ring + stage * P_BYTES;
       const int here = stage;
@@ -747,27 +844,6 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
     }
   }
   volatile int no_abort = 0;
-  if (SPLIT) {
-  } else if (IS_P && leader && walk.asked) {  // given up while an answer is on its way: it lands first
-    ragged_wait<false>(&sched.full[walk.slot], walk.phase, &no_abort);
-  } else if (IS_P && leader && ok && walk.more) {
-    // The tile taken over last lies past the end: the grid counts a tile more
-    // than there may be for every segment.  Take over the rest as well, so
-    // that they do not start only to find nothing to do.
-    uint64_t* bar = sched.empty + SLOTS;
-    for (uint32_t parity = 0;; parity ^= 1u) {
-      if (elect_one_lane()) {
-        mbar_arrive_expect_tx(bar, 16);
-        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
-                     :: "r"(smem_u32(&sched.next[SLOTS])), "r"(smem_u32(bar)) : "memory");
-      }
-      __syncwarp();
-      uint32_t cta;
-      if (!ragged_wait<false>(bar, parity, &no_abort) || !taken_cta(&sched.next[SLOTS], &cta)) break;
-      fence_proxy_async_smem();
-      __syncwarp();
-    }
-  }
   // Every copy has landed before the CTA leaves (the drain ignores the abort
   // flag).  Stages before the current one were last filled in this round of
   // the ring, the others in the one before.
@@ -877,10 +953,15 @@ __device__ __forceinline__ void ragged_body(const RaggedMaps& tmP, const RaggedM
     for (int s = 0; s < ST; s++) { mbar_init(&full[s], 2); mbar_init(&empty[s], 1); }
     for (int a = 0; a < 2; a++) { mbar_init(&acc_full[a], 1); mbar_init(&acc_empty[a], 16); }
     mbar_init(final_bar, 1);
-    // readers of a slot: both CTAs' copy and epilogue warps, the leader's MMA warp
     const RaggedSched sched = ragged_sched(smem);
-    for (int i = 0; i < SLOTS; i++) { mbar_init(&sched.full[i], 1); mbar_init(&sched.empty[i], 21); }
+    for (int i = 0; i < SLOTS; i++) { mbar_init(&sched.full[i], 1); mbar_init(&sched.empty[i], 2); }
     mbar_init(sched.empty + SLOTS, 1);
+    const RaggedFeed tiles(p, smem);
+    for (int i = 0; i < TILES; i++) {
+      mbar_init(&tiles.full[i], 1);
+      mbar_init(&tiles.empty[i], leader ? 11 : 10);  // the copy and epilogue warps, the leader's MMA warp
+      mbar_init(&tiles.ending[i], 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -899,11 +980,13 @@ __device__ __forceinline__ void ragged_body(const RaggedMaps& tmP, const RaggedM
   pdl_wait();
   const uint32_t tmem_base = *tmem_slot;
   RaggedTile T;
-  RaggedWalk<MODE, F32, SPLIT> walk(p, smem);
+  RaggedSource<MODE, F32, SPLIT> feed(p, smem);
   bool mine = false;  // SPLIT, epilogue warps: the pair's sums are there
 
   if (warp == 0) {
     ragged_copies<MODE, F32, true, SPLIT>(tmP, p, smem, rank, first);
+  } else if (!SPLIT && warp == 2) {
+    ragged_tiles<MODE, F32>(p, smem, leader);
   } else if (warp == 3) {
     ragged_copies<MODE, F32, false, SPLIT>(tmQ, p, smem, rank, first);
   } else if (warp == 1) {
@@ -921,7 +1004,7 @@ __device__ __forceinline__ void ragged_body(const RaggedMaps& tmP, const RaggedM
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, ready = false;  // the next stage has already been seen to be full
-      while (ok && walk.next(&T)) {
+      while (ok && feed.next(&T)) {
         if (T.nk == 0) continue;
         if (!ragged_wait<true>(&acc_empty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -964,7 +1047,7 @@ __device__ __forceinline__ void ragged_body(const RaggedMaps& tmP, const RaggedM
       ragged_wait<false>(final_bar, 0, &no_abort);
     }
   } else if (SPLIT && warp >= 4) {
-    if (walk.next(&T)) mine = both_ok(ragged_wait<false>(&acc_full[0], 0, abort_flag), 1 + ((warp - 4) >> 1));
+    if (feed.next(&T)) mine = both_ok(ragged_wait<false>(&acc_full[0], 0, abort_flag), 1 + ((warp - 4) >> 1));
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, h = (warp - 4) >> 2;  // lane quarter (32 features), parity of the 32-token blocks
@@ -972,7 +1055,7 @@ __device__ __forceinline__ void ragged_body(const RaggedMaps& tmP, const RaggedM
     uint8_t* stg = smem + OFF_STG + ((warp - 4) & ~1) * STG;
     int acc = 0;
     uint32_t acc_phase = 0;
-    while (walk.next(&T)) {
+    while (feed.next(&T)) {
       const int64_t col = T.f0 + 128 * rank + 32 * q;
       float bias[4] = {0.f, 0.f, 0.f, 0.f};
       if constexpr (EPI) {
