@@ -29,9 +29,10 @@
 // What bounds it (us at 8192 tokens x 8 choices, 128 experts, skewed, K = 2048,
 // N = 1536; floor 209 at the measured BF16 rate, 189 at the copy rate): forward
 // 275, input gradient 274, weight gradient 287, back to back from a cold chip;
-// 315 / 317 / 347 over seconds, when the power limit holds the clock down.
-// Without MMAs the forward product takes 238: the 64 KB that a 256 x 256 x 64
-// block of the output brings from L2, at 15 TB/s; the MMAs alone about 190.
+// 313 / 312 / 334 over seconds, when the power limit holds the clock down.
+// With one expert for all rows it takes 213 (98 % of the rate), with 64 239, with
+// 128 even ones 266: beside the MMAs the weights come through HBM, 228 us
+// without MMAs.
 // Dense [16384, 2048] x [8192, 2048], GELU and checkpoint: 296 us = 1.86
 // PFLOP/s.  Two pairs sharing the token operand by multicast (clusters of four:
 // 144 of 152 SMs) moved a quarter fewer bytes and were 0 to 3 % slower; an L2
@@ -769,8 +770,8 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
   uint64_t* empty = full + ST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   // Operands stay in L2 ahead of the outputs, which would push them out while
-  // other tiles still need them (ragged fwd train 289 -> 283 us, weight gradient
-  // 365 -> 343); weights that meet one tile of rows only do not stay (61 tokens
+  // other tiles still need them (us, against the default policy: forward 276, 280,
+  // weight gradient 287, 301); weights that meet one tile of rows only do not stay (61 tokens
   // 125.2 -> 120.0 us).
   const uint64_t pol = IS_P && MODE != RAGGED_WGRAD && p.w_once ? l2_policy_evict_first() : l2_policy_evict_last();
   uint8_t* const ring = smem + (IS_P ? 0 : OFF_Q);
