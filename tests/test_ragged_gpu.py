@@ -672,3 +672,36 @@ def test_ragged_gemm_few_rows_of_few_experts(cuda_lib, counts):
     assert mx.mx_get_device_status() == "MX_OK"
     ref, mag = _ragged_ref(a, w, counts, False)
     _check(out, ref, mag, K, 2.0 ** -8)
+
+
+def test_products_on_two_streams_at_once(cuda_lib):
+    """Kernels that hand out their own tiles, share clusters or start early give
+    the same bits beside one another as alone."""
+    mx = cuda_lib
+    gen = torch.Generator().manual_seed(17)
+    G, K, N = 24, 520, 776
+    counts = [(37 * g * g) % 211 for g in range(G)]
+    R, off = sum(counts), _offsets([(37 * g * g) % 211 for g in range(G)])
+    a, w, dy = _bf16((R, K), gen), _bf16((G, N, K), gen), _bf16((R, N), gen)
+    x, lw = _bf16((120, 4104), gen), _bf16((512, 4104), gen)
+    few = _bf16((13, 4104), gen)
+
+    def calls():
+        y = mx.mx_ragged_gemm(a, w, off)
+        return (y, mx.mx_ragged_gemm(y, w, off, layout=mx.W_KN), mx.mx_ragged_gemm_wgrad(dy, a, G, off),
+                mx.mx_ragged_gemm_wgrad_f32(dy, a, G, off, torch.zeros((G, N, K), device="cuda"), accumulate=True),
+                mx.mx_linear_fwd(x, lw, act=mx.ACT_SILU), mx.mx_linear_fwd(few, lw))
+
+    want = calls()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for s, g in zip(streams, got):
+            with torch.cuda.stream(s):
+                g.append(calls())
+    torch.cuda.synchronize()
+    assert mx.mx_get_device_status() == "MX_OK"
+    for outs in got[0] + got[1]:
+        for u, v in zip(outs, want):
+            assert torch.equal(u, v)
