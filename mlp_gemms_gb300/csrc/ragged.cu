@@ -187,11 +187,12 @@ __device__ __forceinline__ void arrive_on_leader_relaxed(uint32_t bar_cl) {
 // (clusterlaunchcontrol.try_cancel), so pairs stay busy whatever the segments'
 // lengths.  Experts come by falling row count, the long ones first.  A warp of
 // each CTA does nothing else: the leader's asks for a tile once the last one's
-// copies come to their end, the answer arrives in both CTAs, and each finds the expert and
-// hands the finished description to its roles.  (Every role finding its
-// tiles for itself held the copies up by 3000 cycles a tile, the lookups queueing
-// behind the warp's own copies: 64 rows of each of 128 experts, weight gradient of
-// [1536, 2048], 151 us, now 134; skewed training segments 301, now 287.)
+// copies come to their end, the answer arrives in both CTAs, and each finds the
+// expert and hands the finished description to its roles.  (Every role finding
+// its tiles for itself held the copies up by 3000 cycles a tile, the lookups
+// queueing behind the warp's own copies: 64 rows of each of 128 experts, weight
+// gradient of [1536, 2048], 151 us, now 134; skewed training segments 301, now
+// 287.)
 struct RaggedSched {
   uint4* next;         // SLOTS answers, and one for the drain
   uint64_t* full;      // each CTA's: the answer is there
@@ -215,9 +216,10 @@ __device__ __forceinline__ bool taken_cta(const uint4* answer, uint32_t* cta) {
   return ok != 0;
 }
 
-// The way through the pair's passes: each of its tiles, and of a tile each part.  Tile indices only grow, so the expert is searched for from the
-// last one on, 32 at a time (one by one the 38 short experts between a pair's
-// tiles took 8000 cycles: 8113 rows of 128 experts, 104 -> 64, 14.0 us, now 8.3).
+// The way through the pair's passes: each of its tiles, and of a tile each part.
+// Tile indices only grow, so the expert is searched for from the last one on, 32
+// at a time (one by one the 38 short experts between a pair's tiles took 8000
+// cycles: 8113 rows of 128 experts, 104 -> 64, 14.0 us, now 8.0).
 template <int MODE, bool F32, bool SPLIT>
 struct RaggedWalk {
   const RaggedK& p;
@@ -770,9 +772,9 @@ __device__ __forceinline__ void ragged_copies(const RaggedMaps& tm, const Ragged
   uint64_t* empty = full + ST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   // Operands stay in L2 ahead of the outputs, which would push them out while
-  // other tiles still need them (us, against the default policy: forward 276, 280,
-  // weight gradient 287, 301); weights that meet one tile of rows only do not stay (61 tokens
-  // 125.2 -> 120.0 us).
+  // other tiles still need them (us, and under the default policy: forward 276,
+  // 280, weight gradient 287, 301); weights that meet one tile of rows only do not
+  // stay (61 tokens 125.2 -> 120.0 us).
   const uint64_t pol = IS_P && MODE != RAGGED_WGRAD && p.w_once ? l2_policy_evict_first() : l2_policy_evict_last();
   uint8_t* const ring = smem + (IS_P ? 0 : OFF_Q);
   const bool leader = rank == 0;
