@@ -1362,8 +1362,12 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* parts, int 
     if constexpr (F32) {
       float4* g = reinterpret_cast<float4*>(static_cast<float*>(grad) + i);
       if (accumulate) {
+        // zero leaves the bits alone, as an empty segment has to
         const float4 v = *g;
-        t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+        t.x = t.x == 0.f ? v.x : t.x + v.x;
+        t.y = t.y == 0.f ? v.y : t.y + v.y;
+        t.z = t.z == 0.f ? v.z : t.z + v.z;
+        t.w = t.w == 0.f ? v.w : t.w + v.w;
       }
       *g = t;
     } else {

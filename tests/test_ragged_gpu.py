@@ -470,12 +470,13 @@ def test_ragged_wgrad_many_tiles(cuda_lib, N, K, kind):
         b += c
 
 
-@pytest.mark.parametrize("G", [3, 170])
-def test_ragged_wgrad_accumulate_leaves_empty_experts_alone(cuda_lib, G):
-    """Bit for bit: negative zeros, subnormals and NaN payloads stay."""
+@pytest.mark.parametrize("G,rows,N,K", [(3, 5, 264, 520), (170, 5, 264, 520), (4, 20000, 136, 264)])
+def test_ragged_wgrad_accumulate_leaves_empty_experts_alone(cuda_lib, G, rows, N, K):
+    """Bit for bit: negative zeros, subnormals and NaN payloads stay (the last
+    case sums its segments in parts)."""
     mx = cuda_lib
-    N, K = 264, 520
-    counts = [0 if g % 3 else 5 for g in range(G)]
+    counts = [0 if g % 3 else rows for g in range(G)]
+    assert (mx.mx_ragged_gemm_wgrad_workspace_bytes(N, K, sum(counts), G) > 0) == (rows > 5)
     gen = torch.Generator().manual_seed(G)
     dy, x = _bf16((sum(counts), N), gen), _bf16((sum(counts), K), gen)
     before = torch.randint(-2 ** 31, 2 ** 31 - 1, (G, N, K), generator=gen, dtype=torch.int32).cuda()
