@@ -58,9 +58,14 @@ __device__ __forceinline__ void read8(const uint2& w, uint32_t b, float (&v)[8])
   scale_values<8>(v, scale_from_byte(b));
 }
 
-// Rows a warp has in flight at a time: its loads are issued before the first
-// of them is used.
-constexpr int BATCH = 4;
+// Rows a backward warp has in flight at a time (its loads are issued before the
+// first of them is used) and blocks of an SM.  What fits the registers: SWIGLU
+// with h takes three rows (us with three and four: [65536, 1536] 82, 83.5; with
+// db 85, 91), without h four (70, 66); the others six (with four: [16384, 8192]
+// GELU with db 117, 124; [333, 8192] 6.3, 6.9) or, with neither h nor db, four
+// in each of three blocks (107, two blocks 120).
+constexpr int bwd_rows(bool glu, bool h, bool db) { return glu ? (h ? 3 : 4) : h || db ? 6 : 4; }
+constexpr int bwd_blocks(bool glu, bool h, bool db) { return glu || h || db ? 2 : 3; }
 
 // Zero the scale layout's padding (rows R .. 128 * ceil(R / 128), column
 // blocks C / 32 .. 4 * ceil(C / 128)), by one block.
@@ -169,13 +174,13 @@ __global__ void __launch_bounds__(256) ckpt_fwd_kernel(const CkptParams p, uint3
   if (blockIdx.x == 0) zero_scale_padding(p);
 }
 
-// Row blocks of the backward pass: one wave of two blocks on every SM (GB300:
-// 152) where the columns alone do not give it, each with a row for each of its
+// Row blocks of the backward pass: one wave of blocks on every SM (GB300: 152),
+// or two, where the columns alone do not give it, each with a row for each of its
 // warps.  col_blocks counts SWIGLU's columns twice: its blocks do two halves'
 // work.
-static int64_t ckpt_row_blocks(int64_t R, int64_t C) {
+static int64_t ckpt_row_blocks(int64_t R, int64_t C, int per_sm) {
   const int64_t col_blocks = (C + COLS - 1) / COLS;
-  int64_t want = 152 * 4 / col_blocks;
+  int64_t want = 152 * 2 * per_sm / col_blocks;
   const int64_t most = (R + WARPS - 1) / WARPS;
   if (want > most) want = most;
   return want < 1 ? 1 : want;
@@ -183,16 +188,18 @@ static int64_t ckpt_row_blocks(int64_t R, int64_t C) {
 
 // Column sums of up to CLUSTER_ROWS rows: a cluster of blocks holds all rows of
 // its columns and adds its blocks' sums through shared memory, with no
-// partials in memory and no second launch (measured on [333, 8192] GELU: 6.9 us
+// partials in memory and no second launch (measured on [333, 8192] GELU: 6.3 us
 // against 7.8, and no workspace to allocate).
 // More rows want more row blocks than a cluster has.
 constexpr int CLUSTER = 8, CLUSTER_ROWS = 512;
-int64_t ckpt_partials(int64_t R, int64_t C) { return R <= CLUSTER_ROWS ? 0 : ckpt_row_blocks(R, C) * C; }
+int64_t ckpt_partials(int64_t R, int64_t C) { return R <= CLUSTER_ROWS ? 0 : ckpt_row_blocks(R, C, 2) * C; }
 
 // DB: 0 no column sums, 1 partials per row block, 2 summed in the cluster.
 template <int ACT, bool H, int DB>
-__global__ void __launch_bounds__(32 * WARPS, 2) ckpt_bwd_kernel(const CkptParams p, int64_t rows_per_block) {
+__global__ void __launch_bounds__(32 * WARPS, bwd_blocks(ACT == MX_ACT_SWIGLU, H, DB != 0))
+ckpt_bwd_kernel(const CkptParams p, int64_t rows_per_block) {
   constexpr bool GLU = ACT == MX_ACT_SWIGLU;
+  constexpr int BATCH = bwd_rows(GLU, H, DB != 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t F = ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C;
   const int64_t c = (int64_t)blockIdx.x * COLS + 8 * lane, sc = p.C >> 5;
@@ -346,7 +353,8 @@ static cudaError_t launch_bwd(const CkptParams& p, cudaStream_t s) {
   const int64_t F = ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C;
   const bool cluster = p.db && p.partials == nullptr;
   const int64_t most = (p.R + WARPS - 1) / WARPS;
-  const int64_t blocks = cluster ? (most < CLUSTER ? most : CLUSTER) : ckpt_row_blocks(p.R, p.C);
+  const int per_sm = bwd_blocks(ACT == MX_ACT_SWIGLU, p.h != nullptr, p.db != nullptr);
+  const int64_t blocks = cluster ? (most < CLUSTER ? most : CLUSTER) : ckpt_row_blocks(p.R, p.C, per_sm);
   const int64_t rows = (p.R + blocks - 1) / blocks;
   const dim3 grid((unsigned)((F + COLS - 1) / COLS), (unsigned)blocks);
   const unsigned cy = (unsigned)blocks;
