@@ -131,12 +131,14 @@ __device__ __forceinline__ void save32(const CkptParams& p, int64_t r, int c, fl
 
 // Forward: a thread owns one 32-column block of a row (SWIGLU: the gate's and
 // the up half's), so the block's amax needs no exchange.  [65536, 1536] SWIGLU:
-// 62.6 us = 6.5 TB/s, 97 % of the copy rate (with 16-byte accesses, which
+// 61.2 us = 6.6 TB/s, 99 % of the copy rate (with 16-byte accesses, which
 // touch each sector twice, 68.5; with 8 columns a lane and the amax by
-// shuffles, 72.8: issue slots).  [16384, 8192]: ReLU 103 us = 98 %, GELU 110 us
-// = 91 % (its activation's issue slots).
+// shuffles, 72.8: issue slots).  [16384, 8192]: GELU 104 us = 97 %, with three
+// blocks an SM (two 110, four spill: 142).  Eight to twelve waves of blocks, each
+// with a few items a thread (two waves 63.3 and 110, as many blocks as items 62.8
+// and 104).
 template <int ACT, bool WIDE>
-__global__ void __launch_bounds__(256) ckpt_fwd_kernel(const CkptParams p, uint32_t per) {
+__global__ void __launch_bounds__(256, ACT == MX_ACT_SWIGLU ? 2 : 3) ckpt_fwd_kernel(const CkptParams p, uint32_t per) {
   constexpr bool GLU = ACT == MX_ACT_SWIGLU;
   const int64_t F = GLU ? p.C / 2 : p.C;
   pdl_trigger();
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(256) ckpt_colsum_kernel(const float* __restric
 template <int ACT>
 static cudaError_t launch_fwd(const CkptParams& p, cudaStream_t s) {
   const int64_t per = (ACT == MX_ACT_SWIGLU ? p.C / 2 : p.C) / 32, blocks = (p.R * per + 255) / 256;
-  const dim3 grid((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8));
+  const dim3 grid((unsigned)(blocks < 152 * 24 ? blocks : 152 * 24));
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.z) | reinterpret_cast<uintptr_t>(p.h) |
                        reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.ld_z * 2) | (uintptr_t)(p.ld_h * 2);
   return (at & 31) == 0 ? launch_pdl(ckpt_fwd_kernel<ACT, true>, grid, 256, 0, s, dim3(1), p, (uint32_t)per)
