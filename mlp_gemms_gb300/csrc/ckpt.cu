@@ -10,7 +10,7 @@ namespace mx {
 // (16 bytes of BF16, 8 of payload) of a row, so every access of a warp covers
 // one contiguous piece of a row, and a block 256 columns (SWIGLU: of each
 // half) and a run of rows, each warp every eighth of them: the column sums
-// stay in registers.  [65536, 1536] SWIGLU with h: 82.6 us = 6.1 TB/s, 91 % of
+// stay in registers.  [65536, 1536] SWIGLU with h: 82.1 us = 6.2 TB/s, 92 % of
 // the copy rate (a thread per 32-column block, as in the forward pass: 137).
 constexpr int COLS = 256, WARPS = 8;
 
