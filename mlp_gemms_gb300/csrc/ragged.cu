@@ -28,8 +28,8 @@
 //
 // What bounds it (us at 8192 tokens x 8 choices, 128 experts, skewed, K = 2048,
 // N = 1536; floor 209 at the measured BF16 rate, 183 at the copy rate): forward
-// 275, input gradient 274, weight gradient 287, back to back from a cold chip;
-// 313 / 312 / 334 over seconds, when the power limit holds the clock down.
+// 275, input gradient 273, weight gradient 288, back to back from a cold chip;
+// 308 / 307 / 328 over seconds, when the power limit holds the clock down.
 // With one expert for all rows it takes 213 (98 % of the rate), with 64 239, with
 // 128 even ones 266: beside the MMAs the weights come through HBM, 228 us
 // without MMAs.
