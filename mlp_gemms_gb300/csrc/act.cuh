@@ -9,8 +9,9 @@ namespace mx {
 // Programmatic launches: everything the stream's earlier kernels wrote is
 // visible after pdl_wait(); pdl_trigger() lets the stream's next kernel start
 // as far as its own pdl_wait().  Global memory is read by plain loads or by
-// volatile asm after the wait, not by __ldg: the compiler may take what a
-// read-only load reads for constant and move it up across the wait.
+// volatile asm after the wait, not by __ldg nor through const __restrict__
+// pointers: the compiler may take what those read for constant and move the
+// load up across the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

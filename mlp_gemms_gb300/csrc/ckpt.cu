@@ -310,8 +310,7 @@ ckpt_bwd_kernel(const CkptParams p, int64_t rows_per_block) {
 
 // Column sums of the partials: a block takes 32 columns, its 8 warps every
 // eighth row block, summed in a fixed order.
-__global__ void __launch_bounds__(256) ckpt_colsum_kernel(const float* __restrict__ part, int64_t blocks, int64_t C,
-                                                          float* __restrict__ db) {
+__global__ void __launch_bounds__(256) ckpt_colsum_kernel(const float* part, int64_t blocks, int64_t C, float* db) {
   __shared__ float s[8][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // C is a multiple of 32
