@@ -772,6 +772,7 @@ MX_API mx_status_t mx_linear_fwd(const void *x_bf16, int64_t M, int64_t K, int64
  *
  * mx_act_ckpt_bwd -- with z^ the values the checkpoint stands for:
  *   dz = dh * act'(z^) (SWIGLU: dg = dh u s (1 + g (1 - s)), du = dh g s),
+ *   (RELU: dh where z^ > 0, else 0, also where dh is Inf or NaN),
  *   h = act(z^) when h_bf16 is not NULL (the next product's input for its
  *   weight gradient), db = the fp32 sum over rows of the unrounded dz when
  *   db is not NULL (fixed order: deterministic).

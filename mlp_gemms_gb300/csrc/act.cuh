@@ -81,20 +81,30 @@ __device__ __forceinline__ void act2(float* a, float* b) {
   }
 }
 
-// act(z) and act'(z) of two values.
+// act(z) and act'(z) of two values (SiLU, GELU).
 template <int ACT>
 __device__ __forceinline__ void act_slope2(uint64_t z, uint64_t* h, uint64_t* d) {
+  const uint64_t z2 = mul2(z, z), s = gate2<ACT>(z, z2);
+  *h = mul2(z, s);
+  const uint64_t t = mul2(*h, fma2(s, both(-1.f), both(1.f)));
+  if constexpr (ACT == MX_ACT_SILU) *d = add2(t, s);
+  else *d = fma2(t, fma2(z2, both(3.f * GELU_B * GELU_2A), both(GELU_2A)), s);
+}
+
+// act(z) and the gradient dh act'(z) of two values.  ReLU selects: an Inf or
+// NaN behind a closed gate is not multiplied by zero.
+template <int ACT>
+__device__ __forceinline__ void act_bwd2(uint64_t z, uint64_t dh, uint64_t* h, uint64_t* dz) {
   if constexpr (ACT == MX_ACT_RELU) {
-    float a, b;
+    float a, b, da, db;
     unpack2(z, &a, &b);
+    unpack2(dh, &da, &db);
     *h = pack2(a < 0.f ? 0.f : a, b < 0.f ? 0.f : b);
-    *d = pack2(a > 0.f ? 1.f : 0.f, b > 0.f ? 1.f : 0.f);
+    *dz = pack2(a > 0.f ? da : 0.f, b > 0.f ? db : 0.f);
   } else {
-    const uint64_t z2 = mul2(z, z), s = gate2<ACT>(z, z2);
-    *h = mul2(z, s);
-    const uint64_t t = mul2(*h, fma2(s, both(-1.f), both(1.f)));
-    if constexpr (ACT == MX_ACT_SILU) *d = add2(t, s);
-    else *d = fma2(t, fma2(z2, both(3.f * GELU_B * GELU_2A), both(GELU_2A)), s);
+    uint64_t slope;
+    act_slope2<ACT>(z, h, &slope);
+    *dz = mul2(dh, slope);
   }
 }
 

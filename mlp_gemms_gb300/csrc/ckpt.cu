@@ -253,10 +253,10 @@ ckpt_bwd_kernel(const CkptParams p, int64_t rows_per_block) {
       } else {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          uint64_t a, s;
-          act_slope2<ACT>(pack2(z[j], z[j + 1]), &a, &s);
+          uint64_t a, g;
+          act_bwd2<ACT>(pack2(z[j], z[j + 1]), pack2(d[j], d[j + 1]), &a, &g);
           unpack2(a, &h[j], &h[j + 1]);
-          unpack2(mul2(pack2(d[j], d[j + 1]), s), &z[j], &z[j + 1]);
+          unpack2(g, &z[j], &z[j + 1]);
         }
       }
 #pragma unroll
