@@ -81,14 +81,21 @@ __device__ __forceinline__ void act2(float* a, float* b) {
   }
 }
 
-// act(z) and act'(z) of two values (SiLU, GELU).
+// act(z) and act'(z) of two values (SiLU, GELU).  GELU: the slope's z^2 ends
+// at 2^20, far past where t has become exactly 0: unbounded it is Inf from
+// |z| = 2^64 on, and 0 times that NaN.  (A NaN z stays one through t.)
 template <int ACT>
 __device__ __forceinline__ void act_slope2(uint64_t z, uint64_t* h, uint64_t* d) {
   const uint64_t z2 = mul2(z, z), s = gate2<ACT>(z, z2);
   *h = mul2(z, s);
   const uint64_t t = mul2(*h, fma2(s, both(-1.f), both(1.f)));
-  if constexpr (ACT == MX_ACT_SILU) *d = add2(t, s);
-  else *d = fma2(t, fma2(z2, both(3.f * GELU_B * GELU_2A), both(GELU_2A)), s);
+  if constexpr (ACT == MX_ACT_SILU) {
+    *d = add2(t, s);
+  } else {
+    float a, b;
+    unpack2(z2, &a, &b);
+    *d = fma2(t, fma2(pack2(fminf(a, 1048576.f), fminf(b, 1048576.f)), both(3.f * GELU_B * GELU_2A), both(GELU_2A)), s);
+  }
 }
 
 // act(z) and the gradient dh act'(z) of two values.  ReLU selects: an Inf or
