@@ -3,8 +3,9 @@
 Argument marshalling only: every function here checks nothing the C layer
 does not, computes nothing, and calls exactly one C-ABI entry point of the
 same name (``mx_mlp_fwd_bwd`` launches the whole step).  PyTorch supplies
-device memory (output buffers are ``torch.empty`` allocations when the
-caller passes none) and the current CUDA stream.
+device memory (outputs and workspaces are ``torch.empty`` allocations when the
+caller passes none, from the memory of the stream that the call launches on)
+and the current CUDA stream.
 
 There is no fallback: if the shared library is missing or fails to load,
 ``load()`` raises and nothing runs.
@@ -184,6 +185,21 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream=None):
+    """torch.empty for a launch on `stream`.  Memory of the current stream would
+    be no other stream's: work still queued here may be using the block,
+    and a workspace goes back to the allocator while the launch runs.  So
+    another stream's buffers are its own, and kept until both are done."""
+    import torch
+    here = None if stream is None else torch.cuda.current_stream()
+    if here is None or here == stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 # --------------------------------------------------------------------------
 # Quantized tensors
 # --------------------------------------------------------------------------
@@ -199,15 +215,15 @@ def scale_bytes(rows, cols):
 
 
 class MX:
-    """A quantized MX tensor [rows, cols] (blocks along cols) in torch buffers."""
+    """A quantized MX tensor [rows, cols] (blocks along cols) in torch buffers;
+    stream: the one that fills them, where that is not the current one."""
 
-    def __init__(self, rows, cols, fmt=E4M3, hadamard=False, device="cuda", data=None, scale=None):
+    def __init__(self, rows, cols, fmt=E4M3, hadamard=False, device="cuda", data=None, scale=None, stream=None):
         import torch
         self.rows, self.cols, self.fmt, self.hadamard = int(rows), int(cols), int(fmt), bool(hadamard)
-        self.data = data if data is not None else torch.empty((rows, payload_bytes(1, cols, fmt)),
-                                                              dtype=torch.uint8, device=device)
-        self.scale = scale if scale is not None else torch.empty(scale_bytes(rows, cols), dtype=torch.uint8,
-                                                                 device=device)
+        self.data = data if data is not None else _empty((rows, payload_bytes(1, cols, fmt)), torch.uint8, device,
+                                                         stream)
+        self.scale = scale if scale is not None else _empty(scale_bytes(rows, cols), torch.uint8, device, stream)
 
     def struct(self):
         return MxTensorStruct(self.data.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.fmt,
@@ -234,16 +250,16 @@ def mx_quantize(x, fmt=E4M3, rowwise=True, colwise=True, hadamard=False, colsum=
     flags = (ROWWISE if rowwise else 0) | (COLWISE if colwise else 0) | (HADAMARD if hadamard else 0) | \
             (COLSUM if colsum else 0)
     if rowwise and out_row is None:
-        out_row = MX(batch * rows, cols, fmt, hadamard, x.device)
+        out_row = MX(batch * rows, cols, fmt, hadamard, x.device, stream=stream)
     if colwise and out_col is None:
-        out_col = MX(batch * cols, rows, fmt, hadamard, x.device)
+        out_col = MX(batch * cols, rows, fmt, hadamard, x.device, stream=stream)
     ws_bytes = 0
     if colsum:
         if colsum_out is None:
-            colsum_out = torch.empty(cols, dtype=torch.float32, device=x.device)
+            colsum_out = _empty(cols, torch.float32, x.device, stream)
         ws_bytes = int(load().mx_quantize_workspace_bytes(rows, cols, flags))
         if workspace is None:
-            workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=x.device)
+            workspace = _empty(max(ws_bytes, 16), torch.uint8, x.device, stream)
         ws_bytes = workspace.numel() * workspace.element_size()
     _check(load().mx_quantize(_ptr(x), batch, rows, cols, ld, fmt, flags, _s(out_row) if rowwise else None,
                               _s(out_col) if colwise else None, _ptr(colsum_out) if colsum else None,
@@ -262,9 +278,9 @@ def mx_quantize_sr(x, fmt, seed, rowwise=True, colwise=True, hadamard=False, out
     ld = x.stride(-2)
     flags = (ROWWISE if rowwise else 0) | (COLWISE if colwise else 0) | (HADAMARD if hadamard else 0)
     if rowwise and out_row is None:
-        out_row = MX(batch * rows, cols, fmt, hadamard, x.device)
+        out_row = MX(batch * rows, cols, fmt, hadamard, x.device, stream=stream)
     if colwise and out_col is None:
-        out_col = MX(batch * cols, rows, fmt, hadamard, x.device)
+        out_col = MX(batch * cols, rows, fmt, hadamard, x.device, stream=stream)
     _check(load().mx_quantize_sr(x.data_ptr(), batch, rows, cols, ld, fmt, flags, int(seed),
                                  _s(out_row) if rowwise else None, _s(out_col) if colwise else None,
                                  _stream(stream)))
@@ -285,12 +301,12 @@ def mx_moe_route_index(topk, G, R_cap=None, offsets=None, src=None, row_of=None,
     T, k = topk.shape
     dev = topk.device
     R_cap = R_cap if R_cap is not None else int(load().mx_moe_route_rows_pad(T, k, G, pad))
-    offsets = offsets if offsets is not None else torch.empty(G, dtype=torch.int32, device=dev)
-    src = src if src is not None else torch.empty(R_cap, dtype=torch.int32, device=dev)
-    row_of = row_of if row_of is not None else torch.empty((T, k), dtype=torch.int32, device=dev)
+    offsets = offsets if offsets is not None else _empty(G, torch.int32, dev, stream)
+    src = src if src is not None else _empty(R_cap, torch.int32, dev, stream)
+    row_of = row_of if row_of is not None else _empty((T, k), torch.int32, dev, stream)
     nbytes = int(load().mx_moe_route_workspace_bytes(T, k, G))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(nbytes, 16), torch.uint8, dev, stream)
     _check(load().mx_moe_route_index_pad(_ptr(topk), T, k, G, pad, _ptr(offsets), _ptr(src), R_cap, _ptr(row_of),
                                           _ptr(workspace), workspace.numel(), _stream(stream)))
     return offsets, src, row_of
@@ -308,9 +324,9 @@ def mx_permute_quantize(x, src, offsets=None, G=0, fmt=E4M3, rowwise=True, colwi
         G = offsets.numel()
     flags = (ROWWISE if rowwise else 0) | (COLWISE if colwise else 0)
     if rowwise and out_row is None:
-        out_row = MX(R_cap, D, fmt, False, x.device)
+        out_row = MX(R_cap, D, fmt, False, x.device, stream=stream)
     if colwise and out_col is None:
-        out_col = MX(D, R_cap, fmt, False, x.device)
+        out_col = MX(D, R_cap, fmt, False, x.device, stream=stream)
     _check(load().mx_permute_quantize(_ptr(x), T, D, x.stride(0), _ptr(src), R_cap, _ptr(offsets), int(G), fmt, flags,
                                       _s(out_row) if rowwise else None, _s(out_col) if colwise else None,
                                       _stream(stream)))
@@ -324,7 +340,7 @@ def mx_moe_unpermute(inp, row_of, weights=None, out=None, stream=None):
     R, D = inp.shape
     T, k = row_of.shape
     if out is None:
-        out = torch.empty((T, D), dtype=torch.bfloat16, device=inp.device)
+        out = _empty((T, D), torch.bfloat16, inp.device, stream)
     _check(load().mx_moe_unpermute(_ptr(inp), R, D, _ptr(row_of), _ptr(weights), T, k, _ptr(out), _stream(stream)))
     return out
 
@@ -339,11 +355,11 @@ def mx_quantize_colsum_noalloc(x, fmt=E4M3, rowwise=True, hadamard=False, out_ro
     rows, cols = x.shape
     flags = COLWISE | COLSUM | (ROWWISE if rowwise else 0) | (HADAMARD if hadamard else 0)
     if rowwise and out_row is None:
-        out_row = MX(rows, cols, fmt, hadamard, x.device)
+        out_row = MX(rows, cols, fmt, hadamard, x.device, stream=stream)
     if out_col is None:
-        out_col = MX(cols, rows, fmt, hadamard, x.device)
+        out_col = MX(cols, rows, fmt, hadamard, x.device, stream=stream)
     if colsum_out is None:
-        colsum_out = torch.empty(cols, dtype=torch.float32, device=x.device)
+        colsum_out = _empty(cols, torch.float32, x.device, stream)
     _check(load().mx_quantize_colsum_noalloc(_ptr(x), rows, cols, x.stride(0), fmt, flags,
                                              _s(out_row) if rowwise else None, _s(out_col), _ptr(colsum_out),
                                              _stream(stream)))
@@ -354,7 +370,7 @@ def mx_grouped_gemm(a, b, G, offsets, out=None, ld_out=None, stream=None):
     import torch
     N = b.rows // G if G else 0
     if out is None:
-        out = torch.empty((a.rows, N), dtype=torch.bfloat16, device=a.data.device)
+        out = _empty((a.rows, N), torch.bfloat16, a.data.device, stream)
     ld = ld_out if ld_out is not None else out.stride(0)
     _check(load().mx_grouped_gemm(_s(a), _s(b), G, _ptr(offsets), _ptr(out), ld, _stream(stream)))
     return out
@@ -366,7 +382,7 @@ def mx_grouped_gemm_2sm(a, b, G, offsets, out=None, ld_out=None, stream=None):
     import torch
     N = b.rows // G if G else 0
     if out is None:
-        out = torch.empty((a.rows, N), dtype=torch.bfloat16, device=a.data.device)
+        out = _empty((a.rows, N), torch.bfloat16, a.data.device, stream)
     ld = ld_out if ld_out is not None else out.stride(0)
     _check(load().mx_grouped_gemm_2sm(_s(a), _s(b), G, _ptr(offsets), _ptr(out), ld, _stream(stream)))
     return out
@@ -378,7 +394,7 @@ def mx_grouped_gemm_bias_2sm(a, b, G, offsets, bias, out=None, ld_out=None, stre
     N = b.rows // G if G else 0
     assert bias.dtype == torch.bfloat16 and bias.is_contiguous()
     if out is None:
-        out = torch.empty((a.rows, N), dtype=torch.bfloat16, device=a.data.device)
+        out = _empty((a.rows, N), torch.bfloat16, a.data.device, stream)
     ld = ld_out if ld_out is not None else out.stride(0)
     _check(load().mx_grouped_gemm_bias_2sm(_s(a), _s(b), G, _ptr(offsets), _ptr(bias), _ptr(out), ld,
                                            _stream(stream)))
@@ -392,7 +408,7 @@ def mx_grouped_gemm_bias(a, b, G, offsets, bias, out=None, ld_out=None, stream=N
     N = b.rows // G if G else 0
     assert bias.dtype == torch.bfloat16 and bias.is_contiguous()
     if out is None:
-        out = torch.empty((a.rows, N), dtype=torch.bfloat16, device=a.data.device)
+        out = _empty((a.rows, N), torch.bfloat16, a.data.device, stream)
     ld = ld_out if ld_out is not None else out.stride(0)
     _check(load().mx_grouped_gemm_bias(_s(a), _s(b), G, _ptr(offsets), _ptr(bias), _ptr(out), ld, _stream(stream)))
     return out
@@ -404,11 +420,11 @@ def mx_grouped_gemm_swiglu_fwd(x_row, w1_row, G, offsets, h_row=None, h_col=None
     F = w1_row.rows // (2 * G)
     dev = x_row.data.device
     if h_row is None:
-        h_row = MX(R, F, E4M3, False, dev)
+        h_row = MX(R, F, E4M3, False, dev, stream=stream)
     if h_col is None:
-        h_col = MX(F, R, E4M3, False, dev)
+        h_col = MX(F, R, E4M3, False, dev, stream=stream)
     if z is None:
-        z = torch.empty((R, 2 * F), dtype=torch.bfloat16, device=dev)
+        z = _empty((R, 2 * F), torch.bfloat16, dev, stream)
     _check(load().mx_grouped_gemm_swiglu_fwd(_s(x_row), _s(w1_row), G, _ptr(offsets), _s(h_row), _s(h_col),
                                              _ptr(z), _stream(stream)))
     return z, h_row, h_col
@@ -420,9 +436,9 @@ def mx_grouped_gemm_swiglu_probs_fwd(x_row, w1_row, G, offsets, probs, h_row=Non
     R = x_row.rows
     F = w1_row.rows // (2 * G)
     dev = x_row.data.device
-    h_row = h_row if h_row is not None else MX(R, F, E4M3, False, dev)
-    h_col = h_col if h_col is not None else MX(F, R, E4M3, False, dev)
-    z = z if z is not None else torch.empty((R, 2 * F), dtype=torch.bfloat16, device=dev)
+    h_row = h_row if h_row is not None else MX(R, F, E4M3, False, dev, stream=stream)
+    h_col = h_col if h_col is not None else MX(F, R, E4M3, False, dev, stream=stream)
+    z = z if z is not None else _empty((R, 2 * F), torch.bfloat16, dev, stream)
     _check(load().mx_grouped_gemm_swiglu_probs_fwd(_s(x_row), _s(w1_row), G, _ptr(offsets), _ptr(probs), _s(h_row),
                                                    _s(h_col), _ptr(z), _stream(stream)))
     return z, h_row, h_col
@@ -435,12 +451,12 @@ def mx_grouped_gemm_dswiglu_probs_bwd(dy_row, w2t_row, z, probs, G, offsets, dz_
     R = dy_row.rows
     F = w2t_row.rows // G
     dev = dy_row.data.device
-    dz_row = dz_row if dz_row is not None else MX(R, 2 * F, E4M3, False, dev)
-    dz_col = dz_col if dz_col is not None else MX(2 * F, R, E4M3, False, dev)
-    dprobs = dprobs if dprobs is not None else torch.empty(R, dtype=torch.float32, device=dev)
+    dz_row = dz_row if dz_row is not None else MX(R, 2 * F, E4M3, False, dev, stream=stream)
+    dz_col = dz_col if dz_col is not None else MX(2 * F, R, E4M3, False, dev, stream=stream)
+    dprobs = dprobs if dprobs is not None else _empty(R, torch.float32, dev, stream)
     nbytes = int(load().mx_dswiglu_probs_workspace_bytes(R, F))
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(nbytes, 16), torch.uint8, dev, stream)
     _check(load().mx_grouped_gemm_dswiglu_probs_bwd(
         _s(dy_row), _s(w2t_row), _ptr(z), _ptr(probs), G, _ptr(offsets), _s(dz_row), _s(dz_col), _ptr(dprobs),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -452,9 +468,9 @@ def mx_grouped_gemm_dswiglu_bwd(dy_row, w2t_row, z, G, offsets, dz_row=None, dz_
     F = w2t_row.rows // G
     dev = dy_row.data.device
     if dz_row is None:
-        dz_row = MX(R, 2 * F, E4M3, False, dev)
+        dz_row = MX(R, 2 * F, E4M3, False, dev, stream=stream)
     if dz_col is None:
-        dz_col = MX(2 * F, R, E4M3, False, dev)
+        dz_col = MX(2 * F, R, E4M3, False, dev, stream=stream)
     _check(load().mx_grouped_gemm_dswiglu_bwd(_s(dy_row), _s(w2t_row), _ptr(z), G, _ptr(offsets), _s(dz_row),
                                               _s(dz_col), _stream(stream)))
     return dz_row, dz_col
@@ -463,7 +479,7 @@ def mx_grouped_gemm_dswiglu_bwd(dy_row, w2t_row, z, G, offsets, dz_row=None, dz_
 def mx_grouped_gemm_wgrad(a_col, b_col, G, offsets, out=None, stream=None):
     import torch
     if out is None:
-        out = torch.empty((G, a_col.rows, b_col.rows), dtype=torch.bfloat16, device=a_col.data.device)
+        out = _empty((G, a_col.rows, b_col.rows), torch.bfloat16, a_col.data.device, stream)
     _check(load().mx_grouped_gemm_wgrad(_s(a_col), _s(b_col), G, _ptr(offsets), _ptr(out), _stream(stream)))
     return out
 
@@ -482,11 +498,11 @@ def mx_grouped_gemm_wgrad_workspace_bytes(N, K, R, G):
     return int(load().mx_grouped_gemm_wgrad_workspace_bytes(N, K, R, G))
 
 
-def _wgrad_ws(a_col, b_col, G, workspace):
+def _wgrad_ws(a_col, b_col, G, workspace, stream):
     import torch
     if workspace is None:
         n = mx_grouped_gemm_wgrad_workspace_bytes(a_col.rows, b_col.rows, a_col.cols, G)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=a_col.data.device)
+        workspace = _empty(max(n, 16), torch.uint8, a_col.data.device, stream)
     return workspace
 
 
@@ -495,8 +511,8 @@ def mx_grouped_gemm_wgrad_ws(a_col, b_col, G, offsets, out=None, workspace=None,
     CTAs (workspace from mx_grouped_gemm_wgrad_workspace_bytes)."""
     import torch
     if out is None:
-        out = torch.empty((G, a_col.rows, b_col.rows), dtype=torch.bfloat16, device=a_col.data.device)
-    ws = _wgrad_ws(a_col, b_col, G, workspace)
+        out = _empty((G, a_col.rows, b_col.rows), torch.bfloat16, a_col.data.device, stream)
+    ws = _wgrad_ws(a_col, b_col, G, workspace, stream)
     _check(load().mx_grouped_gemm_wgrad_ws(_s(a_col), _s(b_col), G, _ptr(offsets), _ptr(out), _ptr(ws), ws.numel(),
                                            _stream(stream)))
     return out
@@ -505,7 +521,7 @@ def mx_grouped_gemm_wgrad_ws(a_col, b_col, G, offsets, out=None, workspace=None,
 def mx_grouped_gemm_wgrad_f32_ws(a_col, b_col, G, offsets, grad, accumulate=False, workspace=None, stream=None):
     import torch
     assert grad.dtype == torch.float32 and grad.is_contiguous()
-    ws = _wgrad_ws(a_col, b_col, G, workspace)
+    ws = _wgrad_ws(a_col, b_col, G, workspace, stream)
     _check(load().mx_grouped_gemm_wgrad_f32_ws(_s(a_col), _s(b_col), G, _ptr(offsets), _ptr(grad),
                                                1 if accumulate else 0, _ptr(ws), ws.numel(), _stream(stream)))
     return grad
@@ -514,7 +530,7 @@ def mx_grouped_gemm_wgrad_f32_ws(a_col, b_col, G, offsets, grad, accumulate=Fals
 def mx_gemm_bias(a, b, bias=None, out=None, ld_out=None, stream=None):
     import torch
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
+        out = _empty((a.rows, b.rows), torch.bfloat16, a.data.device, stream)
     ld = ld_out if ld_out is not None else out.stride(0)
     _check(load().mx_gemm_bias(_s(a), _s(b), _ptr(bias), _ptr(out), ld, _stream(stream)))
     return out
@@ -526,11 +542,11 @@ def mx_gemm_gelu_fwd(x_row, w1_row, b1=None, pre=None, act_row=None, act_col=Non
     M, H = x_row.rows, w1_row.rows
     dev = x_row.data.device
     if pre is None:
-        pre = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        pre = _empty((M, H), torch.bfloat16, dev, stream)
     if act_row is None:
-        act_row = MX(M, H, fmt, hadamard, dev)
+        act_row = MX(M, H, fmt, hadamard, dev, stream=stream)
     if act_col is None:
-        act_col = MX(H, M, fmt, hadamard, dev)
+        act_col = MX(H, M, fmt, hadamard, dev, stream=stream)
     _check(load().mx_gemm_gelu_fwd(_s(x_row), _s(w1_row), _ptr(b1), _ptr(pre), _s(act_row), _s(act_col),
                                    _stream(stream)))
     return pre, act_row, act_col
@@ -546,13 +562,13 @@ def mx_gemm_dgelu_bwd(dy_row, w2t_row, pre, dpre_row=None, dpre_col=None, db1=No
     M, H = dy_row.rows, w2t_row.rows
     dev = dy_row.data.device
     if dpre_row is None:
-        dpre_row = MX(M, H, fmt, hadamard, dev)
+        dpre_row = MX(M, H, fmt, hadamard, dev, stream=stream)
     if dpre_col is None:
-        dpre_col = MX(H, M, fmt, hadamard, dev)
+        dpre_col = MX(H, M, fmt, hadamard, dev, stream=stream)
     if db1 is None:
-        db1 = torch.empty(H, dtype=torch.float32, device=dev)
+        db1 = _empty(H, torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(max(mx_gemm_dgelu_workspace_bytes(M, H), 16), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(mx_gemm_dgelu_workspace_bytes(M, H), 16), torch.uint8, dev, stream)
     _check(load().mx_gemm_dgelu_bwd(_s(dy_row), _s(w2t_row), _ptr(pre), _s(dpre_row), _s(dpre_col), _ptr(db1),
                                     _ptr(workspace), workspace.numel(), _stream(stream)))
     return dpre_row, dpre_col, db1
@@ -573,7 +589,7 @@ def mx_ragged_gemm(a, w, offsets, layout=W_NK, out=None, stream=None):
     G, N = w.shape[0], w.shape[1 if layout == W_NK else 2]
     assert w.shape[2 if layout == W_NK else 1] == K and (offsets is None or offsets.numel() == G)
     if out is None:
-        out = torch.empty((R, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty((R, N), torch.bfloat16, a.device, stream)
     assert out.shape == (R, N) and out.dtype == torch.bfloat16 and out.stride(1) == 1
     _check(load().mx_ragged_gemm(a.data_ptr(), R, K, a.stride(0), w.data_ptr(), N, G, layout, _ptr(offsets),
                                  out.data_ptr(), out.stride(0), _stream(stream)))
@@ -584,7 +600,7 @@ def mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G):
     return int(load().mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G))
 
 
-def _ragged_wgrad_args(dy, x, G, offsets, workspace):
+def _ragged_wgrad_args(dy, x, G, offsets, workspace, stream):
     import torch
     assert dy.dtype == torch.bfloat16 and x.dtype == torch.bfloat16 and dy.shape[0] == x.shape[0]
     assert dy.stride(1) == 1 and x.stride(1) == 1
@@ -593,7 +609,7 @@ def _ragged_wgrad_args(dy, x, G, offsets, workspace):
     K = x.shape[1]
     if workspace is None:
         n = mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
+        workspace = _empty(n, torch.uint8, dy.device, stream) if n else None
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return R, N, K, workspace, nbytes
 
@@ -601,9 +617,9 @@ def _ragged_wgrad_args(dy, x, G, offsets, workspace):
 def mx_ragged_gemm_wgrad(dy, x, G, offsets, out=None, workspace=None, stream=None):
     """Weight gradients [G, N, K] = dy_g^T x_g of ragged segments, BF16."""
     import torch
-    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace)
+    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace, stream)
     if out is None:
-        out = torch.empty((G, N, K), dtype=torch.bfloat16, device=dy.device)
+        out = _empty((G, N, K), torch.bfloat16, dy.device, stream)
     assert out.shape == (G, N, K) and out.dtype == torch.bfloat16 and out.is_contiguous()
     _check(load().mx_ragged_gemm_wgrad(dy.data_ptr(), N, dy.stride(0), x.data_ptr(), K, x.stride(0), R, G,
                                        _ptr(offsets), out.data_ptr(), _ptr(workspace), nbytes, _stream(stream)))
@@ -614,7 +630,7 @@ def mx_ragged_gemm_wgrad_f32(dy, x, G, offsets, grad, accumulate=False, workspac
     """The weight gradients into the caller's fp32 buffer grad [G, N, K]:
     stored (accumulate=False) or added to what it holds."""
     import torch
-    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace)
+    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace, stream)
     assert grad.shape == (G, N, K) and grad.dtype == torch.float32 and grad.is_contiguous()
     _check(load().mx_ragged_gemm_wgrad_f32(dy.data_ptr(), N, dy.stride(0), x.data_ptr(), K, x.stride(0), R, G,
                                            _ptr(offsets), grad.data_ptr(), 1 if accumulate else 0, _ptr(workspace),
@@ -632,7 +648,7 @@ def mx_linear_fwd(x, w, bias=None, act=ACT_NONE, residual=None, out=None, ckpt=N
     assert w.shape == (N, K)
     assert bias is None or (bias.dtype == torch.bfloat16 and bias.shape == (N,) and bias.is_contiguous())
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, N), torch.bfloat16, x.device, stream)
     assert out.shape == (M, N) and out.dtype == torch.bfloat16 and out.stride(1) == 1
     ld_res = 0
     if residual is not None:
@@ -650,10 +666,10 @@ def mx_act_ckpt_fwd(z, act, h=None, ckpt=None, stream=None):
     assert z.dtype == torch.bfloat16 and z.stride(1) == 1
     R, C = z.shape
     if h is None:
-        h = torch.empty((R, C // 2 if act == ACT_SWIGLU else C), dtype=torch.bfloat16, device=z.device)
+        h = _empty((R, C // 2 if act == ACT_SWIGLU else C), torch.bfloat16, z.device, stream)
     assert h.shape == (R, C // 2 if act == ACT_SWIGLU else C) and h.dtype == torch.bfloat16 and h.stride(1) == 1
     if ckpt is None:
-        ckpt = MX(R, C, E4M3, False, z.device)
+        ckpt = MX(R, C, E4M3, False, z.device, stream=stream)
     _check(load().mx_act_ckpt_fwd(z.data_ptr(), R, C, z.stride(0), act, h.data_ptr(), h.stride(0), _s(ckpt),
                                   _stream(stream)))
     return h, ckpt
@@ -675,22 +691,22 @@ def mx_act_ckpt_bwd(ckpt, act, dh, dz=None, recompute=False, h=None, colsum=Fals
     dev, bf16 = dh.device, torch.bfloat16
     assert dh.dtype == bf16 and dh.shape == (R, H) and dh.stride(1) == 1
     if dz is None:
-        dz = torch.empty((R, C), dtype=bf16, device=dev)
+        dz = _empty((R, C), bf16, dev, stream)
     else:
         assert dz.shape == (R, C) and dz.dtype == bf16 and dz.stride(1) == 1
     if h is not None:
         assert h.shape == (R, H) and h.dtype == bf16 and h.stride(1) == 1
     elif recompute:
-        h = torch.empty((R, H), dtype=bf16, device=dev)
+        h = _empty((R, H), bf16, dev, stream)
     if db is not None:
         assert db.shape == (C,) and db.dtype == torch.float32 and db.is_contiguous()
     elif colsum:
-        db = torch.empty(C, dtype=torch.float32, device=dev)
+        db = _empty(C, torch.float32, dev, stream)
     nbytes = 0
     if db is not None:
         if workspace is None:
             n = mx_act_ckpt_workspace_bytes(R, C)
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+            workspace = _empty(n, torch.uint8, dev, stream) if n else None
         if workspace is not None:
             nbytes = workspace.numel() * workspace.element_size()
     _check(load().mx_act_ckpt_bwd(_s(ckpt), act, dh.data_ptr(), dh.stride(0), dz.data_ptr(), dz.stride(0), _ptr(h),
