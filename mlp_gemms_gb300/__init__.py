@@ -1,11 +1,11 @@
 """Thin Python binding of the GB300 MX training-MLP library (``include/mx.h``).
 
-Argument marshalling only: every function here checks nothing the C layer
-does not, computes nothing, and calls exactly one C-ABI entry point of the
-same name (``mx_mlp_fwd_bwd`` launches the whole step).  PyTorch supplies
-device memory (outputs and workspaces are ``torch.empty`` allocations when the
-caller passes none, from the memory of the stream that the call launches on)
-and the current CUDA stream.
+Argument marshalling only: every function here computes nothing, checks what
+the C layer cannot see of a tensor (types, layouts, devices), and calls exactly
+one C-ABI entry point of the same name (``mx_mlp_fwd_bwd`` launches the whole
+step).  PyTorch supplies device memory (outputs and workspaces are
+``torch.empty`` allocations when the caller passes none, from the memory of the
+stream that the call launches on) and the current CUDA stream.
 
 There is no fallback: if the shared library is missing or fails to load,
 ``load()`` raises and nothing runs.
@@ -578,19 +578,29 @@ def mx_gemm_dgelu_bwd(dy_row, w2t_row, pre, dpre_row=None, dpre_col=None, db1=No
 # BF16 layers: ragged products, linear layer, 8-bit activation checkpoints
 # --------------------------------------------------------------------------
 
+def _one_gpu(first, *others):
+    """Refuse host tensors and tensors of several GPUs: the library takes bare
+    pointers."""
+    dev = first.get_device()
+    assert dev >= 0, "a tensor is not on a GPU"
+    for t in others:
+        assert t is None or t.get_device() == dev, "the tensors are not on one GPU"
+
+
 def mx_ragged_gemm(a, w, offsets, layout=W_NK, out=None, stream=None):
     """out[r] = a[r] w[g]^T (W_NK, w [G, N, K]) or a[r] w[g] (W_KN, w [G, K, N])
     for the rows r of expert g's segment, of any length; BF16.  Rows past
     the last segment are not written."""
     import torch
     assert a.dtype == torch.bfloat16 and w.dtype == torch.bfloat16 and w.is_contiguous() and w.dim() == 3
-    assert a.stride(1) == 1 and (offsets is None or offsets.dtype == torch.int32)
+    assert a.stride(1) == 1 and (offsets is None or (offsets.dtype == torch.int32 and offsets.is_contiguous()))
     R, K = a.shape
     G, N = w.shape[0], w.shape[1 if layout == W_NK else 2]
     assert w.shape[2 if layout == W_NK else 1] == K and (offsets is None or offsets.numel() == G)
     if out is None:
         out = _empty((R, N), torch.bfloat16, a.device, stream)
     assert out.shape == (R, N) and out.dtype == torch.bfloat16 and out.stride(1) == 1
+    _one_gpu(a, w, offsets, out)
     _check(load().mx_ragged_gemm(a.data_ptr(), R, K, a.stride(0), w.data_ptr(), N, G, layout, _ptr(offsets),
                                  out.data_ptr(), out.stride(0), _stream(stream)))
     return out
@@ -600,11 +610,13 @@ def mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G):
     return int(load().mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G))
 
 
-def _ragged_wgrad_args(dy, x, G, offsets, workspace, stream):
+def _ragged_wgrad_args(dy, x, G, offsets, grad, workspace, stream):
     import torch
     assert dy.dtype == torch.bfloat16 and x.dtype == torch.bfloat16 and dy.shape[0] == x.shape[0]
     assert dy.stride(1) == 1 and x.stride(1) == 1
-    assert offsets is None or (offsets.dtype == torch.int32 and offsets.numel() == G)
+    assert offsets is None or (offsets.dtype == torch.int32 and offsets.numel() == G and offsets.is_contiguous())
+    assert workspace is None or workspace.is_contiguous()
+    _one_gpu(dy, x, offsets, grad, workspace)
     R, N = dy.shape
     K = x.shape[1]
     if workspace is None:
@@ -617,7 +629,7 @@ def _ragged_wgrad_args(dy, x, G, offsets, workspace, stream):
 def mx_ragged_gemm_wgrad(dy, x, G, offsets, out=None, workspace=None, stream=None):
     """Weight gradients [G, N, K] = dy_g^T x_g of ragged segments, BF16."""
     import torch
-    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace, stream)
+    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, out, workspace, stream)
     if out is None:
         out = _empty((G, N, K), torch.bfloat16, dy.device, stream)
     assert out.shape == (G, N, K) and out.dtype == torch.bfloat16 and out.is_contiguous()
@@ -630,7 +642,7 @@ def mx_ragged_gemm_wgrad_f32(dy, x, G, offsets, grad, accumulate=False, workspac
     """The weight gradients into the caller's fp32 buffer grad [G, N, K]:
     stored (accumulate=False) or added to what it holds."""
     import torch
-    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, workspace, stream)
+    R, N, K, workspace, nbytes = _ragged_wgrad_args(dy, x, G, offsets, grad, workspace, stream)
     assert grad.shape == (G, N, K) and grad.dtype == torch.float32 and grad.is_contiguous()
     _check(load().mx_ragged_gemm_wgrad_f32(dy.data_ptr(), N, dy.stride(0), x.data_ptr(), K, x.stride(0), R, G,
                                            _ptr(offsets), grad.data_ptr(), 1 if accumulate else 0, _ptr(workspace),
@@ -654,6 +666,7 @@ def mx_linear_fwd(x, w, bias=None, act=ACT_NONE, residual=None, out=None, ckpt=N
     if residual is not None:
         assert residual.shape == (M, N) and residual.dtype == torch.bfloat16 and residual.stride(1) == 1
         ld_res = residual.stride(0)
+    _one_gpu(x, w, bias, residual, out)
     _check(load().mx_linear_fwd(x.data_ptr(), M, K, x.stride(0), w.data_ptr(), N, _ptr(bias), act, _ptr(residual),
                                 ld_res, out.data_ptr(), out.stride(0), _s(ckpt), _stream(stream)))
     return out
@@ -670,6 +683,7 @@ def mx_act_ckpt_fwd(z, act, h=None, ckpt=None, stream=None):
     assert h.shape == (R, C // 2 if act == ACT_SWIGLU else C) and h.dtype == torch.bfloat16 and h.stride(1) == 1
     if ckpt is None:
         ckpt = MX(R, C, E4M3, False, z.device, stream=stream)
+    _one_gpu(z, h)
     _check(load().mx_act_ckpt_fwd(z.data_ptr(), R, C, z.stride(0), act, h.data_ptr(), h.stride(0), _s(ckpt),
                                   _stream(stream)))
     return h, ckpt
@@ -708,7 +722,9 @@ def mx_act_ckpt_bwd(ckpt, act, dh, dz=None, recompute=False, h=None, colsum=Fals
             n = mx_act_ckpt_workspace_bytes(R, C)
             workspace = _empty(n, torch.uint8, dev, stream) if n else None
         if workspace is not None:
+            assert workspace.is_contiguous()
             nbytes = workspace.numel() * workspace.element_size()
+    _one_gpu(dh, dz, h, db, workspace)
     _check(load().mx_act_ckpt_bwd(_s(ckpt), act, dh.data_ptr(), dh.stride(0), dz.data_ptr(), dz.stride(0), _ptr(h),
                                   0 if h is None else h.stride(0), _ptr(db), _ptr(workspace), nbytes,
                                   _stream(stream)))
