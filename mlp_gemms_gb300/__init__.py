@@ -587,6 +587,16 @@ def _one_gpu(first, *others):
         assert t is None or t.get_device() == dev, "the tensors are not on one GPU"
 
 
+def _buffers(t):
+    """An MX tensor's (payload, scales), dense and as large as its shape needs."""
+    data, scale = t.data, t.scale
+    assert data.is_contiguous() and data.numel() * data.element_size() >= payload_bytes(t.rows, t.cols, t.fmt), \
+        "the payload is strided or too small"
+    assert scale.is_contiguous() and scale.numel() * scale.element_size() >= scale_bytes(t.rows, t.cols), \
+        "the scales are strided or too small"
+    return data, scale
+
+
 def mx_ragged_gemm(a, w, offsets, layout=W_NK, out=None, stream=None):
     """out[r] = a[r] w[g]^T (W_NK, w [G, N, K]) or a[r] w[g] (W_KN, w [G, K, N])
     for the rows r of expert g's segment, of any length; BF16.  Rows past
@@ -666,7 +676,7 @@ def mx_linear_fwd(x, w, bias=None, act=ACT_NONE, residual=None, out=None, ckpt=N
     if residual is not None:
         assert residual.shape == (M, N) and residual.dtype == torch.bfloat16 and residual.stride(1) == 1
         ld_res = residual.stride(0)
-    _one_gpu(x, w, bias, residual, out)
+    _one_gpu(x, w, bias, residual, out, *(_buffers(ckpt) if ckpt is not None else ()))
     _check(load().mx_linear_fwd(x.data_ptr(), M, K, x.stride(0), w.data_ptr(), N, _ptr(bias), act, _ptr(residual),
                                 ld_res, out.data_ptr(), out.stride(0), _s(ckpt), _stream(stream)))
     return out
@@ -683,7 +693,7 @@ def mx_act_ckpt_fwd(z, act, h=None, ckpt=None, stream=None):
     assert h.shape == (R, C // 2 if act == ACT_SWIGLU else C) and h.dtype == torch.bfloat16 and h.stride(1) == 1
     if ckpt is None:
         ckpt = MX(R, C, E4M3, False, z.device, stream=stream)
-    _one_gpu(z, h)
+    _one_gpu(z, h, *_buffers(ckpt))
     _check(load().mx_act_ckpt_fwd(z.data_ptr(), R, C, z.stride(0), act, h.data_ptr(), h.stride(0), _s(ckpt),
                                   _stream(stream)))
     return h, ckpt
@@ -724,7 +734,7 @@ def mx_act_ckpt_bwd(ckpt, act, dh, dz=None, recompute=False, h=None, colsum=Fals
         if workspace is not None:
             assert workspace.is_contiguous()
             nbytes = workspace.numel() * workspace.element_size()
-    _one_gpu(dh, dz, h, db, workspace)
+    _one_gpu(dh, dz, h, db, workspace, *_buffers(ckpt))
     _check(load().mx_act_ckpt_bwd(_s(ckpt), act, dh.data_ptr(), dh.stride(0), dz.data_ptr(), dz.stride(0), _ptr(h),
                                   0 if h is None else h.stride(0), _ptr(db), _ptr(workspace), nbytes,
                                   _stream(stream)))

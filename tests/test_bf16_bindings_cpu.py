@@ -129,3 +129,31 @@ def test_everything_on_the_host(mx, call):
                              grad=_f(2, 64, 64, where=-1)))
     with pytest.raises(AssertionError):
         call(mx, **t[call.__name__])
+
+
+BAD_CKPT = {
+    "short payload": lambda d, s: (d[:-1], s),
+    "strided payload": lambda d, s: (torch.zeros((d.shape[0], 2 * d.shape[1]), dtype=torch.uint8)[:, ::2], s),
+    "short scales": lambda d, s: (d, s[:-1]),
+    "strided scales": lambda d, s: (d, torch.zeros((s.numel(), 2), dtype=torch.uint8)[:, 0]),
+    "payload on the host": lambda d, s: (At(d, -1), s),
+    "scales on another gpu": lambda d, s: (d, At(s, 1)),
+}
+
+
+@pytest.mark.parametrize("bad", list(BAD_CKPT))
+@pytest.mark.parametrize("call,rows", [(_linear, 40), (_save, 40), (_bwd, 600)], ids=["linear", "save", "bwd"])
+def test_checkpoint_buffers(mx, call, rows, bad):
+    """A checkpoint in the caller's own buffers: dense, as large as its shape
+    needs, on the call's GPU (the kernels write and read all of it)."""
+    data, scale = torch.zeros((rows, 64), dtype=torch.uint8), torch.zeros(mx.scale_bytes(rows, 64), dtype=torch.uint8)
+    data, scale = (t if isinstance(t, At) else At(t) for t in BAD_CKPT[bad](data, scale))
+    with pytest.raises(AssertionError):
+        call(mx, ckpt=mx.MX(rows, 64, data=data, scale=scale))
+
+
+def test_checkpoint_buffers_of_another_type(mx):
+    """Bytes are what counts: a payload held as E4M3 values passes."""
+    ck = _ckpt(mx, 40, 64)
+    ck.data = At(ck.data.t.view(torch.float8_e4m3fn))
+    _linear(mx, ckpt=ck)
