@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(32 * SK_WARPS, MT * NT == 1 ? 3 : 2) skinny_ke
       uint4 qw[SK_BATCH][2 * MT], qx[SK_BATCH][NT];
 #pragma unroll
       for (int b = 0; b < SK_BATCH; b++) {
-        const int k = (c0 + b * SK_WARPS) * 32;
-        const bool kin = k + 8 * t4 < p.K;
+        const uint32_t k = (uint32_t)(c0 + b * SK_WARPS) * 32;  // ends up to 800 columns past K: beyond 2^31
+        const bool kin = k + 8 * t4 < (uint32_t)p.K;
 #pragma unroll
         for (int i = 0; i < 2 * MT; i++) qw[b][i] = kin && win[i] ? ld_stream(w[i] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
