@@ -78,3 +78,19 @@ def test_results_of_another_stream(cuda_lib, name):
         assert all(torch.equal(g, w) for g, w in zip(got, want))
         del got
     assert mx.mx_get_device_status() == "MX_OK"
+
+
+def test_two_streams_at_once(cuda_lib):
+    """The same calls on two streams side by side give the bits that they give
+    alone (weight gradients in parts, checkpoints with column sums)."""
+    mx = cuda_lib
+    calls = [call for _, call in _calls(mx).values()]
+    want = [_flat(call(None)) for call in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[_flat(call(s)) for call in calls] for _ in range(6) for s in streams]
+    torch.cuda.synchronize()
+    assert mx.mx_get_device_status() == "MX_OK"
+    for outs in got:
+        for g, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
