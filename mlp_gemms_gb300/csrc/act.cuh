@@ -44,7 +44,8 @@ __device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
 
 // 1 / (1 + 2^x) of both lanes: the hardware's 2^x and reciprocal (relative
 // error a few 2^-23, against the 2^-9 of the BF16 the results are rounded
-// to).  2^x overflows to +Inf past 128: 0.
+// to; a result below 2^-126, from x = 126 on, is 0).  2^x overflows to +Inf past
+// 128: 0.
 __device__ __forceinline__ uint64_t inv_1p_exp2(uint64_t x) {
   float a, b;
   unpack2(x, &a, &b);

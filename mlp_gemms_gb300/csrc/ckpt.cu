@@ -61,9 +61,9 @@ __device__ __forceinline__ void read8(const uint2& w, uint32_t b, float (&v)[8])
 // Rows a backward warp has in flight at a time (its loads are issued before the
 // first of them is used) and blocks of an SM.  What fits the registers: SWIGLU
 // with h takes three rows (us with three and four: [65536, 1536] 82, 83.5; with
-// db 85, 91), without h four (70, 66); the others six (with four: [16384, 8192]
-// GELU with db 117, 124; [333, 8192] 6.3, 6.9) or, with neither h nor db, four
-// in each of three blocks (107, two blocks 120).
+// db 86, 91), without h four (70, 67); the others six (with four: [16384, 8192]
+// GELU with db 118, 124; [333, 8192] 6.4, 6.9) or, with neither h nor db, four in
+// each of three blocks (108, two blocks 120).
 constexpr int bwd_rows(bool glu, bool h, bool db) { return glu ? (h ? 3 : 4) : h || db ? 6 : 4; }
 constexpr int bwd_blocks(bool glu, bool h, bool db) { return glu || h || db ? 2 : 3; }
 
@@ -133,10 +133,11 @@ __device__ __forceinline__ void save32(const CkptParams& p, int64_t r, int c, fl
 // the up half's), so the block's amax needs no exchange.  [65536, 1536] SWIGLU:
 // 61.2 us = 6.6 TB/s, 99 % of the copy rate (with 16-byte accesses, which
 // touch each sector twice, 68.5; with 8 columns a lane and the amax by
-// shuffles, 72.8: issue slots).  [16384, 8192]: GELU 104 us = 97 %, with three
-// blocks an SM (two 110, four spill: 142).  Eight to twelve waves of blocks, each
-// with a few items a thread (two waves 63.3 and 110, as many blocks as items 62.8
-// and 104).
+// shuffles, 72.8: issue slots).  [16384, 8192]: GELU 104 to 105 us = 96 %, with
+// three blocks an SM, which keep two to four registers of SiLU and GELU in local
+// memory (two blocks 110; four spill in earnest: 142).  Eight to twelve waves of
+// blocks, each with a few items a thread (two waves 63.3 and 110, as many blocks
+// as items 62.8 and 104).
 template <int ACT, bool WIDE>
 __global__ void __launch_bounds__(256, ACT == MX_ACT_SWIGLU ? 2 : 3) ckpt_fwd_kernel(const CkptParams p, uint32_t per) {
   constexpr bool GLU = ACT == MX_ACT_SWIGLU;
@@ -190,7 +191,7 @@ static int64_t ckpt_row_blocks(int64_t R, int64_t C, int per_sm) {
 
 // Column sums of up to CLUSTER_ROWS rows: a cluster of blocks holds all rows of
 // its columns and adds its blocks' sums through shared memory, with no
-// partials in memory and no second launch (measured on [333, 8192] GELU: 6.3 us
+// partials in memory and no second launch (measured on [333, 8192] GELU: 6.4 us
 // against 7.8, and no workspace to allocate).
 // More rows want more row blocks than a cluster has.
 constexpr int CLUSTER = 8, CLUSTER_ROWS = 512;

@@ -27,14 +27,16 @@
 // and store whole 128-byte lines.
 //
 // What bounds it (us at 8192 tokens x 8 choices, 128 experts, skewed, K = 2048,
-// N = 1536; floor 209 at the measured BF16 rate, 183 at the copy rate): forward
-// 275, input gradient 273, weight gradient 288, back to back from a cold chip;
-// 308 / 307 / 328 over seconds, when the power limit holds the clock down.
-// With one expert for all rows it takes 213 (98 % of the rate), with 64 239, with
+// N = 1536): forward 306, input gradient 307, weight gradient 328 over seconds,
+// as a training run sees it, when the power limit holds the clock down (floor
+// 236 at the BF16 rate measured over seconds); 276, 274 and 288 to 291 in short
+// bursts from a cold chip (floor 209 at the burst rate, 183 at the copy rate).
+// In such bursts one expert for all rows takes 213 (98 % of the rate), 64 239,
 // 128 even ones 266: beside the MMAs the weights come through HBM, 228 us
 // without MMAs.
-// Dense [16384, 2048] x [8192, 2048], GELU and checkpoint: 296 us = 1.86
-// PFLOP/s.  Two pairs sharing the token operand by multicast (clusters of four:
+// Dense [16384, 2048] x [8192, 2048], GELU and checkpoint: 350 us = 1.57
+// PFLOP/s over seconds, 295 = 1.87 in bursts.  The sweeps quoted below are
+// bursts.  Two pairs sharing the token operand by multicast (clusters of four:
 // 144 of 152 SMs) moved a quarter fewer bytes and were 0 to 3 % slower; an L2
 // prefetch of the next tile's operands was 6 to 30 % slower.
 //
@@ -1169,8 +1171,9 @@ ragged_split_kernel(const __grid_constant__ RaggedMaps tmP, const __grid_constan
 // The tile width for `rows` output rows in `segments` pieces under n_f column
 // tiles: the one with the least waves x (width + 64).  A tile costs its width
 // in MMA time and about 64 columns' worth besides; narrow tiles pay where wide
-// ones leave pairs idle (777 rows x 2048 columns: 32 tiles of 256 on 76 pairs,
-// 31 us; 72 of 96, 22 us).  Past four waves the width is 256: fewer bytes
+// ones leave pairs idle (777 rows, 5120 -> 2048, a pair to each tile: 32 tiles of
+// 256 on 76 pairs, 31 us; 72 of 96, 22 us; that shape's tiles are shared by now,
+// tile_shape below).  Past four waves the width is 256: fewer bytes
 // to load per product.
 static int tile_width(int64_t rows, int64_t segments, int64_t n_f, int pairs) {
   int best = 256;
@@ -1221,7 +1224,7 @@ static cudaError_t resident_clusters(int splits, int* n) {
 // w + 450 (how long its loads are on their way), joining 4000 + 15 w splits,
 // and all clusters must run at once (36, 23 and 15 of them).  Whole against
 // split, us: 16 rows, 16384 -> 4096, 54.1, 29.5 (three pairs a tile); 128 rows,
-// 5120 -> 2048, 19.2, 12.8; 777 rows, 21.2, 19.7; 600 rows, 8192 -> 1024, 29.1,
+// 5120 -> 2048, 19.2, 12.8; 777 rows, 21.2, 19.7 (20.0 to 20.6 on other boards); 600 rows, 8192 -> 1024, 29.1,
 // 17.6; 53 rows, 2944 -> 128, 10.9, 7.7; 64 rows, 512 -> 256, 4.7, 6.0.
 struct TileShape { int width, splits; };
 static cudaError_t tile_shape(int64_t rows, int64_t segments, int64_t n_f, int64_t nk, int pairs, TileShape* best) {

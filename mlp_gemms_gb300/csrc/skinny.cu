@@ -14,8 +14,9 @@
 // row, 4096 -> 16384, 23.5 us (5.7 TB/s) against 25.7; 2048 -> 2048, 4.5 against
 // 8.3.  Up to 32 rows meet a weight at once, eight to an MMA (16 rows, 2048 ->
 // 2048: 4.9 us).  The rows staged in shared memory by bulk copies instead: 11.9
-// and 23.7 us, but 28 for 8 rows, 4096 -> 16384 (24.5 here), where the tokens'
-// loads wait behind the barrier.
+// and 23.7 us, and 28 for 8 rows, 4096 -> 16384, where the tokens' loads wait
+// behind the barrier (here 27.3 to 27.9; with the checkpoint's 32 features a CTA
+// 24.5).
 #include "act.cuh"
 #include "mx_internal.h"
 
@@ -96,10 +97,10 @@ __device__ __forceinline__ bool find_expert(const RaggedParams& p, int want, int
 }
 
 // Three CTAs an SM with 4 chunks in flight (two with 32 features or more
-// tokens): measured
-// on one token of 4096 -> 16384 against 2 x 8, 4 x 4, 4 x 2 and 5 x 2 chunks
-// 23.9 us against 24.0, 29.0, 24.4, 35.1, and on 8 experts' rows 12.8 against
-// 14.0, 16.5, 13.9, 17.8 (more CTAs spill).
+// tokens): measured on one token of 4096 -> 16384 against 2 x 8, 4 x 4, 4 x 2 and
+// 5 x 2 chunks 23.9 us against 24.0, 29.0, 24.4, 35.1, and on 8 experts' rows
+// 12.8 against 14.0, 16.5, 13.9, 17.8 (more CTAs spill; measured with an earlier
+// search for the expert, which cost the latter 1.1 us more).
 template <int MT, int NT, bool EPI>
 __global__ void __launch_bounds__(32 * SK_WARPS, MT * NT == 1 ? 3 : 2) skinny_kernel(const RaggedParams p) {
   constexpr int ROWS = 16 * MT, TOK = 8 * NT, SK_BATCH = sk_batch(MT, NT);
