@@ -590,10 +590,9 @@ def _one_gpu(first, *others):
 def _buffers(t):
     """An MX tensor's (payload, scales), dense and as large as its shape needs."""
     data, scale = t.data, t.scale
-    assert data.is_contiguous() and data.numel() * data.element_size() >= payload_bytes(t.rows, t.cols, t.fmt), \
+    assert data.is_contiguous() and data.nbytes >= payload_bytes(t.rows, t.cols, t.fmt), \
         "the payload is strided or too small"
-    assert scale.is_contiguous() and scale.numel() * scale.element_size() >= scale_bytes(t.rows, t.cols), \
-        "the scales are strided or too small"
+    assert scale.is_contiguous() and scale.nbytes >= scale_bytes(t.rows, t.cols), "the scales are strided or too small"
     return data, scale
 
 
@@ -693,7 +692,9 @@ def mx_act_ckpt_fwd(z, act, h=None, ckpt=None, stream=None):
     assert h.shape == (R, C // 2 if act == ACT_SWIGLU else C) and h.dtype == torch.bfloat16 and h.stride(1) == 1
     if ckpt is None:
         ckpt = MX(R, C, E4M3, False, z.device, stream=stream)
-    _one_gpu(z, h, *_buffers(ckpt))
+        _one_gpu(z, h)
+    else:
+        _one_gpu(z, h, *_buffers(ckpt))
     _check(load().mx_act_ckpt_fwd(z.data_ptr(), R, C, z.stride(0), act, h.data_ptr(), h.stride(0), _s(ckpt),
                                   _stream(stream)))
     return h, ckpt
