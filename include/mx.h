@@ -792,6 +792,53 @@ MX_API mx_status_t mx_act_ckpt_bwd(const mx_tensor_t *ckpt, int32_t act, const v
                                    void *workspace, size_t workspace_bytes, mx_stream_t stream);
 
 /*
+ * Layer norm of the tokens in front of a layer, with the residual added in the
+ * same pass.
+ * mx_layernorm_fwd -- s = x + res (rounded to x's type; s = x without res),
+ *   y = (s - mean) * rstd * weight + bias, mean and rstd = 1 / sqrt(var + eps)
+ *   over each row of s (var without Bessel's correction), all in fp32 with one
+ *   rounding to BF16.  rms = 1: mean = 0 (the root-mean-square norm).
+ *   x         device [R, D] of x_type (MX_BF16 or MX_F32), row stride ld_x
+ *   res       [R, D] of x_type, row stride ld_res, or NULL
+ *   sum       out, s, of x_type, row stride ld_sum; needed with res (it may be
+ *             x or res itself, with the same row stride), else not used
+ *   weight    [D] of w_type, or NULL (ones)
+ *   bias      [D] of w_type, or NULL (zeros)
+ *   y_bf16    out, device BF16 [R, D], row stride ld_y; overlaps no input
+ *   mean, rstd  out, device fp32 [R], or NULL; with rms mean is not written
+ * mx_layernorm_bwd -- with g = dy * weight, xh = (s - mean) * rstd:
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dres (rms: without mean(g)),
+ *   dweight = sum over rows of dy * xh, dbias = sum over rows of dy, in a fixed
+ *   order (deterministic).
+ *   dy_bf16   device BF16 [R, D], row stride ld_dy
+ *   x         what the forward pass normalised: x, or with res its sum
+ *   mean, rstd  from the forward pass (rms: mean may be NULL)
+ *   dres      [R, D] of x_type, row stride ld_dres: the gradient that reaches s
+ *             past the norm, added to dx; or NULL
+ *   dx        out, [R, D] of x_type, row stride ld_dx; may be dres itself (same
+ *             row stride), overlaps no other input
+ *   dweight, dbias  out, device fp32 [D], or NULL
+ *   accumulate  0: stored, 1: added to what dweight and dbias hold
+ *   workspace with dweight or dbias: >= mx_layernorm_workspace_bytes(R, D)
+ * D is a multiple of 8 of at most 16384 (else MX_ERR_NOT_SUPPORTED), row strides
+ * are multiples of 8 elements; R has no alignment.  mean and rstd are 4-byte
+ * aligned.  R == 0: nothing is written but dweight and dbias (zeros; with
+ * accumulate unchanged).  A row with an Inf or a NaN gives NaN in that row (and
+ * in dweight and dbias).
+ */
+typedef enum { MX_BF16 = 0, MX_F32 = 1 } mx_type_t;
+MX_API mx_status_t mx_layernorm_fwd(const void *x, int32_t x_type, int64_t R, int64_t D, int64_t ld_x,
+                                    const void *res, int64_t ld_res, void *sum, int64_t ld_sum, const void *weight,
+                                    const void *bias, int32_t w_type, float eps, int32_t rms, void *y_bf16,
+                                    int64_t ld_y, float *mean, float *rstd, mx_stream_t stream);
+MX_API size_t mx_layernorm_workspace_bytes(int64_t R, int64_t D);
+MX_API mx_status_t mx_layernorm_bwd(const void *dy_bf16, int64_t ld_dy, const void *x, int32_t x_type, int64_t R,
+                                    int64_t D, int64_t ld_x, const float *mean, const float *rstd,
+                                    const void *weight, int32_t w_type, int32_t rms, const void *dres,
+                                    int64_t ld_dres, void *dx, int64_t ld_dx, float *dweight, float *dbias,
+                                    int32_t accumulate, void *workspace, size_t workspace_bytes, mx_stream_t stream);
+
+/*
  * mx_get_device_status -- synchronise `stream`, then report and clear the
  * device-side status words: MX_ERR_DEVICE_TIMEOUT if a bounded wait inside
  * a kernel expired (the kernel unwound; its outputs are undefined),

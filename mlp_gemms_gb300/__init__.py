@@ -21,6 +21,7 @@ E4M3, E2M3, E2M1 = 0, 1, 2
 ROWWISE, COLWISE, HADAMARD, COLSUM = 1, 2, 4, 8
 ACT_SWIGLU, ACT_GELU_TANH, ACT_NONE, ACT_SILU, ACT_RELU = 0, 1, 2, 3, 4
 W_NK, W_KN = 0, 1
+BF16, F32 = 0, 1  # types of the layers around the expert MLP (layers.py)
 
 STATUS = {
     0: "MX_OK", 1: "MX_ERR_INVALID_ARG", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGNMENT", 4: "MX_ERR_OFFSETS",
@@ -43,7 +44,8 @@ ABI_SYMBOLS = (
     "mx_grouped_gemm_wgrad_workspace_bytes", "mx_grouped_gemm_wgrad_ws", "mx_grouped_gemm_wgrad_f32_ws",
     "mx_mlp_workspace_layout", "mx_moe_route_rows_pad", "mx_moe_route_index_pad", "mx_grouped_gemm_2sm",
     "mx_ragged_gemm", "mx_ragged_gemm_wgrad_workspace_bytes", "mx_ragged_gemm_wgrad", "mx_ragged_gemm_wgrad_f32",
-    "mx_linear_fwd", "mx_act_ckpt_fwd", "mx_act_ckpt_workspace_bytes", "mx_act_ckpt_bwd",
+    "mx_linear_fwd", "mx_act_ckpt_fwd", "mx_act_ckpt_workspace_bytes", "mx_act_ckpt_bwd", "mx_layernorm_fwd",
+    "mx_layernorm_workspace_bytes", "mx_layernorm_bwd",
 )
 
 
@@ -100,6 +102,7 @@ def load(path=None):
         raise RuntimeError("MX CUDA library not built at %s (run __graft_entry__.build())" % path)
     L = ctypes.CDLL(path)
     vp, i64, i32, u32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
+    f32 = ctypes.c_float
     tp = ctypes.POINTER(MxTensorStruct)
     sig = {
         "mx_abi_version": (ctypes.c_int, []),
@@ -149,6 +152,11 @@ def load(path=None):
         "mx_act_ckpt_fwd": (ctypes.c_int, [vp, i64, i64, i64, i32, vp, i64, tp, vp]),
         "mx_act_ckpt_workspace_bytes": (sz, [i64, i64]),
         "mx_act_ckpt_bwd": (ctypes.c_int, [tp, i32, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp]),
+        "mx_layernorm_fwd": (ctypes.c_int, [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, vp, i32, f32, i32, vp, i64,
+                                            vp, vp, vp]),
+        "mx_layernorm_workspace_bytes": (sz, [i64, i64]),
+        "mx_layernorm_bwd": (ctypes.c_int, [vp, i64, vp, i32, i64, i64, i64, vp, vp, vp, i32, i32, vp, i64, vp, i64,
+                                            vp, vp, i32, vp, sz, vp]),
         "mx_debug_tap": (ctypes.c_int, [vp, i64]),
         "mx_mlp_pipeline_create": (ctypes.c_int, [ctypes.POINTER(MlpArgsStruct), vp, ctypes.POINTER(vp)]),
         "mx_mlp_pipeline_run": (ctypes.c_int, [vp, ctypes.POINTER(HostIOStruct)]),
@@ -858,3 +866,13 @@ def mx_debug_tap(tap=None):
 
 def mx_last_error():
     return load().mx_last_error().decode()
+
+
+def __getattr__(name):
+    """The layers around the expert MLP are part of this namespace and live in
+    layers.py, which loads with the first of them."""
+    if name.startswith("mx_") or name == "NVFP4":
+        from . import layers
+        if hasattr(layers, name):
+            return getattr(layers, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,56 +1,18 @@
 // C ABI of the BF16 layers: host-side validation and launches of the ragged
 // products (ragged.cu) and the 8-bit activation checkpoints (ckpt.cu).
 // Nothing here allocates device memory.
-#include <cstdarg>
-#include <cstdio>
 #include <vector>
 
-#include "mx_internal.h"
+#include "api_checks.h"
+
+using mx::aligned;
+using mx::check_dim;
+using mx::check_matrix;
+using mx::check_ptr;
+using mx::check_workspace;
+using mx::cuda_result;
 
 namespace {
-
-mx_status_t fail(mx_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-mx_status_t fail(mx_status_t st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  return mx::set_error(st, buf);
-}
-
-#define MX_CHECK(cond, st, ...) \
-  do {                          \
-    if (!(cond)) return fail(st, __VA_ARGS__); \
-  } while (0)
-
-mx_status_t cuda_result(cudaError_t e, const char* what) {
-  return e == cudaSuccess ? MX_OK : fail(MX_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-mx_status_t check_ptr(const void* p, const char* name) {
-  MX_CHECK(p != nullptr, MX_ERR_INVALID_ARG, "%s is NULL", name);
-  MX_CHECK(aligned16(p), MX_ERR_ALIGNMENT, "%s must be 16-byte aligned", name);
-  return MX_OK;
-}
-
-// A row-major BF16 matrix of `rows` rows of `cols` elements, row stride ld.
-mx_status_t check_matrix(const void* p, const char* name, int64_t rows, int64_t cols, int64_t ld) {
-  MX_CHECK(ld >= cols && ld % 8 == 0, MX_ERR_ALIGNMENT, "ld of %s = %lld must be >= %lld and a multiple of 8", name,
-           (long long)ld, (long long)cols);
-  MX_CHECK(ld < (1ll << 38), MX_ERR_SHAPE, "ld of %s = %lld is too large", name, (long long)ld);
-  MX_CHECK(rows < (1ll << 31) && rows * ld < (1ll << 46), MX_ERR_SHAPE, "%s is too large (%lld rows of %lld)", name,
-           (long long)rows, (long long)ld);
-  return rows == 0 ? MX_OK : check_ptr(p, name);
-}
-
-mx_status_t check_dim(int64_t v, const char* name, int64_t multiple) {
-  MX_CHECK(v > 0 && v % multiple == 0 && v < (1ll << 31), MX_ERR_SHAPE,
-           "%s = %lld must be a positive multiple of %lld below 2^31", name, (long long)v, (long long)multiple);
-  return MX_OK;
-}
 
 mx_status_t check_segments(const int32_t* offsets, int32_t G, int64_t R, cudaStream_t s) {
   MX_CHECK(G >= 1, MX_ERR_INVALID_ARG, "G = %d; at least one expert is required", G);
@@ -58,7 +20,7 @@ mx_status_t check_segments(const int32_t* offsets, int32_t G, int64_t R, cudaStr
   MX_CHECK(R >= 0 && R < (1ll << 31), MX_ERR_SHAPE, "R = %lld is out of range", (long long)R);
   if (offsets == nullptr && G == 1) return MX_OK;
   MX_CHECK(offsets != nullptr, MX_ERR_INVALID_ARG, "offsets is NULL");
-  MX_CHECK((reinterpret_cast<uintptr_t>(offsets) & 3u) == 0, MX_ERR_ALIGNMENT, "offsets must be 4-byte aligned");
+  MX_CHECK(aligned(offsets, 4), MX_ERR_ALIGNMENT, "offsets must be 4-byte aligned");
   if (!mx::validate_offsets_requested()) return MX_OK;
   std::vector<int32_t> h((size_t)G);
   cudaError_t e = cudaMemcpyAsync(h.data(), offsets, sizeof(int32_t) * (size_t)G, cudaMemcpyDeviceToHost, s);
@@ -173,9 +135,7 @@ mx_status_t wgrad(const void* dy, int64_t N, int64_t ld_dy, const void* x, int64
   if ((st = check_matrix(x, "x", R, K, ld_x)) != MX_OK) return st;
   if ((st = check_weights(grad, "grad", G, N, K)) != MX_OK) return st;
   const size_t need = mx_ragged_gemm_wgrad_workspace_bytes(N, K, R, G);
-  MX_CHECK(need == 0 || (workspace != nullptr && workspace_bytes >= need), MX_ERR_WORKSPACE,
-           "workspace needs %zu bytes, got %zu", need, workspace ? workspace_bytes : 0);
-  MX_CHECK(workspace == nullptr || aligned16(workspace), MX_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != MX_OK) return st;
   int sms;
   if ((st = mx::device_sms(&sms)) != MX_OK) return st;
   if (R == 0) {
@@ -269,9 +229,7 @@ mx_status_t mx_act_ckpt_bwd(const mx_tensor_t* ckpt, int32_t act, const void* dh
   if (h_bf16 && (st = check_matrix(h_bf16, "h", R, H, ld_h)) != MX_OK) return st;
   if (db && (st = check_ptr(db, "db")) != MX_OK) return st;
   const size_t need = db ? mx_act_ckpt_workspace_bytes(R, C) : 0;
-  MX_CHECK(need == 0 || (workspace != nullptr && workspace_bytes >= need), MX_ERR_WORKSPACE,
-           "workspace needs %zu bytes, got %zu", need, workspace ? workspace_bytes : 0);
-  MX_CHECK(workspace == nullptr || aligned16(workspace), MX_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != MX_OK) return st;
   int sms;
   if ((st = mx::device_sms(&sms)) != MX_OK) return st;
   if (R == 0) {

@@ -253,6 +253,38 @@ int64_t ckpt_partials(int64_t R, int64_t C);  // 0: none needed
 cudaError_t launch_ckpt_fwd(const CkptParams& p, cudaStream_t s);
 cudaError_t launch_ckpt_bwd(const CkptParams& p, cudaStream_t s);
 
+// Layer norm (norm.cu).
+struct NormParams {
+  int64_t R, D;
+  int x_f32, w_f32;          // types of x, res, sum, dx; of weight, bias
+  int rms;                   // no mean
+  float eps;
+  const void* x;             // [R, D] (backward: what the forward pass normalised)
+  int64_t ld_x;
+  const void* res;           // added to x, or null; backward: gradient added to dx, or null
+  int64_t ld_res;
+  void* sum;                 // x + res
+  int64_t ld_sum;
+  const void* weight;        // [D] or null
+  const void* bias;
+  uint16_t* y;
+  int64_t ld_y;
+  float* mean;
+  float* rstd;
+  const uint16_t* dy;        // backward
+  int64_t ld_dy;
+  void* dx;
+  int64_t ld_dx;
+  float* dweight;            // [D] or null
+  float* dbias;
+  int accumulate;
+  float* partials;           // [norm_bwd_blocks][2][D]
+};
+constexpr int64_t MAX_NORM_D = 16384;  // columns whose rows fit a block's registers
+int64_t norm_bwd_blocks(int64_t R, int64_t D);
+cudaError_t launch_norm_fwd(const NormParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s);
+
 // Host helpers of the ABI layer shared by its translation units (api.cu).
 mx_status_t device_sms(int* sms);   // checks the device; its SM count
 struct TensorMapShape {              // innermost dimension first; strides (bytes) of dimensions 1, 2

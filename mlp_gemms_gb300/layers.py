@@ -1,0 +1,112 @@
+"""Bindings of the layers around the expert MLP: the layer norm, the expert
+routing, the combine's gradient and products of 4-bit tensors.
+
+As in the package's own module, every function checks what the C layer cannot
+see and calls the C-ABI entry point of its name.  All of them are reached as
+``mlp_gemms_gb300.mx_...``.
+"""
+import functools
+
+import mlp_gemms_gb300 as _mx
+
+
+def _here(first, *others):
+    """_one_gpu, and that GPU the current one: it is where the call launches."""
+    _mx._one_gpu(first, *others)
+    _mx._stream()
+    assert first.get_device() == _mx._current[1](), "the tensors are not on the current GPU"
+
+
+def _type(t):
+    import torch
+    assert t.dtype in (torch.bfloat16, torch.float32), "neither BF16 nor fp32"
+    return _mx.F32 if t.dtype == torch.float32 else _mx.BF16
+
+
+def _rows(t, shape, dtype):
+    """A matrix of this shape and type with dense rows; its row stride."""
+    assert t.shape == shape and t.dtype == dtype and t.stride(1) == 1, "a matrix of another shape, type or layout"
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t, n, dtype=None):
+    assert t is None or (t.shape == (n,) and t.is_contiguous() and dtype in (None, t.dtype)), \
+        "a vector of another length, type or layout"
+
+
+def _norm_weights(weight, bias, D):
+    _vector(weight, D)
+    _vector(bias, D, weight.dtype if weight is not None else None)
+    return _mx.BF16 if weight is None and bias is None else _type(weight if weight is not None else bias)
+
+
+def mx_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, residual=None, rms=False, stats=True, out=None, sum_out=None,
+                     mean=None, rstd=None, stream=None):
+    """Layer norm (rms: without the mean) of the rows of s = x + residual (BF16
+    or fp32 [R, D]): returns (y BF16, mean, rstd, s), s being x itself
+    without a residual and mean None with rms; stats=False: no mean and rstd."""
+    import torch
+    R, D = x.shape
+    xt, wt, dev = _type(x), _norm_weights(weight, bias, D), x.device
+    ld_x, ld_res, ld_sum = _rows(x, (R, D), x.dtype), 0, 0
+    if out is None:
+        out = _mx._empty((R, D), torch.bfloat16, dev, stream)
+    if residual is not None:
+        ld_res = _rows(residual, (R, D), x.dtype)
+        if sum_out is None:
+            sum_out = _mx._empty((R, D), x.dtype, dev, stream)
+        ld_sum = _rows(sum_out, (R, D), x.dtype)
+    else:
+        assert sum_out is None, "a sum without a residual"
+    if stats and not rms and mean is None:
+        mean = _mx._empty(R, torch.float32, dev, stream)
+    if stats and rstd is None:
+        rstd = _mx._empty(R, torch.float32, dev, stream)
+    assert mean is None or not rms, "a mean with rms"
+    _vector(mean, R, torch.float32)
+    _vector(rstd, R, torch.float32)
+    _here(x, weight, bias, residual, out, sum_out, mean, rstd)
+    _mx._check(_mx.load().mx_layernorm_fwd(x.data_ptr(), xt, R, D, ld_x, _mx._ptr(residual), ld_res, _mx._ptr(sum_out), ld_sum,
+                                   _mx._ptr(weight), _mx._ptr(bias), wt, eps, 1 if rms else 0, out.data_ptr(),
+                                   _rows(out, (R, D), torch.bfloat16), _mx._ptr(mean), _mx._ptr(rstd), _mx._stream(stream)))
+    return out, mean, rstd, x if residual is None else sum_out
+
+
+@functools.lru_cache(maxsize=256)
+def mx_layernorm_workspace_bytes(R, D):
+    return int(_mx.load().mx_layernorm_workspace_bytes(R, D))
+
+
+def mx_layernorm_bwd(dy, x, mean, rstd, weight=None, dres=None, rms=False, bias=True, wgrad=True, accumulate=False,
+                     dx=None, dweight=None, dbias=None, workspace=None, stream=None):
+    """The layer norm's backward pass; x: what it normalised (the forward's s).
+    Returns (dx, dweight, dbias): dx of x's type with dres added, the others fp32
+    [D], dweight None without wgrad, dbias None without bias; accumulate: added
+    to the dweight and dbias that the caller brings."""
+    import torch
+    R, D = x.shape
+    xt, wt, dev = _type(x), _norm_weights(weight, None, D), x.device
+    ld_x, ld_dy = _rows(x, (R, D), x.dtype), _rows(dy, (R, D), torch.bfloat16)
+    ld_dres = 0 if dres is None else _rows(dres, (R, D), x.dtype)
+    assert not accumulate or ((dweight is not None or not wgrad) and (dbias is not None or not bias)), \
+        "accumulate needs the buffers to add to"
+    if dx is None:
+        dx = _mx._empty((R, D), x.dtype, dev, stream)
+    if wgrad and dweight is None:
+        dweight = _mx._empty(D, torch.float32, dev, stream)
+    if bias and dbias is None:
+        dbias = _mx._empty(D, torch.float32, dev, stream)
+    for t, n in ((mean, R), (rstd, R), (dweight, D), (dbias, D)):
+        _vector(t, n, torch.float32)
+    nbytes = 0
+    if dweight is not None or dbias is not None:
+        if workspace is None:
+            workspace = _mx._empty(max(mx_layernorm_workspace_bytes(R, D), 16), torch.uint8, dev, stream)
+        assert workspace.is_contiguous()
+        nbytes = workspace.nbytes
+    _here(x, dy, mean, rstd, weight, dres, dx, dweight, dbias, workspace)
+    _mx._check(_mx.load().mx_layernorm_bwd(dy.data_ptr(), ld_dy, x.data_ptr(), xt, R, D, ld_x, _mx._ptr(mean), _mx._ptr(rstd),
+                                   _mx._ptr(weight), wt, 1 if rms else 0, _mx._ptr(dres), ld_dres, dx.data_ptr(),
+                                   _rows(dx, (R, D), x.dtype), _mx._ptr(dweight), _mx._ptr(dbias), 1 if accumulate else 0,
+                                   _mx._ptr(workspace), nbytes, _mx._stream(stream)))
+    return dx, dweight, dbias
