@@ -839,6 +839,78 @@ MX_API mx_status_t mx_layernorm_bwd(const void *dy_bf16, int64_t ld_dy, const vo
                                     int32_t accumulate, void *workspace, size_t workspace_bytes, mx_stream_t stream);
 
 /*
+ * Expert routing: each token's k experts and their weights from the router's
+ * logits, and the logits' gradient.
+ * mx_moe_topk -- scores s = softmax(logits) over the row's experts, or
+ *   1 / (1 + exp(-logits)).  The experts are ordered by s + bias (bias NULL: by s),
+ *   largest first, equal ones by index; the order is that of the exact values.
+ *   With groups > 1 the experts are cut into that many groups of consecutive
+ *   ones; a group's value is the sum of its group_top (1 or 2) largest s + bias,
+ *   the topk_groups groups of the largest values are kept (equal ones by index)
+ *   and the experts of the others count as closed.  The k first experts are
+ *   chosen; the weight of choice j is
+ *     scale * s_j (renorm = 0), or scale * s_j / sum of the chosen s (renorm = 1;
+ *     0 where that sum is 0): the bias orders, it does not weigh.
+ *   A logit of -Inf closes its expert for that token: score 0, chosen (by index,
+ *   with weight 0) only when fewer than k open ones are left.  A NaN or +Inf makes
+ *   the row's weights NaN (sigmoid: its expert's); the ids stay distinct and valid.
+ *   logits     device [T, G] of x_type (MX_BF16 or MX_F32), row stride ld >= G
+ *   score      MX_SCORE_SOFTMAX or MX_SCORE_SIGMOID
+ *   bias       device fp32 [G], finite, or NULL
+ *   weights    out, device fp32 [T, k]
+ *   ids        out, device int32 [T, k]: what mx_moe_route_index takes
+ *   load, score_sum  both out or both NULL: device int32 [G], the choices of each
+ *              expert, and fp32 [G], the sum over tokens of its share of the scores
+ *              (softmax: s; sigmoid: s / sum of the row's s), in a fixed order: what a
+ *              balancing loss takes
+ *   workspace  with load: >= mx_moe_topk_workspace_bytes(T, G) bytes
+ * mx_moe_topk_bwd -- the gradient of the logits from that of the weights, and
+ *   (dscore_sum not NULL) of score_sum.  Choices and the bias get none.
+ *   logits, ids, score, renorm, scale   as in the forward pass
+ *   dweights   device fp32 [T, k];  dscore_sum  device fp32 [G] or NULL
+ *   dlogits    out, [T, G] of x_type, row stride ld_d; may be logits itself
+ *   An id of -1 is a dropped choice and has no part (with renorm the others' sum
+ *   is without it); other ids outside [0, G) are skipped likewise and reported as
+ *   MX_ERR_INVALID_ARG by mx_get_device_status.
+ * 1 <= k <= 32, k <= G <= 1024; groups divides G, groups <= 32, 1 <= topk_groups
+ * <= groups, k <= topk_groups * G / groups.  T has no alignment; T == 0 writes
+ * nothing but load and score_sum (zeros).
+ */
+typedef enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SIGMOID = 1 } mx_score_t;
+MX_API size_t mx_moe_topk_workspace_bytes(int64_t T, int32_t G);
+MX_API mx_status_t mx_moe_topk(const void *logits, int32_t x_type, int64_t T, int32_t G, int64_t ld, int32_t k,
+                               int32_t score, const float *bias, int32_t groups, int32_t topk_groups,
+                               int32_t group_top, int32_t renorm, float scale, float *weights, int32_t *ids,
+                               int32_t *load, float *score_sum, void *workspace, size_t workspace_bytes,
+                               mx_stream_t stream);
+MX_API mx_status_t mx_moe_topk_bwd(const void *logits, int32_t x_type, int64_t T, int32_t G, int64_t ld, int32_t k,
+                                   int32_t score, int32_t renorm, float scale, const int32_t *ids,
+                                   const float *dweights, const float *dscore_sum, void *dlogits, int64_t ld_d,
+                                   mx_stream_t stream);
+
+/*
+ * mx_moe_unpermute_bwd -- the gradient of mx_moe_unpermute's weighted sum:
+ *   din[row_of[t, j]] = weights[t, j] * dout[t] (one rounding to BF16) and
+ *   dweights[t, j] = sum over columns of dout[t] * in[row_of[t, j]] (fp32, fixed
+ *   order).
+ *   dout_bf16  device BF16 [T, D], contiguous rows
+ *   in_bf16    what mx_moe_unpermute summed, BF16 [R, D] (NULL without dweights)
+ *   row_of_dev int32 [T, k]; every row is named at most once, -1 is a dropped choice
+ *              (dweights 0)
+ *   weights_dev  fp32 [T, k] or NULL (ones)
+ *   src_dev    int32 [R] or NULL: rows with a negative source (mx_moe_route_index's
+ *              empty rows) are set to zero
+ *   din_bf16   out or NULL, BF16 [R, D]; rows that nothing names and src does not
+ *              mark are left as they were
+ *   dweights   out or NULL, fp32 [T, k]
+ * Shapes: D % 8 == 0.  A row index >= R is skipped and reported as
+ * MX_ERR_INVALID_ARG by mx_get_device_status.
+ */
+MX_API mx_status_t mx_moe_unpermute_bwd(const void *dout_bf16, int64_t T, int64_t D, const void *in_bf16, int64_t R,
+                                        const int32_t *row_of_dev, int32_t k, const float *weights_dev,
+                                        const int32_t *src_dev, void *din_bf16, float *dweights, mx_stream_t stream);
+
+/*
  * mx_get_device_status -- synchronise `stream`, then report and clear the
  * device-side status words: MX_ERR_DEVICE_TIMEOUT if a bounded wait inside
  * a kernel expired (the kernel unwound; its outputs are undefined),

@@ -21,6 +21,7 @@ E4M3, E2M3, E2M1 = 0, 1, 2
 ROWWISE, COLWISE, HADAMARD, COLSUM = 1, 2, 4, 8
 ACT_SWIGLU, ACT_GELU_TANH, ACT_NONE, ACT_SILU, ACT_RELU = 0, 1, 2, 3, 4
 W_NK, W_KN = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 BF16, F32 = 0, 1  # types of the layers around the expert MLP (layers.py)
 
 STATUS = {
@@ -45,7 +46,8 @@ ABI_SYMBOLS = (
     "mx_mlp_workspace_layout", "mx_moe_route_rows_pad", "mx_moe_route_index_pad", "mx_grouped_gemm_2sm",
     "mx_ragged_gemm", "mx_ragged_gemm_wgrad_workspace_bytes", "mx_ragged_gemm_wgrad", "mx_ragged_gemm_wgrad_f32",
     "mx_linear_fwd", "mx_act_ckpt_fwd", "mx_act_ckpt_workspace_bytes", "mx_act_ckpt_bwd", "mx_layernorm_fwd",
-    "mx_layernorm_workspace_bytes", "mx_layernorm_bwd",
+    "mx_layernorm_workspace_bytes", "mx_layernorm_bwd", "mx_moe_topk_workspace_bytes", "mx_moe_topk",
+    "mx_moe_topk_bwd", "mx_moe_unpermute_bwd",
 )
 
 
@@ -157,6 +159,11 @@ def load(path=None):
         "mx_layernorm_workspace_bytes": (sz, [i64, i64]),
         "mx_layernorm_bwd": (ctypes.c_int, [vp, i64, vp, i32, i64, i64, i64, vp, vp, vp, i32, i32, vp, i64, vp, i64,
                                             vp, vp, i32, vp, sz, vp]),
+        "mx_moe_topk_workspace_bytes": (sz, [i64, i32]),
+        "mx_moe_topk": (ctypes.c_int, [vp, i32, i64, i32, i64, i32, i32, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp,
+                                       sz, vp]),
+        "mx_moe_topk_bwd": (ctypes.c_int, [vp, i32, i64, i32, i64, i32, i32, i32, f32, vp, vp, vp, vp, i64, vp]),
+        "mx_moe_unpermute_bwd": (ctypes.c_int, [vp, i64, i64, vp, i64, vp, i32, vp, vp, vp, vp, vp]),
         "mx_debug_tap": (ctypes.c_int, [vp, i64]),
         "mx_mlp_pipeline_create": (ctypes.c_int, [ctypes.POINTER(MlpArgsStruct), vp, ctypes.POINTER(vp)]),
         "mx_mlp_pipeline_run": (ctypes.c_int, [vp, ctypes.POINTER(HostIOStruct)]),

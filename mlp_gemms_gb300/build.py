@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libmxgb300.so")
 SOURCES = ["quantize.cu", "gemm.cu", "gemm_dense.cu", "gemm_f4.cu", "gemm_pair.cu", "permute.cu", "api.cu",
-           "pipeline.cu", "ragged.cu", "skinny.cu", "ckpt.cu", "api_bf16.cu", "norm.cu", "api_layers.cu"]
+           "pipeline.cu", "ragged.cu", "skinny.cu", "ckpt.cu", "api_bf16.cu", "norm.cu", "route.cu", "combine.cu",
+           "api_layers.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "--expt-relaxed-constexpr"]

@@ -1646,18 +1646,20 @@ mx_status_t mx_mlp_fwd_bwd(const mx_mlp_args_t* a, mx_stream_t stream) { return 
 mx_status_t mx_get_device_status(mx_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-  unsigned word = 0, dense = 0, f4 = 0, quant = 0, perm = 0, pairs = 0, ragged = 0, skinny = 0;
+  unsigned word = 0, dense = 0, f4 = 0, quant = 0, perm = 0, pairs = 0, ragged = 0, skinny = 0, route = 0, combine = 0;
   if ((e = mx::read_gemm_status(&word)) != cudaSuccess || (e = mx::read_dense_status(&dense)) != cudaSuccess ||
       (e = mx::read_f4_status(&f4)) != cudaSuccess || (e = mx::read_quant_status(&quant)) != cudaSuccess ||
       (e = mx::read_perm_status(&perm)) != cudaSuccess || (e = mx::read_pair_status(&pairs)) != cudaSuccess ||
-      (e = mx::read_ragged_status(&ragged)) != cudaSuccess || (e = mx::read_skinny_status(&skinny)) != cudaSuccess)
+      (e = mx::read_ragged_status(&ragged)) != cudaSuccess || (e = mx::read_skinny_status(&skinny)) != cudaSuccess ||
+      (e = mx::read_route_status(&route)) != cudaSuccess || (e = mx::read_combine_status(&combine)) != cudaSuccess)
     return cuda_fail(e, "reading device status");
   if ((e = mx::reset_gemm_status()) != cudaSuccess || (e = mx::reset_dense_status()) != cudaSuccess ||
       (e = mx::reset_f4_status()) != cudaSuccess || (e = mx::reset_quant_status()) != cudaSuccess ||
       (e = mx::reset_perm_status()) != cudaSuccess || (e = mx::reset_pair_status()) != cudaSuccess ||
-      (e = mx::reset_ragged_status()) != cudaSuccess || (e = mx::reset_skinny_status()) != cudaSuccess)
+      (e = mx::reset_ragged_status()) != cudaSuccess || (e = mx::reset_skinny_status()) != cudaSuccess ||
+      (e = mx::reset_route_status()) != cudaSuccess || (e = mx::reset_combine_status()) != cudaSuccess)
     return cuda_fail(e, "clearing device status");
-  word |= dense | f4 | quant | perm | pairs | ragged | skinny;
+  word |= dense | f4 | quant | perm | pairs | ragged | skinny | route | combine;
   if (word & 1u) return fail(MX_ERR_DEVICE_TIMEOUT, "a bounded device-side wait expired");
   if (word & 2u) return fail(MX_ERR_OFFSETS, "a kernel saw a malformed offsets segment");
   if (word & 4u) return fail(MX_ERR_INVALID_ARG, "a routing index (expert id or routed row) was out of range");

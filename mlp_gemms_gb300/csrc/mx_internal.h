@@ -285,6 +285,49 @@ int64_t norm_bwd_blocks(int64_t R, int64_t D);
 cudaError_t launch_norm_fwd(const NormParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s);
 
+// Expert routing (route.cu).
+struct RouteParams {
+  int64_t T;
+  int G, k, x_f32, sigmoid, renorm;
+  int groups, topk_groups, group_top;
+  float scale;
+  const void* logits;        // [T, G], BF16 or fp32
+  int64_t ld;
+  const float* bias;         // [G] or null
+  float* weights;            // [T, k]
+  int32_t* ids;              // [T, k] (backward: read)
+  int32_t* load;             // [G] or null
+  float* score_sum;          // [G]
+  int32_t* partial_load;     // [route_blocks][G] or null
+  float* partial_sum;
+  const float* dweights;     // backward
+  const float* dsum;         // [G] or null
+  void* dlogits;
+  int64_t ld_d;
+  int per_lane, wide;        // set by the launch
+};
+int64_t route_blocks(int64_t T);
+cudaError_t launch_route_fwd(RouteParams p, cudaStream_t s);
+cudaError_t launch_route_bwd(RouteParams p, cudaStream_t s);
+cudaError_t read_route_status(unsigned* out);
+cudaError_t reset_route_status();
+
+// The combine's gradient (combine.cu).
+struct CombineBwdParams {
+  int64_t T, R, D;
+  int k;
+  const uint16_t* dout;      // [T, D]
+  const uint16_t* in;        // [R, D], needed for dweights
+  const int32_t* row_of;     // [T, k]
+  const float* weights;      // [T, k] or null (ones)
+  const int32_t* src;        // [R] or null: rows with a negative source are zeroed
+  uint16_t* din;             // [R, D] or null
+  float* dweights;           // [T, k] or null
+};
+cudaError_t launch_combine_bwd(const CombineBwdParams& p, int num_sms, cudaStream_t s);
+cudaError_t read_combine_status(unsigned* out);
+cudaError_t reset_combine_status();
+
 // Host helpers of the ABI layer shared by its translation units (api.cu).
 mx_status_t device_sms(int* sms);   // checks the device; its SM count
 struct TensorMapShape {              // innermost dimension first; strides (bytes) of dimensions 1, 2

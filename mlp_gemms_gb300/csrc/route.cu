@@ -1,0 +1,534 @@
+// The expert routing: each token's k experts from its logits, their weights,
+// and the logits' gradient.
+#include "mx_internal.h"
+#include "vec8.cuh"
+
+namespace mx {
+
+static __device__ unsigned g_route_status = 0;
+
+// A warp takes a token; its lanes hold V consecutive experts each (expert
+// lane * V + i, so that the lowest lane and the lowest slot are the lowest
+// index), and lane j the j-th choice.
+
+// Floating values as integers in the same order; -0 counts as +0, a NaN above
+// everything, and 0 is free for "not there".
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  if ((b & 0x7FFFFFFFFFFFFFFFull) > 0x7FF0000000000000ull) return ~0ull;
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ uint32_t warp_max_key(uint32_t k) { return __reduce_max_sync(0xFFFFFFFFu, k); }
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
+  const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+
+template <typename F> __device__ __forceinline__ F minus_inf();
+template <> __device__ __forceinline__ float minus_inf<float>() { return __uint_as_float(0xFF800000u); }
+template <> __device__ __forceinline__ double minus_inf<double>() { return __longlong_as_double(0xFFF0000000000000ll); }
+template <typename F> struct KeyOf { typedef uint32_t type; };
+template <> struct KeyOf<double> { typedef uint64_t type; };
+
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+template <typename F> __device__ __forceinline__ F sigmoid_of(F v) { return (F)1 / ((F)1 + exp_of(-v)); }
+
+template <typename F>
+__device__ __forceinline__ F warp_sum_of(F v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+template <typename F>
+__device__ __forceinline__ F warp_max_of(F v) {  // a NaN need not survive
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const F u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float load_logit(const RouteParams& p, int64_t t, int e) {
+  if (p.x_f32) return *(static_cast<const float*>(p.logits) + t * p.ld + e);
+  return bf16_bits_to_float(*(static_cast<const uint16_t*>(p.logits) + t * p.ld + e));
+}
+
+// The lane's logits, -Inf past its last expert.
+template <int V>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, float (&x)[V]) {
+  const int e0 = lane * p.per_lane;
+  if (p.wide) {  // per_lane == V, every lane's piece aligned to its size (at most 16 bytes)
+    if (e0 >= p.G) {
+#pragma unroll
+      for (int i = 0; i < V; i++) x[i] = minus_inf<float>();
+      return;
+    }
+    constexpr int E = V < 8 ? V : 8;
+    if (p.x_f32) {
+      const float* q = static_cast<const float*>(p.logits) + t * p.ld + e0;
+      if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const uint4 w = load_stream16(q + i);
+          x[i] = __uint_as_float(w.x); x[i + 1] = __uint_as_float(w.y);
+          x[i + 2] = __uint_as_float(w.z); x[i + 3] = __uint_as_float(w.w);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) x[i] = q[i];
+      }
+    } else {
+      const uint16_t* q = static_cast<const uint16_t*>(p.logits) + t * p.ld + e0;
+      if constexpr (E == 8) {
+#pragma unroll
+        for (int i = 0; i < V; i += 8) {
+          Raw8<false> r;
+          float f[8];
+          r.q[0] = load_stream16(q + i);
+          unpack_raw8<false>(r, f);
+#pragma unroll
+          for (int j = 0; j < 8; j++) x[i + j] = f[j];
+        }
+      } else if constexpr (E == 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(q);
+        x[0] = bf16_bits_to_float(w.x & 0xFFFFu); x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        x[2] = bf16_bits_to_float(w.y & 0xFFFFu); x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) x[i] = bf16_bits_to_float(q[i]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    const int e = e0 + i;
+    x[i] = i < p.per_lane && e < p.G ? load_logit(p, t, e) : minus_inf<float>();
+  }
+}
+
+// The scores' two numbers for a token: softmax: the largest logit (0 if all are
+// -Inf) and 1 / sum of exp(x - it) (0 if that sum is 0); sigmoid: not used.
+template <typename F> struct Softmax { F top, inv; };
+template <typename F, int V>
+__device__ __forceinline__ Softmax<F> softmax_of(const float (&x)[V]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < V; i++) m = fmaxf(m, x[i]);
+  m = warp_max_of(m);
+  Softmax<F> s;
+  s.top = m == minus_inf<float>() ? (F)0 : (F)m;
+  F sum = 0;
+#pragma unroll
+  for (int i = 0; i < V; i++) sum += exp_of((F)x[i] - s.top);
+  sum = warp_sum_of(sum);
+  s.inv = sum == (F)0 ? (F)0 : (F)1 / sum;
+  return s;
+}
+template <typename F, bool SIG>
+__device__ __forceinline__ F score_of(float x, const Softmax<F>& s) {
+  if constexpr (SIG) return sigmoid_of((F)x);
+  else return exp_of((F)x - s.top) * s.inv;
+}
+
+// The largest keys one after the other, the lowest index of equal ones: lane j
+// gets the j-th index.  Taken keys become 0.
+template <int V, typename K>
+__device__ __forceinline__ int take_largest(K (&key)[V], int per_lane, int count, int lane) {
+  int mine = 0;
+  for (int j = 0; j < count; j++) {
+    K m = key[0];
+#pragma unroll
+    for (int i = 1; i < V; i++) m = key[i] > m ? key[i] : m;
+    const K w = warp_max_key(m);
+    const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, m == w)) - 1;
+    int slot = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; i--) slot = key[i] == w ? i : slot;
+    if (lane == owner) {
+#pragma unroll
+      for (int i = 0; i < V; i++) key[i] = i == slot ? 0 : key[i];
+    }
+    const int id = owner * per_lane + __shfl_sync(0xFFFFFFFFu, slot, owner);
+    mine = lane == j ? id : mine;
+  }
+  return mine;
+}
+
+// Which groups are kept, as a bit mask; *close: the last kept group's value
+// and the first dropped one's are nearer than `tol`.  c: the values of all
+// experts in shared memory.
+template <typename F>
+__device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F* c, int lane, F tol, bool* close) {
+  const int size = p.G / p.groups;
+  F a = minus_inf<F>(), b = a;
+  bool nan = false;
+  if (lane < p.groups) {
+    int i = lane % size;  // each lane begins elsewhere: its group's start is the same bank as the others'
+    for (int n = 0; n < size; n++) {
+      const F v = c[lane * size + i];
+      nan |= v != v;
+      b = v > a ? a : (v > b ? v : b);
+      a = v > a ? v : a;
+      i = i + 1 == size ? 0 : i + 1;
+    }
+  }
+  F value = p.group_top == 2 ? a + b : a;
+  typename KeyOf<F>::type key = nan ? ~(typename KeyOf<F>::type)0 : order_key(value);
+  int rank = 0;
+  for (int g = 0; g < p.groups; g++) {
+    const typename KeyOf<F>::type other = __shfl_sync(0xFFFFFFFFu, key, g);
+    rank += other > key || (other == key && g < lane) ? 1 : 0;
+  }
+  const bool in = lane < p.groups;
+  const uint32_t kept = __ballot_sync(0xFFFFFFFFu, in && rank < p.topk_groups);
+  const uint32_t last = __ballot_sync(0xFFFFFFFFu, in && rank == p.topk_groups - 1);
+  const uint32_t next = __ballot_sync(0xFFFFFFFFu, in && rank == p.topk_groups);
+  *close = false;
+  if (next != 0) {
+    const F u = __shfl_sync(0xFFFFFFFFu, value, __ffs(last) - 1), v = __shfl_sync(0xFFFFFFFFu, value, __ffs(next) - 1);
+    *close = u - v <= tol + (F)5e-7 * (u < 0 ? -u : u);  // false for two closed groups: -Inf - -Inf is a NaN
+  }
+  return kept;
+}
+
+// The choice by values that are computed (scores, biased scores) in F.  In
+// fp32 two values nearer to each other than their error leave the order open:
+// *open is set, and the caller repeats the choice in fp64.
+template <int V, bool SIG, typename F>
+__device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const float (&x)[V], F* shared, int lane,
+                                      bool* open) {
+  constexpr bool FAST = sizeof(F) == 4;
+  // relative error of a score and of the values compared, twice over: exp's
+  // (2 units), the sum's (V + 5 roundings, softmax), the quotient's
+  const F err = SIG ? (F)1e-6 : (F)6e-6;
+  const int e0 = lane * p.per_lane;
+  Softmax<F> s{};
+  if constexpr (!SIG) s = softmax_of<F, V>(x);
+  typename KeyOf<F>::type key[V];
+  F c[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    const int e = e0 + i;
+    const bool there = i < p.per_lane && e < p.G;
+    c[i] = x[i] == minus_inf<float>() ? minus_inf<F>()
+                                      : score_of<F, SIG>(x[i], s) + (p.bias != nullptr && there ? (F)*(p.bias + e) : (F)0);
+    // without a bias the logits have the scores' order, exactly
+    key[i] = there ? order_key(p.bias == nullptr ? (F)x[i] : c[i]) : 0;
+  }
+  *open = false;
+  if (p.groups > 1) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; i++)
+      if (i < p.per_lane && e0 + i < p.G)
+        shared[e0 + i] = p.bias == nullptr && p.group_top == 1 ? (F)x[i] : c[i];
+    __syncwarp();
+    bool close;
+    const uint32_t kept = keep_groups<F>(p, shared, lane, 2 * err, &close);
+    *open = FAST && close && !(p.bias == nullptr && p.group_top == 1);
+    const int size = p.G / p.groups;
+    int g = e0 / size, in = e0 - g * size;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      if (key[i] != 0 && !(kept >> g & 1u)) key[i] = order_key(minus_inf<F>());
+      if (++in == size) { in = 0; g++; }
+    }
+  }
+  // one more than k: the first that is left out
+  const bool look = FAST && p.bias != nullptr && p.k < p.G && p.k < 32;
+  const int id = take_largest(key, p.per_lane, p.k + (look ? 1 : 0), lane);
+  if (FAST && p.bias != nullptr) {
+    const int count = p.k + (look ? 1 : 0);
+    const float xi = lane < count ? load_logit(p, t, id) : 0.f, bi = lane < count ? *(p.bias + id) : 0.f;
+    const F si = score_of<F, SIG>(xi, s), ci = si + (F)bi;
+    const F ux = __shfl_up_sync(0xFFFFFFFFu, xi, 1), ub = __shfl_up_sync(0xFFFFFFFFu, bi, 1);
+    const F us = __shfl_up_sync(0xFFFFFFFFu, si, 1), uc = __shfl_up_sync(0xFFFFFFFFu, ci, 1);
+    const F most = si > us ? si : us;
+    // equal logits with equal biases are equal for certain; closed experts are -Inf
+    const bool near = lane > 0 && lane < count && !(xi == ux && bi == ub) && xi != minus_inf<float>() &&
+                      uc - ci <= err * most + (F)2.5e-7 * ((uc < 0 ? -uc : uc) + (ci < 0 ? -ci : ci));
+    *open = *open || __any_sync(0xFFFFFFFFu, near) || (p.k == 32 && p.G > 32);
+  }
+  return id;
+}
+
+// Forward.  The order is that of the exact values: by the logits themselves
+// where there is no bias (both scores grow with them), else by score + bias in
+// fp32 and, for the few tokens where two of them are nearer than their error,
+// again in fp64.
+template <int V, bool SIG>
+__global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
+  extern __shared__ char route_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * p.per_lane;
+  double* const values = reinterpret_cast<double*>(route_smem) + (p.groups > 1 ? warp * p.G : 0);  // groups: G per warp
+  int32_t* const load = reinterpret_cast<int32_t*>(route_smem + (p.groups > 1 ? 8 * p.G * sizeof(double) : 0));
+  float* const sums = reinterpret_cast<float*>(load + p.G);
+  float share[V] = {};
+  const bool stats = p.partial_load != nullptr;
+  if (stats)
+    for (int e = threadIdx.x; e < p.G; e += blockDim.x) {
+      load[e] = 0;
+      sums[e] = 0.f;
+    }
+  __syncthreads();
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t t = (int64_t)blockIdx.x * 8 + warp; t < p.T; t += (int64_t)gridDim.x * 8) {
+    float x[V];
+    load_logits<V>(p, t, lane, x);
+    bool open;
+    int id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
+    if (open) id = choose<V, SIG, double>(p, t, x, values, lane, &open);
+    Softmax<float> s{};
+    if constexpr (!SIG) s = softmax_of<float, V>(x);
+    const bool mine = lane < p.k;
+    float w = mine ? score_of<float, SIG>(load_logit(p, t, id), s) : 0.f;
+    if (p.renorm) {
+      const float total = warp_sum_of(w);
+      w = total == 0.f ? 0.f : w / total;
+    }
+    if (mine) {
+      p.weights[t * p.k + lane] = w * p.scale;
+      p.ids[t * p.k + lane] = id;
+    }
+    if (stats) {
+      float own[V], norm = 1.f;
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        own[i] = i < p.per_lane && e0 + i < p.G ? score_of<float, SIG>(x[i], s) : 0.f;
+      if constexpr (SIG) {
+        norm = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; i++) norm += own[i];
+        norm = warp_sum_of(norm);
+        norm = norm == 0.f ? 0.f : 1.f / norm;
+      }
+#pragma unroll
+      for (int i = 0; i < V; i++) share[i] = fmaf(own[i], norm, share[i]);
+      if (mine) atomicAdd(&load[id], 1);
+    }
+  }
+  if (!stats) return;
+  for (int w = 0; w < 8; w++) {  // the warps' sums in warp order
+    __syncthreads();
+    if (warp == w) {
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (i < p.per_lane && e0 + i < p.G) sums[e0 + i] += share[i];
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.G; e += blockDim.x) {
+    p.partial_load[(int64_t)blockIdx.x * p.G + e] = load[e];
+    p.partial_sum[(int64_t)blockIdx.x * p.G + e] = sums[e];
+  }
+}
+
+// The blocks' counts and sums added in order: a block takes 32 experts, its 8
+// warps every eighth block.
+__global__ void __launch_bounds__(256) route_stats_kernel(const RouteParams p, int blocks) {
+  __shared__ float s[8][32];
+  __shared__ int32_t n[8][32];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
+  float t = 0.f;
+  int32_t c = 0;
+  pdl_trigger();
+  pdl_wait();
+  if (e < p.G) {
+#pragma unroll 4
+    for (int b = w; b < blocks; b += 8) {
+      t += p.partial_sum[(int64_t)b * p.G + e];
+      c += p.partial_load[(int64_t)b * p.G + e];
+    }
+  }
+  s[w][lane] = t;
+  n[w][lane] = c;
+  __syncthreads();
+  if (w == 0 && e < p.G) {
+    t = 0.f;
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      t += s[i][lane];
+      c += n[i][lane];
+    }
+    p.load[e] = c;
+    p.score_sum[e] = t;
+  }
+}
+
+// Backward.  With a_j = scale * dweights_j, s the scores, r_j = s_j / S the
+// renormalised ones (S the choices' sum) and A = sum a_j r_j, the choices give
+//   softmax: r_j (a_j - A), or s_e ([e chosen] a_e - sum a_j s_j) without renorm;
+//   sigmoid: r_j (a_j - A) (1 - s_j), or a_j s_j (1 - s_j),
+// and the gradient v of the scores' sums, with p = softmax, or sigmoid / its sum:
+//   p_e (v_e - sum v p), for the sigmoid times (1 - s_e).
+// (1 - s = sigmoid(-x), without cancellation.)  Closed experts (-Inf): 0.
+template <int V, bool SIG>
+__global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * p.per_lane;
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t t = (int64_t)blockIdx.x * 8 + warp; t < p.T; t += (int64_t)gridDim.x * 8) {
+    float x[V], d[V];
+    load_logits<V>(p, t, lane, x);
+    int id = -1;
+    float a = 0.f;
+    if (lane < p.k) {
+      id = *(p.ids + t * p.k + lane);
+      if (id < 0 || id >= p.G) {  // a dropped choice (-1) has no part
+        if (id != -1) atomicOr(&g_route_status, DEV_BAD_INDEX);
+        id = -1;
+      } else {
+        a = *(p.dweights + t * p.k + lane) * p.scale;
+      }
+    }
+    Softmax<float> s{};
+    if constexpr (!SIG) s = softmax_of<float, V>(x);
+    const float xj = id >= 0 ? load_logit(p, t, id) : minus_inf<float>();
+    const float sj = id >= 0 ? score_of<float, SIG>(xj, s) : 0.f;
+    float r = sj, all = 0.f;
+    if (p.renorm) {
+      const float total = warp_sum_of(sj);
+      r = total == 0.f ? 0.f : sj / total;
+      a -= warp_sum_of(a * r);
+    } else if (!SIG) {
+      all = warp_sum_of(a * r);  // taken from every expert below
+    }
+    float g = r == 0.f ? 0.f : r * a;
+    if (SIG) g *= sigmoid_of(-xj);
+    float own[V], norm = 1.f, v_mean = 0.f;
+    const bool dense = p.dsum != nullptr || (!SIG && !p.renorm);
+#pragma unroll
+    for (int i = 0; i < V; i++) d[i] = 0.f;
+    if (dense) {
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        own[i] = i < p.per_lane && e0 + i < p.G && x[i] != minus_inf<float>() ? score_of<float, SIG>(x[i], s) : 0.f;
+      if (p.dsum != nullptr) {
+        if constexpr (SIG) {
+          norm = 0.f;
+#pragma unroll
+          for (int i = 0; i < V; i++) norm += own[i];
+          norm = warp_sum_of(norm);
+          norm = norm == 0.f ? 0.f : 1.f / norm;
+        }
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          d[i] = i < p.per_lane && e0 + i < p.G ? *(p.dsum + e0 + i) : 0.f;
+          v_mean = fmaf(d[i], own[i] * norm, v_mean);
+        }
+        v_mean = warp_sum_of(v_mean);
+      }
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        d[i] = own[i] == 0.f ? 0.f : own[i] * ((d[i] - v_mean) * norm - all);
+        if (SIG) d[i] *= sigmoid_of(-x[i]);
+      }
+    }
+    for (int j = 0; j < p.k; j++) {  // each choice's part to the lane that has its expert
+      const int e = __shfl_sync(0xFFFFFFFFu, id, j) - e0;
+      const float part = __shfl_sync(0xFFFFFFFFu, g, j);
+#pragma unroll
+      for (int i = 0; i < V; i++) d[i] += e == i && i < p.per_lane ? part : 0.f;
+    }
+    if (p.x_f32) {
+      float* const out = static_cast<float*>(p.dlogits) + t * p.ld_d + e0;
+      if (p.wide && V >= 4) {
+        if (e0 < p.G) {
+#pragma unroll
+          for (int i = 0; i + 3 < V; i += 4) *reinterpret_cast<float4*>(out + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+          if (i < p.per_lane && e0 + i < p.G) out[i] = d[i];
+      }
+    } else {
+      uint16_t* const out = static_cast<uint16_t*>(p.dlogits) + t * p.ld_d + e0;
+      if (p.wide && V >= 4) {
+        if (e0 < p.G) {
+#pragma unroll
+          for (int i = 0; i + 3 < V; i += 4)
+            *reinterpret_cast<uint2*>(out + i) = make_uint2(float2_to_bf16x2(d[i], d[i + 1]), float2_to_bf16x2(d[i + 2], d[i + 3]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+          if (i < p.per_lane && e0 + i < p.G) out[i] = (uint16_t)float2_to_bf16x2(d[i], 0.f);
+      }
+    }
+  }
+}
+
+int64_t route_blocks(int64_t T) {
+  const int64_t want = (T + 7) / 8;
+  return want < 152 * 4 ? want : 152 * 4;
+}
+
+// Lane layout of G experts: V slots, per_lane of them used.
+static int slots(int G) {
+  int v = 1;
+  while (32 * v < G) v *= 2;
+  return v;
+}
+static void set_layout(RouteParams& p) {
+  const int v = slots(p.G), bytes = v * (p.x_f32 ? 4 : 2) < 16 ? v * (p.x_f32 ? 4 : 2) : 16;
+  p.per_lane = (p.G + 31) / 32;
+  if (p.G % v == 0) p.per_lane = v;  // whole pieces for fewer lanes
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | (uintptr_t)(p.ld * (p.x_f32 ? 4 : 2)) |
+                       reinterpret_cast<uintptr_t>(p.dlogits) | (uintptr_t)(p.ld_d * (p.x_f32 ? 4 : 2));
+  p.wide = p.G % v == 0 && (at & (uintptr_t)(bytes - 1)) == 0;
+}
+
+template <int V, bool SIG>
+static cudaError_t launch_v(const RouteParams& p, bool bwd, cudaStream_t s) {
+  const dim3 grid((unsigned)route_blocks(p.T));
+  if (bwd) return launch_pdl(route_bwd_kernel<V, SIG>, grid, 256, 0, s, dim3(1), p);
+  const int smem = (p.groups > 1 ? 8 * p.G * 8 : 0) + (p.partial_load ? 8 * p.G : 0);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = ensure_smem_attr<route_fwd_kernel<V, SIG>>(8 * 1024 * 8 + 8 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(route_fwd_kernel<V, SIG>, grid, 256, smem, s, dim3(1), p);
+}
+template <bool SIG>
+static cudaError_t launch_slots(const RouteParams& p, bool bwd, cudaStream_t s) {
+  switch (slots(p.G)) {
+    case 1: return launch_v<1, SIG>(p, bwd, s);
+    case 2: return launch_v<2, SIG>(p, bwd, s);
+    case 4: return launch_v<4, SIG>(p, bwd, s);
+    case 8: return launch_v<8, SIG>(p, bwd, s);
+    case 16: return launch_v<16, SIG>(p, bwd, s);
+    default: return launch_v<32, SIG>(p, bwd, s);
+  }
+}
+
+cudaError_t launch_route_fwd(RouteParams p, cudaStream_t s) {
+  set_layout(p);
+  const cudaError_t e = p.sigmoid ? launch_slots<true>(p, false, s) : launch_slots<false>(p, false, s);
+  if (e != cudaSuccess || p.partial_load == nullptr) return e;
+  return launch_pdl(route_stats_kernel, dim3((unsigned)((p.G + 31) / 32)), 256, 0, s, dim3(1), p, (int)route_blocks(p.T));
+}
+
+cudaError_t launch_route_bwd(RouteParams p, cudaStream_t s) {
+  set_layout(p);
+  return p.sigmoid ? launch_slots<true>(p, true, s) : launch_slots<false>(p, true, s);
+}
+
+cudaError_t read_route_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_route_status, sizeof(unsigned)); }
+cudaError_t reset_route_status() {
+  const unsigned zero = 0;
+  return cudaMemcpyToSymbol(g_route_status, &zero, sizeof(unsigned));
+}
+
+}  // namespace mx

@@ -110,3 +110,97 @@ def mx_layernorm_bwd(dy, x, mean, rstd, weight=None, dres=None, rms=False, bias=
                                    _rows(dx, (R, D), x.dtype), _mx._ptr(dweight), _mx._ptr(dbias), 1 if accumulate else 0,
                                    _mx._ptr(workspace), nbytes, _mx._stream(stream)))
     return dx, dweight, dbias
+
+
+# --------------------------------------------------------------------------
+# Expert routing and the combine's gradient
+# --------------------------------------------------------------------------
+
+def _table(t, shape, dtype):
+    """A dense table of this shape and type, or None."""
+    assert t is None or (t.shape == shape and t.dtype == dtype and t.is_contiguous()), \
+        "a table of another shape, type or layout"
+
+
+@functools.lru_cache(maxsize=256)
+def mx_moe_topk_workspace_bytes(T, G):
+    return int(_mx.load().mx_moe_topk_workspace_bytes(T, G))
+
+
+def mx_moe_topk(logits, k, score=_mx.SCORE_SOFTMAX, bias=None, groups=1, topk_groups=1, group_top=1, renorm=True,
+                scale=1.0, stats=False, weights=None, ids=None, load=None, score_sum=None, workspace=None, stream=None):
+    """The k experts of each token from its logits (BF16 or fp32 [T, G]) and
+    their weights: returns (weights fp32 [T, k], ids int32 [T, k], load, score_sum),
+    the last two (choices of each expert, sums of its scores) None without stats."""
+    import torch
+    T, G = logits.shape
+    xt, dev = _type(logits), logits.device
+    ld = _rows(logits, (T, G), logits.dtype)
+    if weights is None:
+        weights = _mx._empty((T, k), torch.float32, dev, stream)
+    if ids is None:
+        ids = _mx._empty((T, k), torch.int32, dev, stream)
+    stats = stats or load is not None or score_sum is not None
+    nbytes = 0
+    if stats:
+        load = load if load is not None else _mx._empty(G, torch.int32, dev, stream)
+        score_sum = score_sum if score_sum is not None else _mx._empty(G, torch.float32, dev, stream)
+        if workspace is None:
+            workspace = _mx._empty(max(mx_moe_topk_workspace_bytes(T, G), 16), torch.uint8, dev, stream)
+        assert workspace.is_contiguous()
+        nbytes = workspace.nbytes
+    _table(weights, (T, k), torch.float32)
+    _table(ids, (T, k), torch.int32)
+    _vector(bias, G, torch.float32)
+    _vector(load, G, torch.int32)
+    _vector(score_sum, G, torch.float32)
+    _here(logits, bias, weights, ids, load, score_sum, workspace)
+    _mx._check(_mx.load().mx_moe_topk(logits.data_ptr(), xt, T, G, ld, k, score, _mx._ptr(bias), groups, topk_groups,
+                                      group_top, 1 if renorm else 0, scale, weights.data_ptr(), ids.data_ptr(),
+                                      _mx._ptr(load), _mx._ptr(score_sum), _mx._ptr(workspace), nbytes,
+                                      _mx._stream(stream)))
+    return weights, ids, load, score_sum
+
+
+def mx_moe_topk_bwd(logits, ids, dweights, score=_mx.SCORE_SOFTMAX, renorm=True, scale=1.0, dscore_sum=None,
+                    dlogits=None, stream=None):
+    """The logits' gradient (of their type) from that of the weights, and of
+    score_sum where dscore_sum is given."""
+    import torch
+    T, G = logits.shape
+    k = ids.shape[1]
+    xt, ld = _type(logits), _rows(logits, (T, G), logits.dtype)
+    if dlogits is None:
+        dlogits = _mx._empty((T, G), logits.dtype, logits.device, stream)
+    _table(ids, (T, k), torch.int32)
+    _table(dweights, (T, k), torch.float32)
+    _vector(dscore_sum, G, torch.float32)
+    _here(logits, ids, dweights, dscore_sum, dlogits)
+    _mx._check(_mx.load().mx_moe_topk_bwd(logits.data_ptr(), xt, T, G, ld, k, score, 1 if renorm else 0, scale,
+                                          ids.data_ptr(), dweights.data_ptr(), _mx._ptr(dscore_sum),
+                                          dlogits.data_ptr(), _rows(dlogits, (T, G), logits.dtype),
+                                          _mx._stream(stream)))
+    return dlogits
+
+
+def mx_moe_unpermute_bwd(dout, inp, row_of, weights=None, src=None, din=None, dweights=None, stream=None):
+    """The gradient of mx_moe_unpermute(inp, row_of, weights): returns (din, dweights),
+    din[row_of[t, j]] = weights[t, j] dout[t] and dweights[t, j] = <dout[t], inp[row_of[t, j]]>.
+    src (mx_moe_route_index's): the empty rows of din are zeroed; rows that
+    neither names are left as they were."""
+    import torch
+    T, D = dout.shape
+    R, k = inp.shape[0], row_of.shape[1]
+    if din is None:
+        din = _mx._empty((R, D), torch.bfloat16, dout.device, stream)
+    if dweights is None:
+        dweights = _mx._empty((T, k), torch.float32, dout.device, stream)
+    for t, shape, dtype in ((dout, (T, D), torch.bfloat16), (inp, (R, D), torch.bfloat16), (din, (R, D), torch.bfloat16),
+                            (row_of, (T, k), torch.int32), (weights, (T, k), torch.float32), (src, (R,), torch.int32),
+                            (dweights, (T, k), torch.float32)):
+        _table(t, shape, dtype)
+    _here(dout, inp, row_of, weights, src, din, dweights)
+    _mx._check(_mx.load().mx_moe_unpermute_bwd(dout.data_ptr(), T, D, inp.data_ptr(), R, row_of.data_ptr(), k,
+                                               _mx._ptr(weights), _mx._ptr(src), din.data_ptr(), dweights.data_ptr(),
+                                               _mx._stream(stream)))
+    return din, dweights
