@@ -911,6 +911,62 @@ MX_API mx_status_t mx_moe_unpermute_bwd(const void *dout_bf16, int64_t T, int64_
                                         const int32_t *src_dev, void *din_bf16, float *dweights, mx_stream_t stream);
 
 /*
+ * 4-bit tensors with a scale for every 16 values, and their product: weights and
+ * activations of a layer served in 4 bits.
+ *
+ * mx_nvfp4_t -- logical [rows, cols], cols % 32 == 0: value (r, c) is
+ *   E2M1 code (r, c) * E4M3 scale (r, c / 16) * row_scale[r].
+ *   data       packed codes, row-major, cols / 2 bytes a row, the even column in
+ *              the low nibble
+ *   scale      E4M3 bytes (not negative) of the [rows, cols / 16] scale matrix in the
+ *              blocked layout of mx_tensor_t: scale (r, c) at ((r/128) *
+ *              ceil(cols/64) + c/4) * 512 + (r%32)*16 + ((r%128)/32)*4 + c%4,
+ *              padding columns zero; mx_nvfp4_scale_bytes(rows, cols) bytes
+ *   row_scale  fp32 [rows]; as an operand of mx_nvfp4_gemm also NULL (ones).  A
+ *              tensor with one scale for all of it holds that in every row.
+ *
+ * mx_nvfp4_quantize -- BF16 rows to 4 bits in one pass; each row for itself, so
+ *   that a token's result does not depend on the batch around it:
+ *     row_scale = the smallest 2^e >= 2^-100 with amax(row) <= 6 * 448 * 2^e,
+ *     scale = E4M3(amax(16 values) / 2^e / 6), to nearest even,
+ *     code = E2M1(x / (2^e * scale)), to nearest even, saturated (0 where the scale
+ *     is 0; a code of 0 may carry either sign).
+ *   A row with an Inf or a NaN gets row_scale NaN, scales and codes 0.
+ *   x_bf16     device BF16 [T, K], row stride ld
+ *   src_dev    int32 [R]: row r of the output is x's row src[r], zeros where src[r]
+ *              is negative (mx_moe_route_index's); or NULL: R = T, row r itself
+ *   offsets_dev  int32 [G]: rows from offsets[G-1] on are not produced; or NULL
+ *   out        [R, K]
+ *   K % 32 == 0, K <= 32768 (else MX_ERR_NOT_SUPPORTED).  A source index >= T is
+ *   read as a row of zeros and reported as MX_ERR_INVALID_ARG by
+ *   mx_get_device_status.  Without offsets the scale layout's rows past R are
+ *   written as zero.
+ *
+ * mx_nvfp4_gemm -- out[r, n] = sum over k of a[r, k] * b[g(r) * N + n, k], fp32
+ *   accumulation on .kind::mxf4nvf4, the two row scales applied to the fp32 sum, one
+ *   rounding to BF16.
+ *   a          [R, K];  b  [G * N, K], expert g owns rows [g * N, (g + 1) * N)
+ *   offsets_dev  as for mx_grouped_gemm (segments and R multiples of 128); NULL
+ *              with G == 1: all R rows, any number of them
+ *   out_bf16   out, device BF16 [R, N], row stride ld_out; rows past the last
+ *              segment are not written
+ *   K % 32 == 0; N % 8 == 0, with G > 1 N % 128 == 0; G <= 1024 (else
+ *   MX_ERR_NOT_SUPPORTED).  R == 0: MX_OK, nothing is written.
+ */
+typedef struct {
+  void *data;
+  uint8_t *scale;
+  float *row_scale;
+  int64_t rows, cols;
+} mx_nvfp4_t;
+MX_API size_t mx_nvfp4_scale_bytes(int64_t rows, int64_t cols);
+MX_API mx_status_t mx_nvfp4_quantize(const void *x_bf16, int64_t T, int64_t K, int64_t ld, const int32_t *src_dev,
+                                     const int32_t *offsets_dev, int32_t G, const mx_nvfp4_t *out,
+                                     mx_stream_t stream);
+MX_API mx_status_t mx_nvfp4_gemm(const mx_nvfp4_t *a, const mx_nvfp4_t *b, int32_t G, const int32_t *offsets_dev,
+                                 void *out_bf16, int64_t ld_out, mx_stream_t stream);
+
+/*
  * mx_get_device_status -- synchronise `stream`, then report and clear the
  * device-side status words: MX_ERR_DEVICE_TIMEOUT if a bounded wait inside
  * a kernel expired (the kernel unwound; its outputs are undefined),

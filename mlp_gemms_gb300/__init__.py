@@ -47,7 +47,7 @@ ABI_SYMBOLS = (
     "mx_ragged_gemm", "mx_ragged_gemm_wgrad_workspace_bytes", "mx_ragged_gemm_wgrad", "mx_ragged_gemm_wgrad_f32",
     "mx_linear_fwd", "mx_act_ckpt_fwd", "mx_act_ckpt_workspace_bytes", "mx_act_ckpt_bwd", "mx_layernorm_fwd",
     "mx_layernorm_workspace_bytes", "mx_layernorm_bwd", "mx_moe_topk_workspace_bytes", "mx_moe_topk",
-    "mx_moe_topk_bwd", "mx_moe_unpermute_bwd",
+    "mx_moe_topk_bwd", "mx_moe_unpermute_bwd", "mx_nvfp4_scale_bytes", "mx_nvfp4_quantize", "mx_nvfp4_gemm",
 )
 
 
@@ -61,6 +61,11 @@ class MXError(RuntimeError):
 class MxTensorStruct(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("fmt", ctypes.c_int32), ("hadamard", ctypes.c_int32)]
+
+
+class Nvfp4Struct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("row_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
 class MlpArgsStruct(ctypes.Structure):
@@ -164,6 +169,9 @@ def load(path=None):
                                        sz, vp]),
         "mx_moe_topk_bwd": (ctypes.c_int, [vp, i32, i64, i32, i64, i32, i32, i32, f32, vp, vp, vp, vp, i64, vp]),
         "mx_moe_unpermute_bwd": (ctypes.c_int, [vp, i64, i64, vp, i64, vp, i32, vp, vp, vp, vp, vp]),
+        "mx_nvfp4_scale_bytes": (sz, [i64, i64]),
+        "mx_nvfp4_quantize": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, i32, ctypes.POINTER(Nvfp4Struct), vp]),
+        "mx_nvfp4_gemm": (ctypes.c_int, [ctypes.POINTER(Nvfp4Struct), ctypes.POINTER(Nvfp4Struct), i32, vp, vp, i64, vp]),
         "mx_debug_tap": (ctypes.c_int, [vp, i64]),
         "mx_mlp_pipeline_create": (ctypes.c_int, [ctypes.POINTER(MlpArgsStruct), vp, ctypes.POINTER(vp)]),
         "mx_mlp_pipeline_run": (ctypes.c_int, [vp, ctypes.POINTER(HostIOStruct)]),

@@ -243,6 +243,17 @@ mx_status_t make_tmap_bytes(CUtensorMap* m, const void* base, int64_t rows, int6
 
 }  // namespace
 
+mx_status_t mx::encode_packed_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k) {
+  return make_tmap_packed(m, base, rows, k);
+}
+mx_status_t mx::encode_scales_map(CUtensorMap* m, const void* base, int64_t rows, int64_t scale_cols, int blocks,
+                                  int chunks) {
+  return make_tmap_scales(m, base, rows, 32 * scale_cols, blocks, chunks);
+}
+mx_status_t mx::encode_out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld) {
+  return make_tmap_out(m, base, rows, cols, ld);
+}
+
 mx_status_t mx::encode_bf16_map(CUtensorMap* m, const void* base, const TensorMapShape& s) {
   mx_status_t st = get_encoder();
   if (st != MX_OK) return st;
@@ -374,6 +385,14 @@ mx_status_t check_offsets(const int32_t* offsets, int32_t G, int64_t R, cudaStre
   if (env_validate_offsets()) return validate_offsets_values(offsets, G, R, s);
   return MX_OK;
 }
+
+}  // namespace
+
+mx_status_t mx::check_padded_offsets(const int32_t* offsets, int32_t G, int64_t R, cudaStream_t s) {
+  return check_offsets(offsets, G, R, s);
+}
+
+namespace {
 
 // Bytes one pipeline stage completes on its barrier: the A box (128 rows),
 // the B boxes (bn rows) and the scale chunks.  For the packed sub-byte types
@@ -1646,20 +1665,22 @@ mx_status_t mx_mlp_fwd_bwd(const mx_mlp_args_t* a, mx_stream_t stream) { return 
 mx_status_t mx_get_device_status(mx_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-  unsigned word = 0, dense = 0, f4 = 0, quant = 0, perm = 0, pairs = 0, ragged = 0, skinny = 0, route = 0, combine = 0;
+  unsigned word = 0, dense = 0, f4 = 0, quant = 0, perm = 0, pairs = 0, ragged = 0, skinny = 0, route = 0, combine = 0, nvfp4 = 0;
   if ((e = mx::read_gemm_status(&word)) != cudaSuccess || (e = mx::read_dense_status(&dense)) != cudaSuccess ||
       (e = mx::read_f4_status(&f4)) != cudaSuccess || (e = mx::read_quant_status(&quant)) != cudaSuccess ||
       (e = mx::read_perm_status(&perm)) != cudaSuccess || (e = mx::read_pair_status(&pairs)) != cudaSuccess ||
       (e = mx::read_ragged_status(&ragged)) != cudaSuccess || (e = mx::read_skinny_status(&skinny)) != cudaSuccess ||
-      (e = mx::read_route_status(&route)) != cudaSuccess || (e = mx::read_combine_status(&combine)) != cudaSuccess)
+      (e = mx::read_route_status(&route)) != cudaSuccess || (e = mx::read_combine_status(&combine)) != cudaSuccess ||
+      (e = mx::read_nvfp4_status(&nvfp4)) != cudaSuccess)
     return cuda_fail(e, "reading device status");
   if ((e = mx::reset_gemm_status()) != cudaSuccess || (e = mx::reset_dense_status()) != cudaSuccess ||
       (e = mx::reset_f4_status()) != cudaSuccess || (e = mx::reset_quant_status()) != cudaSuccess ||
       (e = mx::reset_perm_status()) != cudaSuccess || (e = mx::reset_pair_status()) != cudaSuccess ||
       (e = mx::reset_ragged_status()) != cudaSuccess || (e = mx::reset_skinny_status()) != cudaSuccess ||
-      (e = mx::reset_route_status()) != cudaSuccess || (e = mx::reset_combine_status()) != cudaSuccess)
+      (e = mx::reset_route_status()) != cudaSuccess || (e = mx::reset_combine_status()) != cudaSuccess ||
+      (e = mx::reset_nvfp4_status()) != cudaSuccess)
     return cuda_fail(e, "clearing device status");
-  word |= dense | f4 | quant | perm | pairs | ragged | skinny | route | combine;
+  word |= dense | f4 | quant | perm | pairs | ragged | skinny | route | combine | nvfp4;
   if (word & 1u) return fail(MX_ERR_DEVICE_TIMEOUT, "a bounded device-side wait expired");
   if (word & 2u) return fail(MX_ERR_OFFSETS, "a kernel saw a malformed offsets segment");
   if (word & 4u) return fail(MX_ERR_INVALID_ARG, "a routing index (expert id or routed row) was out of range");

@@ -13,8 +13,9 @@
 // TMA loads whose bytes are all counted on the leader CTA's stage barrier.
 // The leader's MMA thread issues tcgen05.mma .cta_group::2 (M = 256, N = 256,
 // K = 32 on .kind::mxf8f6f4; K = 64 on .kind::mxf4 for packed E2M1 operands,
-// whose stages hold 256 K-elements and two scale chunks), each CTA's tensor
-// memory holding its 128 x 256 fp32 accumulator,
+// whose stages hold 256 K-elements and two scale chunks; K = 64 on
+// .kind::mxf4nvf4 with E4M3 scales per 16, four scale chunks a stage), each CTA's
+// tensor memory holding its 128 x 256 fp32 accumulator,
 // and its commits arrive on both CTAs' barriers.  A warp of the leader of
 // its own copies each stage's scale chunks into both CTAs' tensor memory
 // (tcgen05.cp .cta_group::2) and signals the MMA thread, which then issues
@@ -36,11 +37,13 @@ namespace pair {
 constexpr int THREADS = 352;                          // producer, MMA, 8 epilogue warps, scale copies
 constexpr int SCALE_WARP = 10;
 constexpr uint32_t SF_TMEM = 256;                     // scale slots after the accumulator
-// F4: packed E2M1 operands on .kind::mxf4 -- a stage's 128-byte rows hold
-// 256 K-elements, i.e. KC = 2 scale chunks per 128-row block.
-template <bool F4> struct PCfg {
-  static constexpr int KC = F4 ? 2 : 1;
-  static constexpr int ST = F4 ? 5 : 6;               // 33.5 KB (35 KB with F4) stages
+// F4, NV4: packed E2M1 operands -- a stage's 128-byte rows hold 256 K-elements,
+// i.e. per 128-row block KC = 2 chunks of scales per 32 (F4, .kind::mxf4) or 4 of
+// scales per 16 (NV4, .kind::mxf4nvf4).
+enum Op : int { MX8 = 0, F4 = 1, NV4 = 2 };
+template <int OP> struct PCfg {
+  static constexpr int KC = OP == NV4 ? 4 : OP == F4 ? 2 : 1;
+  static constexpr int ST = OP == MX8 ? 6 : 5;        // 33.5 KB (F4 35 KB, NV4 38 KB) stages
   static constexpr int A_BYTES = 16384, B_BYTES = 16384;
   // A's KC chunks, then B's two row blocks of KC chunks each
   static constexpr int SF_BYTES = KC * 1536;
@@ -75,13 +78,42 @@ __device__ __forceinline__ PairTile get_pair_tile(const PairParams& p, const int
   return T;
 }
 
-template <bool F4>
+// Row r's and the columns' fp32 scales onto a lane's 128 accumulators (32 a piece).
+__device__ __forceinline__ void scale_rows_cols(const PairParams& p, const PairTile& T, int64_t r, int half,
+                                                uint32_t (&v)[4][32]) {
+  const float rs = p.a_scale == nullptr ? 1.f : r < p.rows ? __ldg(p.a_scale + r) : 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; c++) {
+    const int64_t n = T.n0 + half * 128 + 32 * c;
+    if (n >= p.Nb) break;
+    const float* cs = p.b_scale + T.g * p.Nb + n;
+    const bool whole = p.b_scale != nullptr && n + 32 <= p.Nb && (p.Nb & 3) == 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+      if (whole) {
+        w = __ldg(reinterpret_cast<const float4*>(cs + i));
+      } else if (p.b_scale != nullptr) {
+        w.x = n + i < p.Nb ? __ldg(cs + i) : 0.f;
+        w.y = n + i + 1 < p.Nb ? __ldg(cs + i + 1) : 0.f;
+        w.z = n + i + 2 < p.Nb ? __ldg(cs + i + 2) : 0.f;
+        w.w = n + i + 3 < p.Nb ? __ldg(cs + i + 3) : 0.f;
+      }
+      v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * w.x * rs);
+      v[c][i + 1] = __float_as_uint(__uint_as_float(v[c][i + 1]) * w.y * rs);
+      v[c][i + 2] = __float_as_uint(__uint_as_float(v[c][i + 2]) * w.z * rs);
+      v[c][i + 3] = __float_as_uint(__uint_as_float(v[c][i + 3]) * w.w * rs);
+    }
+  }
+}
+
+template <int OP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::THREADS, 1)
 mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                     const __grid_constant__ CUtensorMap tmO, const PairParams p) {
   using namespace pair;
-  using C = PCfg<F4>;
+  using C = PCfg<OP>;
   constexpr int ST = C::ST, KC = C::KC;
   constexpr int A_BYTES = C::A_BYTES, B_BYTES = C::B_BYTES, SF_BYTES = C::SF_BYTES;
   constexpr int OFF_B = C::OFF_B, OFF_SF = C::OFF_SF;
@@ -128,7 +160,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int64_t pidx = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int nc = (int)(p.K / 128);        // 128-K scale chunks
+  const int nc = OP == NV4 ? (int)((p.K + 63) / 64) : (int)(p.K / 128);  // scale chunks
   const int nk = (nc + KC - 1) / KC;     // stages per tile
 
   if (warp == 0) {
@@ -152,8 +184,8 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             armed[stage] = (int)phase;
           }
           // x: 128 elements (F4: 128 bytes = 256 packed elements) per stage.
-          // F4's last stage of an odd chunk count reads its second half past
-          // K: zero-filled and counted like the rest of the box, read by no MMA.
+          // The last stage of packed operands may read past K: zero-filled and
+          // counted like the rest of the box, and read by no MMA past the last chunk.
           tma2_load_2d(smem + stage * A_BYTES, &tmA, kb * 128, (int)(T.m0 + 128 * rank), fb, pol_a);
           tma2_load_2d(smem + OFF_B + stage * B_BYTES, &tmB, kb * 128, (int)(brow + 128 * rank), fb, pol_b);
           uint8_t* sf = smem + OFF_SF + stage * SF_BYTES;
@@ -175,8 +207,9 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     if (lane == 0 && leader) {
       const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, 2);
       const uint64_t b_desc0 = smem_desc(smem_u32(smem + OFF_B), 16, 1024, 2);
-      const uint32_t idesc0 = F4 ? mma_idesc_mx(MXF4_E2M1, MXF4_E2M1, 256, 256, 0, 0)
-                                 : mma_idesc_mx((uint32_t)p.a_type, (uint32_t)p.b_type, 256, 256, 0, 0);
+      const uint32_t idesc0 = OP == NV4 ? mma_idesc_nvf4(256, 256)
+                              : OP == F4 ? mma_idesc_mx(MXF4_E2M1, MXF4_E2M1, 256, 256, 0, 0)
+                                         : mma_idesc_mx((uint32_t)p.a_type, (uint32_t)p.b_type, 256, 256, 0, 0);
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -192,7 +225,13 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           const uint32_t sf_t = tmem_base + SF_TMEM + (uint32_t)(stage * C::SF_COLS);
           const uint64_t ad = a_desc0 + (uint64_t)((stage * A_BYTES) >> 4);
           const uint64_t bd = b_desc0 + (uint64_t)((stage * B_BYTES) >> 4);
-          if constexpr (F4) {
+          if constexpr (OP == NV4) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)  // K = 64 per MMA, a chunk of scales each
+              if (4 * kb + j < nc)
+                tc2_mma_nvf4(tmem_base, ad + 2 * j, bd + 2 * j, idesc0, sf_t + 4 * j, sf_t + 16 + 8 * j,
+                             (kb | j) != 0 ? 1u : 0u);
+          } else if constexpr (OP == F4) {
             const int nch = (2 * kb + 1 < nc) ? 2 : 1;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -240,18 +279,17 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           tc_fence_after();
           const uint32_t sf_t = tmem_base + SF_TMEM + (uint32_t)(stage * C::SF_COLS);
           const uint64_t sd = sf_desc0 + (uint64_t)((stage * SF_BYTES) >> 4);
-          if constexpr (F4) {
+          if constexpr (OP != MX8) {
             // A's chunk c at column 4c (each CTA its own rows), B's chunk c of
-            // row block i at 8 + 8c + 4i; shared memory holds A's chunks, then
-            // B's row blocks of two chunks
-            const int nch = (2 * kb + 1 < nc) ? 2 : 1;
+            // row block i at 4 KC + 8c + 4i; shared memory holds A's KC chunks,
+            // then B's row blocks of KC chunks
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-              if (c < nch) {
+            for (int c = 0; c < KC; c++) {
+              if (KC * kb + c < nc) {
                 tc2_copy_scales(sf_t + 4 * c, sd + (uint64_t)((512 * c) >> 4));
 #pragma unroll
                 for (int i = 0; i < 2; i++)
-                  tc2_copy_scales(sf_t + 8 + 8 * c + 4 * i, sd + (uint64_t)((1024 + 512 * (2 * i + c)) >> 4));
+                  tc2_copy_scales(sf_t + 4 * KC + 8 * c + 4 * i, sd + (uint64_t)((512 * (KC + KC * i + c)) >> 4));
               }
             }
           } else {
@@ -322,8 +360,11 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       }
       const int64_t row0 = T.m0 + 128 * rank + q * 32;
       if (leader || T.upper) {  // an upper half past the expert's segment is not stored
+        if constexpr (OP == NV4) scale_rows_cols(p, T, row0 + lane, half, v);
 #pragma unroll
         for (int c = 0; c < 4; c++) {
+          // NV4: columns past the expert's are another's, rows past the tensor none
+          if (OP == NV4 && (T.n0 + half * 128 + 32 * c >= p.Nb || row0 >= p.rows)) break;
           stage_reuse_wait(lane);
           store_bf16_block(reinterpret_cast<const float*>(v[c]), stg, lane, &tmO, T.n0 + half * 128 + 32 * c, row0);
         }
@@ -346,16 +387,20 @@ cudaError_t launch_gemm_pair(const PairParams& p, const CUtensorMap& ta, const C
                              int num_sms) {
   int64_t pairs = p.num_tiles < num_sms / 2 ? p.num_tiles : num_sms / 2;
   if (pairs < 1) pairs = 1;
-  if (p.f4) {
-    constexpr int smem = pair::PCfg<true>::SMEM;
-    const cudaError_t e = ensure_smem_attr<mx_gemm_pair_kernel<true>>(smem);
-    if (e != cudaSuccess) return e;
-    mx_gemm_pair_kernel<true><<<(unsigned)(2 * pairs), pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
+  const dim3 grid((unsigned)(2 * pairs));
+  cudaError_t e;
+  if (p.nv4) {
+    constexpr int smem = pair::PCfg<pair::NV4>::SMEM;
+    if ((e = ensure_smem_attr<mx_gemm_pair_kernel<pair::NV4>>(smem)) != cudaSuccess) return e;
+    mx_gemm_pair_kernel<pair::NV4><<<grid, pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
+  } else if (p.f4) {
+    constexpr int smem = pair::PCfg<pair::F4>::SMEM;
+    if ((e = ensure_smem_attr<mx_gemm_pair_kernel<pair::F4>>(smem)) != cudaSuccess) return e;
+    mx_gemm_pair_kernel<pair::F4><<<grid, pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
   } else {
-    constexpr int smem = pair::PCfg<false>::SMEM;
-    const cudaError_t e = ensure_smem_attr<mx_gemm_pair_kernel<false>>(smem);
-    if (e != cudaSuccess) return e;
-    mx_gemm_pair_kernel<false><<<(unsigned)(2 * pairs), pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
+    constexpr int smem = pair::PCfg<pair::MX8>::SMEM;
+    if ((e = ensure_smem_attr<mx_gemm_pair_kernel<pair::MX8>>(smem)) != cudaSuccess) return e;
+    mx_gemm_pair_kernel<pair::MX8><<<grid, pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
   }
   return cudaGetLastError();
 }

@@ -446,6 +446,12 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uin
       : "memory");
 }
 
+// Instruction descriptor of .kind::mxf4nvf4 with packed E2M1 operands and UE4M3
+// scales (bit 23 clear), four scale bytes per row and K = 64 step.
+__host__ __device__ constexpr uint32_t mma_idesc_nvf4(uint32_t M, uint32_t N) {
+  return mma_idesc_mx(MXF4_E2M1, MXF4_E2M1, M, N, 0, 0) & ~(1u << 23);
+}
+
 // 32 lanes x 32 consecutive 32-bit columns -> 32 registers per thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(

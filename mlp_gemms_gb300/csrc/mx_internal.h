@@ -138,6 +138,10 @@ struct PairParams {
   int f4;                  // packed E2M1 operands on .kind::mxf4 (256 K-elements a stage)
   const uint16_t* bias;    // BF16 bias added to the fp32 accumulator before the rounding, or null
   int64_t bias_ld;         // elements between experts' bias rows (0: one row for all)
+  int nv4;                 // packed E2M1 operands with E4M3 scales per 16 (.kind::mxf4nvf4), and with it:
+  int64_t rows;            // rows of A and the output (R: rounded up to 128)
+  const float* a_scale;    // fp32 scale of each row of A, or null (ones)
+  const float* b_scale;    // of each row of B
 };
 cudaError_t launch_gemm_pair(const PairParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
                              const CUtensorMap& tsa, const CUtensorMap& tsb, const CUtensorMap& to, cudaStream_t s,
@@ -328,6 +332,23 @@ cudaError_t launch_combine_bwd(const CombineBwdParams& p, int num_sms, cudaStrea
 cudaError_t read_combine_status(unsigned* out);
 cudaError_t reset_combine_status();
 
+// Quantization to packed E2M1 with E4M3 scales per 16 (nvfp4.cu).
+struct Nvfp4Params {
+  int64_t T, K, R;           // x [T, K], output rows
+  const uint16_t* x;
+  int64_t ld;
+  const int32_t* src;        // [R] or null: row r is x's row src[r], zero where negative
+  const int32_t* offsets;    // or null: rows from offsets[G - 1] on are not produced
+  int G;
+  uint8_t* data;             // [R, K / 2]
+  uint8_t* scale;            // blocked, K / 16 columns
+  float* row_scale;          // [R]
+};
+constexpr int64_t MAX_NVFP4_K = 32768;  // columns whose rows fit a block's registers
+cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, int num_sms, cudaStream_t s);
+cudaError_t read_nvfp4_status(unsigned* out);
+cudaError_t reset_nvfp4_status();
+
 // Host helpers of the ABI layer shared by its translation units (api.cu).
 mx_status_t device_sms(int* sms);   // checks the device; its SM count
 struct TensorMapShape {              // innermost dimension first; strides (bytes) of dimensions 1, 2
@@ -338,6 +359,13 @@ struct TensorMapShape {              // innermost dimension first; strides (byte
 // A BF16 tensor as a TMA operand: 128-byte swizzle, out-of-range elements zero.
 mx_status_t encode_bf16_map(CUtensorMap* m, const void* base, const TensorMapShape& s);
 bool validate_offsets_requested();  // MX_VALIDATE_OFFSETS=1
+// Segments that are multiples of 128 rows (their values only with MX_VALIDATE_OFFSETS=1).
+mx_status_t check_padded_offsets(const int32_t* offsets, int32_t G, int64_t R, cudaStream_t s);
+// The CTA-pair GEMM's maps: packed E2M1 operand [rows, k], blocked scales of
+// scale_cols columns (boxes of `chunks` chunks of `blocks` row blocks), BF16 output.
+mx_status_t encode_packed_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k);
+mx_status_t encode_scales_map(CUtensorMap* m, const void* base, int64_t rows, int64_t scale_cols, int blocks, int chunks);
+mx_status_t encode_out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld);
 
 // The tensors of one MLP step that the host pipeline moves: raw inputs the
 // step reads once (X, W1, W2, dY, b1, b2) and outputs it writes (y, dX, dW1,

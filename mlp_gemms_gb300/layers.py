@@ -204,3 +204,80 @@ def mx_moe_unpermute_bwd(dout, inp, row_of, weights=None, src=None, din=None, dw
                                                _mx._ptr(weights), _mx._ptr(src), din.data_ptr(), dweights.data_ptr(),
                                                _mx._stream(stream)))
     return din, dweights
+
+
+# --------------------------------------------------------------------------
+# 4-bit tensors with a scale for every 16 values
+# --------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def nvfp4_scale_bytes(rows, cols):
+    return int(_mx.load().mx_nvfp4_scale_bytes(rows, cols))
+
+
+class NVFP4:
+    """A 4-bit tensor [rows, cols] in torch buffers: packed E2M1 codes (uint8
+    [rows, cols / 2]), E4M3 scales per 16 values in the blocked layout (uint8),
+    fp32 scale of each row (None as an operand: ones); stream: the one that fills
+    them, where that is not the current one."""
+
+    def __init__(self, rows, cols, device="cuda", data=None, scale=None, row_scale=None, stream=None):
+        import torch
+        self.rows, self.cols = int(rows), int(cols)
+        if data is None:
+            data = _mx._empty((rows, cols // 2), torch.uint8, device, stream)
+            row_scale = row_scale if row_scale is not None else _mx._empty(rows, torch.float32, device, stream)
+        self.data, self.row_scale = data, row_scale
+        self.scale = scale if scale is not None else _mx._empty(nvfp4_scale_bytes(rows, cols), torch.uint8, device, stream)
+
+    def struct(self):
+        return _mx.Nvfp4Struct(self.data.data_ptr(), self.scale.data_ptr(), _mx._ptr(self.row_scale), self.rows, self.cols)
+
+
+def _fp4_buffers(t):
+    """A 4-bit tensor's buffers, dense and as large as its shape needs."""
+    assert t.data.is_contiguous() and t.data.nbytes >= t.rows * (t.cols // 2), "the codes are strided or too few"
+    assert t.scale.is_contiguous() and t.scale.nbytes >= nvfp4_scale_bytes(t.rows, t.cols), \
+        "the scales are strided or too few"
+    import torch
+    _vector(t.row_scale, t.rows, torch.float32)
+    return t.data, t.scale, t.row_scale
+
+
+def mx_nvfp4_quantize(x, src=None, offsets=None, out=None, stream=None):
+    """BF16 rows [T, K] as a 4-bit tensor; src int32 [R]: row r is x's row src[r],
+    zeros where that is negative; offsets: rows from offsets[-1] on are not produced."""
+    import ctypes
+
+    import torch
+    T, K = x.shape
+    R = T if src is None else src.numel()
+    ld = _rows(x, (T, K), torch.bfloat16)
+    _vector(src, R, torch.int32)
+    G = 0 if offsets is None else offsets.numel()
+    _vector(offsets, G, torch.int32)
+    if out is None:
+        out = NVFP4(R, K, x.device, stream=stream)
+    assert out.rows == R and out.cols == K, "a result of another shape"
+    _here(x, src, offsets, *_fp4_buffers(out))
+    _mx._check(_mx.load().mx_nvfp4_quantize(x.data_ptr(), T, K, ld, _mx._ptr(src), _mx._ptr(offsets), G,
+                                            ctypes.byref(out.struct()), _mx._stream(stream)))
+    return out
+
+
+def mx_nvfp4_gemm(a, b, G=1, offsets=None, out=None, stream=None):
+    """out[r] = a[r] b[g(r)]^T in BF16 from 4-bit operands a [R, K], b [G * N, K];
+    rows past the last segment are not written."""
+    import ctypes
+
+    import torch
+    N = b.rows // G if G > 0 else 0
+    _vector(offsets, G, torch.int32)
+    if out is None:
+        out = _mx._empty((a.rows, N), torch.bfloat16, a.data.device, stream)
+    ld = _rows(out, (a.rows, N), torch.bfloat16)
+    data, scale, row_scale = _fp4_buffers(a)
+    _here(data, scale, row_scale, offsets, out, *_fp4_buffers(b))
+    _mx._check(_mx.load().mx_nvfp4_gemm(ctypes.byref(a.struct()), ctypes.byref(b.struct()), G, _mx._ptr(offsets),
+                                        out.data_ptr(), ld, _mx._stream(stream)))
+    return out
