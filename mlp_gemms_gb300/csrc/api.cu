@@ -138,12 +138,12 @@ mx_status_t make_tmap(CUtensorMap* m, const void* base, int64_t rows, int64_t k,
 
 // Packed E2M1 payload [rows, K elements] as bytes (two elements each) for
 // .kind::mxf4: box 128 bytes (256 elements) x 128 rows, 128-byte swizzle.
-mx_status_t make_tmap_packed(CUtensorMap* m, const void* base, int64_t rows, int64_t k) {
+mx_status_t make_tmap_packed(CUtensorMap* m, const void* base, int64_t rows, int64_t k, int box_rows = 128) {
   mx_status_t st = get_encoder();
   if (st != MX_OK) return st;
   cuuint64_t dims[2] = {(cuuint64_t)(k / 2), (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)(k / 2)};
-  cuuint32_t box[2] = {128, 128};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -243,17 +243,13 @@ mx_status_t make_tmap_bytes(CUtensorMap* m, const void* base, int64_t rows, int6
 
 }  // namespace
 
-mx_status_t mx::encode_packed_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k) {
-  return make_tmap_packed(m, base, rows, k);
+mx_status_t mx::encode_packed_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k, int box_rows) {
+  return make_tmap_packed(m, base, rows, k, box_rows);
 }
 mx_status_t mx::encode_scales_map(CUtensorMap* m, const void* base, int64_t rows, int64_t scale_cols, int blocks,
                                   int chunks) {
   return make_tmap_scales(m, base, rows, 32 * scale_cols, blocks, chunks);
 }
-mx_status_t mx::encode_out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld) {
-  return make_tmap_out(m, base, rows, cols, ld);
-}
-
 mx_status_t mx::encode_bf16_map(CUtensorMap* m, const void* base, const TensorMapShape& s) {
   mx_status_t st = get_encoder();
   if (st != MX_OK) return st;

@@ -82,16 +82,22 @@ mx_status_t mx_nvfp4_gemm(const mx_nvfp4_t* a, const mx_nvfp4_t* b, int32_t G, c
   // 256-row tiles per expert segment: at most R / 256 plus one half-filled
   // tile for every expert with an odd number of 128-row blocks
   p.num_tiles = ((p.R + 255) / 256 + (offsets_dev ? (G + 1) / 2 : 0)) * p.n_tiles;
-  // one CTA's stage: 128 bytes of 128 rows of A and B, four scale chunks of A's row block and of both of B's
-  p.tx_bytes = 2u * 16384u + 12u * 512u;
-  CUtensorMap ta, tb, tsa, tsb, to;
-  if ((st = mx::encode_packed_map(&ta, a->data, R, K)) != MX_OK ||
-      (st = mx::encode_packed_map(&tb, b->data, b->rows, K)) != MX_OK ||
+  // Fewer than 128 rows in all: A's boxes end with them.  The MMA's rows past them
+  // hold what the shared memory held, reach only their own outputs and are not
+  // stored.  (Boxes of 128 rows of which 127 lie outside the tensor: 44 us for one
+  // row, 4096 -> 16384; 14 like this.)
+  const int a_rows = R < 128 ? (int)mx::round_up_i64(R, 8) : 128;
+  // one CTA's stage: 128 bytes of A's and B's rows, four scale chunks of A's row block and of both of B's
+  p.tx_bytes = 128u * (uint32_t)a_rows + 16384u + 12u * 512u;
+  p.out = static_cast<uint16_t*>(out_bf16); p.ld_out = ld_out;
+  p.wide = aligned(out_bf16, 32) && ld_out % 16 == 0;
+  CUtensorMap ta, tb, tsa, tsb;
+  if ((st = mx::encode_packed_map(&ta, a->data, R, K, a_rows)) != MX_OK ||
+      (st = mx::encode_packed_map(&tb, b->data, b->rows, K, 128)) != MX_OK ||
       (st = mx::encode_scales_map(&tsa, a->scale, R, K / 16, 1, 4)) != MX_OK ||
-      (st = mx::encode_scales_map(&tsb, b->scale, b->rows, K / 16, 2, 4)) != MX_OK ||
-      (st = mx::encode_out_map(&to, out_bf16, R, N, ld_out)) != MX_OK)
+      (st = mx::encode_scales_map(&tsb, b->scale, b->rows, K / 16, 2, 4)) != MX_OK)
     return st;
-  return cuda_result(mx::launch_gemm_pair(p, ta, tb, tsa, tsb, to, s, sms), "4-bit GEMM launch");
+  return cuda_result(mx::launch_gemm_pair(p, ta, tb, tsa, tsb, ta, s, sms), "4-bit GEMM launch");
 }
 
 }  // extern "C"

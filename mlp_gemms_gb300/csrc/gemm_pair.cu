@@ -34,8 +34,7 @@ namespace mx {
 static __device__ unsigned g_pair_status = 0;
 
 namespace pair {
-constexpr int THREADS = 352;                          // producer, MMA, 8 epilogue warps, scale copies
-constexpr int SCALE_WARP = 10;
+constexpr int SCALE_WARP = 10;                        // after producer, MMA and 8 epilogue warps
 constexpr uint32_t SF_TMEM = 256;                     // scale slots after the accumulator
 // F4, NV4: packed E2M1 operands -- a stage's 128-byte rows hold 256 K-elements,
 // i.e. per 128-row block KC = 2 chunks of scales per 32 (F4, .kind::mxf4) or 4 of
@@ -43,6 +42,11 @@ constexpr uint32_t SF_TMEM = 256;                     // scale slots after the a
 enum Op : int { MX8 = 0, F4 = 1, NV4 = 2 };
 template <int OP> struct PCfg {
   static constexpr int KC = OP == NV4 ? 4 : OP == F4 ? 2 : 1;
+  // Warps that copy scales: NV4's twelve copies a stage are more than one thread
+  // issues beside a stage's MMAs ([8192, 8192] x 8192: one warp 255 us, two 191,
+  // without copies 174).
+  static constexpr int SCALE_WARPS = OP == NV4 ? 2 : 1;
+  static constexpr int THREADS = 32 * (SCALE_WARP + SCALE_WARPS);
   static constexpr int ST = OP == MX8 ? 6 : 5;        // 33.5 KB (F4 35 KB, NV4 38 KB) stages
   static constexpr int A_BYTES = 16384, B_BYTES = 16384;
   // A's KC chunks, then B's two row blocks of KC chunks each
@@ -55,7 +59,7 @@ template <int OP> struct PCfg {
   static constexpr int NUM_BARS = 3 * ST + 5;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;  // tmem slot, abort flag
   static constexpr int OFF_STG = (OFF_MISC + 64 + 1023) / 1024 * 1024;  // eight 2 KB staging buffers
-  static constexpr int OFF_PREF = OFF_STG + 8 * 2048;     // pair row tiles before expert g, g = 0..G
+  static constexpr int OFF_PREF = OFF_STG + (OP == NV4 ? 0 : 8 * 2048);  // (NV4 stores directly) pair row tiles before expert g, g = 0..G
   static constexpr int SMEM = OFF_PREF + 4 * (MAX_PAIR_G + 1) + 1024;  // + slack for 1024-byte alignment
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static_assert(SF_TMEM + ST * SF_COLS <= 512, "scale slots must fit");
@@ -78,37 +82,50 @@ __device__ __forceinline__ PairTile get_pair_tile(const PairParams& p, const int
   return T;
 }
 
-// Row r's and the columns' fp32 scales onto a lane's 128 accumulators (32 a piece).
-__device__ __forceinline__ void scale_rows_cols(const PairParams& p, const PairTile& T, int64_t r, int half,
-                                                uint32_t (&v)[4][32]) {
-  const float rs = p.a_scale == nullptr ? 1.f : r < p.rows ? __ldg(p.a_scale + r) : 0.f;
+// NV4's epilogue: row r's and the columns' fp32 scales onto a lane's 128
+// accumulators (32 a piece), rounded and stored by the lane itself, 32 bytes at a
+// time (whole sectors) where the rows allow: through shared memory and TMA, a
+// piece waits for the last one's copy, and with the scales' loads a tile's
+// epilogue took longer than the 2048-long products of the next (8192 x 8192 x
+// 2048: 91 us, 65 this way).  Rows past the tensor and columns past the
+// expert's (another's) are not stored.
+__device__ __forceinline__ void store_scaled(const PairParams& p, const PairTile& T, int64_t r, int half,
+                                             uint32_t (&v)[4][32]) {
+  if (r >= p.rows) return;
+  const float rs = p.a_scale == nullptr ? 1.f : __ldg(p.a_scale + r);
+  uint16_t* const row = p.out + r * p.ld_out;
 #pragma unroll
   for (int c = 0; c < 4; c++) {
     const int64_t n = T.n0 + half * 128 + 32 * c;
-    if (n >= p.Nb) break;
-    const float* cs = p.b_scale + T.g * p.Nb + n;
-    const bool whole = p.b_scale != nullptr && n + 32 <= p.Nb && (p.Nb & 3) == 0;
+    const int64_t left = p.Nb - n;  // a multiple of 8
+    if (left <= 0) break;
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (whole) {
-        w = __ldg(reinterpret_cast<const float4*>(cs + i));
-      } else if (p.b_scale != nullptr) {
-        w.x = n + i < p.Nb ? __ldg(cs + i) : 0.f;
-        w.y = n + i + 1 < p.Nb ? __ldg(cs + i + 1) : 0.f;
-        w.z = n + i + 2 < p.Nb ? __ldg(cs + i + 2) : 0.f;
-        w.w = n + i + 3 < p.Nb ? __ldg(cs + i + 3) : 0.f;
+    for (int i = 0; i < 32; i += 16) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        float4 cs = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (p.b_scale != nullptr && i + j < left)
+          cs = __ldg(reinterpret_cast<const float4*>(p.b_scale + T.g * p.Nb + n + i + j));
+        const float* a = reinterpret_cast<const float*>(&v[c][i + j]);
+        w[j / 2] = float2_to_bf16x2(a[0] * cs.x * rs, a[1] * cs.y * rs);
+        w[j / 2 + 1] = float2_to_bf16x2(a[2] * cs.z * rs, a[3] * cs.w * rs);
       }
-      v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * w.x * rs);
-      v[c][i + 1] = __float_as_uint(__uint_as_float(v[c][i + 1]) * w.y * rs);
-      v[c][i + 2] = __float_as_uint(__uint_as_float(v[c][i + 2]) * w.z * rs);
-      v[c][i + 3] = __float_as_uint(__uint_as_float(v[c][i + 3]) * w.w * rs);
+      uint16_t* const to = row + n + i;
+      if (p.wide && i + 16 <= left) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     :: "l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+      } else {
+        if (i + 8 <= left) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (i + 16 <= left) *reinterpret_cast<uint4*>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
     }
   }
 }
 
 template <int OP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::PCfg<OP>::THREADS, 1)
 mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                     const __grid_constant__ CUtensorMap tmO, const PairParams p) {
@@ -139,8 +156,8 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     mbar_init(acc_empty, 9);
     mbar_init(final_bar, 1);
     mbar_init(peer_read, 8);
-    for (int s2 = 0; s2 < ST; s2++) mbar_init(&sf_ready[s2], 1);
-    mbar_init(sf_final, 1);
+    for (int s2 = 0; s2 < ST; s2++) mbar_init(&sf_ready[s2], C::SCALE_WARPS);
+    mbar_init(sf_final, C::SCALE_WARPS);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -260,7 +277,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       tc2_commit_local(final_bar);
       mbar_wait_bounded(final_bar, 0, &no_abort, WAIT_BUDGET_NS);
     }
-  } else if (warp == SCALE_WARP) {
+  } else if (warp >= SCALE_WARP) {
     // ------------------------------------------------------------ scale copies (leader)
     // In the MMA thread's stage order: wait for the stage's bytes (both
     // CTAs'), copy its scale chunks into both CTAs' tensor memory and signal
@@ -284,7 +301,8 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
             // row block i at 4 KC + 8c + 4i; shared memory holds A's KC chunks,
             // then B's row blocks of KC chunks
 #pragma unroll
-            for (int c = 0; c < KC; c++) {
+            for (int i0 = 0; i0 < KC / C::SCALE_WARPS; i0++) {
+              const int c = (warp - SCALE_WARP) * (KC / C::SCALE_WARPS) + i0;
               if (KC * kb + c < nc) {
                 tc2_copy_scales(sf_t + 4 * c, sd + (uint64_t)((512 * c) >> 4));
 #pragma unroll
@@ -360,13 +378,14 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       }
       const int64_t row0 = T.m0 + 128 * rank + q * 32;
       if (leader || T.upper) {  // an upper half past the expert's segment is not stored
-        if constexpr (OP == NV4) scale_rows_cols(p, T, row0 + lane, half, v);
+        if constexpr (OP == NV4) {
+          store_scaled(p, T, row0 + lane, half, v);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          // NV4: columns past the expert's are another's, rows past the tensor none
-          if (OP == NV4 && (T.n0 + half * 128 + 32 * c >= p.Nb || row0 >= p.rows)) break;
-          stage_reuse_wait(lane);
-          store_bf16_block(reinterpret_cast<const float*>(v[c]), stg, lane, &tmO, T.n0 + half * 128 + 32 * c, row0);
+          for (int c = 0; c < 4; c++) {
+            stage_reuse_wait(lane);
+            store_bf16_block(reinterpret_cast<const float*>(v[c]), stg, lane, &tmO, T.n0 + half * 128 + 32 * c, row0);
+          }
         }
       }
     }
@@ -392,15 +411,15 @@ cudaError_t launch_gemm_pair(const PairParams& p, const CUtensorMap& ta, const C
   if (p.nv4) {
     constexpr int smem = pair::PCfg<pair::NV4>::SMEM;
     if ((e = ensure_smem_attr<mx_gemm_pair_kernel<pair::NV4>>(smem)) != cudaSuccess) return e;
-    mx_gemm_pair_kernel<pair::NV4><<<grid, pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
+    mx_gemm_pair_kernel<pair::NV4><<<grid, pair::PCfg<pair::NV4>::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
   } else if (p.f4) {
     constexpr int smem = pair::PCfg<pair::F4>::SMEM;
     if ((e = ensure_smem_attr<mx_gemm_pair_kernel<pair::F4>>(smem)) != cudaSuccess) return e;
-    mx_gemm_pair_kernel<pair::F4><<<grid, pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
+    mx_gemm_pair_kernel<pair::F4><<<grid, pair::PCfg<pair::F4>::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
   } else {
     constexpr int smem = pair::PCfg<pair::MX8>::SMEM;
     if ((e = ensure_smem_attr<mx_gemm_pair_kernel<pair::MX8>>(smem)) != cudaSuccess) return e;
-    mx_gemm_pair_kernel<pair::MX8><<<grid, pair::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
+    mx_gemm_pair_kernel<pair::MX8><<<grid, pair::PCfg<pair::MX8>::THREADS, smem, s>>>(ta, tb, tsa, tsb, to, p);
   }
   return cudaGetLastError();
 }

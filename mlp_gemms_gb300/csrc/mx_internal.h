@@ -141,7 +141,10 @@ struct PairParams {
   int nv4;                 // packed E2M1 operands with E4M3 scales per 16 (.kind::mxf4nvf4), and with it:
   int64_t rows;            // rows of A and the output (R: rounded up to 128)
   const float* a_scale;    // fp32 scale of each row of A, or null (ones)
-  const float* b_scale;    // of each row of B
+  const float* b_scale;    // of each row of B (null: ones)
+  uint16_t* out;           // BF16 [rows, Nb]
+  int64_t ld_out;
+  int wide;                // rows that start on 32 bytes
 };
 cudaError_t launch_gemm_pair(const PairParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
                              const CUtensorMap& tsa, const CUtensorMap& tsb, const CUtensorMap& to, cudaStream_t s,
@@ -362,10 +365,9 @@ bool validate_offsets_requested();  // MX_VALIDATE_OFFSETS=1
 // Segments that are multiples of 128 rows (their values only with MX_VALIDATE_OFFSETS=1).
 mx_status_t check_padded_offsets(const int32_t* offsets, int32_t G, int64_t R, cudaStream_t s);
 // The CTA-pair GEMM's maps: packed E2M1 operand [rows, k], blocked scales of
-// scale_cols columns (boxes of `chunks` chunks of `blocks` row blocks), BF16 output.
-mx_status_t encode_packed_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k);
+// scale_cols columns (boxes of `chunks` chunks of `blocks` row blocks).
+mx_status_t encode_packed_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k, int box_rows);
 mx_status_t encode_scales_map(CUtensorMap* m, const void* base, int64_t rows, int64_t scale_cols, int blocks, int chunks);
-mx_status_t encode_out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld);
 
 // The tensors of one MLP step that the host pipeline moves: raw inputs the
 // step reads once (X, W1, W2, dY, b1, b2) and outputs it writes (y, dX, dW1,

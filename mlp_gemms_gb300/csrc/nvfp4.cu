@@ -23,21 +23,26 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a) {
 // -100), for every 16 values the scale s = E4M3(block amax / 2^e / 6), for every
 // value the E2M1 code nearest to x / (2^e s), of two equally near ones the even.
 //
-// The quotient's rounding must not decide: x has 8 significant bits, s 4, a
-// midpoint m of two codes 3, so x / (2^e s) either is m or differs from it by at
-// least 1 / 255 of its value, 2^-10 for the smallest (m = 1 / 4).  The product with
-// the rounded reciprocal is off by 2^-22, and adding and taking away 6144 rounds
+// No rounding on the way may decide.  x has 8 significant bits, s 4, a midpoint m
+// of two codes 3: so x / (2^e s) either is m or differs from it by at least 1 / 255
+// of its value, 2^-10 for the smallest (m = 1 / 4).  The product with the
+// approximate reciprocal is off by 2^-22, and adding and taking away 6144 rounds
 // it to a multiple of 2^-11: a quotient that is a midpoint becomes exactly that,
-// and none crosses one.
+// and none crosses one.  Likewise amax / 6 and the E4M3 midpoints (5 bits): the
+// product with fl(1 / 6), off by 2^-25, rounds to a midpoint where the quotient is
+// one (their significands are at most 1.9375, half a unit is then more than that).
 //
-// Bound by memory (2 bytes read, 9 / 16 written a value).  A group of W warps
-// holds a row in its registers, 16 values a lane and piece, as the norm does.
+// Reads 2 bytes and writes 9 / 16 a value, but about six instructions a value are
+// the nearer limit.  A group of W warps holds a row in its registers, 16 values a
+// lane and piece; the next row's loads (and the source after that) are issued
+// before this row's maximum is exchanged.
 template <int C>
 __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p, int W) {
   __shared__ uint32_t part[2][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / W, wr = warp - group * W, groups = (blockDim.x >> 5) / W;
-  const int64_t c0 = ((int64_t)wr * 32 + lane) * 16, step = (int64_t)W * 512, sc = p.K >> 4;
+  const int c0 = (wr * 32 + lane) * 16, step = W * 512, K = (int)p.K;
+  const int64_t chunks = (p.K + 63) >> 6, stride = (int64_t)gridDim.x * groups;
   int flip = 0;
   pdl_trigger();
   pdl_wait();
@@ -46,35 +51,43 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
     const int64_t end = *(p.offsets + p.G - 1);
     rows = end < 0 ? 0 : end < rows ? end : rows;
   }
-  for (int64_t r = (int64_t)blockIdx.x * groups + group; r < rows; r += (int64_t)gridDim.x * groups) {
-    int64_t from = r;
-    if (p.src != nullptr) {
-      from = *(p.src + r);
-      if (from >= p.T) {
-        if (wr == 0 && lane == 0) atomicOr(&g_nvfp4_status, DEV_BAD_INDEX);
-        from = -1;
-      }
-    }
-    uint4 x[C][2];
-    uint32_t amax[C], top = 0;
+  const auto source = [&](int64_t r) -> int64_t {
+    if (r >= rows) return -1;
+    if (p.src == nullptr) return r;
+    const int64_t from = *(p.src + r);
+    if (from < p.T) return from;
+    if (wr == 0 && lane == 0) atomicOr(&g_nvfp4_status, DEV_BAD_INDEX);
+    return -1;
+  };
+  uint4 next[C][2];
+  const auto load_row = [&](int64_t from) {
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int64_t at = c0 + c * step;
-      x[c][0] = x[c][1] = make_uint4(0, 0, 0, 0);
-      if (from >= 0 && at < p.K) {
-        x[c][0] = load_stream16(p.x + from * p.ld + at);
-        x[c][1] = load_stream16(p.x + from * p.ld + at + 8);
+      const int at = c0 + c * step;
+      next[c][0] = next[c][1] = make_uint4(0, 0, 0, 0);
+      if (from >= 0 && at < K) {
+        next[c][0] = load_stream16(p.x + from * p.ld + at);
+        next[c][1] = load_stream16(p.x + from * p.ld + at + 8);
       }
     }
+  };
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  load_row(source(r));
+  int64_t after = source(r + stride);
+  for (; r < rows; r += stride) {
+    uint32_t x[C][8], amax[C], top = 0;
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      uint32_t a = max_abs_bf16x2(x[c][0].x, x[c][0].y);
-      a = max_abs_bf16x2(a, max_abs_bf16x2(x[c][0].z, x[c][0].w));
-      a = max_abs_bf16x2(a, max_abs_bf16x2(x[c][1].x, x[c][1].y));
-      a = max_abs_bf16x2(a, max_abs_bf16x2(x[c][1].z, x[c][1].w));
-      amax[c] = max_halves(a);
+      const uint4 a = next[c][0], b = next[c][1];
+      x[c][0] = a.x; x[c][1] = a.y; x[c][2] = a.z; x[c][3] = a.w;
+      x[c][4] = b.x; x[c][5] = b.y; x[c][6] = b.z; x[c][7] = b.w;
+      const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(x[c][0], x[c][1]), max_abs_bf16x2(x[c][2], x[c][3])),
+                                        max_abs_bf16x2(max_abs_bf16x2(x[c][4], x[c][5]), max_abs_bf16x2(x[c][6], x[c][7])));
+      amax[c] = max_halves(m);
       top = amax[c] > top ? amax[c] : top;
     }
+    load_row(after);
+    after = source(r + 2 * stride);
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (W > 1) {
       if (lane == 0) part[flip][warp] = top;
@@ -88,60 +101,73 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
     const bool finite = top < 0x7F80u;
     int e = (int)(top >> 7) - 127 - 11 + ((top & 0x7Fu) > 40u ? 1 : 0);  // 6 * 448 = 1.3125 * 2^11; 40 / 128 = 0.3125
     e = e < -100 ? -100 : e;
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, e in [-100, 117]
+    const float down = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;  // 2^-e, e in [-100, 117]
     if (wr == 0 && lane == 0)
       p.row_scale[r] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+    // scale (r, c) of the blocked layout: the row's place in a chunk, then a chunk every four columns
+    uint8_t* const scales = p.scale + (r >> 7) * chunks * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+    uint8_t* const data = p.data + r * (p.K >> 1);
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int64_t at = c0 + c * step;
-      const float want = __fdiv_rn(bf16_bits_to_float(amax[c]) * down, 6.f);
-      const uint32_t s8 = finite ? cvt_e4m3x2(want, 0.f) & 0xFFu : 0u;
+      const int at = c0 + c * step;
+      const float want = finite ? bf16_bits_to_float(amax[c]) * down * (1.f / 6.f) : 0.f;
+      const uint32_t s8 = cvt_e4m3x2(want, 0.f) & 0xFFu;
       uint32_t h;
-      float s, unused;
+      float s, inv;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)s8));
-      asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
-          : "=f"(s), "=f"(unused) : "r"(h));
-      const float inv = s8 == 0 ? 0.f : __fdiv_rn(1.f, s) * down;
-      const uint32_t w[8] = {x[c][0].x, x[c][0].y, x[c][0].z, x[c][0].w, x[c][1].x, x[c][1].y, x[c][1].z, x[c][1].w};
-      uint32_t out[2] = {0, 0};
+      asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(s) : "r"(h));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+      inv = s8 == 0 ? 0.f : inv * down;
+      uint32_t out[2];
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        float lo, hi;
-        const uint64_t v = pack2(bf16_bits_to_float(w[i] & 0xFFFFu), __uint_as_float(w[i] & 0xFFFF0000u));
-        unpack2(add2(fma2(v, both(inv), both(6144.f)), both(-6144.f)), &lo, &hi);
-        out[i >> 2] |= cvt_e2m1x2(lo, hi) << (8 * (i & 3));
+      for (int o = 0; o < 2; o++) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          float lo, hi;
+          const uint32_t w = x[c][4 * o + i];
+          const uint64_t v = pack2(bf16_bits_to_float(w & 0xFFFFu), __uint_as_float(w & 0xFFFF0000u));
+          unpack2(add2(fma2(v, both(inv), both(6144.f)), both(-6144.f)), &lo, &hi);
+          b[i] = cvt_e2m1x2(lo, hi);
+        }
+        out[o] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        if (!finite) out[o] = 0;  // Inf * 0 is a NaN
       }
-      if (at < p.K)
-        *reinterpret_cast<uint2*>(p.data + r * (p.K >> 1) + (at >> 1)) = finite ? make_uint2(out[0], out[1]) : make_uint2(0, 0);
       // the scale bytes of four lanes make a word of the blocked layout; past the
       // row's last block they are the padding's zeros
-      uint32_t word = at < p.K ? s8 : 0u;
+      uint32_t word = at < K ? s8 : 0u;
       word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1) << 8;
       word = (word & 0xFFFFu) | __shfl_xor_sync(0xFFFFFFFFu, word, 2) << 16;
-      if ((lane & 3) == 0 && at < p.K) *reinterpret_cast<uint32_t*>(p.scale + blocked_offset(r, at >> 4, sc)) = word;
+      if (at < K) {
+        *reinterpret_cast<uint2*>(data + (at >> 1)) = make_uint2(out[0], out[1]);
+        if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(scales + (at >> 6) * 512) = word;
+      }
     }
   }
-  if (blockIdx.x == 0 && p.offsets == nullptr) {  // the layout's rows past the last
-    const int64_t chunks = (sc + 3) / 4, top_row = (p.R + 127) / 128 * 128;
-    for (int64_t i = threadIdx.x; i < (top_row - p.R) * chunks; i += blockDim.x)
-      *reinterpret_cast<uint32_t*>(p.scale + blocked_offset(p.R + i / chunks, i % chunks * 4, sc)) = 0u;
+  if ((p.R & 127) != 0 && p.offsets == nullptr) {
+    // the layout's rows past the last: a warp takes a chunk of the last row block,
+    // a lane the four rows that share its 16 bytes
+    const int first = (int)(p.R & 127);
+    for (int64_t c = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp; c < chunks; c += (int64_t)gridDim.x * (blockDim.x >> 5)) {
+      uint32_t* const to = reinterpret_cast<uint32_t*>(p.scale + ((p.R >> 7) * chunks + c) * 512 + lane * 16);
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        if (32 * q + lane >= first) to[q] = 0u;
+    }
   }
 }
 
 cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, int num_sms, cudaStream_t s) {
   const int64_t v = (p.K + 15) / 16;
   int W = 1;
-  while ((int64_t)W * 32 * 4 < v && W < 16) W *= 2;
+  while ((int64_t)W * 32 * 2 < v && W < 16) W *= 2;
   const int C = (int)((v + 32 * W - 1) / (32 * W));
   const int threads = W * 32 > 256 ? W * 32 : 256, groups = threads / (32 * W);
-  const int64_t want = (p.R + groups - 1) / groups, cap = (int64_t)num_sms * 16;
+  const int64_t want = (p.R + groups - 1) / groups, cap = (int64_t)num_sms * (threads > 256 ? 4 : 8);
   const dim3 grid((unsigned)(want < cap ? want : cap));
-  switch (C) {
-    case 1: return launch_pdl(nvfp4_quantize_kernel<1>, grid, threads, 0, s, dim3(1), p, W);
-    case 2: return launch_pdl(nvfp4_quantize_kernel<2>, grid, threads, 0, s, dim3(1), p, W);
-    case 3: return launch_pdl(nvfp4_quantize_kernel<3>, grid, threads, 0, s, dim3(1), p, W);
-    default: return launch_pdl(nvfp4_quantize_kernel<4>, grid, threads, 0, s, dim3(1), p, W);
-  }
+  if (C == 1) return launch_pdl(nvfp4_quantize_kernel<1>, grid, threads, 0, s, dim3(1), p, W);
+  if (C == 2) return launch_pdl(nvfp4_quantize_kernel<2>, grid, threads, 0, s, dim3(1), p, W);
+  return launch_pdl(nvfp4_quantize_kernel<4>, grid, threads, 0, s, dim3(1), p, W);
 }
 
 cudaError_t read_nvfp4_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_nvfp4_status, sizeof(unsigned)); }
