@@ -937,6 +937,9 @@ MX_API mx_status_t mx_moe_unpermute_bwd(const void *dout_bf16, int64_t T, int64_
  *              is negative (mx_moe_route_index's); or NULL: R = T, row r itself
  *   offsets_dev  int32 [G]: rows from offsets[G-1] on are not produced; or NULL
  *   out        [R, K]
+ *   workspace  NULL, or with src at least mx_nvfp4_quantize_workspace_bytes(T, K, R)
+ *              bytes: where that is not 0 each token is then quantized once and
+ *              copied to the rows that name it.  The same bytes either way.
  *   K % 32 == 0, K <= 32768 (else MX_ERR_NOT_SUPPORTED).  A source index >= T is
  *   read as a row of zeros and reported as MX_ERR_INVALID_ARG by
  *   mx_get_device_status.  Without offsets the scale layout's rows past R are
@@ -960,9 +963,10 @@ typedef struct {
   int64_t rows, cols;
 } mx_nvfp4_t;
 MX_API size_t mx_nvfp4_scale_bytes(int64_t rows, int64_t cols);
+MX_API size_t mx_nvfp4_quantize_workspace_bytes(int64_t T, int64_t K, int64_t R);
 MX_API mx_status_t mx_nvfp4_quantize(const void *x_bf16, int64_t T, int64_t K, int64_t ld, const int32_t *src_dev,
-                                     const int32_t *offsets_dev, int32_t G, const mx_nvfp4_t *out,
-                                     mx_stream_t stream);
+                                     const int32_t *offsets_dev, int32_t G, const mx_nvfp4_t *out, void *workspace,
+                                     size_t workspace_bytes, mx_stream_t stream);
 MX_API mx_status_t mx_nvfp4_gemm(const mx_nvfp4_t *a, const mx_nvfp4_t *b, int32_t G, const int32_t *offsets_dev,
                                  void *out_bf16, int64_t ld_out, mx_stream_t stream);
 

@@ -47,7 +47,8 @@ ABI_SYMBOLS = (
     "mx_ragged_gemm", "mx_ragged_gemm_wgrad_workspace_bytes", "mx_ragged_gemm_wgrad", "mx_ragged_gemm_wgrad_f32",
     "mx_linear_fwd", "mx_act_ckpt_fwd", "mx_act_ckpt_workspace_bytes", "mx_act_ckpt_bwd", "mx_layernorm_fwd",
     "mx_layernorm_workspace_bytes", "mx_layernorm_bwd", "mx_moe_topk_workspace_bytes", "mx_moe_topk",
-    "mx_moe_topk_bwd", "mx_moe_unpermute_bwd", "mx_nvfp4_scale_bytes", "mx_nvfp4_quantize", "mx_nvfp4_gemm",
+    "mx_moe_topk_bwd", "mx_moe_unpermute_bwd", "mx_nvfp4_scale_bytes",
+    "mx_nvfp4_quantize_workspace_bytes", "mx_nvfp4_quantize", "mx_nvfp4_gemm",
 )
 
 
@@ -170,7 +171,8 @@ def load(path=None):
         "mx_moe_topk_bwd": (ctypes.c_int, [vp, i32, i64, i32, i64, i32, i32, i32, f32, vp, vp, vp, vp, i64, vp]),
         "mx_moe_unpermute_bwd": (ctypes.c_int, [vp, i64, i64, vp, i64, vp, i32, vp, vp, vp, vp, vp]),
         "mx_nvfp4_scale_bytes": (sz, [i64, i64]),
-        "mx_nvfp4_quantize": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, i32, ctypes.POINTER(Nvfp4Struct), vp]),
+        "mx_nvfp4_quantize_workspace_bytes": (sz, [i64, i64, i64]),
+        "mx_nvfp4_quantize": (ctypes.c_int, [vp, i64, i64, i64, vp, vp, i32, ctypes.POINTER(Nvfp4Struct), vp, sz, vp]),
         "mx_nvfp4_gemm": (ctypes.c_int, [ctypes.POINTER(Nvfp4Struct), ctypes.POINTER(Nvfp4Struct), i32, vp, vp, i64, vp]),
         "mx_debug_tap": (ctypes.c_int, [vp, i64]),
         "mx_mlp_pipeline_create": (ctypes.c_int, [ctypes.POINTER(MlpArgsStruct), vp, ctypes.POINTER(vp)]),
@@ -883,11 +885,19 @@ def mx_last_error():
     return load().mx_last_error().decode()
 
 
+_layers = None
+
+
 def __getattr__(name):
     """The layers around the expert MLP are part of this namespace and live in
     layers.py, which loads with the first of them."""
-    if name.startswith("mx_") or name == "NVFP4":
-        from . import layers
-        if hasattr(layers, name):
-            return getattr(layers, name)
-    raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    global _layers
+    if _layers is None:
+        if name[:3] != "mx_" and name not in ("NVFP4", "nvfp4_scale_bytes"):
+            raise AttributeError("module %r has no attribute %r" % (__name__, name))
+        import importlib
+        _layers = importlib.import_module(__name__ + ".layers")
+    try:
+        return _layers.__dict__[name]
+    except KeyError:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name)) from None

@@ -76,7 +76,9 @@ mx_status_t mx_layernorm_fwd(const void* x, int32_t x_type, int64_t R, int64_t D
 
 size_t mx_layernorm_workspace_bytes(int64_t R, int64_t D) {
   if (R <= 0 || D <= 0 || D > mx::MAX_NORM_D) return 0;
-  return (size_t)mx::norm_bwd_blocks(R, D) * 2 * (size_t)D * sizeof(float);
+  int64_t blocks = mx::norm_bwd_blocks(R, D, false);
+  if (mx::norm_bwd_blocks(R, D, true) > blocks) blocks = mx::norm_bwd_blocks(R, D, true);
+  return (size_t)blocks * 2 * (size_t)D * sizeof(float);
 }
 
 mx_status_t mx_layernorm_bwd(const void* dy_bf16, int64_t ld_dy, const void* x, int32_t x_type, int64_t R, int64_t D,

@@ -32,8 +32,14 @@ size_t mx_nvfp4_scale_bytes(int64_t rows, int64_t cols) {
   return mx::scale_bytes(rows, (cols + 15) / 16);
 }
 
+size_t mx_nvfp4_quantize_workspace_bytes(int64_t T, int64_t K, int64_t R) {
+  if (T <= 0 || K <= 0 || R <= 0 || T >= (1ll << 31) || K > mx::MAX_NVFP4_K || R >= (1ll << 31)) return 0;
+  return mx::nvfp4_workspace(T, K, R);
+}
+
 mx_status_t mx_nvfp4_quantize(const void* x_bf16, int64_t T, int64_t K, int64_t ld, const int32_t* src_dev,
-                              const int32_t* offsets_dev, int32_t G, const mx_nvfp4_t* out, mx_stream_t stream) {
+                              const int32_t* offsets_dev, int32_t G, const mx_nvfp4_t* out, void* workspace,
+                              size_t workspace_bytes, mx_stream_t stream) {
   mx_status_t st;
   if ((st = check_dim(K, "K", 32)) != MX_OK) return st;
   MX_CHECK(K <= mx::MAX_NVFP4_K, MX_ERR_NOT_SUPPORTED, "K = %lld; rows of at most %lld columns", (long long)K,
@@ -44,6 +50,8 @@ mx_status_t mx_nvfp4_quantize(const void* x_bf16, int64_t T, int64_t K, int64_t 
            (long long)out->rows, (long long)out->cols);
   MX_CHECK(aligned(src_dev, 4) && aligned(offsets_dev, 4), MX_ERR_ALIGNMENT, "src and offsets must be 4-byte aligned");
   MX_CHECK(offsets_dev == nullptr || G >= 1, MX_ERR_INVALID_ARG, "G = %d; at least one expert is required", G);
+  const size_t need = src_dev && workspace ? mx_nvfp4_quantize_workspace_bytes(T, K, out->rows) : 0;
+  if ((st = mx::check_workspace(workspace, workspace_bytes, need)) != MX_OK) return st;
   if (out->rows == 0) return MX_OK;
   int sms;
   if ((st = mx::device_sms(&sms)) != MX_OK) return st;
@@ -52,7 +60,8 @@ mx_status_t mx_nvfp4_quantize(const void* x_bf16, int64_t T, int64_t K, int64_t 
   p.x = static_cast<const uint16_t*>(x_bf16); p.ld = ld;
   p.src = src_dev; p.offsets = offsets_dev; p.G = G;
   p.data = static_cast<uint8_t*>(out->data); p.scale = out->scale; p.row_scale = out->row_scale;
-  return cuda_result(mx::launch_nvfp4_quantize(p, sms, reinterpret_cast<cudaStream_t>(stream)), "quantization launch");
+  return cuda_result(mx::launch_nvfp4_quantize(p, need ? workspace : nullptr, sms,
+                                               reinterpret_cast<cudaStream_t>(stream)), "quantization launch");
 }
 
 mx_status_t mx_nvfp4_gemm(const mx_nvfp4_t* a, const mx_nvfp4_t* b, int32_t G, const int32_t* offsets_dev,

@@ -288,7 +288,7 @@ struct NormParams {
   float* partials;           // [norm_bwd_blocks][2][D]
 };
 constexpr int64_t MAX_NORM_D = 16384;  // columns whose rows fit a block's registers
-int64_t norm_bwd_blocks(int64_t R, int64_t D);
+int64_t norm_bwd_blocks(int64_t R, int64_t D, bool x_f32);
 cudaError_t launch_norm_fwd(const NormParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s);
 
@@ -346,9 +346,12 @@ struct Nvfp4Params {
   uint8_t* data;             // [R, K / 2]
   uint8_t* scale;            // blocked, K / 16 columns
   float* row_scale;          // [R]
+  int linear;                // scales row-major, whole words a row (the launch's own, in its workspace)
 };
 constexpr int64_t MAX_NVFP4_K = 32768;  // columns whose rows fit a block's registers
-cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, int num_sms, cudaStream_t s);
+size_t nvfp4_workspace(int64_t T, int64_t K, int64_t R);  // 0: none used
+// workspace: nvfp4_workspace(T, K, R) bytes, or null
+cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, void* workspace, int num_sms, cudaStream_t s);
 cudaError_t read_nvfp4_status(unsigned* out);
 cudaError_t reset_nvfp4_status();
 

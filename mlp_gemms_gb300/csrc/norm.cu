@@ -7,9 +7,28 @@
 namespace mx {
 
 // Both kernels are bound by memory: every value is read once and written once.
-// A row is held in the registers of `W` warps (a power of two), 8 C columns a
-// lane, so that its statistics, its centred squares and its result need no
+// A row is held in the registers of `W` warps, 8 C columns a lane, so that its statistics, its centred squares and its result need no
 // second read; a block's warps form groups of W, each with a row of its own.
+
+// A vector [8 n8] of all rows in shared memory, as fp32: the first four values of
+// each lane's eight, then the last four, so that neighbouring lanes read
+// neighbouring 16 bytes.
+__device__ __forceinline__ void keep_vector(const void* p, bool f32, int n8, float4* to) {
+  if (p == nullptr) return;
+  for (int i = threadIdx.x; i < n8; i += blockDim.x) {
+    float v[8];
+    load_shared8(p, f32, (int64_t)i * 8, v);
+    to[i] = make_float4(v[0], v[1], v[2], v[3]);
+    to[n8 + i] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+__device__ __forceinline__ void kept_pairs(const float4* kept, int n8, int i, uint64_t (&v)[4]) {
+  const float4 a = kept[i], b = kept[n8 + i];
+  v[0] = pack2(a.x, a.y);
+  v[1] = pack2(a.z, a.w);
+  v[2] = pack2(b.x, b.y);
+  v[3] = pack2(b.z, b.w);
+}
 
 // The group's barrier: its W warps, W > 1.
 __device__ __forceinline__ void group_bar(int group, int W) { named_bar(1 + group, 32 * W); }
@@ -19,68 +38,84 @@ __device__ __forceinline__ void group_bar(int group, int W) { named_bar(1 + grou
 // and the squares around that, and the parts join as
 //   mean = sum n_w mean_w / D,  M2 = sum (M2_w + n_w (mean_w - mean)^2)
 // (Chan, Golub and LeVeque's pairwise formula).
-template <bool F32, int C, bool RES>
+// Weight and bias wait in shared memory, as fp32, and the next row's loads are
+// issued before this row's sums are exchanged.  FULL: the group's columns are the
+// row's, with no lane past its end.
+template <bool F32, int C, bool RES, bool FULL>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int W) {
+  extern __shared__ float4 vectors[];
   __shared__ float2 part[2][16];
   __shared__ float count[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / W, wr = warp - group * W, groups = (blockDim.x >> 5) / W;
-  const int64_t c0 = ((int64_t)wr * 32 + lane) * 8, step = (int64_t)W * 256;
+  const int D = (int)p.D, c0 = (wr * 32 + lane) * 8, step = W * 256;
+  const auto in = [&](int c) { return FULL || c0 + c * step < D; };
   int n_lane = 0;
 #pragma unroll
-  for (int c = 0; c < C; c++) n_lane += c0 + c * step < p.D ? 8 : 0;
-  const float n_w = warp_sum((float)n_lane), inv_nw = n_w > 0.f ? 1.f / n_w : 0.f, inv_d = 1.f / (float)p.D;
+  for (int c = 0; c < C; c++) n_lane += in(c) ? 8 : 0;
+  const float n_w = FULL ? (float)(C * 256) : warp_sum((float)n_lane);
+  const float inv_nw = n_w > 0.f ? 1.f / n_w : 0.f, inv_d = 1.f / (float)D;
   if (lane == 0) count[warp] = n_w;
   int flip = 0;
-  pdl_trigger();
-  pdl_wait();
-  for (int64_t r = (int64_t)blockIdx.x * groups + group; r < p.R; r += (int64_t)gridDim.x * groups) {
-    float v[C][8];
+  Raw8<F32> next[C], next_res[RES ? C : 1];
+  const auto load_row = [&](int64_t r) {
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int64_t at = c0 + c * step;
-      if (at < p.D) {
-        unpack_raw8<F32>(load_raw8<F32>(p.x, r * p.ld_x + at), v[c]);
-        if constexpr (RES) {
-          float a[8];
-          unpack_raw8<F32>(load_raw8<F32>(p.res, r * p.ld_res + at), a);
+      if (!FULL) next[c] = {};
+      if (!in(c)) continue;
+      next[c] = load_raw8<F32>(p.x, r * p.ld_x + c0 + c * step);
+      if constexpr (RES) next_res[c] = load_raw8<F32>(p.res, r * p.ld_res + c0 + c * step);
+    }
+  };
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  pdl_trigger();
+  pdl_wait();
+  if (r < p.R) load_row(r);
+  const int n8 = D >> 3;
+  keep_vector(p.weight, p.w_f32, n8, vectors);
+  keep_vector(p.bias, p.w_f32, n8, vectors + 2 * n8);
+  __syncthreads();
+  for (; r < p.R; r += stride) {
+    uint64_t v[C][4], total[4] = {}, squares[4] = {};  // four sums each: short chains
 #pragma unroll
-          for (int i = 0; i < 8; i++) a[i] += v[c][i];
-          const Raw8<F32> s = pack_raw8<F32>(a);  // the stream's own rounding: what the norm and its backward pass see
-          store_raw8<F32>(p.sum, r * p.ld_sum + at, s);
-          unpack_raw8<F32>(s, v[c]);
+    for (int c = 0; c < C; c++) {
+      unpack_pairs<F32>(next[c], v[c]);
+      if constexpr (RES) {
+        if (in(c)) {
+          uint64_t a[4];
+          unpack_pairs<F32>(next_res[c], a);
+#pragma unroll
+          for (int i = 0; i < 4; i++) a[i] = add2(a[i], v[c][i]);
+          const Raw8<F32> s = pack_pairs<F32>(a);  // the stream's own rounding: what the norm and its backward pass see
+          store_raw8<F32>(p.sum, r * p.ld_sum + c0 + c * step, s);
+          unpack_pairs<F32>(s, v[c]);
         }
-      } else {
+      }
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[c][i] = 0.f;
+      for (int i = 0; i < 4; i++) total[i] = add2(total[i], v[c][i]);
+    }
+    if (r + stride < p.R) load_row(r + stride);
+    float mean = p.rms ? 0.f : warp_sum(sum_pairs(total)) * inv_nw;
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+      if (!in(c)) continue;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint64_t d = add2(v[c][i], both(-mean));
+        squares[i] = fma2(d, d, squares[i]);
       }
     }
-    float mean = 0.f;
-    if (!p.rms) {
-#pragma unroll
-      for (int c = 0; c < C; c++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) mean += v[c][i];
-      mean = warp_sum(mean) * inv_nw;
-    }
-    float m2 = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const float d = v[c][i] - mean;
-        m2 = c0 + c * step < p.D ? fmaf(d, d, m2) : m2;
-      }
-    m2 = warp_sum(m2);
+    float m2 = warp_sum(sum_pairs(squares));
     if (W > 1) {
       if (lane == 0) part[flip][warp] = make_float2(mean, m2);
       group_bar(group, W);
       const float2* q = &part[flip][group * W];
-      float total = 0.f;
-      m2 = 0.f;
       const float* n = &count[group * W];
-      for (int w = 0; w < W; w++) total = fmaf(q[w].x, n[w], total);
-      mean = total * inv_d;
+      float sum = 0.f;
+      m2 = 0.f;
+      for (int w = 0; w < W; w++) sum = fmaf(q[w].x, n[w], sum);
+      mean = sum * inv_d;
       for (int w = 0; w < W; w++) {
         const float d = q[w].x - mean;
         m2 += fmaf(d * d, n[w], q[w].y);
@@ -94,22 +129,22 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int W
     }
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int64_t at = c0 + c * step;
-      if (at >= p.D) continue;
-      float w[8];
+      if (!in(c)) continue;
+      const int at = (c0 + c * step) >> 3;
 #pragma unroll
-      for (int i = 0; i < 8; i++) v[c][i] = (v[c][i] - mean) * rstd;
+      for (int i = 0; i < 4; i++) v[c][i] = mul2(add2(v[c][i], both(-mean)), both(rstd));
+      uint64_t w[4];
       if (p.weight != nullptr) {
-        load_shared8(p.weight, p.w_f32, at, w);
+        kept_pairs(vectors, n8, at, w);
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[c][i] *= w[i];
+        for (int i = 0; i < 4; i++) v[c][i] = mul2(v[c][i], w[i]);
       }
       if (p.bias != nullptr) {
-        load_shared8(p.bias, p.w_f32, at, w);
+        kept_pairs(vectors + 2 * n8, n8, at, w);
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[c][i] += w[i];
+        for (int i = 0; i < 4; i++) v[c][i] = add2(v[c][i], w[i]);
       }
-      store_raw8<false>(p.y, r * p.ld_y + at, pack_raw8<false>(v[c]));
+      store_raw8<false>(p.y, r * p.ld_y + c0 + c * step, pack_pairs<false>(v[c]));
     }
   }
 }
@@ -121,16 +156,19 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int W
 // where a row's values fill the registers).  The block's groups then add theirs
 // in order, and a second launch the blocks': no atomics, the same bits each time.
 // The next row's loads are issued before this row's sums are exchanged.
-template <bool F32, int C, bool DRES, bool WG, bool SMEM>
+template <bool F32, int C, bool DRES, bool WG, bool SMEM, bool FULL>
 __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, int W) {
-  extern __shared__ float acc_smem[];
+  extern __shared__ float4 vectors[];  // the weight, then the lanes' sums
   __shared__ float2 part[2][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = warp / W, wr = warp - group * W, groups = (blockDim.x >> 5) / W;
-  const int64_t c0 = ((int64_t)wr * 32 + lane) * 8, step = (int64_t)W * 256;
-  const float inv_d = 1.f / (float)p.D;
+  const int D = (int)p.D, c0 = (wr * 32 + lane) * 8, step = W * 256;
+  const int n8 = D >> 3;
+  float* const acc_smem = reinterpret_cast<float*>(vectors + 2 * n8);
+  const float inv_d = 1.f / (float)D;
+  const auto in = [&](int c) { return FULL || c0 + c * step < D; };
   constexpr int A = WG && !SMEM ? C : 1;
-  float dw[A][8] = {}, db[A][8] = {};
+  uint64_t dw[A][4] = {}, db[A][4] = {};
   if constexpr (WG && SMEM)
 #pragma unroll 1
     for (int i = 0; i < 16 * C; i++) acc_smem[i * blockDim.x + tid] = 0.f;
@@ -143,12 +181,10 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
   const auto load_row = [&](int64_t row) {
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int64_t at = c0 + c * step;
-      if (at < p.D) {
-        xr[c] = load_raw8<F32>(p.x, row * p.ld_x + at);
-        dr[c] = load_raw8<false>(p.dy, row * p.ld_dy + at);
-        if constexpr (DRES) sr[c] = load_raw8<F32>(p.res, row * p.ld_res + at);
-      }
+      if (!in(c)) continue;
+      xr[c] = load_raw8<F32>(p.x, row * p.ld_x + c0 + c * step);
+      dr[c] = load_raw8<false>(p.dy, row * p.ld_dy + c0 + c * step);
+      if constexpr (DRES) sr[c] = load_raw8<F32>(p.res, row * p.ld_res + c0 + c * step);
     }
     if (!p.rms) mean = *(p.mean + row);
     rstd = *(p.rstd + row);
@@ -156,50 +192,55 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
   pdl_trigger();
   pdl_wait();
 #pragma unroll
-  for (int c = 0; c < C; c++) {  // columns past the row add nothing
+  for (int c = 0; c < C; c++) {
     xr[c] = {};
     dr[c] = {};
     sr[c] = {};
   }
   if (r < p.R) load_row(r);
+  keep_vector(p.weight, p.w_f32, n8, vectors);
+  __syncthreads();
   for (; r < p.R; r += stride) {
-    float xh[C][8], g[C][8], s1 = 0.f, s2 = 0.f;
+    uint64_t xh[C][4], g[C][4], t1[4] = {}, t2[4] = {};
     Raw8<F32> skip[C];
     const float inv = rstd;
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int64_t at = c0 + c * step;
-      unpack_raw8<F32>(xr[c], xh[c]);
-      unpack_raw8<false>(dr[c], g[c]);
+      unpack_pairs<F32>(xr[c], xh[c]);
+      unpack_pairs<false>(dr[c], g[c]);
       if constexpr (DRES) skip[c] = sr[c];
-      if (at >= p.D) continue;  // x = 0 there, but xh need not be
+      if (!in(c)) continue;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        xh[c][i] = (xh[c][i] - mean) * rstd;
+      for (int i = 0; i < 4; i++) {
+        xh[c][i] = mul2(add2(xh[c][i], both(-mean)), both(rstd));
         if constexpr (WG && !SMEM) {
-          dw[c][i] = fmaf(g[c][i], xh[c][i], dw[c][i]);
-          db[c][i] += g[c][i];
+          dw[c][i] = fma2(g[c][i], xh[c][i], dw[c][i]);
+          db[c][i] = add2(db[c][i], g[c][i]);
         }
         if constexpr (WG && SMEM) {
-          acc_smem[(c * 8 + i) * blockDim.x + tid] += g[c][i] * xh[c][i];
-          acc_smem[((C + c) * 8 + i) * blockDim.x + tid] += g[c][i];
+          float a, b, u, v;
+          unpack2(mul2(g[c][i], xh[c][i]), &a, &b);
+          unpack2(g[c][i], &u, &v);
+          acc_smem[(c * 8 + 2 * i) * blockDim.x + tid] += a;
+          acc_smem[(c * 8 + 2 * i + 1) * blockDim.x + tid] += b;
+          acc_smem[((C + c) * 8 + 2 * i) * blockDim.x + tid] += u;
+          acc_smem[((C + c) * 8 + 2 * i + 1) * blockDim.x + tid] += v;
         }
       }
       if (p.weight != nullptr) {
-        float w[8];
-        load_shared8(p.weight, p.w_f32, at, w);
+        uint64_t w[4];
+        kept_pairs(vectors, n8, (c0 + c * step) >> 3, w);
 #pragma unroll
-        for (int i = 0; i < 8; i++) g[c][i] *= w[i];
+        for (int i = 0; i < 4; i++) g[c][i] = mul2(g[c][i], w[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        s1 += g[c][i];
-        s2 = fmaf(g[c][i], xh[c][i], s2);
+      for (int i = 0; i < 4; i++) {
+        t1[i] = add2(t1[i], g[c][i]);
+        t2[i] = fma2(g[c][i], xh[c][i], t2[i]);
       }
     }
     if (r + stride < p.R) load_row(r + stride);
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    float s1 = warp_sum(sum_pairs(t1)), s2 = warp_sum(sum_pairs(t2));
     if (W > 1) {
       if (lane == 0) part[flip][warp] = make_float2(s1, s2);
       group_bar(group, W);
@@ -215,41 +256,49 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
     s2 *= inv_d;
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      const int64_t at = c0 + c * step;
-      if (at >= p.D) continue;
-      float d[8] = {};
-      if constexpr (DRES) unpack_raw8<F32>(skip[c], d);
+      if (!in(c)) continue;
+      uint64_t d[4] = {};
+      if constexpr (DRES) unpack_pairs<F32>(skip[c], d);
 #pragma unroll
-      for (int i = 0; i < 8; i++) d[i] = fmaf(inv, fmaf(-xh[c][i], s2, g[c][i] - s1), d[i]);
-      store_raw8<F32>(p.dx, r * p.ld_dx + at, pack_raw8<F32>(d));
+      for (int i = 0; i < 4; i++)
+        d[i] = fma2(both(inv), fma2(xh[c][i], both(-s2), add2(g[c][i], both(-s1))), d[i]);
+      store_raw8<F32>(p.dx, r * p.ld_dx + c0 + c * step, pack_pairs<F32>(d));
     }
   }
   if constexpr (WG) {
     float* const out = p.partials + (int64_t)blockIdx.x * 2 * p.D;
-#pragma unroll 1
+#pragma unroll
     for (int which = 0; which < 2; which++) {
       if (!SMEM && groups > 1) {
         __syncthreads();
+        if constexpr (!SMEM) {
 #pragma unroll
-        for (int c = 0; c < C; c++)
+          for (int c = 0; c < C; c++)
 #pragma unroll
-          for (int i = 0; i < 8; i++)
-            if constexpr (!SMEM) acc_smem[(c * 8 + i) * blockDim.x + tid] = which ? db[c][i] : dw[c][i];
+            for (int i = 0; i < 4; i++) {
+              float a, b;
+              unpack2(which ? db[c][i] : dw[c][i], &a, &b);
+              acc_smem[(c * 8 + 2 * i) * blockDim.x + tid] = a;
+              acc_smem[(c * 8 + 2 * i + 1) * blockDim.x + tid] = b;
+            }
+        }
         __syncthreads();
       }
       if (group != 0) continue;
 #pragma unroll
       for (int c = 0; c < C; c++) {
-        const int64_t at = c0 + c * step;
-        if (at >= p.D) continue;
+        if (!in(c)) continue;
         float t[8];
+        if constexpr (!SMEM) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) unpack2(which ? db[c][i] : dw[c][i], &t[2 * i], &t[2 * i + 1]);
+        }
 #pragma unroll
         for (int i = 0; i < 8; i++) {
           if constexpr (SMEM) t[i] = acc_smem[((which * C + c) * 8 + i) * blockDim.x + tid];
-          else t[i] = which ? db[c][i] : dw[c][i];
           for (int k = 1; k < groups; k++) t[i] += acc_smem[(c * 8 + i) * blockDim.x + k * W * 32 + tid];
         }
-        store_raw8<true>(out, which * p.D + at, pack_raw8<true>(t));
+        store_raw8<true>(out, which * p.D + c0 + c * step, pack_raw8<true>(t));
       }
     }
   }
@@ -280,32 +329,47 @@ __global__ void __launch_bounds__(256) norm_wgrad_kernel(const NormParams p, int
   }
 }
 
-// Warps of a row and 8-column pieces of a lane.  Forward: up to four pieces a
-// lane; backward: one as long as 16 warps cover the row.
-struct NormShape { int W, C; };
+// Warps of a row and 8-column pieces of a lane: `most` pieces where the row is
+// long enough, and a number of warps whose columns are the row's where there is one
+// (warps need not be a power of two: 5120 columns are 5 x 4 pieces of 256, 7168 7 x
+// 4).
+struct NormShape {
+  int W, C;
+  bool full;
+};
 static NormShape norm_shape(int64_t D, int most) {
-  const int64_t v = (D + 7) / 8;
-  int W = 1;
-  while ((int64_t)W * 32 * most < v && W < 16) W *= 2;
-  return {W, (int)((v + 32 * W - 1) / (32 * W))};
+  const int v = (int)((D + 7) / 8), least = (v + 32 * most - 1) / (32 * most);
+  for (int W = least; W <= 16 && W <= least + 2; W++)
+    if (D % 8 == 0 && v % (32 * W) == 0) return {W, v / (32 * W), true};
+  return {least, (v + 32 * least - 1) / (32 * least), false};
 }
-static NormShape bwd_shape(int64_t D) {
-  const NormShape s = norm_shape(D, 1);
-  return {s.W, s.C > 2 ? 4 : s.C};
-}
+static int norm_groups(int W, int warps) { return W >= warps ? 1 : warps / W; }
 
-template <bool F32, bool RES>
-static cudaError_t launch_fwd(const NormParams& p, int sms, cudaStream_t s) {
-  const NormShape n = norm_shape(p.D, 4);
-  const int threads = n.W * 32 > 256 ? n.W * 32 : 256, groups = threads / (32 * n.W);
-  const int64_t want = (p.R + groups - 1) / groups, cap = (int64_t)sms * 16;
+template <bool F32, bool RES, bool FULL, int C>
+static cudaError_t launch_fwd(const NormParams& p, int W, dim3 grid, int threads, cudaStream_t s) {
+  const int smem = (p.weight || p.bias ? 8 : 0) * (int)p.D;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = ensure_smem_attr<norm_fwd_kernel<F32, C, RES, FULL>>(8 * (int)MAX_NORM_D);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(norm_fwd_kernel<F32, C, RES, FULL>, grid, threads, smem, s, dim3(1), p, W);
+}
+template <bool F32, bool RES, bool FULL>
+static cudaError_t launch_fwd(const NormParams& p, const NormShape& n, int sms, cudaStream_t s) {
+  const int groups = norm_groups(n.W, 8), threads = 32 * n.W * groups;
+  const int64_t want = (p.R + groups - 1) / groups, cap = (int64_t)sms * ((n.C == 1 ? 1024 : 512) / threads);
   const dim3 grid((unsigned)(want < cap ? want : cap));
   switch (n.C) {
-    case 1: return launch_pdl(norm_fwd_kernel<F32, 1, RES>, grid, threads, 0, s, dim3(1), p, n.W);
-    case 2: return launch_pdl(norm_fwd_kernel<F32, 2, RES>, grid, threads, 0, s, dim3(1), p, n.W);
-    case 3: return launch_pdl(norm_fwd_kernel<F32, 3, RES>, grid, threads, 0, s, dim3(1), p, n.W);
-    default: return launch_pdl(norm_fwd_kernel<F32, 4, RES>, grid, threads, 0, s, dim3(1), p, n.W);
+    case 1: return launch_fwd<F32, RES, FULL, 1>(p, n.W, grid, threads, s);
+    case 2: return launch_fwd<F32, RES, FULL, 2>(p, n.W, grid, threads, s);
+    case 3: return launch_fwd<F32, RES, FULL, 3>(p, n.W, grid, threads, s);
+    default: return launch_fwd<F32, RES, FULL, 4>(p, n.W, grid, threads, s);
   }
+}
+template <bool F32, bool RES>
+static cudaError_t launch_fwd(const NormParams& p, int sms, cudaStream_t s) {
+  const NormShape n = norm_shape(p.D, F32 && RES && p.D <= 8192 ? 2 : 4);
+  return n.full ? launch_fwd<F32, RES, true>(p, n, sms, s) : launch_fwd<F32, RES, false>(p, n, sms, s);
 }
 
 cudaError_t launch_norm_fwd(const NormParams& p, int sms, cudaStream_t s) {
@@ -313,42 +377,60 @@ cudaError_t launch_norm_fwd(const NormParams& p, int sms, cudaStream_t s) {
   return p.res ? launch_fwd<false, true>(p, sms, s) : launch_fwd<false, false>(p, sms, s);
 }
 
-int64_t norm_bwd_blocks(int64_t R, int64_t D) {
-  const int groups = 16 / bwd_shape(D).W;
+// Fewer warps a row, with more columns a lane, exchange less (us: [65536, 2048]
+// BF16 with two pieces a lane 152, with one 193; [20000, 2728] 89 and 120), as long
+// as the sums and the next row fit the registers: fp32 rows with one piece
+// ([32768, 4096] with dres 310, with two 398).  Above that the sums live in shared
+// memory.
+static NormShape bwd_shape(int64_t D, bool f32) {
+  for (int most = f32 ? 1 : 2; most <= 2; most++)
+    if (D <= 256 * 16 * most) return norm_shape(D, most);
+  return norm_shape(D, 4);
+}
+int64_t norm_bwd_blocks(int64_t R, int64_t D, bool f32) {
+  const int groups = norm_groups(bwd_shape(D, f32).W, 16);
   const int64_t want = (R + groups - 1) / groups;
   return want < 152 ? want : 152;  // one on every SM (GB300: 152)
 }
 
-template <bool F32, int C, bool DRES, bool WG>
+template <bool F32, int C, bool DRES, bool WG, bool FULL>
 static cudaError_t launch_bwd(const NormParams& p, int W, cudaStream_t s) {
-  constexpr bool SMEM = WG && C == 4;
-  const int64_t blocks = norm_bwd_blocks(p.R, p.D);
-  const int smem = !WG ? 0 : (SMEM ? 2 : 1) * C * 8 * 512 * 4;
-  const cudaError_t e = smem > 48 * 1024 ? ensure_smem_attr<norm_bwd_kernel<F32, C, DRES, WG, SMEM>>(smem) : cudaSuccess;
+  constexpr bool SMEM = WG && C > 2;
+  const int64_t blocks = norm_bwd_blocks(p.R, p.D, F32);
+  const int threads = 32 * W * norm_groups(W, 16);
+  const int smem = 4 * (int)p.D + (WG ? (SMEM ? 2 : 1) * C * 8 * threads * 4 : 0);
+  const int most = 4 * (int)MAX_NORM_D + 2 * C * 8 * 512 * 4;
+  const cudaError_t e = smem > 32 * 1024 ? ensure_smem_attr<norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>>(most) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  const cudaError_t l = launch_pdl(norm_bwd_kernel<F32, C, DRES, WG, SMEM>, dim3((unsigned)blocks), 512, smem, s, dim3(1), p, W);
+  const cudaError_t l = launch_pdl(norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>, dim3((unsigned)blocks), threads, smem, s,
+                                   dim3(1), p, W);
   if (l != cudaSuccess || !WG) return l;
   return launch_pdl(norm_wgrad_kernel, dim3((unsigned)((2 * p.D + 31) / 32)), 256, 0, s, dim3(1), p, blocks);
 }
 
-template <bool F32, bool DRES, bool WG>
-static cudaError_t launch_bwd_c(const NormParams& p, cudaStream_t s) {
-  const NormShape n = bwd_shape(p.D);
+template <bool F32, bool DRES, bool WG, bool FULL>
+static cudaError_t launch_bwd_c(const NormParams& p, const NormShape& n, cudaStream_t s) {
   switch (n.C) {
-    case 1: return launch_bwd<F32, 1, DRES, WG>(p, n.W, s);
-    case 2: return launch_bwd<F32, 2, DRES, WG>(p, n.W, s);
-    default: return launch_bwd<F32, 4, DRES, WG>(p, n.W, s);
+    case 1: return launch_bwd<F32, 1, DRES, WG, FULL>(p, n.W, s);
+    case 2: return launch_bwd<F32, 2, DRES, WG, FULL>(p, n.W, s);
+    case 3: return launch_bwd<F32, 3, DRES, WG, FULL>(p, n.W, s);
+    default: return launch_bwd<F32, 4, DRES, WG, FULL>(p, n.W, s);
   }
+}
+template <bool F32, bool DRES, bool WG>
+static cudaError_t launch_bwd_f(const NormParams& p, cudaStream_t s) {
+  const NormShape n = bwd_shape(p.D, F32);
+  return n.full ? launch_bwd_c<F32, DRES, WG, true>(p, n, s) : launch_bwd_c<F32, DRES, WG, false>(p, n, s);
 }
 
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
   const bool wg = p.dweight != nullptr || p.dbias != nullptr;
   if (p.x_f32) {
-    if (p.res) return wg ? launch_bwd_c<true, true, true>(p, s) : launch_bwd_c<true, true, false>(p, s);
-    return wg ? launch_bwd_c<true, false, true>(p, s) : launch_bwd_c<true, false, false>(p, s);
+    if (p.res) return wg ? launch_bwd_f<true, true, true>(p, s) : launch_bwd_f<true, true, false>(p, s);
+    return wg ? launch_bwd_f<true, false, true>(p, s) : launch_bwd_f<true, false, false>(p, s);
   }
-  if (p.res) return wg ? launch_bwd_c<false, true, true>(p, s) : launch_bwd_c<false, true, false>(p, s);
-  return wg ? launch_bwd_c<false, false, true>(p, s) : launch_bwd_c<false, false, false>(p, s);
+  if (p.res) return wg ? launch_bwd_f<false, true, true>(p, s) : launch_bwd_f<false, true, false>(p, s);
+  return wg ? launch_bwd_f<false, false, true>(p, s) : launch_bwd_f<false, false, false>(p, s);
 }
 
 }  // namespace mx

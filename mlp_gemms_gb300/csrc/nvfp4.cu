@@ -7,16 +7,40 @@ namespace mx {
 
 static __device__ unsigned g_nvfp4_status = 0;
 
-// Largest |value| of BF16 pairs, NaN if any is one (as bit patterns: a NaN's
-// magnitude is above Inf's).
+// Larger magnitude of BF16 pairs, a NaN if either is one (the sign bits are
+// meaningless); as bit patterns a NaN's magnitude is above Inf's.
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// Eight fp32 values -> eight E2M1 codes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
 __device__ __forceinline__ uint32_t max_halves(uint32_t a) {
-  const uint32_t lo = a & 0xFFFFu, hi = a >> 16;
+  const uint32_t lo = a & 0x7FFFu, hi = a >> 16 & 0x7FFFu;
   return lo > hi ? lo : hi;
+}
+
+// Row r's first scale byte in the blocked layout.
+__device__ __forceinline__ int64_t row_place(int64_t r, int64_t chunks) {
+  return (r >> 7) * chunks * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+}
+// The layout's rows past the last, zero: a warp takes a chunk of the last row
+// block, a lane the four rows that share its 16 bytes.
+__device__ __forceinline__ void pad_scales(const Nvfp4Params& p, int64_t chunks) {
+  const int first = (int)(p.R & 127), warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  for (int64_t c = (int64_t)blockIdx.x * warps + warp; c < chunks; c += (int64_t)gridDim.x * warps) {
+    uint32_t* const to = reinterpret_cast<uint32_t*>(p.scale + ((p.R >> 7) * chunks + c) * 512 + lane * 16);
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      if (32 * q + lane >= first) to[q] = 0u;
+  }
 }
 
 // For every row: 2^e the smallest power of two with amax <= 6 * 448 * 2^e (e >=
@@ -42,7 +66,7 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / W, wr = warp - group * W, groups = (blockDim.x >> 5) / W;
   const int c0 = (wr * 32 + lane) * 16, step = W * 512, K = (int)p.K;
-  const int64_t chunks = (p.K + 63) >> 6, stride = (int64_t)gridDim.x * groups;
+  const int64_t chunks = (p.K + 63) >> 6, chunk_bytes = p.linear ? 4 : 512, stride = (int64_t)gridDim.x * groups;
   int flip = 0;
   pdl_trigger();
   pdl_wait();
@@ -105,7 +129,7 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
     if (wr == 0 && lane == 0)
       p.row_scale[r] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
     // scale (r, c) of the blocked layout: the row's place in a chunk, then a chunk every four columns
-    uint8_t* const scales = p.scale + (r >> 7) * chunks * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+    uint8_t* const scales = p.scale + (p.linear ? r * chunks * 4 : row_place(r, chunks));
     uint8_t* const data = p.data + r * (p.K >> 1);
 #pragma unroll
     for (int c = 0; c < C; c++) {
@@ -121,16 +145,14 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
       uint32_t out[2];
 #pragma unroll
       for (int o = 0; o < 2; o++) {
-        uint32_t b[4];
+        float q[8];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          float lo, hi;
           const uint32_t w = x[c][4 * o + i];
           const uint64_t v = pack2(bf16_bits_to_float(w & 0xFFFFu), __uint_as_float(w & 0xFFFF0000u));
-          unpack2(add2(fma2(v, both(inv), both(6144.f)), both(-6144.f)), &lo, &hi);
-          b[i] = cvt_e2m1x2(lo, hi);
+          unpack2(add2(fma2(v, both(inv), both(6144.f)), both(-6144.f)), &q[2 * i], &q[2 * i + 1]);
         }
-        out[o] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        out[o] = cvt_e2m1x8(q);
         if (!finite) out[o] = 0;  // Inf * 0 is a NaN
       }
       // the scale bytes of four lanes make a word of the blocked layout; past the
@@ -140,24 +162,76 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
       word = (word & 0xFFFFu) | __shfl_xor_sync(0xFFFFFFFFu, word, 2) << 16;
       if (at < K) {
         *reinterpret_cast<uint2*>(data + (at >> 1)) = make_uint2(out[0], out[1]);
-        if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(scales + (at >> 6) * 512) = word;
+        if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(scales + (at >> 6) * chunk_bytes) = word;
       }
     }
   }
-  if ((p.R & 127) != 0 && p.offsets == nullptr) {
-    // the layout's rows past the last: a warp takes a chunk of the last row block,
-    // a lane the four rows that share its 16 bytes
-    const int first = (int)(p.R & 127);
-    for (int64_t c = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp; c < chunks; c += (int64_t)gridDim.x * (blockDim.x >> 5)) {
-      uint32_t* const to = reinterpret_cast<uint32_t*>(p.scale + ((p.R >> 7) * chunks + c) * 512 + lane * 16);
-#pragma unroll
-      for (int q = 0; q < 4; q++)
-        if (32 * q + lane >= first) to[q] = 0u;
-    }
-  }
+  if ((p.R & 127) != 0 && p.offsets == nullptr && !p.linear) pad_scales(p, chunks);
 }
 
-cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, int num_sms, cudaStream_t s) {
+// Gathered rows of tokens that are quantized already (each for itself, so all of
+// a token's rows are the same bytes): codes, scales (row-major, whole words) and
+// row scales of T tokens, copied to every row that names one.  A warp takes ROWS
+// rows at a time, whose loads are all in flight together.
+constexpr int ROWS = 4;
+__global__ void __launch_bounds__(256) nvfp4_gather_kernel(const Nvfp4Params p, const uint8_t* data, const uint8_t* scale,
+                                                           const float* row_scale) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t chunks = (p.K + 63) >> 6, bytes = p.K >> 1, stride = (int64_t)gridDim.x * 8 * ROWS;
+  pdl_trigger();
+  pdl_wait();
+  int64_t rows = p.R;
+  if (p.offsets != nullptr) {
+    const int64_t end = *(p.offsets + p.G - 1);
+    rows = end < 0 ? 0 : end < rows ? end : rows;
+  }
+  for (int64_t r0 = ((int64_t)blockIdx.x * 8 + warp) * ROWS; r0 < rows; r0 += stride) {
+    int64_t from[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; i++) {
+      from[i] = r0 + i < rows ? (int64_t)*(p.src + r0 + i) : -1;
+      if (from[i] >= p.T) {
+        if (lane == 0) atomicOr(&g_nvfp4_status, DEV_BAD_INDEX);
+        from[i] = -1;
+      }
+    }
+    for (int64_t at = lane * 16; at < bytes; at += 512) {
+      uint4 q[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; i++)
+        q[i] = from[i] >= 0 ? *reinterpret_cast<const uint4*>(data + from[i] * bytes + at) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < ROWS; i++)
+        if (r0 + i < rows) *reinterpret_cast<uint4*>(p.data + (r0 + i) * bytes + at) = q[i];
+    }
+    for (int64_t c = lane; c < chunks; c += 32) {
+      uint32_t w[ROWS];
+#pragma unroll
+      for (int i = 0; i < ROWS; i++)
+        w[i] = from[i] >= 0 ? *reinterpret_cast<const uint32_t*>(scale + (from[i] * chunks + c) * 4) : 0u;
+#pragma unroll
+      for (int i = 0; i < ROWS; i++)
+        if (r0 + i < rows) *reinterpret_cast<uint32_t*>(p.scale + row_place(r0 + i, chunks) + c * 512) = w[i];
+    }
+    if (lane < ROWS && r0 + lane < rows) {
+      const int64_t f = from[0] * (lane == 0) + from[1] * (lane == 1) + from[2] * (lane == 2) + from[3] * (lane == 3);
+      p.row_scale[r0 + lane] = f >= 0 ? *(row_scale + f) : __uint_as_float((uint32_t)(127 - 100) << 23);
+    }
+  }
+  if ((p.R & 127) != 0 && p.offsets == nullptr) pad_scales(p, chunks);
+}
+
+// Where rows name tokens three times on average and there is enough to save for
+// the second launch, they are copied from the tokens' quantization (us, each row
+// quantized for itself in brackets): 8192 tokens of 2048 columns to 73700 rows 36
+// (68), to 32768 rows 23 (31), to 16384 rows 17.3 (17.5); 64 tokens to 512 rows 5.4
+// (2.8).
+size_t nvfp4_workspace(int64_t T, int64_t K, int64_t R) {
+  if (R < 3 * T || (R - T) * K < (1 << 24)) return 0;
+  return (size_t)round_up_i64(T * (K >> 1), 16) + (size_t)round_up_i64(T * ((K + 63) >> 6) * 4, 16) + (size_t)T * 4;
+}
+
+static cudaError_t launch_rows(const Nvfp4Params& p, int num_sms, cudaStream_t s) {
   const int64_t v = (p.K + 15) / 16;
   int W = 1;
   while ((int64_t)W * 32 * 2 < v && W < 16) W *= 2;
@@ -168,6 +242,22 @@ cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, int num_sms, cudaStream_
   if (C == 1) return launch_pdl(nvfp4_quantize_kernel<1>, grid, threads, 0, s, dim3(1), p, W);
   if (C == 2) return launch_pdl(nvfp4_quantize_kernel<2>, grid, threads, 0, s, dim3(1), p, W);
   return launch_pdl(nvfp4_quantize_kernel<4>, grid, threads, 0, s, dim3(1), p, W);
+}
+
+cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, void* workspace, int num_sms, cudaStream_t s) {
+  if (workspace == nullptr) return launch_rows(p, num_sms, s);
+  Nvfp4Params t = p;
+  t.R = p.T;
+  t.src = t.offsets = nullptr;
+  t.linear = 1;
+  t.data = static_cast<uint8_t*>(workspace);
+  t.scale = t.data + round_up_i64(p.T * (p.K >> 1), 16);
+  t.row_scale = reinterpret_cast<float*>(t.scale + round_up_i64(p.T * ((p.K + 63) >> 6) * 4, 16));
+  const cudaError_t e = launch_rows(t, num_sms, s);
+  if (e != cudaSuccess) return e;
+  const int64_t want = (p.R + 8 * ROWS - 1) / (8 * ROWS), cap = (int64_t)num_sms * 16;
+  return launch_pdl(nvfp4_gather_kernel, dim3((unsigned)(want < cap ? want : cap)), 256, 0, s, dim3(1), p, t.data, t.scale,
+                    t.row_scale);
 }
 
 cudaError_t read_nvfp4_status(unsigned* out) { return cudaMemcpyFromSymbol(out, g_nvfp4_status, sizeof(unsigned)); }

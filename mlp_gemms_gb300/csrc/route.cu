@@ -495,7 +495,7 @@ static cudaError_t launch_v(const RouteParams& p, bool bwd, cudaStream_t s) {
   const dim3 grid((unsigned)route_blocks(p.T));
   if (bwd) return launch_pdl(route_bwd_kernel<V, SIG>, grid, 256, 0, s, dim3(1), p);
   const int smem = (p.groups > 1 ? 8 * p.G * 8 : 0) + (p.partial_load ? 8 * p.G : 0);
-  if (smem > 48 * 1024) {
+  if (smem > 32 * 1024) {
     const cudaError_t e = ensure_smem_attr<route_fwd_kernel<V, SIG>>(8 * 1024 * 8 + 8 * 1024);
     if (e != cudaSuccess) return e;
   }

@@ -56,6 +56,27 @@ __device__ __forceinline__ void store_raw8(void* base, int64_t at, const Raw8<F3
   p[0] = r.q[0];
   if constexpr (F32) p[1] = r.q[1];
 }
+// Eight values as four fp32 pairs for the packed instructions.
+template <bool F32>
+__device__ __forceinline__ void unpack_pairs(const Raw8<F32>& r, uint64_t (&v)[4]) {
+  float f[8];
+  unpack_raw8<F32>(r, f);
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> pack_pairs(const uint64_t (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; i++) unpack2(v[i], &f[2 * i], &f[2 * i + 1]);
+  return pack_raw8<F32>(f);
+}
+__device__ __forceinline__ float sum_pairs(const uint64_t (&v)[4]) {
+  float a, b;
+  unpack2(add2(add2(v[0], v[1]), add2(v[2], v[3])), &a, &b);
+  return a + b;
+}
+
 // Eight values of a vector that many rows share (kept in L1).
 __device__ __forceinline__ void load_shared8(const void* base, bool f32, int64_t at, float (&v)[8]) {
   if (f32) {
@@ -68,6 +89,13 @@ __device__ __forceinline__ void load_shared8(const void* base, bool f32, int64_t
     r.q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
     unpack_raw8<false>(r, v);
   }
+}
+
+__device__ __forceinline__ void load_shared_pairs(const void* base, bool f32, int64_t at, uint64_t (&v)[4]) {
+  float f[8];
+  load_shared8(base, f32, at, f);
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

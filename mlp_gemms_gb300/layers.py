@@ -5,70 +5,116 @@ As in the package's own module, every function checks what the C layer cannot
 see and calls the C-ABI entry point of its name.  All of them are reached as
 ``mlp_gemms_gb300.mx_...``.
 """
+import ctypes
 import functools
+
+import torch
 
 import mlp_gemms_gb300 as _mx
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
-def _here(first, *others):
-    """_one_gpu, and that GPU the current one: it is where the call launches."""
-    _mx._one_gpu(first, *others)
-    _mx._stream()
-    assert first.get_device() == _mx._current[1](), "the tensors are not on the current GPU"
+
+# Each tensor's attributes are asked for once: the checks are a good part of a
+# small call's time.
+
+def _gpu(t):
+    """The tensor's GPU, which has to be the current one: the call launches there,
+    and the library takes bare pointers."""
+    if _mx._current is None:
+        _mx._stream()
+    dev = t.get_device()
+    assert dev >= 0 and dev == _mx._current[1](), "a tensor is not on the current GPU"
+    return dev
 
 
 def _type(t):
-    import torch
-    assert t.dtype in (torch.bfloat16, torch.float32), "neither BF16 nor fp32"
-    return _mx.F32 if t.dtype == torch.float32 else _mx.BF16
+    dtype = t.dtype
+    assert dtype is _BF16 or dtype is _F32, "neither BF16 nor fp32"
+    return _mx.F32 if dtype is _F32 else _mx.BF16
 
 
-def _rows(t, shape, dtype):
-    """A matrix of this shape and type with dense rows; its row stride."""
-    assert t.shape == shape and t.dtype == dtype and t.stride(1) == 1, "a matrix of another shape, type or layout"
-    return t.stride(0) if shape[0] > 1 else shape[1]
+def _rows(t, shape, dtype, dev):
+    """Pointer and row stride of a matrix of this shape and type with dense rows."""
+    step, one = t.stride()
+    assert t.shape == shape and t.dtype is dtype and one == 1 and t.get_device() == dev, \
+        "a matrix of another shape, type or layout, or on another GPU"
+    return t.data_ptr(), step if shape[0] > 1 else shape[1]
 
 
-def _vector(t, n, dtype=None):
-    assert t is None or (t.shape == (n,) and t.is_contiguous() and dtype in (None, t.dtype)), \
-        "a vector of another length, type or layout"
+def _dense(t, shape, dtype, dev):
+    """Pointer of a dense tensor of this shape and type, or None."""
+    if t is None:
+        return None
+    assert t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev, \
+        "a tensor of another shape, type or layout, or on another GPU"
+    return t.data_ptr()
 
 
-def _norm_weights(weight, bias, D):
-    _vector(weight, D)
-    _vector(bias, D, weight.dtype if weight is not None else None)
-    return _mx.BF16 if weight is None and bias is None else _type(weight if weight is not None else bias)
+def _new(shape, dtype, like, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _mx._empty(shape, dtype, like.device, stream)
 
+
+def _workspace(workspace, nbytes, like, dev, stream):
+    """(workspace, its pointer, its size), allocated where the caller brings none."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = _new(nbytes, _U8, like, stream)
+        return workspace, workspace.data_ptr(), nbytes
+    assert workspace.is_contiguous() and workspace.get_device() == dev, "a strided workspace, or on another GPU"
+    return workspace, workspace.data_ptr(), workspace.nbytes
+
+
+# --------------------------------------------------------------------------
+# Layer norm
+# --------------------------------------------------------------------------
 
 def mx_layernorm_fwd(x, weight=None, bias=None, eps=1e-5, residual=None, rms=False, stats=True, out=None, sum_out=None,
                      mean=None, rstd=None, stream=None):
     """Layer norm (rms: without the mean) of the rows of s = x + residual (BF16
     or fp32 [R, D]): returns (y BF16, mean, rstd, s), s being x itself
     without a residual and mean None with rms; stats=False: no mean and rstd."""
-    import torch
-    R, D = x.shape
-    xt, wt, dev = _type(x), _norm_weights(weight, bias, D), x.device
-    ld_x, ld_res, ld_sum = _rows(x, (R, D), x.dtype), 0, 0
-    if out is None:
-        out = _mx._empty((R, D), torch.bfloat16, dev, stream)
+    shape, dev, dtype = x.shape, _gpu(x), x.dtype
+    R, D = shape
+    xt = _type(x)
+    xp, ld_x = _rows(x, shape, dtype, dev)
+    wt, wp, bp = _mx.BF16, None, None
+    if weight is not None:
+        wt, wp = _type(weight), _dense(weight, (D,), weight.dtype, dev)
+    if bias is not None:
+        wt, bp = _type(bias), _dense(bias, (D,), bias.dtype if weight is None else weight.dtype, dev)
+    rp, ld_res, sp, ld_sum = None, 0, None, 0
     if residual is not None:
-        ld_res = _rows(residual, (R, D), x.dtype)
+        rp, ld_res = _rows(residual, shape, dtype, dev)
         if sum_out is None:
-            sum_out = _mx._empty((R, D), x.dtype, dev, stream)
-        ld_sum = _rows(sum_out, (R, D), x.dtype)
+            sum_out = _new(shape, dtype, x, stream)
+            sp, ld_sum = sum_out.data_ptr(), D
+        else:
+            sp, ld_sum = _rows(sum_out, shape, dtype, dev)
     else:
         assert sum_out is None, "a sum without a residual"
-    if stats and not rms and mean is None:
-        mean = _mx._empty(R, torch.float32, dev, stream)
-    if stats and rstd is None:
-        rstd = _mx._empty(R, torch.float32, dev, stream)
+    if out is None:
+        out = _new(shape, _BF16, x, stream)
+        yp, ld_y = out.data_ptr(), D
+    else:
+        yp, ld_y = _rows(out, shape, _BF16, dev)
+    mp = sdp = None
     assert mean is None or not rms, "a mean with rms"
-    _vector(mean, R, torch.float32)
-    _vector(rstd, R, torch.float32)
-    _here(x, weight, bias, residual, out, sum_out, mean, rstd)
-    _mx._check(_mx.load().mx_layernorm_fwd(x.data_ptr(), xt, R, D, ld_x, _mx._ptr(residual), ld_res, _mx._ptr(sum_out), ld_sum,
-                                   _mx._ptr(weight), _mx._ptr(bias), wt, eps, 1 if rms else 0, out.data_ptr(),
-                                   _rows(out, (R, D), torch.bfloat16), _mx._ptr(mean), _mx._ptr(rstd), _mx._stream(stream)))
+    if mean is not None:
+        mp = _dense(mean, (R,), _F32, dev)
+    elif stats and not rms:
+        mean = _new(R, _F32, x, stream)
+        mp = mean.data_ptr()
+    if rstd is not None:
+        sdp = _dense(rstd, (R,), _F32, dev)
+    elif stats:
+        rstd = _new(R, _F32, x, stream)
+        sdp = rstd.data_ptr()
+    _mx._check(_mx.load().mx_layernorm_fwd(xp, xt, R, D, ld_x, rp, ld_res, sp, ld_sum, wp, bp, wt, eps, 1 if rms else 0,
+                                           yp, ld_y, mp, sdp, _mx._stream(stream)))
     return out, mean, rstd, x if residual is None else sum_out
 
 
@@ -83,44 +129,43 @@ def mx_layernorm_bwd(dy, x, mean, rstd, weight=None, dres=None, rms=False, bias=
     Returns (dx, dweight, dbias): dx of x's type with dres added, the others fp32
     [D], dweight None without wgrad, dbias None without bias; accumulate: added
     to the dweight and dbias that the caller brings."""
-    import torch
-    R, D = x.shape
-    xt, wt, dev = _type(x), _norm_weights(weight, None, D), x.device
-    ld_x, ld_dy = _rows(x, (R, D), x.dtype), _rows(dy, (R, D), torch.bfloat16)
-    ld_dres = 0 if dres is None else _rows(dres, (R, D), x.dtype)
+    shape, dev, dtype = x.shape, _gpu(x), x.dtype
+    R, D = shape
+    xt = _type(x)
+    xp, ld_x = _rows(x, shape, dtype, dev)
+    dyp, ld_dy = _rows(dy, shape, _BF16, dev)
+    wt, wp = (_mx.BF16, None) if weight is None else (_type(weight), _dense(weight, (D,), weight.dtype, dev))
+    rp, ld_res = (None, 0) if dres is None else _rows(dres, shape, dtype, dev)
+    mp, sdp = _dense(mean, (R,), _F32, dev), _dense(rstd, (R,), _F32, dev)
     assert not accumulate or ((dweight is not None or not wgrad) and (dbias is not None or not bias)), \
         "accumulate needs the buffers to add to"
     if dx is None:
-        dx = _mx._empty((R, D), x.dtype, dev, stream)
-    if wgrad and dweight is None:
-        dweight = _mx._empty(D, torch.float32, dev, stream)
-    if bias and dbias is None:
-        dbias = _mx._empty(D, torch.float32, dev, stream)
-    for t, n in ((mean, R), (rstd, R), (dweight, D), (dbias, D)):
-        _vector(t, n, torch.float32)
-    nbytes = 0
-    if dweight is not None or dbias is not None:
-        if workspace is None:
-            workspace = _mx._empty(max(mx_layernorm_workspace_bytes(R, D), 16), torch.uint8, dev, stream)
-        assert workspace.is_contiguous()
-        nbytes = workspace.nbytes
-    _here(x, dy, mean, rstd, weight, dres, dx, dweight, dbias, workspace)
-    _mx._check(_mx.load().mx_layernorm_bwd(dy.data_ptr(), ld_dy, x.data_ptr(), xt, R, D, ld_x, _mx._ptr(mean), _mx._ptr(rstd),
-                                   _mx._ptr(weight), wt, 1 if rms else 0, _mx._ptr(dres), ld_dres, dx.data_ptr(),
-                                   _rows(dx, (R, D), x.dtype), _mx._ptr(dweight), _mx._ptr(dbias), 1 if accumulate else 0,
-                                   _mx._ptr(workspace), nbytes, _mx._stream(stream)))
+        dx = _new(shape, dtype, x, stream)
+        dxp, ld_dx = dx.data_ptr(), D
+    else:
+        dxp, ld_dx = _rows(dx, shape, dtype, dev)
+    dwp = dbp = None
+    if dweight is not None:
+        dwp = _dense(dweight, (D,), _F32, dev)
+    elif wgrad:
+        dweight = _new(D, _F32, x, stream)
+        dwp = dweight.data_ptr()
+    if dbias is not None:
+        dbp = _dense(dbias, (D,), _F32, dev)
+    elif bias:
+        dbias = _new(D, _F32, x, stream)
+        dbp = dbias.data_ptr()
+    nbytes = 0 if dwp is None and dbp is None else mx_layernorm_workspace_bytes(R, D)
+    workspace, wsp, nbytes = _workspace(workspace, nbytes, x, dev, stream)
+    _mx._check(_mx.load().mx_layernorm_bwd(dyp, ld_dy, xp, xt, R, D, ld_x, mp, sdp, wp, wt, 1 if rms else 0, rp, ld_res,
+                                           dxp, ld_dx, dwp, dbp, 1 if accumulate else 0, wsp, nbytes,
+                                           _mx._stream(stream)))
     return dx, dweight, dbias
 
 
 # --------------------------------------------------------------------------
 # Expert routing and the combine's gradient
 # --------------------------------------------------------------------------
-
-def _table(t, shape, dtype):
-    """A dense table of this shape and type, or None."""
-    assert t is None or (t.shape == shape and t.dtype == dtype and t.is_contiguous()), \
-        "a table of another shape, type or layout"
-
 
 @functools.lru_cache(maxsize=256)
 def mx_moe_topk_workspace_bytes(T, G):
@@ -132,33 +177,30 @@ def mx_moe_topk(logits, k, score=_mx.SCORE_SOFTMAX, bias=None, groups=1, topk_gr
     """The k experts of each token from its logits (BF16 or fp32 [T, G]) and
     their weights: returns (weights fp32 [T, k], ids int32 [T, k], load, score_sum),
     the last two (choices of each expert, sums of its scores) None without stats."""
-    import torch
-    T, G = logits.shape
-    xt, dev = _type(logits), logits.device
-    ld = _rows(logits, (T, G), logits.dtype)
+    shape, dev = logits.shape, _gpu(logits)
+    T, G = shape
+    xt = _type(logits)
+    xp, ld = _rows(logits, shape, logits.dtype, dev)
+    bp = _dense(bias, (G,), _F32, dev)
     if weights is None:
-        weights = _mx._empty((T, k), torch.float32, dev, stream)
+        weights = _new((T, k), _F32, logits, stream)
+        wp = weights.data_ptr()
+    else:
+        wp = _dense(weights, (T, k), _F32, dev)
     if ids is None:
-        ids = _mx._empty((T, k), torch.int32, dev, stream)
-    stats = stats or load is not None or score_sum is not None
+        ids = _new((T, k), _I32, logits, stream)
+        ip = ids.data_ptr()
+    else:
+        ip = _dense(ids, (T, k), _I32, dev)
+    lp = sp = wsp = None
     nbytes = 0
-    if stats:
-        load = load if load is not None else _mx._empty(G, torch.int32, dev, stream)
-        score_sum = score_sum if score_sum is not None else _mx._empty(G, torch.float32, dev, stream)
-        if workspace is None:
-            workspace = _mx._empty(max(mx_moe_topk_workspace_bytes(T, G), 16), torch.uint8, dev, stream)
-        assert workspace.is_contiguous()
-        nbytes = workspace.nbytes
-    _table(weights, (T, k), torch.float32)
-    _table(ids, (T, k), torch.int32)
-    _vector(bias, G, torch.float32)
-    _vector(load, G, torch.int32)
-    _vector(score_sum, G, torch.float32)
-    _here(logits, bias, weights, ids, load, score_sum, workspace)
-    _mx._check(_mx.load().mx_moe_topk(logits.data_ptr(), xt, T, G, ld, k, score, _mx._ptr(bias), groups, topk_groups,
-                                      group_top, 1 if renorm else 0, scale, weights.data_ptr(), ids.data_ptr(),
-                                      _mx._ptr(load), _mx._ptr(score_sum), _mx._ptr(workspace), nbytes,
-                                      _mx._stream(stream)))
+    if stats or load is not None or score_sum is not None:
+        load = load if load is not None else _new(G, _I32, logits, stream)
+        score_sum = score_sum if score_sum is not None else _new(G, _F32, logits, stream)
+        lp, sp = _dense(load, (G,), _I32, dev), _dense(score_sum, (G,), _F32, dev)
+        workspace, wsp, nbytes = _workspace(workspace, mx_moe_topk_workspace_bytes(T, G), logits, dev, stream)
+    _mx._check(_mx.load().mx_moe_topk(xp, xt, T, G, ld, k, score, bp, groups, topk_groups, group_top, 1 if renorm else 0,
+                                      scale, wp, ip, lp, sp, wsp, nbytes, _mx._stream(stream)))
     return weights, ids, load, score_sum
 
 
@@ -166,19 +208,18 @@ def mx_moe_topk_bwd(logits, ids, dweights, score=_mx.SCORE_SOFTMAX, renorm=True,
                     dlogits=None, stream=None):
     """The logits' gradient (of their type) from that of the weights, and of
     score_sum where dscore_sum is given."""
-    import torch
-    T, G = logits.shape
+    shape, dev, dtype = logits.shape, _gpu(logits), logits.dtype
+    T, G = shape
     k = ids.shape[1]
-    xt, ld = _type(logits), _rows(logits, (T, G), logits.dtype)
+    xt = _type(logits)
+    xp, ld = _rows(logits, shape, dtype, dev)
+    ip, ap, sp = _dense(ids, (T, k), _I32, dev), _dense(dweights, (T, k), _F32, dev), _dense(dscore_sum, (G,), _F32, dev)
     if dlogits is None:
-        dlogits = _mx._empty((T, G), logits.dtype, logits.device, stream)
-    _table(ids, (T, k), torch.int32)
-    _table(dweights, (T, k), torch.float32)
-    _vector(dscore_sum, G, torch.float32)
-    _here(logits, ids, dweights, dscore_sum, dlogits)
-    _mx._check(_mx.load().mx_moe_topk_bwd(logits.data_ptr(), xt, T, G, ld, k, score, 1 if renorm else 0, scale,
-                                          ids.data_ptr(), dweights.data_ptr(), _mx._ptr(dscore_sum),
-                                          dlogits.data_ptr(), _rows(dlogits, (T, G), logits.dtype),
+        dlogits = _new(shape, dtype, logits, stream)
+        dp, ld_d = dlogits.data_ptr(), G
+    else:
+        dp, ld_d = _rows(dlogits, shape, dtype, dev)
+    _mx._check(_mx.load().mx_moe_topk_bwd(xp, xt, T, G, ld, k, score, 1 if renorm else 0, scale, ip, ap, sp, dp, ld_d,
                                           _mx._stream(stream)))
     return dlogits
 
@@ -188,21 +229,22 @@ def mx_moe_unpermute_bwd(dout, inp, row_of, weights=None, src=None, din=None, dw
     din[row_of[t, j]] = weights[t, j] dout[t] and dweights[t, j] = <dout[t], inp[row_of[t, j]]>.
     src (mx_moe_route_index's): the empty rows of din are zeroed; rows that
     neither names are left as they were."""
-    import torch
+    dev = _gpu(dout)
     T, D = dout.shape
     R, k = inp.shape[0], row_of.shape[1]
+    op, xp, rp = _dense(dout, (T, D), _BF16, dev), _dense(inp, (R, D), _BF16, dev), _dense(row_of, (T, k), _I32, dev)
+    wp, sp = _dense(weights, (T, k), _F32, dev), _dense(src, (R,), _I32, dev)
     if din is None:
-        din = _mx._empty((R, D), torch.bfloat16, dout.device, stream)
+        din = _new((R, D), _BF16, dout, stream)
+        dp = din.data_ptr()
+    else:
+        dp = _dense(din, (R, D), _BF16, dev)
     if dweights is None:
-        dweights = _mx._empty((T, k), torch.float32, dout.device, stream)
-    for t, shape, dtype in ((dout, (T, D), torch.bfloat16), (inp, (R, D), torch.bfloat16), (din, (R, D), torch.bfloat16),
-                            (row_of, (T, k), torch.int32), (weights, (T, k), torch.float32), (src, (R,), torch.int32),
-                            (dweights, (T, k), torch.float32)):
-        _table(t, shape, dtype)
-    _here(dout, inp, row_of, weights, src, din, dweights)
-    _mx._check(_mx.load().mx_moe_unpermute_bwd(dout.data_ptr(), T, D, inp.data_ptr(), R, row_of.data_ptr(), k,
-                                               _mx._ptr(weights), _mx._ptr(src), din.data_ptr(), dweights.data_ptr(),
-                                               _mx._stream(stream)))
+        dweights = _new((T, k), _F32, dout, stream)
+        gp = dweights.data_ptr()
+    else:
+        gp = _dense(dweights, (T, k), _F32, dev)
+    _mx._check(_mx.load().mx_moe_unpermute_bwd(op, T, D, xp, R, rp, k, wp, sp, dp, gp, _mx._stream(stream)))
     return din, dweights
 
 
@@ -222,62 +264,64 @@ class NVFP4:
     them, where that is not the current one."""
 
     def __init__(self, rows, cols, device="cuda", data=None, scale=None, row_scale=None, stream=None):
-        import torch
         self.rows, self.cols = int(rows), int(cols)
         if data is None:
-            data = _mx._empty((rows, cols // 2), torch.uint8, device, stream)
-            row_scale = row_scale if row_scale is not None else _mx._empty(rows, torch.float32, device, stream)
+            data = _mx._empty((rows, cols // 2), _U8, device, stream)
+            row_scale = row_scale if row_scale is not None else _mx._empty(rows, _F32, device, stream)
         self.data, self.row_scale = data, row_scale
-        self.scale = scale if scale is not None else _mx._empty(nvfp4_scale_bytes(rows, cols), torch.uint8, device, stream)
+        self.scale = scale if scale is not None else _mx._empty(nvfp4_scale_bytes(rows, cols), _U8, device, stream)
 
     def struct(self):
         return _mx.Nvfp4Struct(self.data.data_ptr(), self.scale.data_ptr(), _mx._ptr(self.row_scale), self.rows, self.cols)
 
 
-def _fp4_buffers(t):
-    """A 4-bit tensor's buffers, dense and as large as its shape needs."""
-    assert t.data.is_contiguous() and t.data.nbytes >= t.rows * (t.cols // 2), "the codes are strided or too few"
-    assert t.scale.is_contiguous() and t.scale.nbytes >= nvfp4_scale_bytes(t.rows, t.cols), \
-        "the scales are strided or too few"
-    import torch
-    _vector(t.row_scale, t.rows, torch.float32)
-    return t.data, t.scale, t.row_scale
+def _fp4(t, dev):
+    """A 4-bit tensor's structure; its buffers are dense, as large as its shape needs
+    and on this GPU."""
+    data, scale, row = t.data, t.scale, t.row_scale
+    assert data.is_contiguous() and data.nbytes >= t.rows * (t.cols // 2) and data.get_device() == dev, \
+        "the codes are strided, too few or on another GPU"
+    assert scale.is_contiguous() and scale.nbytes >= nvfp4_scale_bytes(t.rows, t.cols) and scale.get_device() == dev, \
+        "the scales are strided, too few or on another GPU"
+    return _mx.Nvfp4Struct(data.data_ptr(), scale.data_ptr(), _dense(row, (t.rows,), _F32, dev), t.rows, t.cols)
 
 
-def mx_nvfp4_quantize(x, src=None, offsets=None, out=None, stream=None):
+@functools.lru_cache(maxsize=256)
+def mx_nvfp4_quantize_workspace_bytes(T, K, R):
+    return int(_mx.load().mx_nvfp4_quantize_workspace_bytes(T, K, R))
+
+
+def mx_nvfp4_quantize(x, src=None, offsets=None, out=None, workspace=None, stream=None):
     """BF16 rows [T, K] as a 4-bit tensor; src int32 [R]: row r is x's row src[r],
     zeros where that is negative; offsets: rows from offsets[-1] on are not produced."""
-    import ctypes
-
-    import torch
-    T, K = x.shape
+    shape, dev = x.shape, _gpu(x)
+    T, K = shape
+    xp, ld = _rows(x, shape, _BF16, dev)
     R = T if src is None else src.numel()
-    ld = _rows(x, (T, K), torch.bfloat16)
-    _vector(src, R, torch.int32)
+    sp = _dense(src, (R,), _I32, dev)
     G = 0 if offsets is None else offsets.numel()
-    _vector(offsets, G, torch.int32)
+    op = _dense(offsets, (G,), _I32, dev)
     if out is None:
         out = NVFP4(R, K, x.device, stream=stream)
     assert out.rows == R and out.cols == K, "a result of another shape"
-    _here(x, src, offsets, *_fp4_buffers(out))
-    _mx._check(_mx.load().mx_nvfp4_quantize(x.data_ptr(), T, K, ld, _mx._ptr(src), _mx._ptr(offsets), G,
-                                            ctypes.byref(out.struct()), _mx._stream(stream)))
+    nbytes = 0 if src is None else mx_nvfp4_quantize_workspace_bytes(T, K, R)
+    workspace, wsp, nbytes = _workspace(workspace, nbytes, x, dev, stream)
+    _mx._check(_mx.load().mx_nvfp4_quantize(xp, T, K, ld, sp, op, G, ctypes.byref(_fp4(out, dev)), wsp, nbytes,
+                                            _mx._stream(stream)))
     return out
 
 
 def mx_nvfp4_gemm(a, b, G=1, offsets=None, out=None, stream=None):
     """out[r] = a[r] b[g(r)]^T in BF16 from 4-bit operands a [R, K], b [G * N, K];
     rows past the last segment are not written."""
-    import ctypes
-
-    import torch
-    N = b.rows // G if G > 0 else 0
-    _vector(offsets, G, torch.int32)
+    dev = _gpu(a.data)
+    R, N = a.rows, b.rows // G if G > 0 else 0
     if out is None:
-        out = _mx._empty((a.rows, N), torch.bfloat16, a.data.device, stream)
-    ld = _rows(out, (a.rows, N), torch.bfloat16)
-    data, scale, row_scale = _fp4_buffers(a)
-    _here(data, scale, row_scale, offsets, out, *_fp4_buffers(b))
-    _mx._check(_mx.load().mx_nvfp4_gemm(ctypes.byref(a.struct()), ctypes.byref(b.struct()), G, _mx._ptr(offsets),
-                                        out.data_ptr(), ld, _mx._stream(stream)))
+        out = _new((R, N), _BF16, a.data, stream)
+        yp, ld = out.data_ptr(), N
+    else:
+        yp, ld = _rows(out, (R, N), _BF16, dev)
+    op = _dense(offsets, (G,), _I32, dev)
+    _mx._check(_mx.load().mx_nvfp4_gemm(ctypes.byref(_fp4(a, dev)), ctypes.byref(_fp4(b, dev)), G, op, yp, ld,
+                                        _mx._stream(stream)))
     return out
