@@ -305,24 +305,25 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
 }
 
 // The blocks' sums added in order, to what the gradients hold if `accumulate`: a
-// block takes 32 columns of [dw | db], its 8 warps every eighth block.
-__global__ void __launch_bounds__(256) norm_wgrad_kernel(const NormParams p, int64_t blocks) {
-  __shared__ float s[8][32];
+// block takes 32 columns of [dw | db], its 16 warps every 16th block each, all of
+// them in flight at a time.
+__global__ void __launch_bounds__(512) norm_wgrad_kernel(const NormParams p, int64_t blocks) {
+  __shared__ float s[16][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t j = (int64_t)blockIdx.x * 32 + lane;
   float t = 0.f;
   pdl_trigger();
   pdl_wait();
   if (j < 2 * p.D) {
-#pragma unroll 4
-    for (int64_t b = w; b < blocks; b += 8) t += p.partials[b * 2 * p.D + j];
+#pragma unroll 10
+    for (int64_t b = w; b < blocks; b += 16) t += p.partials[b * 2 * p.D + j];
   }
   s[w][lane] = t;
   __syncthreads();
   if (w == 0 && j < 2 * p.D) {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) a += s[i][lane];
+    for (int i = 0; i < 16; i++) a += s[i][lane];
     float* const out = j < p.D ? p.dweight : p.dbias;
     const int64_t c = j < p.D ? j : j - p.D;
     if (out != nullptr) out[c] = p.accumulate ? out[c] + a : a;
@@ -405,7 +406,7 @@ static cudaError_t launch_bwd(const NormParams& p, int W, cudaStream_t s) {
   const cudaError_t l = launch_pdl(norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>, dim3((unsigned)blocks), threads, smem, s,
                                    dim3(1), p, W);
   if (l != cudaSuccess || !WG) return l;
-  return launch_pdl(norm_wgrad_kernel, dim3((unsigned)((2 * p.D + 31) / 32)), 256, 0, s, dim3(1), p, blocks);
+  return launch_pdl(norm_wgrad_kernel, dim3((unsigned)((2 * p.D + 31) / 32)), 512, 0, s, dim3(1), p, blocks);
 }
 
 template <bool F32, bool DRES, bool WG, bool FULL>

@@ -30,6 +30,11 @@ __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
   return (uint64_t)hi << 32 | lo;
 }
 
+// The value of a 32-bit key.
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
 template <typename F> __device__ __forceinline__ F minus_inf();
 template <> __device__ __forceinline__ float minus_inf<float>() { return __uint_as_float(0xFF800000u); }
 template <> __device__ __forceinline__ double minus_inf<double>() { return __longlong_as_double(0xFFF0000000000000ll); }
@@ -133,10 +138,54 @@ __device__ __forceinline__ Softmax<F> softmax_of(const float (&x)[V]) {
   s.inv = sum == (F)0 ? (F)0 : (F)1 / sum;
   return s;
 }
+// Where scores are weighed and not compared: exp(x - top) as the hardware's power
+// of two of the scaled difference (a relative error of 2^-22 and 2 |x - top|
+// roundings of 2^-24; results below 2^-126 are 0), an eighth of expf's
+// instructions.
+__device__ __forceinline__ float exp_near(float d) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * LOG2E));
+  return r;
+}
+// The exponentials of a row above `top` (any value near the largest logit) and 1 /
+// their sum.
+template <int V>
+__device__ __forceinline__ float exps_of(const float (&x)[V], float top, float (&e)[V]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    e[i] = exp_near(x[i] - top);
+    sum += e[i];
+  }
+  sum = warp_sum(sum);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sum));
+  return sum == 0.f ? 0.f : inv;
+}
+// A value near the largest logit for exps_of; 0 where none is open.
+template <int V>
+__device__ __forceinline__ float top_of(const float (&x)[V]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < V; i++) m = fmaxf(m, x[i]);
+  m = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(m)));
+  return m == minus_inf<float>() ? 0.f : m;
+}
 template <typename F, bool SIG>
 __device__ __forceinline__ F score_of(float x, const Softmax<F>& s) {
   if constexpr (SIG) return sigmoid_of((F)x);
   else return exp_of((F)x - s.top) * s.inv;
+}
+
+// Each lane's share of the softmax over the lanes' own values (-Inf: none): the
+// chosen scores over their sum, without the row's sum and without its underflow.
+__device__ __forceinline__ float chosen_share(float xj) {
+  float m = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(xj)));
+  m = m == minus_inf<float>() ? 0.f : m;
+  const float e = exp_near(xj - m), total = warp_sum(e);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(total));
+  return total == 0.f ? 0.f : e * inv;
 }
 
 // The largest keys one after the other, the lowest index of equal ones: lane j
@@ -212,15 +261,17 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const flo
   const F err = SIG ? (F)1e-6 : (F)6e-6;
   const int e0 = lane * p.per_lane;
   Softmax<F> s{};
-  if constexpr (!SIG) s = softmax_of<F, V>(x);
+  const bool scored = p.bias != nullptr || (p.groups > 1 && p.group_top == 2);  // else the logits order everything
+  if constexpr (!SIG)
+    if (scored) s = softmax_of<F, V>(x);
   typename KeyOf<F>::type key[V];
   F c[V];
 #pragma unroll
   for (int i = 0; i < V; i++) {
     const int e = e0 + i;
     const bool there = i < p.per_lane && e < p.G;
-    c[i] = x[i] == minus_inf<float>() ? minus_inf<F>()
-                                      : score_of<F, SIG>(x[i], s) + (p.bias != nullptr && there ? (F)*(p.bias + e) : (F)0);
+    c[i] = !scored || x[i] == minus_inf<float>() ? (F)x[i]
+                                                  : score_of<F, SIG>(x[i], s) + (p.bias != nullptr && there ? (F)*(p.bias + e) : (F)0);
     // without a bias the logits have the scores' order, exactly
     key[i] = there ? order_key(p.bias == nullptr ? (F)x[i] : c[i]) : 0;
   }
@@ -230,11 +281,11 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const flo
 #pragma unroll
     for (int i = 0; i < V; i++)
       if (i < p.per_lane && e0 + i < p.G)
-        shared[e0 + i] = p.bias == nullptr && p.group_top == 1 ? (F)x[i] : c[i];
+        shared[e0 + i] = c[i];
     __syncwarp();
     bool close;
     const uint32_t kept = keep_groups<F>(p, shared, lane, 2 * err, &close);
-    *open = FAST && close && !(p.bias == nullptr && p.group_top == 1);
+    *open = FAST && close && scored;
     const int size = p.G / p.groups;
     int g = e0 / size, in = e0 - g * size;
 #pragma unroll
@@ -261,11 +312,80 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const flo
   return id;
 }
 
+// Compare-exchange of a descending sort, and the networks of up to eight values
+// (Batcher's odd-even merge sort).
+__device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = a > b ? a : b;
+  b = a > b ? b : a;
+  a = hi;
+}
+template <int V>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; i++)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) order_pair(k[i + j], k[i + j + q]);
+}
+
+// The choice by the logits alone, where nothing else orders them.  A key is the
+// logit's upper bits with the index below them, the lower one larger, so that
+// one warp maximum gives a choice with its index and equal logits go by index.
+// BF16 logits fit whole.  Of fp32 ones the last bits make room: where two of the
+// k + 1 first keys differ in the index alone, *open is set, and the caller
+// chooses by the whole logits.  *first: a value near the largest logit (truncated);
+// *own: lane j's key.
+template <int V>
+__device__ __forceinline__ int choose_plain(const RouteParams& p, const float (&x)[V], int lane, bool* open, float* first,
+                                            uint32_t* own) {
+  constexpr uint32_t MASK = 32 * V - 1;
+  const int e0 = lane * p.per_lane;
+  uint32_t key[V], mine = 0;
+#pragma unroll
+  for (int i = 0; i < V; i++)
+    key[i] = i < p.per_lane && e0 + i < p.G ? (order_key(x[i]) & ~MASK) | (MASK - (uint32_t)(e0 + i)) : 0u;
+  constexpr bool SORTED = V <= 8;  // heads of sorted lists are popped; longer lists are searched each time
+  if constexpr (SORTED) sort_down<V>(key);
+  const int count = p.x_f32 && p.k < 32 && p.k < p.G ? p.k + 1 : p.k;
+  for (int j = 0; j < count; j++) {
+    uint32_t m = key[0];
+    if constexpr (!SORTED) {
+#pragma unroll
+      for (int i = 1; i < V; i++) m = key[i] > m ? key[i] : m;
+    }
+    const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, m);
+    if constexpr (SORTED) {
+      if (m == w) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; i++) key[i] = key[i + 1];
+        key[V - 1] = 0;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i++) key[i] = key[i] == w ? 0u : key[i];
+    }
+    mine = lane == j ? w : mine;
+  }
+  const uint32_t top = __shfl_sync(0xFFFFFFFFu, mine, 0);
+  const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
+  *open = p.x_f32 && (__any_sync(0xFFFFFFFFu, lane > 0 && lane < count && ((mine ^ up) & ~MASK) == 0u) ||
+                      (p.k == 32 && p.G > 32));
+  // nothing open: 0 instead of -Inf
+  *first = (top & ~MASK) == (order_key(minus_inf<float>()) & ~MASK) ? 0.f : key_value(top & ~MASK);
+  *own = mine;
+  return (int)(MASK - (mine & MASK));
+}
+
 // Forward.  The order is that of the exact values: by the logits themselves
 // where there is no bias (both scores grow with them), else by score + bias in
 // fp32 and, for the few tokens where two of them are nearer than their error,
 // again in fp64.
-template <int V, bool SIG>
+// PLAIN: neither bias nor groups.
+template <int V, bool SIG, bool PLAIN>
 __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
   extern __shared__ char route_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * p.per_lane;
@@ -286,31 +406,59 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
     float x[V];
     load_logits<V>(p, t, lane, x);
     bool open;
-    int id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
-    if (open) id = choose<V, SIG, double>(p, t, x, values, lane, &open);
-    Softmax<float> s{};
-    if constexpr (!SIG) s = softmax_of<float, V>(x);
+    int id;
     const bool mine = lane < p.k;
-    float w = mine ? score_of<float, SIG>(load_logit(p, t, id), s) : 0.f;
-    if (p.renorm) {
-      const float total = warp_sum_of(w);
-      w = total == 0.f ? 0.f : w / total;
+    float xj, own[V], norm = 1.f;
+    Softmax<float> s{};
+    if constexpr (PLAIN) {
+      uint32_t key;
+      id = choose_plain<V>(p, x, lane, &open, &s.top, &key);
+      // a BF16 logit is its key's upper half
+      xj = p.x_f32 ? 0.f : key_value((key & 0x80000000u) ? key & 0xFFFF0000u : key | 0xFFFFu);
+      if (open) id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
+      if (p.x_f32 && mine) xj = load_logit(p, t, id);
+    } else {
+      id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
+      if (open) id = choose<V, SIG, double>(p, t, x, values, lane, &open);
+      if constexpr (!SIG) s.top = top_of<V>(x);
+      xj = mine ? load_logit(p, t, id) : 0.f;
+      if constexpr (!SIG) {  // a NaN or +Inf anywhere in the row is one in all of its scores
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < V; i++) bad |= !(x[i] < __uint_as_float(0x7F800000u));
+        if (__any_sync(0xFFFFFFFFu, bad)) xj = __uint_as_float(0x7FC00000u);
+      }
+    }
+    if (!mine) xj = minus_inf<float>();
+    if (!SIG && (stats || !p.renorm)) s.inv = exps_of<V>(x, s.top, own);
+    float w;
+    if constexpr (SIG) {
+      w = mine ? sigmoid_of(xj) : 0.f;
+      if (p.renorm) {
+        const float total = warp_sum_of(w);
+        w = total == 0.f ? 0.f : w / total;
+      }
+    } else if (p.renorm) {
+      w = chosen_share(xj);
+    } else {
+      w = exp_near(xj - s.top) * s.inv;
     }
     if (mine) {
       p.weights[t * p.k + lane] = w * p.scale;
       p.ids[t * p.k + lane] = id;
     }
     if (stats) {
-      float own[V], norm = 1.f;
-#pragma unroll
-      for (int i = 0; i < V; i++)
-        own[i] = i < p.per_lane && e0 + i < p.G ? score_of<float, SIG>(x[i], s) : 0.f;
       if constexpr (SIG) {
         norm = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; i++) norm += own[i];
+        for (int i = 0; i < V; i++) {
+          own[i] = i < p.per_lane && e0 + i < p.G ? sigmoid_of(x[i]) : 0.f;
+          norm += own[i];
+        }
         norm = warp_sum_of(norm);
         norm = norm == 0.f ? 0.f : 1.f / norm;
+      } else {
+        norm = s.inv;
       }
 #pragma unroll
       for (int i = 0; i < V; i++) share[i] = fmaf(own[i], norm, share[i]);
@@ -333,19 +481,19 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
   }
 }
 
-// The blocks' counts and sums added in order: a block takes 32 experts, its 8
-// warps every eighth block.
-__global__ void __launch_bounds__(256) route_stats_kernel(const RouteParams p, int blocks) {
-  __shared__ float s[8][32];
-  __shared__ int32_t n[8][32];
+// The blocks' counts and sums added in order: a block takes 32 experts, its 32
+// warps every 32nd block each, with eight of them in flight at a time.
+__global__ void __launch_bounds__(1024) route_stats_kernel(const RouteParams p, int blocks) {
+  __shared__ float s[32][32];
+  __shared__ int32_t n[32][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
   float t = 0.f;
   int32_t c = 0;
   pdl_trigger();
   pdl_wait();
   if (e < p.G) {
-#pragma unroll 4
-    for (int b = w; b < blocks; b += 8) {
+#pragma unroll 8
+    for (int b = w; b < blocks; b += 32) {
       t += p.partial_sum[(int64_t)b * p.G + e];
       c += p.partial_load[(int64_t)b * p.G + e];
     }
@@ -357,7 +505,7 @@ __global__ void __launch_bounds__(256) route_stats_kernel(const RouteParams p, i
     t = 0.f;
     c = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
+    for (int i = 0; i < 32; i++) {
       t += s[i][lane];
       c += n[i][lane];
     }
@@ -372,15 +520,18 @@ __global__ void __launch_bounds__(256) route_stats_kernel(const RouteParams p, i
 //   sigmoid: r_j (a_j - A) (1 - s_j), or a_j s_j (1 - s_j),
 // and the gradient v of the scores' sums, with p = softmax, or sigmoid / its sum:
 //   p_e (v_e - sum v p), for the sigmoid times (1 - s_e).
-// (1 - s = sigmoid(-x), without cancellation.)  Closed experts (-Inf): 0.
+// (1 - s = sigmoid(-x), without cancellation; 0 where a score is 0, as of a closed
+// expert.)
 template <int V, bool SIG>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * p.per_lane;
   pdl_trigger();
   pdl_wait();
+  // With renormalised weights and no gradient of the sums, all but the choices' get 0.
+  const bool dense = p.dsum != nullptr || (!SIG && !p.renorm);
   for (int64_t t = (int64_t)blockIdx.x * 8 + warp; t < p.T; t += (int64_t)gridDim.x * 8) {
     float x[V], d[V];
-    load_logits<V>(p, t, lane, x);
+    if (dense) load_logits<V>(p, t, lane, x);
     int id = -1;
     float a = 0.f;
     if (lane < p.k) {
@@ -392,28 +543,34 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
         a = *(p.dweights + t * p.k + lane) * p.scale;
       }
     }
-    Softmax<float> s{};
-    if constexpr (!SIG) s = softmax_of<float, V>(x);
     const float xj = id >= 0 ? load_logit(p, t, id) : minus_inf<float>();
-    const float sj = id >= 0 ? score_of<float, SIG>(xj, s) : 0.f;
-    float r = sj, all = 0.f;
-    if (p.renorm) {
-      const float total = warp_sum_of(sj);
-      r = total == 0.f ? 0.f : sj / total;
-      a -= warp_sum_of(a * r);
-    } else if (!SIG) {
-      all = warp_sum_of(a * r);  // taken from every expert below
+    float own[V], norm = 1.f, v_mean = 0.f, top = 0.f, inv = 0.f;
+    if (!SIG && dense) {
+      top = top_of<V>(x);
+      inv = exps_of<V>(x, top, own);
     }
+    float r, all = 0.f;
+    if constexpr (SIG) {
+      r = id >= 0 ? sigmoid_of(xj) : 0.f;
+      if (p.renorm) {
+        const float total = warp_sum_of(r);
+        r = total == 0.f ? 0.f : r / total;
+      }
+    } else {
+      r = p.renorm ? chosen_share(xj) : exp_near(xj - top) * inv;
+    }
+    if (p.renorm) a -= warp_sum_of(a * r);
+    else if (!SIG) all = warp_sum_of(a * r);  // taken from every expert below
     float g = r == 0.f ? 0.f : r * a;
     if (SIG) g *= sigmoid_of(-xj);
-    float own[V], norm = 1.f, v_mean = 0.f;
-    const bool dense = p.dsum != nullptr || (!SIG && !p.renorm);
 #pragma unroll
     for (int i = 0; i < V; i++) d[i] = 0.f;
     if (dense) {
 #pragma unroll
-      for (int i = 0; i < V; i++)
-        own[i] = i < p.per_lane && e0 + i < p.G && x[i] != minus_inf<float>() ? score_of<float, SIG>(x[i], s) : 0.f;
+      for (int i = 0; i < V; i++) {
+        if constexpr (SIG) own[i] = i < p.per_lane && e0 + i < p.G ? sigmoid_of(x[i]) : 0.f;
+        else own[i] *= inv;
+      }
       if (p.dsum != nullptr) {
         if constexpr (SIG) {
           norm = 0.f;
@@ -435,11 +592,12 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
         if (SIG) d[i] *= sigmoid_of(-x[i]);
       }
     }
+#pragma unroll 4
     for (int j = 0; j < p.k; j++) {  // each choice's part to the lane that has its expert
       const int e = __shfl_sync(0xFFFFFFFFu, id, j) - e0;
       const float part = __shfl_sync(0xFFFFFFFFu, g, j);
 #pragma unroll
-      for (int i = 0; i < V; i++) d[i] += e == i && i < p.per_lane ? part : 0.f;
+      for (int i = 0; i < V; i++) d[i] += e == i ? part : 0.f;
     }
     if (p.x_f32) {
       float* const out = static_cast<float*>(p.dlogits) + t * p.ld_d + e0;
@@ -493,13 +651,14 @@ static void set_layout(RouteParams& p) {
 template <int V, bool SIG>
 static cudaError_t launch_v(const RouteParams& p, bool bwd, cudaStream_t s) {
   const dim3 grid((unsigned)route_blocks(p.T));
-  if (bwd) return launch_pdl(route_bwd_kernel<V, SIG>, grid, 256, 0, s, dim3(1), p);
+  if (bwd) return launch_pdl(route_bwd_kernel<V, SIG>, dim3((unsigned)(p.T < 152 * 64 ? (p.T + 7) / 8 : 152 * 8)), 256, 0, s, dim3(1), p);
   const int smem = (p.groups > 1 ? 8 * p.G * 8 : 0) + (p.partial_load ? 8 * p.G : 0);
+  if (p.bias == nullptr && p.groups <= 1) return launch_pdl(route_fwd_kernel<V, SIG, true>, grid, 256, smem, s, dim3(1), p);
   if (smem > 32 * 1024) {
-    const cudaError_t e = ensure_smem_attr<route_fwd_kernel<V, SIG>>(8 * 1024 * 8 + 8 * 1024);
+    const cudaError_t e = ensure_smem_attr<route_fwd_kernel<V, SIG, false>>(8 * 1024 * 8 + 8 * 1024);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(route_fwd_kernel<V, SIG>, grid, 256, smem, s, dim3(1), p);
+  return launch_pdl(route_fwd_kernel<V, SIG, false>, grid, 256, smem, s, dim3(1), p);
 }
 template <bool SIG>
 static cudaError_t launch_slots(const RouteParams& p, bool bwd, cudaStream_t s) {
@@ -517,7 +676,7 @@ cudaError_t launch_route_fwd(RouteParams p, cudaStream_t s) {
   set_layout(p);
   const cudaError_t e = p.sigmoid ? launch_slots<true>(p, false, s) : launch_slots<false>(p, false, s);
   if (e != cudaSuccess || p.partial_load == nullptr) return e;
-  return launch_pdl(route_stats_kernel, dim3((unsigned)((p.G + 31) / 32)), 256, 0, s, dim3(1), p, (int)route_blocks(p.T));
+  return launch_pdl(route_stats_kernel, dim3((unsigned)((p.G + 31) / 32)), 1024, 0, s, dim3(1), p, (int)route_blocks(p.T));
 }
 
 cudaError_t launch_route_bwd(RouteParams p, cudaStream_t s) {
