@@ -258,27 +258,57 @@ def nvfp4_scale_bytes(rows, cols):
 
 
 class NVFP4:
-    """A 4-bit tensor [rows, cols] in torch buffers: packed E2M1 codes (uint8
-    [rows, cols / 2]), E4M3 scales per 16 values in the blocked layout (uint8),
-    fp32 scale of each row (None as an operand: ones); stream: the one that fills
-    them, where that is not the current one."""
+    """A 4-bit tensor [rows, cols] in torch buffers: `data`, packed E2M1 codes (uint8
+    [rows, cols / 2]), `scale`, E4M3 scales per 16 values in the blocked layout
+    (uint8), `row_scale`, fp32 of each row (None as an operand: ones).  Without buffers
+    of the caller's the three are views of one allocation, made when they are asked
+    for; stream: the one that fills them, where that is not the current one."""
 
     def __init__(self, rows, cols, device="cuda", data=None, scale=None, row_scale=None, stream=None):
-        self.rows, self.cols = int(rows), int(cols)
+        self.rows, self.cols = rows, cols = int(rows), int(cols)
+        self._buffer, self._own = None, None
         if data is None:
-            data = _mx._empty((rows, cols // 2), _U8, device, stream)
-            row_scale = row_scale if row_scale is not None else _mx._empty(rows, _F32, device, stream)
-        self.data, self.row_scale = data, row_scale
-        self.scale = scale if scale is not None else _mx._empty(nvfp4_scale_bytes(rows, cols), _U8, device, stream)
+            assert scale is None and row_scale is None, "scales without codes"
+            self._sizes = rows * cols // 2, nvfp4_scale_bytes(rows, cols), 4 * rows
+            at = (self._sizes[0] + 15) // 16 * 16
+            self._at = 0, at, at + self._sizes[1]    # the scales are whole blocks of 512 bytes
+            nbytes = self._at[2] + self._sizes[2]
+            self._buffer = torch.empty(nbytes, dtype=_U8, device=device) if stream is None else \
+                _mx._empty(nbytes, _U8, device, stream)
+        else:
+            if scale is None:
+                scale = _mx._empty(nvfp4_scale_bytes(rows, cols), _U8, device, stream)
+            self._own = [data, scale, row_scale]
+
+    def _parts(self):
+        if self._own is None:
+            d, s, r = (self._buffer[a:a + n] for a, n in zip(self._at, self._sizes))
+            self._own = [d.view(self.rows, self.cols // 2), s, r.view(_F32)]
+        return self._own
+
+    def _set(self, i, value):
+        self._parts()[i] = value
+
+    data = property(lambda self: self._parts()[0], lambda self, v: self._set(0, v))
+    scale = property(lambda self: self._parts()[1], lambda self, v: self._set(1, v))
+    row_scale = property(lambda self: self._parts()[2], lambda self, v: self._set(2, v))
 
     def struct(self):
-        return _mx.Nvfp4Struct(self.data.data_ptr(), self.scale.data_ptr(), _mx._ptr(self.row_scale), self.rows, self.cols)
+        return _fp4(self, self._parts()[0].get_device())
+
+
+def _fp4_first(t):
+    return t._buffer if t._own is None else t._own[0]
 
 
 def _fp4(t, dev):
     """A 4-bit tensor's structure; its buffers are dense, as large as its shape needs
     and on this GPU."""
-    data, scale, row = t.data, t.scale, t.row_scale
+    if t._own is None:
+        assert t._buffer.get_device() == dev, "a 4-bit tensor on another GPU"
+        p, at = t._buffer.data_ptr(), t._at
+        return _mx.Nvfp4Struct(p, p + at[1], p + at[2], t.rows, t.cols)
+    data, scale, row = t._own
     assert data.is_contiguous() and data.nbytes >= t.rows * (t.cols // 2) and data.get_device() == dev, \
         "the codes are strided, too few or on another GPU"
     assert scale.is_contiguous() and scale.nbytes >= nvfp4_scale_bytes(t.rows, t.cols) and scale.get_device() == dev, \
@@ -314,10 +344,11 @@ def mx_nvfp4_quantize(x, src=None, offsets=None, out=None, workspace=None, strea
 def mx_nvfp4_gemm(a, b, G=1, offsets=None, out=None, stream=None):
     """out[r] = a[r] b[g(r)]^T in BF16 from 4-bit operands a [R, K], b [G * N, K];
     rows past the last segment are not written."""
-    dev = _gpu(a.data)
+    first = _fp4_first(a)
+    dev = _gpu(first)
     R, N = a.rows, b.rows // G if G > 0 else 0
     if out is None:
-        out = _new((R, N), _BF16, a.data, stream)
+        out = _new((R, N), _BF16, first, stream)
         yp, ld = out.data_ptr(), N
     else:
         yp, ld = _rows(out, (R, N), _BF16, dev)
