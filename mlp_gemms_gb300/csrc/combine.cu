@@ -7,77 +7,101 @@ namespace mx {
 
 static __device__ unsigned g_combine_status = 0;
 
+// The sums over a warp of eight values a lane: after each exchange a lane keeps
+// half of its values, so that lane l ends with the sum of value l / 4 (9 shuffles
+// instead of 40).
+__device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
+#pragma unroll
+  for (int half = 4; half >= 1; half >>= 1) {
+    const bool up = lane & (4 * half);
+#pragma unroll
+    for (int i = 0; i < half; i++) {
+      const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, 4 * half);
+    }
+  }
+  float s = v[0];
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+  return s + __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+}
+
 // din[row of (t, j)] = w[t, j] dout[t], dw[t, j] = sum over columns of
 // dout[t] in[row].  Bound by memory: a token's gradient is read once for all its
-// choices, every expert row read and written once.  A block takes a token, a
-// thread 8 columns of it at a time for up to 8 choices, whose loads are all in
-// flight together; the dot products' sums meet in shared memory, in a fixed
-// order.
+// choices, every expert row read and written once.  A block takes a token and up
+// to 8 choices at a time, a thread 8 columns of them, whose loads are all in flight
+// together; the next item's rows and weights are asked for before this one's
+// columns.  The dot products' sums meet in shared memory, in a fixed order.
 constexpr int JB = 8;
-__global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdParams p) {
+__global__ void __launch_bounds__(256, 3) combine_bwd_kernel(const CombineBwdParams p) {
   __shared__ float part[2][8][JB];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  int flip = 0;
+  const int per = (p.k + JB - 1) / JB;
+  const int64_t items = p.T * per;
+  int flip = 0, row_next = -1;
+  float w_next = 1.f;
   pdl_trigger();
   pdl_wait();
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    for (int j0 = 0; j0 < p.k; j0 += JB) {
-      const int n = p.k - j0 < JB ? p.k - j0 : JB;
-      int64_t row[JB];
-      float w[JB], dot[JB] = {};
-#pragma unroll
-      for (int j = 0; j < JB; j++) {
-        row[j] = -1;
-        w[j] = 1.f;
-        if (j < n) {
-          row[j] = *(p.row_of + t * p.k + j0 + j);
-          if (p.weights != nullptr) w[j] = *(p.weights + t * p.k + j0 + j);
-        }
-        if (row[j] >= p.R) {
-          if (tid == 0) atomicOr(&g_combine_status, DEV_BAD_INDEX);
-          row[j] = -1;
-        }
-      }
-      for (int64_t c = (int64_t)tid * 8; c < p.D; c += (int64_t)blockDim.x * 8) {
-        const Raw8<false> dr = load_raw8<false>(p.dout, t * p.D + c);
-        Raw8<false> xr[JB];
-        if (p.dweights != nullptr) {
-#pragma unroll
-          for (int j = 0; j < JB; j++)
-            if (row[j] >= 0) xr[j] = load_raw8<false>(p.in, row[j] * p.D + c);
-        }
-        float d[8];
-        unpack_raw8<false>(dr, d);
-#pragma unroll
-        for (int j = 0; j < JB; j++) {
-          if (row[j] < 0) continue;
-          float v[8];
-          if (p.dweights != nullptr) {
-            unpack_raw8<false>(xr[j], v);
-#pragma unroll
-            for (int i = 0; i < 8; i++) dot[j] = fmaf(d[i], v[i], dot[j]);
-          }
-          if (p.din != nullptr) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = w[j] * d[i];
-            store_raw8<false>(p.din, row[j] * p.D + c, pack_raw8<false>(v));
-          }
-        }
-      }
-      if (p.dweights == nullptr) continue;
-#pragma unroll
-      for (int j = 0; j < JB; j++) {
-        const float s = warp_sum(dot[j]);
-        if (lane == 0) part[flip][warp][j] = s;
-      }
-      __syncthreads();
-      if (tid < n) {
-        float s = 0.f;
-        for (int i = 0; i < warps; i++) s += part[flip][i][tid];
-        p.dweights[t * p.k + j0 + tid] = s;
-      }
-      flip ^= 1;  // the next sums go elsewhere while these are read
+  const auto ask = [&](int64_t item) {  // lane j: choice j of the item
+    row_next = -1;
+    if (item >= items) return;
+    const int64_t t = per == 1 ? item : item / per;
+    const int j = (int)(item - t * per) * JB + lane;
+    if (lane >= JB || j >= p.k) return;
+    row_next = *(p.row_of + t * p.k + j);
+    if (p.weights != nullptr) w_next = *(p.weights + t * p.k + j);
+  };
+  ask(blockIdx.x);
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t t = per == 1 ? item : item / per;
+    const int j0 = (int)(item - t * per) * JB;
+    int row_mine = row_next;
+    const float w_mine = w_next;
+    if (row_mine >= p.R) {
+      if (warp == 0) atomicOr(&g_combine_status, DEV_BAD_INDEX);
+      row_mine = -1;
     }
+    ask(item + gridDim.x);
+    float dot[JB] = {};
+    for (int64_t c0 = (int64_t)warp * 256; c0 < p.D; c0 += (int64_t)blockDim.x * 8) {  // the whole warp
+      const int64_t c = c0 + lane * 8;
+      const bool in = c < p.D;
+      Raw8<false> dr = {}, xr[JB];
+      if (in) dr = load_raw8<false>(p.dout, t * p.D + c);
+#pragma unroll
+      for (int j = 0; j < JB; j++) {
+        const int row = __shfl_sync(0xFFFFFFFFu, row_mine, j);
+        xr[j] = {};
+        if (p.dweights != nullptr && in && row >= 0) xr[j] = load_raw8<false>(p.in, (int64_t)row * p.D + c);
+      }
+      uint64_t d[4];
+      unpack_pairs<false>(dr, d);
+#pragma unroll
+      for (int j = 0; j < JB; j++) {
+        const float w = __shfl_sync(0xFFFFFFFFu, w_mine, j);
+        const int row = __shfl_sync(0xFFFFFFFFu, row_mine, j);
+        if (row < 0) continue;  // the same for the whole warp
+        uint64_t v[4];
+        unpack_pairs<false>(xr[j], v);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = mul2(d[i], v[i]);
+        dot[j] += sum_pairs(v);
+        if (p.din != nullptr && in) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) v[i] = mul2(both(w), d[i]);
+          store_raw8<false>(p.din, (int64_t)row * p.D + c, pack_pairs<false>(v));
+        }
+      }
+    }
+    if (p.dweights == nullptr) continue;
+    const float s8 = warp_sum8(dot, lane);
+    if ((lane & 3) == 0) part[flip][warp][lane >> 2] = s8;
+    __syncthreads();
+    if (tid < JB && j0 + tid < p.k) {
+      float s = 0.f;
+      for (int i = 0; i < warps; i++) s += part[flip][i][tid];
+      p.dweights[t * p.k + j0 + tid] = s;
+    }
+    flip ^= 1;  // the next sums go elsewhere while these are read
   }
   if (p.src == nullptr || p.din == nullptr) return;
   // empty rows, 32 of a warp's at a time
@@ -93,8 +117,9 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineBwdParams
 
 cudaError_t launch_combine_bwd(const CombineBwdParams& p, int num_sms, cudaStream_t s) {
   const int threads = p.D >= 2048 ? 256 : (int)((p.D / 8 + 31) / 32 * 32);
-  const int64_t cap = (int64_t)num_sms * 8, rows = p.src && p.din ? (p.R + 31) / 32 : 0;
-  int64_t want = p.T > rows ? p.T : rows;
+  const int64_t cap = (int64_t)num_sms * 3 * (256 / threads), rows = p.src && p.din ? (p.R + 31) / 32 : 0;
+  int64_t want = p.T * ((p.k + JB - 1) / JB);
+  want = want > rows ? want : rows;
   want = want < 1 ? 1 : want < cap ? want : cap;
   return launch_pdl(combine_bwd_kernel, dim3((unsigned)want), threads, 0, s, dim3(1), p);
 }

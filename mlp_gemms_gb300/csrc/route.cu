@@ -14,8 +14,7 @@ static __device__ unsigned g_route_status = 0;
 // Floating values as integers in the same order; -0 counts as +0, a NaN above
 // everything, and 0 is free for "not there".
 __device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(v + 0.f);  // a NaN comes out of the sum as 0x7FFFFFFF
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t order_key(double v) {
@@ -179,13 +178,15 @@ __device__ __forceinline__ F score_of(float x, const Softmax<F>& s) {
 
 // Each lane's share of the softmax over the lanes' own values (-Inf: none): the
 // chosen scores over their sum, without the row's sum and without its underflow.
-__device__ __forceinline__ float chosen_share(float xj) {
-  float m = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(xj)));
-  m = m == minus_inf<float>() ? 0.f : m;
-  const float e = exp_near(xj - m), total = warp_sum(e);
+__device__ __forceinline__ float share_above(float xj, float top) {  // top: near the largest
+  const float e = exp_near(xj - top), total = warp_sum(e);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(total));
   return total == 0.f ? 0.f : e * inv;
+}
+__device__ __forceinline__ float chosen_share(float xj) {
+  const float m = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(xj)));
+  return share_above(xj, m == minus_inf<float>() ? 0.f : m);
 }
 
 // The largest keys one after the other, the lowest index of equal ones: lane j
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
         w = total == 0.f ? 0.f : w / total;
       }
     } else if (p.renorm) {
-      w = chosen_share(xj);
+      w = PLAIN ? share_above(xj, s.top) : chosen_share(xj);
     } else {
       w = exp_near(xj - s.top) * s.inv;
     }
