@@ -155,7 +155,14 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int W
 // their own columns over all of them (in registers; SMEM: in shared memory,
 // where a row's values fill the registers).  The block's groups then add theirs
 // in order, and a second launch the blocks': no atomics, the same bits each time.
-// The next row's loads are issued before this row's sums are exchanged.
+// The next one or two rows are on their way into shared memory: with one row ahead
+// in registers, the sums left room for 32 KB of loads in flight an SM ([65536,
+// 2048] BF16 152 us, 137 this way; [32768, 4096] fp32 with dres 310, 279 = 99 % of
+// the copy rate; [16384, 8192] fp32 489, 275).  Rows of
+// more than 8192 columns keep their sums there and the next row in registers.
+constexpr int bwd_stages(bool f32, int C, bool res) {
+  return C > 2 ? 1 : ((f32 ? 32 : 16) * (res ? 2 : 1) + 16) * C * 512 * 3 <= 150 * 1024 ? 3 : 2;
+}
 template <bool F32, int C, bool DRES, bool WG, bool SMEM, bool FULL>
 __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, int W) {
   extern __shared__ float4 vectors[];  // the weight, then the lanes' sums
@@ -164,7 +171,10 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
   const int group = warp / W, wr = warp - group * W, groups = (blockDim.x >> 5) / W;
   const int D = (int)p.D, c0 = (wr * 32 + lane) * 8, step = W * 256;
   const int n8 = D >> 3;
-  float* const acc_smem = reinterpret_cast<float*>(vectors + 2 * n8);
+  constexpr int S = bwd_stages(F32, C, DRES), Q = F32 ? 2 : 1;
+  uint4* const ring = reinterpret_cast<uint4*>(vectors + 2 * n8) + threadIdx.x;
+  const int stage_size = ((DRES ? 2 : 1) * Q + 1) * C * blockDim.x;
+  float* const acc_smem = reinterpret_cast<float*>(vectors + 2 * n8 + (S > 1 ? S * stage_size : 0));
   const float inv_d = 1.f / (float)D;
   const auto in = [&](int c) { return FULL || c0 + c * step < D; };
   constexpr int A = WG && !SMEM ? C : 1;
@@ -172,44 +182,87 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
   if constexpr (WG && SMEM)
 #pragma unroll 1
     for (int i = 0; i < 16 * C; i++) acc_smem[i * blockDim.x + tid] = 0.f;
-  Raw8<F32> xr[C], sr[C];
-  Raw8<false> dr[C];
-  float mean = 0.f, rstd = 0.f;
-  int flip = 0;
+  constexpr int AHEAD = S > 1 ? S - 1 : 1;
+  float means[AHEAD] = {}, rstds[AHEAD] = {};  // of the rows ahead
+  constexpr int K = S > 1 ? 1 : C;             // the next row in registers
+  Raw8<F32> xr[K] = {}, sr[K] = {};
+  Raw8<false> dr[K] = {};
+  int flip = 0, stage = 0;
   const int64_t stride = (int64_t)gridDim.x * groups;
   int64_t r = (int64_t)blockIdx.x * groups + group;
-  const auto load_row = [&](int64_t row) {
+  // pieces of a stage: dy's, then x's, then dres's
+  const auto slot = [&](int st, int c, int which) {
+    return ring + st * stage_size + (which == 0 ? c : C + ((which - 1) * C + c) * Q) * blockDim.x;
+  };
+  // An fp32 piece is 1024 bytes of a warp, copied 512 at a time (32 bytes a lane
+  // would take half of each sector with either copy) and read by other lanes.
+  const auto copy_x = [&](int st, int c, int which, const void* base, int64_t row_at) {
+    if constexpr (F32) {
+      const int64_t at = row_at + (c0 - lane * 8) + c * step;  // the warp's first column
+      uint4* const to = slot(st, c, which) - tid + warp * 64;
 #pragma unroll
-    for (int c = 0; c < C; c++) {
-      if (!in(c)) continue;
-      xr[c] = load_raw8<F32>(p.x, row * p.ld_x + c0 + c * step);
-      dr[c] = load_raw8<false>(p.dy, row * p.ld_dy + c0 + c * step);
-      if constexpr (DRES) sr[c] = load_raw8<F32>(p.res, row * p.ld_res + c0 + c * step);
+      for (int h = 0; h < 2; h++)
+        if (FULL || (c0 - lane * 8) + c * step + h * 128 + lane * 4 < D)
+          copy_ahead16(to + h * 32 + lane, static_cast<const float*>(base) + at + h * 128 + lane * 4);
+    } else {
+      copy_ahead16(slot(st, c, which), static_cast<const uint16_t*>(base) + row_at + c0 + c * step);
     }
-    if (!p.rms) mean = *(p.mean + row);
-    rstd = *(p.rstd + row);
+  };
+  const auto take_x = [&](int st, int c, int which) {
+    Raw8<F32> v;
+    const uint4* const from = F32 ? slot(st, c, which) - tid + warp * 64 + lane * 2 : slot(st, c, which);
+    v.q[0] = from[0];
+    if constexpr (F32) v.q[1] = from[1];
+    return v;
+  };
+  const auto load_row = [&](int64_t row, int st, float* m, float* s) {
+    if (row < p.R) {
+#pragma unroll
+      for (int c = 0; c < C; c++) {
+        if constexpr (S > 1) {
+          if (F32 || in(c)) {
+            copy_x(st, c, 1, p.x, row * p.ld_x);
+            if constexpr (DRES) copy_x(st, c, 2, p.res, row * p.ld_res);
+          }
+          if (in(c)) copy_ahead16(slot(st, c, 0), p.dy + row * p.ld_dy + c0 + c * step);
+        } else if (in(c)) {
+          xr[c] = load_raw8<F32>(p.x, row * p.ld_x + c0 + c * step);
+          dr[c] = load_raw8<false>(p.dy, row * p.ld_dy + c0 + c * step);
+          if constexpr (DRES) sr[c] = load_raw8<F32>(p.res, row * p.ld_res + c0 + c * step);
+        }
+      }
+      if (!p.rms) *m = *(p.mean + row);
+      *s = *(p.rstd + row);
+    }
+    commit_ahead();
   };
   pdl_trigger();
   pdl_wait();
 #pragma unroll
-  for (int c = 0; c < C; c++) {
-    xr[c] = {};
-    dr[c] = {};
-    sr[c] = {};
-  }
-  if (r < p.R) load_row(r);
+  for (int i = 0; i < AHEAD; i++) load_row(r + i * stride, i, &means[i], &rstds[i]);
   keep_vector(p.weight, p.w_f32, n8, vectors);
   __syncthreads();
   for (; r < p.R; r += stride) {
     uint64_t xh[C][4], g[C][4], t1[4] = {}, t2[4] = {};
-    Raw8<F32> skip[C];
-    const float inv = rstd;
+    const float mean = means[0], rstd = rstds[0];
+    Raw8<F32> skip[K];
+    if constexpr (S > 1) {
+      wait_ahead<S - 2>();
+      if constexpr (F32) __syncwarp();
+    }
 #pragma unroll
     for (int c = 0; c < C; c++) {
-      unpack_pairs<F32>(xr[c], xh[c]);
-      unpack_pairs<false>(dr[c], g[c]);
-      if constexpr (DRES) skip[c] = sr[c];
       if (!in(c)) continue;
+      if constexpr (S > 1) {
+        Raw8<false> d;
+        d.q[0] = *slot(stage, c, 0);
+        unpack_pairs<F32>(take_x(stage, c, 1), xh[c]);
+        unpack_pairs<false>(d, g[c]);
+      } else {
+        unpack_pairs<F32>(xr[c], xh[c]);
+        unpack_pairs<false>(dr[c], g[c]);
+        skip[c] = sr[c];
+      }
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         xh[c][i] = mul2(add2(xh[c][i], both(-mean)), both(rstd));
@@ -239,7 +292,13 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
         t2[i] = fma2(g[c][i], xh[c][i], t2[i]);
       }
     }
-    if (r + stride < p.R) load_row(r + stride);
+#pragma unroll
+    for (int i = 0; i + 1 < AHEAD; i++) {
+      means[i] = means[i + 1];
+      rstds[i] = rstds[i + 1];
+    }
+    if constexpr (F32 && S > 1) __syncwarp();  // the row before, whose place is copied over, has been read by all lanes
+    load_row(r + AHEAD * stride, stage == 0 ? S - 1 : stage - 1, &means[AHEAD - 1], &rstds[AHEAD - 1]);
     float s1 = warp_sum(sum_pairs(t1)), s2 = warp_sum(sum_pairs(t2));
     if (W > 1) {
       if (lane == 0) part[flip][warp] = make_float2(s1, s2);
@@ -258,12 +317,14 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
     for (int c = 0; c < C; c++) {
       if (!in(c)) continue;
       uint64_t d[4] = {};
-      if constexpr (DRES) unpack_pairs<F32>(skip[c], d);
+      if constexpr (DRES && S > 1) unpack_pairs<F32>(take_x(stage, c, 2), d);
+      if constexpr (DRES && S == 1) unpack_pairs<F32>(skip[c], d);
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        d[i] = fma2(both(inv), fma2(xh[c][i], both(-s2), add2(g[c][i], both(-s1))), d[i]);
+        d[i] = fma2(both(rstd), fma2(xh[c][i], both(-s2), add2(g[c][i], both(-s1))), d[i]);
       store_raw8<F32>(p.dx, r * p.ld_dx + c0 + c * step, pack_pairs<F32>(d));
     }
+    stage = stage == S - 1 ? 0 : stage + 1;
   }
   if constexpr (WG) {
     float* const out = p.partials + (int64_t)blockIdx.x * 2 * p.D;
@@ -334,6 +395,7 @@ __global__ void __launch_bounds__(512) norm_wgrad_kernel(const NormParams p, int
 // long enough, and a number of warps whose columns are the row's where there is one
 // (warps need not be a power of two: 5120 columns are 5 x 4 pieces of 256, 7168 7 x
 // 4).
+constexpr int SMEM_MOST = 226 * 1024;  // dynamic, beside the kernels' own few hundred bytes
 struct NormShape {
   int W, C;
   bool full;
@@ -378,11 +440,10 @@ cudaError_t launch_norm_fwd(const NormParams& p, int sms, cudaStream_t s) {
   return p.res ? launch_fwd<false, true>(p, sms, s) : launch_fwd<false, false>(p, sms, s);
 }
 
-// Fewer warps a row, with more columns a lane, exchange less (us: [65536, 2048]
-// BF16 with two pieces a lane 152, with one 193; [20000, 2728] 89 and 120), as long
-// as the sums and the next row fit the registers: fp32 rows with one piece
-// ([32768, 4096] with dres 310, with two 398).  Above that the sums live in shared
-// memory.
+// Fewer warps a row, with more columns a lane, exchange less (us, one row ahead in
+// registers: [65536, 2048] BF16 with two pieces a lane 152, with one 193; [20000,
+// 2728] 89 and 120).  fp32 rows, twice as long in bytes, take two where one does not
+// cover them.  Above 8192 columns the sums live in shared memory.
 static NormShape bwd_shape(int64_t D, bool f32) {
   for (int most = f32 ? 1 : 2; most <= 2; most++)
     if (D <= 256 * 16 * most) return norm_shape(D, most);
@@ -399,9 +460,10 @@ static cudaError_t launch_bwd(const NormParams& p, int W, cudaStream_t s) {
   constexpr bool SMEM = WG && C > 2;
   const int64_t blocks = norm_bwd_blocks(p.R, p.D, F32);
   const int threads = 32 * W * norm_groups(W, 16);
-  const int smem = 4 * (int)p.D + (WG ? (SMEM ? 2 : 1) * C * 8 * threads * 4 : 0);
-  const int most = 4 * (int)MAX_NORM_D + 2 * C * 8 * 512 * 4;
-  const cudaError_t e = smem > 32 * 1024 ? ensure_smem_attr<norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>>(most) : cudaSuccess;
+  constexpr int S = bwd_stages(F32, C, DRES);
+  constexpr int RING = S > 1 ? S * ((F32 ? 32 : 16) * (DRES ? 2 : 1) + 16) * C : 0;  // bytes a thread
+  const int smem = 4 * (int)p.D + RING * threads + (WG ? (SMEM ? 2 : 1) * C * 8 * threads * 4 : 0);
+  const cudaError_t e = smem > 32 * 1024 ? ensure_smem_attr<norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>>(SMEM_MOST) : cudaSuccess;
   if (e != cudaSuccess) return e;
   const cudaError_t l = launch_pdl(norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>, dim3((unsigned)blocks), threads, smem, s,
                                    dim3(1), p, W);

@@ -98,6 +98,15 @@ __device__ __forceinline__ void load_shared_pairs(const void* base, bool f32, in
   for (int i = 0; i < 4; i++) v[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
+// Rows copied ahead into shared memory, 16 bytes at a time, by the thread that will
+// read them: no barrier, no registers held by what is in flight.  A ring of S
+// stages: wait_ahead<S - 2>() leaves the newest S - 2 rows in flight.
+__device__ __forceinline__ void copy_ahead16(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void commit_ahead() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_ahead() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
