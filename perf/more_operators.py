@@ -368,7 +368,8 @@ def _library(s):
         y, mean, rstd, out = mx.mx_layernorm_fwd(s["x"], s["w"], s["b"], eps=EPS, residual=s["res"], rms=case["rms"])
         return y, mean, rstd, out if case["res"] else None
     if op == "norm_bwd":
-        return mx.mx_layernorm_bwd(s["dy"], s["x"], s["mean"], s["rstd"], s["w"], dres=s["res"], bias=case["bias"])
+        return mx.mx_layernorm_bwd(s["dy"], s["x"], s["mean"], s["rstd"], s["w"], dres=s["res"], rms=case["rms"],
+                                   bias=case["bias"])
     if op in ("route", "route_bwd"):
         score = mx.SCORE_SIGMOID if case["score"] == "sigmoid" else mx.SCORE_SOFTMAX
     if op == "route":
