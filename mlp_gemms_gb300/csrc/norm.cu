@@ -2,6 +2,7 @@
 // the same pass, and the backward pass with the weight's and the bias's
 // gradients.
 #include "mx_internal.h"
+#include "pair_common.cuh"
 #include "vec8.cuh"
 
 namespace mx {
@@ -152,44 +153,53 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int W
 // Backward.  With g = dy w and xh = (x - mean) rstd:
 //   dx = rstd (g - sum(g) / D - xh sum(g xh) / D) (+ dres),  dw = sum over rows dy xh,  db = sum over rows dy.
 // A group takes every `stride`th row; its lanes keep the sums of dw and db of
-// their own columns over all of them (in registers; SMEM: in shared memory,
-// where a row's values fill the registers).  The block's groups then add theirs
-// in order, and a second launch the blocks': no atomics, the same bits each time.
-// The next one or two rows are on their way into shared memory: with one row ahead
-// in registers, the sums left room for 32 KB of loads in flight an SM ([65536,
-// 2048] BF16 152 us, 137 this way; [32768, 4096] fp32 with dres 310, 279 = 99 % of
-// the copy rate; [16384, 8192] fp32 489, 275).  Rows of
-// more than 8192 columns keep their sums there and the next row in registers.
+// their own columns over all of them in registers.  The block's groups then add
+// theirs in order, and a second launch the blocks': no atomics, the same bits each
+// time.  The next one or two rows are on their way into shared memory: with one
+// row ahead in registers, the sums left room for 32 KB of loads in flight an SM
+// ([65536, 2048] BF16 152 us, 137 this way; [32768, 4096] fp32 with dres 310, 279 =
+// 99 % of the copy rate; [16384, 8192] fp32 489, 275).
+// PAIR: more than 8192 columns, half of them in each block of a cluster of two,
+// which exchange their halves of a row's two sums ([10217, 13136] BF16 with dres in one block
+// with the sums of dw and db in shared memory 638 us, 344 this way; [8192, 16384]
+// without 219 and 263: two exchanges a row, 2.4 us).
+__host__ __device__ constexpr int bwd_half(int D) { return ((D >> 3) + 1) / 2 * 8; }
 constexpr int bwd_stages(bool f32, int C, bool res) {
-  return C > 2 ? 1 : ((f32 ? 32 : 16) * (res ? 2 : 1) + 16) * C * 512 * 3 <= 150 * 1024 ? 3 : 2;
+  return ((f32 ? 32 : 16) * (res ? 2 : 1) + 16) * C * 512 * 3 <= 150 * 1024 ? 3 : 2;
 }
-template <bool F32, int C, bool DRES, bool WG, bool SMEM, bool FULL>
-__global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, int W) {
-  extern __shared__ float4 vectors[];  // the weight, then the lanes' sums
+template <bool F32, int C, bool DRES, bool WG, bool FULL, bool PAIR>
+__global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, int W) {
+  extern __shared__ float4 vectors[];  // the weight, the ring, the groups' sums
   __shared__ float2 part[2][16];
+  __shared__ float2 other[2];  // PAIR: the other block's half of a row's sums
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = warp / W, wr = warp - group * W, groups = (blockDim.x >> 5) / W;
-  const int D = (int)p.D, c0 = (wr * 32 + lane) * 8, step = W * 256;
+  const int c0 = (wr * 32 + lane) * 8, step = W * 256;
+  const float inv_d = 1.f / (float)p.D;
+  int D = (int)p.D, first = 0;  // this block's columns
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  if constexpr (PAIR) {
+    const int half = bwd_half(D);
+    first = rank ? half : 0;
+    D = rank ? D - half : half;
+    p.x = static_cast<const char*>(p.x) + first * (F32 ? 4 : 2);
+    p.dx = static_cast<char*>(p.dx) + first * (F32 ? 4 : 2);
+    if (DRES) p.res = static_cast<const char*>(p.res) + first * (F32 ? 4 : 2);
+    p.dy += first;
+    if (p.weight != nullptr) p.weight = static_cast<const char*>(p.weight) + first * (p.w_f32 ? 4 : 2);
+  }
   const int n8 = D >> 3;
   constexpr int S = bwd_stages(F32, C, DRES), Q = F32 ? 2 : 1;
   uint4* const ring = reinterpret_cast<uint4*>(vectors + 2 * n8) + threadIdx.x;
   const int stage_size = ((DRES ? 2 : 1) * Q + 1) * C * blockDim.x;
-  float* const acc_smem = reinterpret_cast<float*>(vectors + 2 * n8 + (S > 1 ? S * stage_size : 0));
-  const float inv_d = 1.f / (float)D;
+  float* const acc_smem = reinterpret_cast<float*>(vectors + 2 * n8 + S * stage_size);
   const auto in = [&](int c) { return FULL || c0 + c * step < D; };
-  constexpr int A = WG && !SMEM ? C : 1;
+  constexpr int A = WG ? C : 1;
   uint64_t dw[A][4] = {}, db[A][4] = {};
-  if constexpr (WG && SMEM)
-#pragma unroll 1
-    for (int i = 0; i < 16 * C; i++) acc_smem[i * blockDim.x + tid] = 0.f;
-  constexpr int AHEAD = S > 1 ? S - 1 : 1;
-  float means[AHEAD] = {}, rstds[AHEAD] = {};  // of the rows ahead
-  constexpr int K = S > 1 ? 1 : C;             // the next row in registers
-  Raw8<F32> xr[K] = {}, sr[K] = {};
-  Raw8<false> dr[K] = {};
+  float means[S - 1] = {}, rstds[S - 1] = {};  // of the rows ahead
   int flip = 0, stage = 0;
-  const int64_t stride = (int64_t)gridDim.x * groups;
-  int64_t r = (int64_t)blockIdx.x * groups + group;
+  const int64_t stride = (int64_t)(PAIR ? gridDim.x / 2 : gridDim.x) * groups;
+  int64_t r = (int64_t)(PAIR ? blockIdx.x / 2 : blockIdx.x) * groups + group;
   // pieces of a stage: dy's, then x's, then dres's
   const auto slot = [&](int st, int c, int which) {
     return ring + st * stage_size + (which == 0 ? c : C + ((which - 1) * C + c) * Q) * blockDim.x;
@@ -219,17 +229,11 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
     if (row < p.R) {
 #pragma unroll
       for (int c = 0; c < C; c++) {
-        if constexpr (S > 1) {
-          if (F32 || in(c)) {
-            copy_x(st, c, 1, p.x, row * p.ld_x);
-            if constexpr (DRES) copy_x(st, c, 2, p.res, row * p.ld_res);
-          }
-          if (in(c)) copy_ahead16(slot(st, c, 0), p.dy + row * p.ld_dy + c0 + c * step);
-        } else if (in(c)) {
-          xr[c] = load_raw8<F32>(p.x, row * p.ld_x + c0 + c * step);
-          dr[c] = load_raw8<false>(p.dy, row * p.ld_dy + c0 + c * step);
-          if constexpr (DRES) sr[c] = load_raw8<F32>(p.res, row * p.ld_res + c0 + c * step);
+        if (F32 || in(c)) {
+          copy_x(st, c, 1, p.x, row * p.ld_x);
+          if constexpr (DRES) copy_x(st, c, 2, p.res, row * p.ld_res);
         }
+        if (in(c)) copy_ahead16(slot(st, c, 0), p.dy + row * p.ld_dy + c0 + c * step);
       }
       if (!p.rms) *m = *(p.mean + row);
       *s = *(p.rstd + row);
@@ -239,45 +243,27 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
   pdl_trigger();
   pdl_wait();
 #pragma unroll
-  for (int i = 0; i < AHEAD; i++) load_row(r + i * stride, i, &means[i], &rstds[i]);
+  for (int i = 0; i < S - 1; i++) load_row(r + i * stride, i, &means[i], &rstds[i]);
   keep_vector(p.weight, p.w_f32, n8, vectors);
   __syncthreads();
   for (; r < p.R; r += stride) {
     uint64_t xh[C][4], g[C][4], t1[4] = {}, t2[4] = {};
     const float mean = means[0], rstd = rstds[0];
-    Raw8<F32> skip[K];
-    if constexpr (S > 1) {
-      wait_ahead<S - 2>();
-      if constexpr (F32) __syncwarp();
-    }
+    wait_ahead<S - 2>();
+    if constexpr (F32) __syncwarp();
 #pragma unroll
     for (int c = 0; c < C; c++) {
       if (!in(c)) continue;
-      if constexpr (S > 1) {
-        Raw8<false> d;
-        d.q[0] = *slot(stage, c, 0);
-        unpack_pairs<F32>(take_x(stage, c, 1), xh[c]);
-        unpack_pairs<false>(d, g[c]);
-      } else {
-        unpack_pairs<F32>(xr[c], xh[c]);
-        unpack_pairs<false>(dr[c], g[c]);
-        skip[c] = sr[c];
-      }
+      Raw8<false> d;
+      d.q[0] = *slot(stage, c, 0);
+      unpack_pairs<F32>(take_x(stage, c, 1), xh[c]);
+      unpack_pairs<false>(d, g[c]);
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         xh[c][i] = mul2(add2(xh[c][i], both(-mean)), both(rstd));
-        if constexpr (WG && !SMEM) {
+        if constexpr (WG) {
           dw[c][i] = fma2(g[c][i], xh[c][i], dw[c][i]);
           db[c][i] = add2(db[c][i], g[c][i]);
-        }
-        if constexpr (WG && SMEM) {
-          float a, b, u, v;
-          unpack2(mul2(g[c][i], xh[c][i]), &a, &b);
-          unpack2(g[c][i], &u, &v);
-          acc_smem[(c * 8 + 2 * i) * blockDim.x + tid] += a;
-          acc_smem[(c * 8 + 2 * i + 1) * blockDim.x + tid] += b;
-          acc_smem[((C + c) * 8 + 2 * i) * blockDim.x + tid] += u;
-          acc_smem[((C + c) * 8 + 2 * i + 1) * blockDim.x + tid] += v;
         }
       }
       if (p.weight != nullptr) {
@@ -293,12 +279,12 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
       }
     }
 #pragma unroll
-    for (int i = 0; i + 1 < AHEAD; i++) {
+    for (int i = 0; i + 2 < S; i++) {
       means[i] = means[i + 1];
       rstds[i] = rstds[i + 1];
     }
-    if constexpr (F32 && S > 1) __syncwarp();  // the row before, whose place is copied over, has been read by all lanes
-    load_row(r + AHEAD * stride, stage == 0 ? S - 1 : stage - 1, &means[AHEAD - 1], &rstds[AHEAD - 1]);
+    if constexpr (F32) __syncwarp();  // the row before, whose place is copied over, has been read by all lanes
+    load_row(r + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1, &means[S - 2], &rstds[S - 2]);
     float s1 = warp_sum(sum_pairs(t1)), s2 = warp_sum(sum_pairs(t2));
     if (W > 1) {
       if (lane == 0) part[flip][warp] = make_float2(s1, s2);
@@ -309,6 +295,18 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
         s1 += q.x;
         s2 += q.y;
       }
+      if constexpr (PAIR) {  // both halves, the first block's first
+        if (tid == 0) {
+          const uint32_t to = rank ? leader_addr(&other[flip]) : peer_addr(&other[flip]);
+          st_cluster_u32(to, __float_as_uint(s1));
+          st_cluster_u32(to + 4, __float_as_uint(s2));
+        }
+        __syncwarp();
+        cluster_sync_all();
+        const float2 o = other[flip];
+        s1 = rank ? o.x + s1 : s1 + o.x;
+        s2 = rank ? o.y + s2 : s2 + o.y;
+      }
       flip ^= 1;
     }
     s1 = p.rms ? 0.f : s1 * inv_d;
@@ -317,8 +315,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
     for (int c = 0; c < C; c++) {
       if (!in(c)) continue;
       uint64_t d[4] = {};
-      if constexpr (DRES && S > 1) unpack_pairs<F32>(take_x(stage, c, 2), d);
-      if constexpr (DRES && S == 1) unpack_pairs<F32>(skip[c], d);
+      if constexpr (DRES) unpack_pairs<F32>(take_x(stage, c, 2), d);
 #pragma unroll
       for (int i = 0; i < 4; i++)
         d[i] = fma2(both(rstd), fma2(xh[c][i], both(-s2), add2(g[c][i], both(-s1))), d[i]);
@@ -327,22 +324,20 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
     stage = stage == S - 1 ? 0 : stage + 1;
   }
   if constexpr (WG) {
-    float* const out = p.partials + (int64_t)blockIdx.x * 2 * p.D;
+    float* const out = p.partials + (int64_t)(PAIR ? blockIdx.x / 2 : blockIdx.x) * 2 * p.D + first;
 #pragma unroll
     for (int which = 0; which < 2; which++) {
-      if (!SMEM && groups > 1) {
+      if (groups > 1) {
         __syncthreads();
-        if constexpr (!SMEM) {
 #pragma unroll
-          for (int c = 0; c < C; c++)
+        for (int c = 0; c < C; c++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-              float a, b;
-              unpack2(which ? db[c][i] : dw[c][i], &a, &b);
-              acc_smem[(c * 8 + 2 * i) * blockDim.x + tid] = a;
-              acc_smem[(c * 8 + 2 * i + 1) * blockDim.x + tid] = b;
-            }
-        }
+          for (int i = 0; i < 4; i++) {
+            float a, b;
+            unpack2(which ? db[c][i] : dw[c][i], &a, &b);
+            acc_smem[(c * 8 + 2 * i) * blockDim.x + tid] = a;
+            acc_smem[(c * 8 + 2 * i + 1) * blockDim.x + tid] = b;
+          }
         __syncthreads();
       }
       if (group != 0) continue;
@@ -350,15 +345,11 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormParams p, in
       for (int c = 0; c < C; c++) {
         if (!in(c)) continue;
         float t[8];
-        if constexpr (!SMEM) {
 #pragma unroll
-          for (int i = 0; i < 4; i++) unpack2(which ? db[c][i] : dw[c][i], &t[2 * i], &t[2 * i + 1]);
-        }
+        for (int i = 0; i < 4; i++) unpack2(which ? db[c][i] : dw[c][i], &t[2 * i], &t[2 * i + 1]);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          if constexpr (SMEM) t[i] = acc_smem[((which * C + c) * 8 + i) * blockDim.x + tid];
+        for (int i = 0; i < 8; i++)
           for (int k = 1; k < groups; k++) t[i] += acc_smem[(c * 8 + i) * blockDim.x + k * W * 32 + tid];
-        }
         store_raw8<true>(out, which * p.D + c0 + c * step, pack_raw8<true>(t));
       }
     }
@@ -443,47 +434,52 @@ cudaError_t launch_norm_fwd(const NormParams& p, int sms, cudaStream_t s) {
 // Fewer warps a row, with more columns a lane, exchange less (us, one row ahead in
 // registers: [65536, 2048] BF16 with two pieces a lane 152, with one 193; [20000,
 // 2728] 89 and 120).  fp32 rows, twice as long in bytes, take two where one does not
-// cover them.  Above 8192 columns the sums live in shared memory.
-static NormShape bwd_shape(int64_t D, bool f32) {
-  for (int most = f32 ? 1 : 2; most <= 2; most++)
-    if (D <= 256 * 16 * most) return norm_shape(D, most);
-  return norm_shape(D, 4);
+// cover them.
+struct BwdShape {
+  NormShape n;  // of a block's columns
+  bool pair;
+};
+static BwdShape bwd_shape(int64_t D, bool f32) {
+  if (D > 8192) {
+    const int64_t half = bwd_half((int)D);
+    NormShape n = norm_shape(half, 2);
+    n.full = n.full && 2 * half == D;
+    return {n, true};
+  }
+  return {norm_shape(D, f32 && D <= 4096 ? 1 : 2), false};
 }
 int64_t norm_bwd_blocks(int64_t R, int64_t D, bool f32) {
-  const int groups = norm_groups(bwd_shape(D, f32).W, 16);
+  const BwdShape b = bwd_shape(D, f32);
+  const int groups = norm_groups(b.n.W, 16), most = b.pair ? 76 : 152;  // a block on every SM (GB300: 152)
   const int64_t want = (R + groups - 1) / groups;
-  return want < 152 ? want : 152;  // one on every SM (GB300: 152)
+  return want < most ? want : most;
 }
 
-template <bool F32, int C, bool DRES, bool WG, bool FULL>
+template <bool F32, int C, bool DRES, bool WG, bool FULL, bool PAIR>
 static cudaError_t launch_bwd(const NormParams& p, int W, cudaStream_t s) {
-  constexpr bool SMEM = WG && C > 2;
-  const int64_t blocks = norm_bwd_blocks(p.R, p.D, F32);
-  const int threads = 32 * W * norm_groups(W, 16);
-  constexpr int S = bwd_stages(F32, C, DRES);
-  constexpr int RING = S > 1 ? S * ((F32 ? 32 : 16) * (DRES ? 2 : 1) + 16) * C : 0;  // bytes a thread
-  const int smem = 4 * (int)p.D + RING * threads + (WG ? (SMEM ? 2 : 1) * C * 8 * threads * 4 : 0);
-  const cudaError_t e = smem > 32 * 1024 ? ensure_smem_attr<norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>>(SMEM_MOST) : cudaSuccess;
+  const int64_t blocks = norm_bwd_blocks(p.R, p.D, F32);  // PAIR: pairs
+  const int threads = 32 * W * norm_groups(W, 16), D = PAIR ? bwd_half((int)p.D) : (int)p.D;
+  constexpr int RING = bwd_stages(F32, C, DRES) * ((F32 ? 32 : 16) * (DRES ? 2 : 1) + 16) * C;  // bytes a thread
+  const int smem = 4 * D + RING * threads + (WG ? C * 8 * threads * 4 : 0);
+  const cudaError_t e =
+      smem > 32 * 1024 ? ensure_smem_attr<norm_bwd_kernel<F32, C, DRES, WG, FULL, PAIR>>(SMEM_MOST) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  const cudaError_t l = launch_pdl(norm_bwd_kernel<F32, C, DRES, WG, SMEM, FULL>, dim3((unsigned)blocks), threads, smem, s,
-                                   dim3(1), p, W);
+  const cudaError_t l = launch_pdl(norm_bwd_kernel<F32, C, DRES, WG, FULL, PAIR>, dim3((unsigned)blocks * (PAIR ? 2 : 1)),
+                                   threads, smem, s, dim3(PAIR ? 2 : 1), p, W);
   if (l != cudaSuccess || !WG) return l;
   return launch_pdl(norm_wgrad_kernel, dim3((unsigned)((2 * p.D + 31) / 32)), 512, 0, s, dim3(1), p, blocks);
 }
 
 template <bool F32, bool DRES, bool WG, bool FULL>
-static cudaError_t launch_bwd_c(const NormParams& p, const NormShape& n, cudaStream_t s) {
-  switch (n.C) {
-    case 1: return launch_bwd<F32, 1, DRES, WG, FULL>(p, n.W, s);
-    case 2: return launch_bwd<F32, 2, DRES, WG, FULL>(p, n.W, s);
-    case 3: return launch_bwd<F32, 3, DRES, WG, FULL>(p, n.W, s);
-    default: return launch_bwd<F32, 4, DRES, WG, FULL>(p, n.W, s);
-  }
+static cudaError_t launch_bwd_c(const NormParams& p, const BwdShape& b, cudaStream_t s) {
+  if (b.pair) return launch_bwd<F32, 2, DRES, WG, FULL, true>(p, b.n.W, s);  // half of more than 8192: two pieces
+  return b.n.C == 1 ? launch_bwd<F32, 1, DRES, WG, FULL, false>(p, b.n.W, s)
+                    : launch_bwd<F32, 2, DRES, WG, FULL, false>(p, b.n.W, s);
 }
 template <bool F32, bool DRES, bool WG>
 static cudaError_t launch_bwd_f(const NormParams& p, cudaStream_t s) {
-  const NormShape n = bwd_shape(p.D, F32);
-  return n.full ? launch_bwd_c<F32, DRES, WG, true>(p, n, s) : launch_bwd_c<F32, DRES, WG, false>(p, n, s);
+  const BwdShape b = bwd_shape(p.D, F32);
+  return b.n.full ? launch_bwd_c<F32, DRES, WG, true>(p, b, s) : launch_bwd_c<F32, DRES, WG, false>(p, b, s);
 }
 
 cudaError_t launch_norm_bwd(const NormParams& p, cudaStream_t s) {
