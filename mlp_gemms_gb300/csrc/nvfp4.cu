@@ -31,6 +31,8 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a) {
 __device__ __forceinline__ int64_t row_place(int64_t r, int64_t chunks) {
   return (r >> 7) * chunks * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
 }
+// Bytes of a row of scales kept row-major, in whole 16-byte pieces.
+__host__ __device__ __forceinline__ int64_t scale_pitch(int64_t K) { return (K + 255) / 256 * 16; }
 // The layout's rows past the last, zero: a warp takes a chunk of the last row
 // block, a lane the four rows that share its 16 bytes.
 __device__ __forceinline__ void pad_scales(const Nvfp4Params& p, int64_t chunks) {
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
     if (wr == 0 && lane == 0)
       p.row_scale[r] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7FC00000u);
     // scale (r, c) of the blocked layout: the row's place in a chunk, then a chunk every four columns
-    uint8_t* const scales = p.scale + (p.linear ? r * chunks * 4 : row_place(r, chunks));
+    uint8_t* const scales = p.scale + (p.linear ? r * scale_pitch(p.K) : row_place(r, chunks));
     uint8_t* const data = p.data + r * (p.K >> 1);
 #pragma unroll
     for (int c = 0; c < C; c++) {
@@ -170,14 +172,17 @@ __global__ void __launch_bounds__(512) nvfp4_quantize_kernel(const Nvfp4Params p
 }
 
 // Gathered rows of tokens that are quantized already (each for itself, so all of
-// a token's rows are the same bytes): codes, scales (row-major, whole words) and
-// row scales of T tokens, copied to every row that names one.  A warp takes ROWS
-// rows at a time, whose loads are all in flight together.
-constexpr int ROWS = 4;
-__global__ void __launch_bounds__(256) nvfp4_gather_kernel(const Nvfp4Params p, const uint8_t* data, const uint8_t* scale,
-                                                           const float* row_scale) {
+// a token's rows are the same bytes): codes, scales (row-major, 16-byte pieces) and
+// row scales of T tokens, copied to every row that names one.  A block takes a row
+// block of 128: a warp copies the codes of 16 rows, four at a time, and turns the
+// scales of four chunks, where a lane holds the four rows that share 16 bytes of the
+// layout (written row by row, as words: 36 us for 8192 tokens' quantization and
+// 73700 rows; 28 this way).
+__global__ void __launch_bounds__(256, 4) nvfp4_gather_kernel(const Nvfp4Params p, const uint8_t* data, const uint8_t* scale,
+                                                              const float* row_scale) {
+  __shared__ int from_s[128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t chunks = (p.K + 63) >> 6, bytes = p.K >> 1, stride = (int64_t)gridDim.x * 8 * ROWS;
+  const int64_t chunks = (p.K + 63) >> 6, bytes = p.K >> 1, pitch = scale_pitch(p.K);
   pdl_trigger();
   pdl_wait();
   int64_t rows = p.R;
@@ -185,50 +190,67 @@ __global__ void __launch_bounds__(256) nvfp4_gather_kernel(const Nvfp4Params p, 
     const int64_t end = *(p.offsets + p.G - 1);
     rows = end < 0 ? 0 : end < rows ? end : rows;
   }
-  for (int64_t r0 = ((int64_t)blockIdx.x * 8 + warp) * ROWS; r0 < rows; r0 += stride) {
-    int64_t from[ROWS];
+  for (int64_t b0 = (int64_t)blockIdx.x * 128; b0 < rows; b0 += (int64_t)gridDim.x * 128) {
+    __syncthreads();  // the block before has been copied
+    if (threadIdx.x < 128) {
+      const int64_t r = b0 + threadIdx.x;
+      int from = r < rows ? *(p.src + r) : -1;
+      if (from >= p.T) {
+        atomicOr(&g_nvfp4_status, DEV_BAD_INDEX);
+        from = -1;
+      }
+      from_s[threadIdx.x] = from;
+      if (r < rows) p.row_scale[r] = from >= 0 ? *(row_scale + from) : __uint_as_float((uint32_t)(127 - 100) << 23);
+    }
+    __syncthreads();
+    for (int i0 = warp * 16; i0 < warp * 16 + 16; i0 += 4) {
+      for (int64_t at = lane * 16; at < bytes; at += 512) {
+        uint4 q[4];
 #pragma unroll
-    for (int i = 0; i < ROWS; i++) {
-      from[i] = r0 + i < rows ? (int64_t)*(p.src + r0 + i) : -1;
-      if (from[i] >= p.T) {
-        if (lane == 0) atomicOr(&g_nvfp4_status, DEV_BAD_INDEX);
-        from[i] = -1;
+        for (int i = 0; i < 4; i++) {
+          const int64_t from = from_s[i0 + i];
+          q[i] = from >= 0 ? *reinterpret_cast<const uint4*>(data + from * bytes + at) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (b0 + i0 + i < rows) *reinterpret_cast<uint4*>(p.data + (b0 + i0 + i) * bytes + at) = q[i];
       }
     }
-    for (int64_t at = lane * 16; at < bytes; at += 512) {
-      uint4 q[ROWS];
+    // rows past the last: the layout's padding, zero; with offsets not this call's
+    const int64_t limit = p.offsets != nullptr ? rows - b0 : 128;
+    for (int64_t c0 = warp * 4; c0 < chunks; c0 += 32) {
+      uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < ROWS; i++)
-        q[i] = from[i] >= 0 ? *reinterpret_cast<const uint4*>(data + from[i] * bytes + at) : make_uint4(0, 0, 0, 0);
+      for (int q = 0; q < 4; q++) {
+        const int64_t from = from_s[lane + 32 * q];
+        v[q] = from >= 0 ? *reinterpret_cast<const uint4*>(scale + from * pitch + c0 * 4) : make_uint4(0, 0, 0, 0);
+      }
+      const uint32_t w[4][4] = {{v[0].x, v[1].x, v[2].x, v[3].x}, {v[0].y, v[1].y, v[2].y, v[3].y},
+                                {v[0].z, v[1].z, v[2].z, v[3].z}, {v[0].w, v[1].w, v[2].w, v[3].w}};
 #pragma unroll
-      for (int i = 0; i < ROWS; i++)
-        if (r0 + i < rows) *reinterpret_cast<uint4*>(p.data + (r0 + i) * bytes + at) = q[i];
-    }
-    for (int64_t c = lane; c < chunks; c += 32) {
-      uint32_t w[ROWS];
+      for (int j = 0; j < 4; j++) {
+        if (c0 + j >= chunks) break;
+        uint32_t* const to = reinterpret_cast<uint32_t*>(p.scale + ((b0 >> 7) * chunks + c0 + j) * 512 + lane * 16);
+        if (limit >= 128) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+        } else {
 #pragma unroll
-      for (int i = 0; i < ROWS; i++)
-        w[i] = from[i] >= 0 ? *reinterpret_cast<const uint32_t*>(scale + (from[i] * chunks + c) * 4) : 0u;
-#pragma unroll
-      for (int i = 0; i < ROWS; i++)
-        if (r0 + i < rows) *reinterpret_cast<uint32_t*>(p.scale + row_place(r0 + i, chunks) + c * 512) = w[i];
-    }
-    if (lane < ROWS && r0 + lane < rows) {
-      const int64_t f = from[0] * (lane == 0) + from[1] * (lane == 1) + from[2] * (lane == 2) + from[3] * (lane == 3);
-      p.row_scale[r0 + lane] = f >= 0 ? *(row_scale + f) : __uint_as_float((uint32_t)(127 - 100) << 23);
+          for (int q = 0; q < 4; q++)
+            if (lane + 32 * q < limit) to[q] = w[j][q];
+        }
+      }
     }
   }
-  if ((p.R & 127) != 0 && p.offsets == nullptr) pad_scales(p, chunks);
 }
 
 // Where rows name tokens three times on average and there is enough to save for
 // the second launch, they are copied from the tokens' quantization (us, each row
-// quantized for itself in brackets): 8192 tokens of 2048 columns to 73700 rows 36
-// (68), to 32768 rows 23 (31), to 16384 rows 17.3 (17.5); 64 tokens to 512 rows 5.4
+// quantized for itself in brackets): 8192 tokens of 2048 columns to 73700 rows 28
+// (68), to 32768 rows 25 (31), to 16384 rows 17.3 (17.5); 64 tokens to 512 rows 5.4
 // (2.8).
 size_t nvfp4_workspace(int64_t T, int64_t K, int64_t R) {
   if (R < 3 * T || (R - T) * K < (1 << 24)) return 0;
-  return (size_t)round_up_i64(T * (K >> 1), 16) + (size_t)round_up_i64(T * ((K + 63) >> 6) * 4, 16) + (size_t)T * 4;
+  return (size_t)round_up_i64(T * (K >> 1), 16) + (size_t)(T * scale_pitch(K)) + (size_t)T * 4;
 }
 
 static cudaError_t launch_rows(const Nvfp4Params& p, int num_sms, cudaStream_t s) {
@@ -252,10 +274,10 @@ cudaError_t launch_nvfp4_quantize(const Nvfp4Params& p, void* workspace, int num
   t.linear = 1;
   t.data = static_cast<uint8_t*>(workspace);
   t.scale = t.data + round_up_i64(p.T * (p.K >> 1), 16);
-  t.row_scale = reinterpret_cast<float*>(t.scale + round_up_i64(p.T * ((p.K + 63) >> 6) * 4, 16));
+  t.row_scale = reinterpret_cast<float*>(t.scale + p.T * scale_pitch(p.K));
   const cudaError_t e = launch_rows(t, num_sms, s);
   if (e != cudaSuccess) return e;
-  const int64_t want = (p.R + 8 * ROWS - 1) / (8 * ROWS), cap = (int64_t)num_sms * 16;
+  const int64_t want = (p.R + 127) / 128, cap = (int64_t)num_sms * 4;
   return launch_pdl(nvfp4_gather_kernel, dim3((unsigned)(want < cap ? want : cap)), 256, 0, s, dim3(1), p, t.data, t.scale,
                     t.row_scale);
 }

@@ -76,6 +76,24 @@ def test_forward(cuda_lib, R, D, dtype):
     _check_fwd(t, cuda_lib.mx_layernorm_fwd(t["x"], t["w"], rms=True, eps=1e-6), 1e-6, True, t["w"], None)
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [1280, 1288, 2560, 3584, 4088, 4104, 5112, 6136, 6144, 6152, 8184, 8208, 10240, 12288, 16376])
+def test_row_lengths(cuda_lib, D, dtype):
+    """Every number of warps and pieces a row takes, with and without lanes past its
+    end, and the sizes where shared memory passes what a launch has unasked."""
+    for R, res in ((2, True), (161, False)):
+        t = _inputs(R, D, dtype, seed=7, res=res)
+        s = cuda_lib.mx_layernorm_fwd(t["x"], t["w"], t["b"], residual=t["res"])
+        _check_fwd(t, s, 1e-5, False, t["w"], t["b"])
+        got = cuda_lib.mx_layernorm_bwd(t["dy"], t["x"], s[1], s[2], t["w"], dres=t["res"])
+        if not res:
+            _check_bwd(t, got, s[1], s[2], False, t["w"], dtype)
+        else:  # the forward's sum is what the backward pass takes
+            u = dict(t, x=s[3])
+            _check_bwd(u, cuda_lib.mx_layernorm_bwd(t["dy"], s[3], s[1], s[2], t["w"], dres=t["res"]), s[1], s[2], False,
+                       t["w"], dtype)
+
+
 @pytest.mark.parametrize("wtype", [BF, F], ids=["bf16", "f32"])
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf16", "f32"])
 @pytest.mark.parametrize("R,D", [(3, 64), (5, 1000), (131, 2048), (2, 8200), (2, 16384)])

@@ -148,6 +148,38 @@ def test_quantize_gathered_rows(cuda_lib):
     assert (t.data[2] == 0).all() and cuda_lib.mx_get_device_status() == "MX_OK"
 
 
+@pytest.mark.parametrize("ends", [None, [200, 700], [0, 900]], ids=["all", "whole", "part"])
+@pytest.mark.parametrize("T,K,R", [(70, 32768, 1030), (64, 16416, 1152), (1000, 2080, 9100), (3000, 1024, 20000)])
+def test_quantize_copied_rows(cuda_lib, T, K, R, ends):
+    """Rows that name tokens many times, copied from the tokens' quantization: the
+    bytes of each row quantized for itself."""
+    import ctypes
+    gen = torch.Generator().manual_seed(T)
+    x = _rand((T, K), T).cuda()
+    x[T // 2, 5] = float("nan")
+    src = torch.randint(-1, T, (R,), generator=gen, dtype=torch.int32).cuda()
+    need = cuda_lib.mx_nvfp4_quantize_workspace_bytes(T, K, R)
+    assert need > 0
+    offsets = None if ends is None else torch.tensor([ends[0], ends[1] * R // 1000], dtype=torch.int32, device="cuda")
+
+    def fresh():
+        t = cuda_lib.NVFP4(R, K)
+        t.data.fill_(0x55), t.scale.fill_(0x2A), t.row_scale.fill_(7)
+        return t
+
+    copied, itself = fresh(), fresh()
+    cuda_lib.mx_nvfp4_quantize(x, src=src, offsets=offsets, out=copied)
+    L = cuda_lib.load()
+    assert L.mx_nvfp4_quantize(x.data_ptr(), T, K, K, src.data_ptr(), None if offsets is None else offsets.data_ptr(),
+                               0 if offsets is None else 2, ctypes.byref(itself.struct()), None, 0, None) == 0
+    assert torch.equal(copied.data, itself.data) and torch.equal(copied.scale, itself.scale)
+    assert torch.equal(copied.row_scale.nan_to_num(-1.0), itself.row_scale.nan_to_num(-1.0))
+    src[0] = T
+    again = cuda_lib.mx_nvfp4_quantize(x, src=src, offsets=offsets)
+    assert cuda_lib.mx_get_device_status() == "MX_ERR_INVALID_ARG" and (again.data[0] == 0).all()
+    assert cuda_lib.mx_get_device_status() == "MX_OK"
+
+
 def test_quantize_a_row_does_not_depend_on_the_others(cuda_lib):
     x = _rand((50, 512), 4).cuda()
     t, one = cuda_lib.mx_nvfp4_quantize(x), cuda_lib.mx_nvfp4_quantize(x[33:34])
