@@ -311,7 +311,7 @@ struct RouteParams {
   const float* dsum;         // [G] or null
   void* dlogits;
   int64_t ld_d;
-  int per_lane, wide;        // set by the launch
+  int per_lane, wide, by_lanes;  // set by the launch
 };
 int64_t route_blocks(int64_t T);
 cudaError_t launch_route_fwd(RouteParams p, cudaStream_t s);

@@ -232,6 +232,7 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F* c
     }
   }
   F value = p.group_top == 2 ? a + b : a;
+  const F most = value > minus_inf<F>() ? (a < 0 ? -a : a) + (p.group_top < 2 ? (F)0 : b < 0 ? -b : b) : (F)0;
   typename KeyOf<F>::type key = nan ? ~(typename KeyOf<F>::type)0 : order_key(value);
   int rank = 0;
   for (int g = 0; g < p.groups; g++) {
@@ -244,8 +245,10 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F* c
   const uint32_t next = __ballot_sync(0xFFFFFFFFu, in && rank == p.topk_groups);
   *close = false;
   if (next != 0) {
-    const F u = __shfl_sync(0xFFFFFFFFu, value, __ffs(last) - 1), v = __shfl_sync(0xFFFFFFFFu, value, __ffs(next) - 1);
-    *close = u - v <= tol + (F)5e-7 * (u < 0 ? -u : u);  // false for two closed groups: -Inf - -Inf is a NaN
+    const int i = __ffs(last) - 1, j = __ffs(next) - 1;
+    const F u = __shfl_sync(0xFFFFFFFFu, value, i), v = __shfl_sync(0xFFFFFFFFu, value, j);
+    const F m = __shfl_sync(0xFFFFFFFFu, most, i), n = __shfl_sync(0xFFFFFFFFu, most, j);
+    *close = u - v <= tol + (F)5e-7 * (m > n ? m : n);  // false for two closed groups: -Inf - -Inf is a NaN
   }
   return kept;
 }
@@ -381,10 +384,220 @@ __device__ __forceinline__ int choose_plain(const RouteParams& p, const float (&
   return (int)(MASK - (mine & MASK));
 }
 
+// sigmoid(x) where fp32's last bits do not matter: off by s (1 - s) (2 |x| + 4) +
+// 2 s roundings of 2^-24.
+__device__ __forceinline__ float sigmoid_near(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_near(-x)));
+  return r;
+}
+
+// The softmax in FP64 of a row with the largest logit `top`.  Rows that need it are few, so
+// the loop is not unrolled: instructions that are fetched for one row cost more
+// than they compute.
+__device__ __forceinline__ Softmax<double> softmax_exact(const RouteParams& p, int64_t t, float top, int lane) {
+  Softmax<double> s;
+  s.top = (double)top;
+  double sum = 0.;
+#pragma unroll 1
+  for (int e = lane; e < p.G; e += 32) sum += exp_of((double)load_logit(p, t, e) - s.top);
+  sum = warp_sum_of(sum);
+  s.inv = sum == 0. ? 0. : 1. / sum;
+  return s;
+}
+
+// The place of the lane's group (of `lanes` lanes) by exact values; `bad`: it has a NaN.
+template <bool SIG>
+__device__ __forceinline__ int group_rank_exact(const RouteParams& p, int64_t t, float top, int lane, int lanes, bool bad) {
+  const double closed = minus_inf<double>();
+  double first = closed, second = closed;
+  Softmax<double> s{};
+  if constexpr (!SIG) s = softmax_exact(p, t, top, lane);
+#pragma unroll 1
+  for (int i = 0; i < p.per_lane; i++) {
+    const int e = lane * p.per_lane + i;
+    const float x = load_logit(p, t, e);
+    const double c = x == minus_inf<float>() ? closed : score_of<double, SIG>(x, s) + (p.bias != nullptr ? (double)*(p.bias + e) : 0.);
+    second = c > first ? first : (c > second ? c : second);
+    first = c > first ? c : first;
+  }
+#pragma unroll 1
+  for (int o = 1; o < lanes; o <<= 1) {
+    const double a = __shfl_xor_sync(0xFFFFFFFFu, first, o), b = __shfl_xor_sync(0xFFFFFFFFu, second, o);
+    const double low = a < first ? a : first;
+    second = low > second ? low : second;
+    second = b > second ? b : second;
+    first = a > first ? a : first;
+  }
+  const uint64_t order = bad ? ~0ull : order_key(p.group_top == 2 ? first + second : first);
+  int rank = 0;
+#pragma unroll 1
+  for (int l = 0; l < 32; l += lanes) {
+    const uint64_t other = __shfl_sync(0xFFFFFFFFu, order, l);
+    rank += other > order || (other == order && l + lanes <= lane) ? 1 : 0;
+  }
+  return rank;
+}
+
+// The choice by scores, biases and groups in fp32 with the hardware's functions, for
+// groups that are whole lanes (`by_lanes`).  A key's last bits hold the slot.  Where
+// choices or groups are nearer than their errors, or keys equal but for the slot, exact
+// values order them; *open is set where that does not settle it, and the caller
+// takes choose().
+// s: the softmax's top and 1 / sum, own[]: exp(x - top), bias: the lane's.
+template <int V, bool SIG>
+__device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, const float (&x)[V], const float (&own)[V],
+                                             const Softmax<float>& s, const float (&bias)[V], bool scored, int lane,
+                                             bool* open) {
+  constexpr uint32_t MASK = V - 1;
+  const float closed = minus_inf<float>();
+  const int e0 = lane * p.per_lane;
+  uint32_t key[V];
+  float first = closed, second = closed;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    const bool there = i < p.per_lane && e0 + i < p.G;
+    float c = x[i];
+    if (scored && x[i] != closed) c = (SIG ? sigmoid_near(x[i]) : own[i] * s.inv) + bias[i];
+    key[i] = there ? (order_key(p.bias == nullptr ? x[i] : c) & ~MASK) | (MASK - (uint32_t)i) : 0u;
+    if (there) {
+      nan |= c != c;
+      second = c > first ? first : (c > second ? c : second);
+      first = c > first ? c : first;
+    }
+  }
+  if (p.groups > 1) {
+    const int lanes = 32 / p.groups, mine = lane / lanes;
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float a = __shfl_xor_sync(0xFFFFFFFFu, first, o), b = __shfl_xor_sync(0xFFFFFFFFu, second, o);
+      const float low = a < first ? a : first;
+      second = low > second ? low : second;
+      second = b > second ? b : second;
+      first = a > first ? a : first;
+    }
+    const float value = p.group_top == 2 ? first + second : first;
+    const float size = fabsf(value) <= 3e38f ? fabsf(first) + (p.group_top == 2 ? fabsf(second) : 0.f) : 0.f;
+    const uint32_t bad = __ballot_sync(0xFFFFFFFFu, nan) >> (mine * lanes) & (lanes == 32 ? ~0u : (1u << lanes) - 1u);
+    const uint32_t order = bad ? 0xFFFFFFFFu : order_key(value);
+    int rank = 0;
+    for (int g = 0; g < p.groups; g++) {
+      const uint32_t other = __shfl_sync(0xFFFFFFFFu, order, g * lanes);
+      rank += other > order || (other == order && g < mine) ? 1 : 0;
+    }
+    const uint32_t last = __ballot_sync(0xFFFFFFFFu, rank == p.topk_groups - 1);
+    const uint32_t next = __ballot_sync(0xFFFFFFFFu, rank == p.topk_groups);
+    if (scored && next != 0) {
+      const int a = __ffs(last) - 1, b = __ffs(next) - 1;
+      const float u = __shfl_sync(0xFFFFFFFFu, value, a), v = __shfl_sync(0xFFFFFFFFu, value, b);
+      const float most = fmaxf(__shfl_sync(0xFFFFFFFFu, size, a), __shfl_sync(0xFFFFFFFFu, size, b));
+      // units of 2^-24: sigmoids are off by at most 5 each, the softmax's scores, which
+      // sum to 1, by 70 together; sums and values add 2 of their size each.  False
+      // for two closed groups.
+      if (u - v <= (SIG ? 2e-6f : 1.2e-5f) + 5e-7f * most) rank = group_rank_exact<SIG>(p, t, s.top, lane, lanes, bad != 0);
+    }
+    if (rank >= p.topk_groups) {
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (key[i] != 0) key[i] = (order_key(closed) & ~MASK) | (MASK - (uint32_t)i);
+    }
+  }
+  constexpr bool SORTED = V <= 8;
+  if constexpr (SORTED) sort_down<V>(key);
+  uint32_t mine = 0;
+  int id = 0;
+  const auto take = [&](int from, int to) {  // lane j: the j-th largest key and its index, of equal keys the lowest
+    for (int j = from; j < to; j++) {
+      uint32_t m = key[0];
+      if constexpr (!SORTED) {
+#pragma unroll
+        for (int i = 1; i < V; i++) m = key[i] > m ? key[i] : m;
+      }
+      const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, m & ~MASK);
+      const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, (m & ~MASK) == w)) - 1;
+      const int taken = owner * p.per_lane + (int)(MASK - (__shfl_sync(0xFFFFFFFFu, m, owner) & MASK));
+      if (lane == owner) {
+        if constexpr (SORTED) {
+#pragma unroll
+          for (int i = 0; i + 1 < V; i++) key[i] = key[i + 1];
+          key[V - 1] = 0;
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; i++) key[i] = key[i] == m ? 0u : key[i];
+        }
+      }
+      mine = lane == j ? w : mine;
+      id = lane == j ? taken : id;
+    }
+  };
+  // The choices in `lanes` and the one that lane `from` (not above its own) has:
+  // may exact values order them otherwise?  Below the last key taken nothing is
+  // larger by more than the bits that hold the slot.
+  const uint32_t last_key = order_key(closed) & ~MASK;  // closed ones go by index
+  float xi = 0.f, bi = 0.f;
+  const auto close_to = [&](int from, bool asked) {
+    const uint32_t up = __shfl_sync(0xFFFFFFFFu, mine, from);
+    bool near;
+    if (p.bias == nullptr) {  // BF16 logits fit whole
+      near = p.x_f32 && mine == up;
+    } else {
+      const float si = SIG ? sigmoid_near(xi) : exp_near(xi - s.top) * s.inv, ci = si + bi;
+      const float ux = __shfl_sync(0xFFFFFFFFu, xi, from), us = __shfl_sync(0xFFFFFFFFu, si, from);
+      const float uc = __shfl_sync(0xFFFFFFFFu, ci, from);
+      // units of 2^-24 of a score: 7 + 2.5 |x| (softmax: from the top), two of them; a
+      // sum with a bias 1; the slot's bits 2 V of the value; the softmax's sum 60,
+      // the same part of both scores
+      const float far = SIG ? fmaxf(fabsf(xi), fabsf(ux)) : fmaxf(fabsf(xi - s.top), fabsf(ux - s.top));
+      const float tol = (1.2e-6f + 3.2e-7f * far) * fmaxf(si, us) + (SIG ? 0.f : 4e-6f * fabsf(us - si));
+      near = uc - ci <= tol + (2.5e-7f + V * 1.2e-7f) * (fabsf(uc) + fabsf(ci)) + 1e-36f;
+    }
+    return __any_sync(0xFFFFFFFFu, asked && near && mine != last_key) != 0;
+  };
+  const auto reload = [&](int from, int to) {
+    if (lane >= from && lane < to) {
+      xi = load_logit(p, t, id);
+      if (p.bias != nullptr) bi = *(p.bias + id);
+    }
+  };
+  const int count = p.k < 32 && p.k < p.G ? p.k + 1 : p.k;  // with the first that is left out
+  take(0, count);
+  if (p.bias != nullptr) reload(0, count);
+  *open = p.k == 32 && p.G > 32;
+  if (*open || !close_to(lane > 0 ? lane - 1 : 0, lane > 0 && lane < count)) return id;
+  // Eight more, and the order of these by exact values, a lane each: an eighth of the
+  // FP64 instructions of all experts' (at 8 a lane), of which an SM does two a clock.
+  const int n = min(count + 8, min(p.G, 32));
+  take(count, n);
+  reload(p.bias != nullptr ? count : 0, n);
+  *open = n < p.G && close_to(p.k - 1, lane == n - 1);
+  if (*open) return id;
+  double value = (double)xi;
+  if (p.bias != nullptr) {
+    Softmax<double> exact{};
+    if constexpr (!SIG) exact = softmax_exact(p, t, s.top, lane);
+    value = score_of<double, SIG>(xi, exact) + (double)bi;
+  }
+  const uint64_t order = lane >= n ? 0 : mine == last_key ? order_key((double)closed) : order_key(value);
+  int rank = 0;
+  for (int j = 0; j < n; j++) {
+    const uint64_t other = __shfl_sync(0xFFFFFFFFu, order, j);
+    const int other_id = __shfl_sync(0xFFFFFFFFu, id, j);
+    rank += other > order || (other == order && other_id < id) ? 1 : 0;
+  }
+  int chosen = 0;
+  for (int j = 0; j < n; j++) {
+    const int to = __shfl_sync(0xFFFFFFFFu, rank, j), what = __shfl_sync(0xFFFFFFFFu, id, j);
+    chosen = lane == to ? what : chosen;
+  }
+  return chosen;
+}
+
 // Forward.  The order is that of the exact values: by the logits themselves
 // where there is no bias (both scores grow with them), else by score + bias in
 // fp32 and, for the few tokens where two of them are nearer than their error,
-// again in fp64.
+// in fp64: with all values of such a token again in fp64, 16384 x 256 sigmoids with
+// bias and groups took 57 us, a token alone 20 of them; with the candidates' and the
+// groups' alone 31.  32768 x 128 with a bias: 24 us, without 15.
 // PLAIN: neither bias nor groups.
 template <int V, bool SIG, bool PLAIN>
 __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
@@ -403,6 +616,11 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
   __syncthreads();
   pdl_trigger();
   pdl_wait();
+  const bool scored = p.bias != nullptr || (p.groups > 1 && p.group_top == 2);  // else the logits order everything
+  float bias[PLAIN ? 1 : V];
+#pragma unroll
+  for (int i = 0; i < (PLAIN ? 1 : V); i++)
+    bias[i] = !PLAIN && p.bias != nullptr && i < p.per_lane && e0 + i < p.G ? *(p.bias + e0 + i) : 0.f;
   for (int64_t t = (int64_t)blockIdx.x * 8 + warp; t < p.T; t += (int64_t)gridDim.x * 8) {
     float x[V];
     load_logits<V>(p, t, lane, x);
@@ -419,9 +637,17 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
       if (open) id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
       if (p.x_f32 && mine) xj = load_logit(p, t, id);
     } else {
-      id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
+      if constexpr (!SIG) {
+        s.top = top_of<V>(x);
+        if (scored) s.inv = exps_of<V>(x, s.top, own);
+      }
+      if (p.by_lanes) {
+        id = choose_scored<V, SIG>(p, t, x, own, s, bias, scored, lane, &open);
+      } else {
+        open = true;
+      }
+      if (open) id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
       if (open) id = choose<V, SIG, double>(p, t, x, values, lane, &open);
-      if constexpr (!SIG) s.top = top_of<V>(x);
       xj = mine ? load_logit(p, t, id) : 0.f;
       if constexpr (!SIG) {  // a NaN or +Inf anywhere in the row is one in all of its scores
         bool bad = false;
@@ -431,7 +657,7 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
       }
     }
     if (!mine) xj = minus_inf<float>();
-    if (!SIG && (stats || !p.renorm)) s.inv = exps_of<V>(x, s.top, own);
+    if (!SIG && (stats || !p.renorm) && (PLAIN || !scored)) s.inv = exps_of<V>(x, s.top, own);
     float w;
     if constexpr (SIG) {
       w = mine ? sigmoid_of(xj) : 0.f;
@@ -646,6 +872,8 @@ static void set_layout(RouteParams& p) {
   if (p.G % v == 0) p.per_lane = v;  // whole pieces for fewer lanes
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | (uintptr_t)(p.ld * (p.x_f32 ? 4 : 2)) |
                        reinterpret_cast<uintptr_t>(p.dlogits) | (uintptr_t)(p.ld_d * (p.x_f32 ? 4 : 2));
+  // groups of whole lanes, 32 lanes in all
+  p.by_lanes = p.groups <= 1 || (p.G == 32 * p.per_lane && 32 % p.groups == 0);
   p.wide = p.G % v == 0 && (at & (uintptr_t)(bytes - 1)) == 0;
 }
 

@@ -158,6 +158,34 @@ def test_values_nearer_than_fp32(cuda_lib, sigmoid, groups):
     _check(cuda_lib, x, k, sigmoid, bias, groups, max(1, groups // 2), 1 if groups == 1 else 2)
 
 
+@pytest.mark.parametrize("G,groups", [(64, 1), (256, 1), (256, 8), (512, 4), (60, 1), (60, 5)])
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+def test_few_values_nearer_than_fp32(cuda_lib, sigmoid, G, groups):
+    """Each expert of the first half has one in the second whose sum with its bias is
+    equal up to a few 2^-27, the second's logit a little larger: pairs, and with
+    groups the groups of a pair, are as near, all others far apart."""
+    T, k = 64, 6
+    half = G // 2 - (G // 2) % (G // groups) if groups > 1 else G // 2
+    x = _logits(1, G, F, 9, std=1.0)
+    x[:, half:2 * half] = x[:, :half] + 0.125
+    s = _scores(x.to(D), sigmoid)[0]
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    bias = 0.2 * torch.rand(G, device="cuda", generator=gen)
+    bias[half:2 * half] = (bias[:half].to(D) + s[:half] - s[half:2 * half]).to(F)
+    step = torch.randint(-3, 4, (T, G), device="cuda", generator=gen) * 2.0 ** -24
+    for row in range(0, T, 16):
+        b = (bias + step[row] * 0.25).to(F)
+        _check(cuda_lib, x.expand(T, G).contiguous() + step, k, sigmoid, b, groups, (groups + 1) // 2, 1 if groups == 1 else 2)
+
+
+@pytest.mark.parametrize("G", [64, 60])
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+def test_biases_that_cancel_in_a_group(cuda_lib, sigmoid, G):
+    """Groups of two with biases of 100 and -100: their values are what is left of it."""
+    bias = 100.0 - 200.0 * (torch.arange(G, device="cuda") % 2)
+    _check(cuda_lib, _logits(2000, G, F, 4, std=0.3), 6, sigmoid, bias, G // 2, 5, 2)
+
+
 def test_equal_logits_go_by_index(cuda_lib):
     x = torch.zeros((3, 96), dtype=BF, device="cuda")
     x[1, 40:50] = 2.0
