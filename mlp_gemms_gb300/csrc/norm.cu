@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(NormParams p, int W) {
 #pragma unroll
   for (int i = 0; i < S - 1; i++) load_row(r + i * stride, i, &means[i], &rstds[i]);
   keep_vector(p.weight, p.w_f32, n8, vectors);
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // the other block runs: its memory may be stored to
+  else __syncthreads();
   for (; r < p.R; r += stride) {
     uint64_t xh[C][4], g[C][4], t1[4] = {}, t2[4] = {};
     const float mean = means[0], rstd = rstds[0];
