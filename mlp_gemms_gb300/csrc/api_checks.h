@@ -34,13 +34,16 @@ inline mx_status_t check_ptr(const void* p, const char* name) {
   return MX_OK;
 }
 
+// rows * ld below 2^46 elements, without a product that may wrap.
+inline bool fits(int64_t rows, int64_t ld) { return rows <= 0 || ld <= ((1ll << 46) - 1) / rows; }
+
 // A row-major matrix of `rows` rows of `cols` elements, row stride ld, every
 // row 16-byte aligned for elements of two bytes or more.
 inline mx_status_t check_matrix(const void* p, const char* name, int64_t rows, int64_t cols, int64_t ld) {
   MX_CHECK(ld >= cols && ld % 8 == 0, MX_ERR_ALIGNMENT, "ld of %s = %lld must be >= %lld and a multiple of 8", name,
            (long long)ld, (long long)cols);
   MX_CHECK(ld < (1ll << 38), MX_ERR_SHAPE, "ld of %s = %lld is too large", name, (long long)ld);
-  MX_CHECK(rows < (1ll << 31) && rows * ld < (1ll << 46), MX_ERR_SHAPE, "%s is too large (%lld rows of %lld)", name,
+  MX_CHECK(rows < (1ll << 31) && fits(rows, ld), MX_ERR_SHAPE, "%s is too large (%lld rows of %lld)", name,
            (long long)rows, (long long)ld);
   return rows == 0 ? MX_OK : check_ptr(p, name);
 }

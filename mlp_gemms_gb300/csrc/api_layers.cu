@@ -140,8 +140,8 @@ mx_status_t check_route(const void* logits, int32_t x_type, int64_t T, int32_t G
   MX_CHECK(G <= 1024, MX_ERR_NOT_SUPPORTED, "G = %d; at most 1024 experts", G);
   MX_CHECK(k >= 1 && k <= G, MX_ERR_INVALID_ARG, "k = %d of %d experts", k, G);
   MX_CHECK(k <= 32, MX_ERR_NOT_SUPPORTED, "k = %d; at most 32 choices", k);
-  MX_CHECK(T >= 0 && T * k < (1ll << 31), MX_ERR_SHAPE, "T = %lld is out of range", (long long)T);
-  MX_CHECK(ld >= G && ld < (1ll << 38) && T * ld < (1ll << 46), MX_ERR_SHAPE, "ld = %lld of logits with %d experts",
+  MX_CHECK(T >= 0 && T < (1ll << 31) && T * k < (1ll << 31), MX_ERR_SHAPE, "T = %lld is out of range", (long long)T);
+  MX_CHECK(ld >= G && ld < (1ll << 38) && mx::fits(T, ld), MX_ERR_SHAPE, "ld = %lld of logits with %d experts",
            (long long)ld, G);
   return T == 0 ? MX_OK : check_ptr(logits, "logits");
 }
@@ -203,7 +203,7 @@ mx_status_t mx_moe_topk_bwd(const void* logits, int32_t x_type, int64_t T, int32
                             const float* dscore_sum, void* dlogits, int64_t ld_d, mx_stream_t stream) {
   mx_status_t st;
   if ((st = check_route(logits, x_type, T, G, ld, k, score, renorm, scale)) != MX_OK) return st;
-  MX_CHECK(ld_d >= G && ld_d < (1ll << 38) && T * ld_d < (1ll << 46), MX_ERR_SHAPE, "ld of dlogits = %lld",
+  MX_CHECK(ld_d >= G && ld_d < (1ll << 38) && mx::fits(T, ld_d), MX_ERR_SHAPE, "ld of dlogits = %lld",
            (long long)ld_d);
   MX_CHECK(dlogits != logits || ld_d == ld || T == 0, MX_ERR_ALIGNMENT, "dlogits is logits with another row stride");
   if ((st = check_floats(dscore_sum, "dscore_sum")) != MX_OK) return st;
