@@ -146,8 +146,7 @@ __device__ __forceinline__ float exp_near(float d) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * LOG2E));
   return r;
 }
-// The exponentials of a row above `top` (any value near the largest logit) and 1 /
-// their sum.
+// The exponentials of a row above `top`, its largest logit, and 1 / their sum.
 template <int V>
 __device__ __forceinline__ float exps_of(const float (&x)[V], float top, float (&e)[V]) {
   float sum = 0.f;
@@ -161,7 +160,7 @@ __device__ __forceinline__ float exps_of(const float (&x)[V], float top, float (
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sum));
   return sum == 0.f ? 0.f : inv;
 }
-// A value near the largest logit for exps_of; 0 where none is open.
+// The largest logit for exps_of; 0 where none is open.
 template <int V>
 __device__ __forceinline__ float top_of(const float (&x)[V]) {
   float m = x[0];
@@ -178,7 +177,7 @@ __device__ __forceinline__ F score_of(float x, const Softmax<F>& s) {
 
 // Each lane's share of the softmax over the lanes' own values (-Inf: none): the
 // chosen scores over their sum, without the row's sum and without its underflow.
-__device__ __forceinline__ float share_above(float xj, float top) {  // top: near the largest
+__device__ __forceinline__ float share_above(float xj, float top) {  // top: the largest
   const float e = exp_near(xj - top), total = warp_sum(e);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(total));
@@ -341,11 +340,9 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
 // one warp maximum gives a choice with its index and equal logits go by index.
 // BF16 logits fit whole.  Of fp32 ones the last bits make room: where two of the
 // k + 1 first keys differ in the index alone, *open is set, and the caller
-// chooses by the whole logits.  *first: a value near the largest logit (truncated);
-// *own: lane j's key.
+// chooses by the whole logits.  *own: lane j's key.
 template <int V>
-__device__ __forceinline__ int choose_plain(const RouteParams& p, const float (&x)[V], int lane, bool* open, float* first,
-                                            uint32_t* own) {
+__device__ __forceinline__ int choose_plain(const RouteParams& p, const float (&x)[V], int lane, bool* open, uint32_t* own) {
   constexpr uint32_t MASK = 32 * V - 1;
   const int e0 = lane * p.per_lane;
   uint32_t key[V], mine = 0;
@@ -374,12 +371,9 @@ __device__ __forceinline__ int choose_plain(const RouteParams& p, const float (&
     }
     mine = lane == j ? w : mine;
   }
-  const uint32_t top = __shfl_sync(0xFFFFFFFFu, mine, 0);
   const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, mine, 1);
   *open = p.x_f32 && (__any_sync(0xFFFFFFFFu, lane > 0 && lane < count && ((mine ^ up) & ~MASK) == 0u) ||
                       (p.k == 32 && p.G > 32));
-  // nothing open: 0 instead of -Inf
-  *first = (top & ~MASK) == (order_key(minus_inf<float>()) & ~MASK) ? 0.f : key_value(top & ~MASK);
   *own = mine;
   return (int)(MASK - (mine & MASK));
 }
@@ -631,11 +625,17 @@ __global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
     Softmax<float> s{};
     if constexpr (PLAIN) {
       uint32_t key;
-      id = choose_plain<V>(p, x, lane, &open, &s.top, &key);
+      id = choose_plain<V>(p, x, lane, &open, &key);
       // a BF16 logit is its key's upper half
       xj = p.x_f32 ? 0.f : key_value((key & 0x80000000u) ? key & 0xFFFF0000u : key | 0xFFFFu);
       if (open) id = choose<V, SIG, float>(p, t, x, reinterpret_cast<float*>(values), lane, &open);
       if (p.x_f32 && mine) xj = load_logit(p, t, id);
+      if constexpr (!SIG) {
+        // The first choice's logit, whole: the cut bits of a key are worth hundreds where
+        // the logits are 1e9 (a finite mask).  Nothing open: 0 instead of -Inf.
+        const float top = __shfl_sync(0xFFFFFFFFu, xj, 0);
+        s.top = top == minus_inf<float>() ? 0.f : top;
+      }
     } else {
       if constexpr (!SIG) {
         s.top = top_of<V>(x);
