@@ -592,9 +592,10 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
 // in fp64: with all values of such a token again in fp64, 16384 x 256 sigmoids with
 // bias and groups took 57 us, a token alone 20 of them; with the candidates' and the
 // groups' alone 31.  32768 x 128 with a bias: 24 us, without 15.
-// PLAIN: neither bias nor groups.
+// PLAIN: neither bias nor groups; of 257 to 512 experts held to the registers of two
+// blocks an SM (138 of its own accord, one block: 8192 x 512 17.8 us, 12.5 this way).
 template <int V, bool SIG, bool PLAIN>
-__global__ void __launch_bounds__(256) route_fwd_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(256, V == 16 && PLAIN ? 2 : 0) route_fwd_kernel(const RouteParams p) {
   extern __shared__ char route_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * p.per_lane;
   double* const values = reinterpret_cast<double*>(route_smem) + (p.groups > 1 ? warp * p.G : 0);  // groups: G per warp
