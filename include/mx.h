@@ -850,7 +850,7 @@ MX_API mx_status_t mx_layernorm_bwd(const void *dy_bf16, int64_t ld_dy, const vo
  *   and the experts of the others count as closed.  The k first experts are
  *   chosen; the weight of choice j is
  *     scale * s_j (renorm = 0), or scale * s_j / sum of the chosen s (renorm = 1;
- *     0 where that sum is 0): the bias orders, it does not weigh.
+ *     0 where all of them are closed): the bias orders, it does not weigh.
  *   A logit of -Inf closes its expert for that token: score 0, chosen (by index,
  *   with weight 0) only when fewer than k open ones are left.  A NaN or +Inf makes
  *   the row's weights NaN (sigmoid: its expert's); the ids stay distinct and valid.

@@ -188,6 +188,35 @@ __device__ __forceinline__ float chosen_share(float xj) {
   return share_above(xj, m == minus_inf<float>() ? 0.f : m);
 }
 
+// Below this sum of sigmoids each of them is below 2^-26, and exp(x) to 2^-26 of
+// itself: their shares are a softmax's, where sigmoids leave fp32's range (below -87)
+// included.
+// (A vote, so that the branch is known to be the warp's: 16384 x 256 sigmoids with bias
+// and groups 28.9 us, 29.4 without it.)
+constexpr float LOW_SIGMOIDS = 1.f / (1 << 26);
+
+// Each lane's sigmoid over the sum of the lanes' (not `there`: none, xj -Inf; 1 / Inf is
+// the division's long way).
+__device__ __forceinline__ float sigmoid_share(float xj, bool there) {
+  const float w = there ? sigmoid_of(xj) : 0.f, total = warp_sum(w);
+  if (__any_sync(0xFFFFFFFFu, total < LOW_SIGMOIDS)) return chosen_share(xj);
+  return w / total;
+}
+// The sigmoids of a row, 0 past its last expert, and 1 / their sum; a low row's in units
+// of its largest.
+template <int V>
+__device__ __forceinline__ float sigmoids_of(const RouteParams& p, const float (&x)[V], int e0, float (&s)[V]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    s[i] = i < p.per_lane && e0 + i < p.G ? sigmoid_of(x[i]) : 0.f;
+    sum += s[i];
+  }
+  sum = warp_sum(sum);
+  if (__any_sync(0xFFFFFFFFu, sum < LOW_SIGMOIDS)) return exps_of<V>(x, top_of<V>(x), s);
+  return 1.f / sum;
+}
+
 // The largest keys one after the other, the lowest index of equal ones: lane j
 // gets the j-th index.  Taken keys become 0.
 template <int V, typename K>
@@ -661,11 +690,7 @@ __global__ void __launch_bounds__(256, V == 16 && PLAIN ? 2 : 0) route_fwd_kerne
     if (!SIG && (stats || !p.renorm) && (PLAIN || !scored)) s.inv = exps_of<V>(x, s.top, own);
     float w;
     if constexpr (SIG) {
-      w = mine ? sigmoid_of(xj) : 0.f;
-      if (p.renorm) {
-        const float total = warp_sum_of(w);
-        w = total == 0.f ? 0.f : w / total;
-      }
+      w = p.renorm ? sigmoid_share(xj, mine) : mine ? sigmoid_of(xj) : 0.f;
     } else if (p.renorm) {
       w = PLAIN ? share_above(xj, s.top) : chosen_share(xj);
     } else {
@@ -677,14 +702,7 @@ __global__ void __launch_bounds__(256, V == 16 && PLAIN ? 2 : 0) route_fwd_kerne
     }
     if (stats) {
       if constexpr (SIG) {
-        norm = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-          own[i] = i < p.per_lane && e0 + i < p.G ? sigmoid_of(x[i]) : 0.f;
-          norm += own[i];
-        }
-        norm = warp_sum_of(norm);
-        norm = norm == 0.f ? 0.f : 1.f / norm;
+        norm = sigmoids_of<V>(p, x, e0, own);
       } else {
         norm = s.inv;
       }
@@ -779,11 +797,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
     }
     float r, all = 0.f;
     if constexpr (SIG) {
-      r = id >= 0 ? sigmoid_of(xj) : 0.f;
-      if (p.renorm) {
-        const float total = warp_sum_of(r);
-        r = total == 0.f ? 0.f : r / total;
-      }
+      r = p.renorm ? sigmoid_share(xj, id >= 0) : id >= 0 ? sigmoid_of(xj) : 0.f;
     } else {
       r = p.renorm ? chosen_share(xj) : exp_near(xj - top) * inv;
     }
@@ -794,19 +808,13 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
 #pragma unroll
     for (int i = 0; i < V; i++) d[i] = 0.f;
     if (dense) {
+      if constexpr (SIG) {
+        norm = sigmoids_of<V>(p, x, e0, own);
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; i++) {
-        if constexpr (SIG) own[i] = i < p.per_lane && e0 + i < p.G ? sigmoid_of(x[i]) : 0.f;
-        else own[i] *= inv;
+        for (int i = 0; i < V; i++) own[i] *= inv;
       }
       if (p.dsum != nullptr) {
-        if constexpr (SIG) {
-          norm = 0.f;
-#pragma unroll
-          for (int i = 0; i < V; i++) norm += own[i];
-          norm = warp_sum_of(norm);
-          norm = norm == 0.f ? 0.f : 1.f / norm;
-        }
 #pragma unroll
         for (int i = 0; i < V; i++) {
           d[i] = i < p.per_lane && e0 + i < p.G ? *(p.dsum + e0 + i) : 0.f;
