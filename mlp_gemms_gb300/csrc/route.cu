@@ -42,7 +42,12 @@ template <> struct KeyOf<double> { typedef uint64_t type; };
 
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
-template <typename F> __device__ __forceinline__ F sigmoid_of(F v) { return (F)1 / ((F)1 + exp_of(-v)); }
+// A sum that is never joined with the product before it: a score and its sum with a bias
+// are the same bits in every slot of a lane, so that equal ones tie (joined in some slots
+// of the unrolled loops and not in others, they did not).
+__device__ __forceinline__ float add_alone(float a, float b) { return __fadd_rn(a, b); }
+__device__ __forceinline__ double add_alone(double a, double b) { return __dadd_rn(a, b); }
+template <typename F> __device__ __forceinline__ F sigmoid_of(F v) { return (F)1 / add_alone((F)1, exp_of(-v)); }
 
 template <typename F>
 __device__ __forceinline__ F warp_sum_of(F v) {
@@ -302,8 +307,9 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const flo
   for (int i = 0; i < V; i++) {
     const int e = e0 + i;
     const bool there = i < p.per_lane && e < p.G;
-    c[i] = !scored || x[i] == minus_inf<float>() ? (F)x[i]
-                                                  : score_of<F, SIG>(x[i], s) + (p.bias != nullptr && there ? (F)*(p.bias + e) : (F)0);
+    c[i] = !scored || x[i] == minus_inf<float>()
+               ? (F)x[i]
+               : add_alone(score_of<F, SIG>(x[i], s), p.bias != nullptr && there ? (F)*(p.bias + e) : (F)0);
     // without a bias the logits have the scores' order, exactly
     key[i] = there ? order_key(p.bias == nullptr ? (F)x[i] : c[i]) : 0;
   }
@@ -440,7 +446,7 @@ __device__ __forceinline__ int group_rank_exact(const RouteParams& p, int64_t t,
   for (int i = 0; i < p.per_lane; i++) {
     const int e = lane * p.per_lane + i;
     const float x = load_logit(p, t, e);
-    const double c = x == minus_inf<float>() ? closed : score_of<double, SIG>(x, s) + (p.bias != nullptr ? (double)*(p.bias + e) : 0.);
+    const double c = x == minus_inf<float>() ? closed : add_alone(score_of<double, SIG>(x, s), p.bias != nullptr ? (double)*(p.bias + e) : 0.);
     second = c > first ? first : (c > second ? c : second);
     first = c > first ? c : first;
   }
@@ -482,7 +488,7 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
   for (int i = 0; i < V; i++) {
     const bool there = i < p.per_lane && e0 + i < p.G;
     float c = x[i];
-    if (scored && x[i] != closed) c = (SIG ? sigmoid_near(x[i]) : own[i] * s.inv) + bias[i];
+    if (scored && x[i] != closed) c = SIG ? sigmoid_near(x[i]) + bias[i] : fmaf(own[i], s.inv, bias[i]);
     key[i] = there ? (order_key(p.bias == nullptr ? x[i] : c) & ~MASK) | (MASK - (uint32_t)i) : 0u;
     if (there) {
       nan |= c != c;
@@ -598,7 +604,7 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
   if (p.bias != nullptr) {
     Softmax<double> exact{};
     if constexpr (!SIG) exact = softmax_exact(p, t, s.top, lane);
-    value = score_of<double, SIG>(xi, exact) + (double)bi;
+    value = add_alone(score_of<double, SIG>(xi, exact), (double)bi);
   }
   const uint64_t order = lane >= n ? 0 : mine == last_key ? order_key((double)closed) : order_key(value);
   int rank = 0;
