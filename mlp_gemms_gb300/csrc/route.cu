@@ -246,9 +246,11 @@ __device__ __forceinline__ int take_largest(K (&key)[V], int per_lane, int count
   return mine;
 }
 
-// Which groups are kept, as a bit mask; *close: the last kept group's value
-// and the first dropped one's are nearer than `tol`.  c: the values of all
-// experts in shared memory.
+// Which groups are kept, as a bit mask; *close (fp32): some kept group's value less its
+// error is not above some dropped one's with its error.  A group's error goes by its own
+// terms, so one far from the border may be the one that is out of place (1000 and -999
+// beside groups whose terms are around 1).  `tol`: the scores' part of the error.  c: the
+// values of all experts in shared memory.
 template <typename F>
 __device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F* c, int lane, F tol, bool* close) {
   const int size = p.G / p.groups;
@@ -265,7 +267,6 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F* c
     }
   }
   F value = p.group_top == 2 ? a + b : a;
-  const F most = value > minus_inf<F>() ? (a < 0 ? -a : a) + (p.group_top < 2 ? (F)0 : b < 0 ? -b : b) : (F)0;
   typename KeyOf<F>::type key = nan ? ~(typename KeyOf<F>::type)0 : order_key(value);
   int rank = 0;
   for (int g = 0; g < p.groups; g++) {
@@ -274,14 +275,14 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F* c
   }
   const bool in = lane < p.groups;
   const uint32_t kept = __ballot_sync(0xFFFFFFFFu, in && rank < p.topk_groups);
-  const uint32_t last = __ballot_sync(0xFFFFFFFFu, in && rank == p.topk_groups - 1);
-  const uint32_t next = __ballot_sync(0xFFFFFFFFu, in && rank == p.topk_groups);
   *close = false;
-  if (next != 0) {
-    const int i = __ffs(last) - 1, j = __ffs(next) - 1;
-    const F u = __shfl_sync(0xFFFFFFFFu, value, i), v = __shfl_sync(0xFFFFFFFFu, value, j);
-    const F m = __shfl_sync(0xFFFFFFFFu, most, i), n = __shfl_sync(0xFFFFFFFFu, most, j);
-    *close = u - v <= tol + (F)5e-7 * (m > n ? m : n);  // false for two closed groups: -Inf - -Inf is a NaN
+  if constexpr (sizeof(F) == 4) {
+    // closed groups and those with a NaN are in their exact places
+    const bool real = in && !nan && fabsf(value) <= 3e38f;
+    const float err = tol + 2.5e-7f * (fabsf(a) + (p.group_top == 2 ? fabsf(b) : 0.f));
+    const uint32_t low = __reduce_min_sync(0xFFFFFFFFu, real && rank < p.topk_groups ? order_key(value - err) : ~0u);
+    const uint32_t high = __reduce_max_sync(0xFFFFFFFFu, real && rank >= p.topk_groups ? order_key(value + err) : 0u);
+    *close = high >= low;
   }
   return kept;
 }
@@ -322,7 +323,7 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const flo
         shared[e0 + i] = c[i];
     __syncwarp();
     bool close;
-    const uint32_t kept = keep_groups<F>(p, shared, lane, 2 * err, &close);
+    const uint32_t kept = keep_groups<F>(p, shared, lane, err, &close);
     *open = FAST && close && scored;
     const int size = p.G / p.groups;
     int g = e0 / size, in = e0 - g * size;
@@ -506,7 +507,6 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
       first = a > first ? a : first;
     }
     const float value = p.group_top == 2 ? first + second : first;
-    const float size = fabsf(value) <= 3e38f ? fabsf(first) + (p.group_top == 2 ? fabsf(second) : 0.f) : 0.f;
     const uint32_t bad = __ballot_sync(0xFFFFFFFFu, nan) >> (mine * lanes) & (lanes == 32 ? ~0u : (1u << lanes) - 1u);
     const uint32_t order = bad ? 0xFFFFFFFFu : order_key(value);
     int rank = 0;
@@ -514,16 +514,15 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
       const uint32_t other = __shfl_sync(0xFFFFFFFFu, order, g * lanes);
       rank += other > order || (other == order && g < mine) ? 1 : 0;
     }
-    const uint32_t last = __ballot_sync(0xFFFFFFFFu, rank == p.topk_groups - 1);
-    const uint32_t next = __ballot_sync(0xFFFFFFFFu, rank == p.topk_groups);
-    if (scored && next != 0) {
-      const int a = __ffs(last) - 1, b = __ffs(next) - 1;
-      const float u = __shfl_sync(0xFFFFFFFFu, value, a), v = __shfl_sync(0xFFFFFFFFu, value, b);
-      const float most = fmaxf(__shfl_sync(0xFFFFFFFFu, size, a), __shfl_sync(0xFFFFFFFFu, size, b));
-      // units of 2^-24: sigmoids are off by at most 5 each, the softmax's scores, which
-      // sum to 1, by 70 together; sums and values add 2 of their size each.  False
-      // for two closed groups.
-      if (u - v <= (SIG ? 2e-6f : 1.2e-5f) + 5e-7f * most) rank = group_rank_exact<SIG>(p, t, s.top, lane, lanes, bad != 0);
+    if (scored) {
+      // As in keep_groups.  Units of 2^-24: two sigmoids are off by at most 10, the
+      // softmax's scores, which sum to 1, by 70 together (16 and 100 here); the sums
+      // by 2 of their size (4 here).
+      const bool real = !bad && fabsf(value) <= 3e38f;
+      const float err = (SIG ? 1e-6f : 6e-6f) + 2.5e-7f * (fabsf(first) + (p.group_top == 2 ? fabsf(second) : 0.f));
+      const uint32_t low = __reduce_min_sync(0xFFFFFFFFu, real && rank < p.topk_groups ? order_key(value - err) : ~0u);
+      const uint32_t high = __reduce_max_sync(0xFFFFFFFFu, real && rank >= p.topk_groups ? order_key(value + err) : 0u);
+      if (high >= low) rank = group_rank_exact<SIG>(p, t, s.top, lane, lanes, bad != 0);
     }
     if (rank >= p.topk_groups) {
 #pragma unroll
