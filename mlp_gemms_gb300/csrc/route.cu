@@ -342,7 +342,10 @@ __device__ __forceinline__ int choose(const RouteParams& p, int64_t t, const flo
     const F si = score_of<F, SIG>(xi, s), ci = si + (F)bi;
     const F ux = __shfl_up_sync(0xFFFFFFFFu, xi, 1), ub = __shfl_up_sync(0xFFFFFFFFu, bi, 1);
     const F us = __shfl_up_sync(0xFFFFFFFFu, si, 1), uc = __shfl_up_sync(0xFFFFFFFFu, ci, 1);
-    const F most = si > us ? si : us;
+    F most = si > us ? si : us;
+    // Behind the first that is left out any expert may stand, with a score up to the
+    // largest, that its bias cancels.
+    if (look && lane == p.k) most = SIG ? (F)1 : s.inv;
     // equal logits with equal biases are equal for certain; closed experts are -Inf
     const bool near = lane > 0 && lane < count && !(xi == ux && bi == ub) && xi != minus_inf<float>() &&
                       uc - ci <= err * most + (F)2.5e-7 * ((uc < 0 ? -uc : uc) + (ci < 0 ? -ci : ci));
@@ -558,12 +561,15 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
       id = lane == j ? taken : id;
     }
   };
-  // The choices in `lanes` and the one that lane `from` (not above its own) has:
-  // may exact values order them otherwise?  Below the last key taken nothing is
-  // larger by more than the bits that hold the slot.
+  // The lane's choice and the one that lane `from` (not above its own) has: may exact
+  // values order them otherwise?  Below the last key taken nothing is larger by more
+  // than the bits that hold the slot; but a score there may be any, and its error with
+  // it, so `last` stands for all behind it: units of 2^-24, two sigmoids are off by 10
+  // (20 here), two of the softmax's scores by 74 of the largest (92 here).
+  const float any_score = SIG ? 1.2e-6f : 5.5e-6f * s.inv;
   const uint32_t last_key = order_key(closed) & ~MASK;  // closed ones go by index
   float xi = 0.f, bi = 0.f;
-  const auto close_to = [&](int from, bool asked) {
+  const auto close_to = [&](int from, bool asked, bool last) {
     const uint32_t up = __shfl_sync(0xFFFFFFFFu, mine, from);
     bool near;
     if (p.bias == nullptr) {  // BF16 logits fit whole
@@ -576,7 +582,8 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
       // sum with a bias 1; the slot's bits 2 V of the value; the softmax's sum 60,
       // the same part of both scores
       const float far = SIG ? fmaxf(fabsf(xi), fabsf(ux)) : fmaxf(fabsf(xi - s.top), fabsf(ux - s.top));
-      const float tol = (1.2e-6f + 3.2e-7f * far) * fmaxf(si, us) + (SIG ? 0.f : 4e-6f * fabsf(us - si));
+      const float pair = (1.2e-6f + 3.2e-7f * far) * fmaxf(si, us) + (SIG ? 0.f : 4e-6f * fabsf(us - si));
+      const float tol = last ? fmaxf(pair, any_score) : pair;
       near = uc - ci <= tol + (2.5e-7f + V * 1.2e-7f) * (fabsf(uc) + fabsf(ci)) + 1e-36f;
     }
     return __any_sync(0xFFFFFFFFu, asked && near && mine != last_key) != 0;
@@ -591,13 +598,13 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
   take(0, count);
   if (p.bias != nullptr) reload(0, count);
   *open = p.k == 32 && p.G > 32;
-  if (*open || !close_to(lane > 0 ? lane - 1 : 0, lane > 0 && lane < count)) return id;
+  if (*open || !close_to(lane > 0 ? lane - 1 : 0, lane > 0 && lane < count, lane == p.k)) return id;
   // Eight more, and the order of these by exact values, a lane each: an eighth of the
   // FP64 instructions of all experts' (at 8 a lane), of which an SM does two a clock.
   const int n = min(count + 8, min(p.G, 32));
   take(count, n);
   reload(p.bias != nullptr ? count : 0, n);
-  *open = n < p.G && close_to(p.k - 1, lane == n - 1);
+  *open = n < p.G && close_to(p.k - 1, lane == n - 1, true);
   if (*open) return id;
   double value = (double)xi;
   if (p.bias != nullptr) {
