@@ -823,8 +823,9 @@ MX_API mx_status_t mx_act_ckpt_bwd(const mx_tensor_t *ckpt, int32_t act, const v
  * D is a multiple of 8 of at most 16384 (else MX_ERR_NOT_SUPPORTED), row strides
  * are multiples of 8 elements; R has no alignment.  mean and rstd are 4-byte
  * aligned.  R == 0: nothing is written but dweight and dbias (zeros; with
- * accumulate unchanged).  A row with an Inf or a NaN gives NaN in that row (and
- * in dweight and dbias).
+ * accumulate unchanged).  A row with an Inf or a NaN, or whose centred squares (rms:
+ * squares) sum past fp32's range, gives NaN in all of that row's y, in its rstd and dx,
+ * and in dweight.
  */
 typedef enum { MX_BF16 = 0, MX_F32 = 1 } mx_type_t;
 MX_API mx_status_t mx_layernorm_fwd(const void *x, int32_t x_type, int64_t R, int64_t D, int64_t ld_x,

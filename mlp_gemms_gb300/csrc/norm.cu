@@ -123,7 +123,9 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int W
       }
       flip ^= 1;  // the next row's parts go elsewhere: this row's are still being read
     }
-    const float rstd = rsqrtf(fmaf(m2, inv_d, p.eps));
+    // Squares past fp32's range (an Inf in the row among them) are no statistics: NaN for
+    // the whole row, where rsqrt(Inf) = 0 would pass for values of 0.
+    const float rstd = m2 <= 3.4028235e38f ? rsqrtf(fmaf(m2, inv_d, p.eps)) : __uint_as_float(0x7FC00000u);
     if (wr == 0 && lane == 0) {
       if (p.mean != nullptr && !p.rms) p.mean[r] = mean;
       if (p.rstd != nullptr) p.rstd[r] = rstd;
