@@ -885,19 +885,26 @@ def mx_last_error():
     return load().mx_last_error().decode()
 
 
+# The layers around the expert MLP are part of this namespace and live in
+# layers.py, which loads with the first of them.
+_LAYERS = ("NVFP4", "mx_layernorm_bwd", "mx_layernorm_fwd", "mx_layernorm_workspace_bytes", "mx_moe_topk",
+           "mx_moe_topk_bwd", "mx_moe_topk_workspace_bytes", "mx_moe_unpermute_bwd", "mx_nvfp4_gemm",
+           "mx_nvfp4_quantize", "mx_nvfp4_quantize_workspace_bytes", "nvfp4_scale_bytes")
 _layers = None
 
 
 def __getattr__(name):
-    """The layers around the expert MLP are part of this namespace and live in
-    layers.py, which loads with the first of them."""
     global _layers
+    if name not in _LAYERS:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
     if _layers is None:
-        if name[:3] != "mx_" and name not in ("NVFP4", "nvfp4_scale_bytes"):
-            raise AttributeError("module %r has no attribute %r" % (__name__, name))
         import importlib
-        _layers = importlib.import_module(__name__ + ".layers")
-    try:
-        return _layers.__dict__[name]
-    except KeyError:
-        raise AttributeError("module %r has no attribute %r" % (__name__, name)) from None
+        _layers = importlib.import_module(__name__ + ".layers").__dict__
+    return _layers[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_LAYERS})
+
+
+__all__ = [n for n in globals() if n[0] != "_"] + list(_LAYERS)
