@@ -8,8 +8,9 @@
 namespace mx {
 
 // Both kernels are bound by memory: every value is read once and written once.
-// A row is held in the registers of `W` warps, 8 C columns a lane, so that its statistics, its centred squares and its result need no
-// second read; a block's warps form groups of W, each with a row of its own.
+// A row is held in the registers of `W` warps, 8 C columns a lane, so that its
+// statistics, its centred squares and its result need no second read; a block's warps
+// form groups of W, each with a row of its own.
 
 // A vector [8 n8] of all rows in shared memory, as fp32: the first four values of
 // each lane's eight, then the last four, so that neighbouring lanes read

@@ -91,16 +91,11 @@ __device__ __forceinline__ void load_shared8(const void* base, bool f32, int64_t
   }
 }
 
-__device__ __forceinline__ void load_shared_pairs(const void* base, bool f32, int64_t at, uint64_t (&v)[4]) {
-  float f[8];
-  load_shared8(base, f32, at, f);
-#pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = pack2(f[2 * i], f[2 * i + 1]);
-}
-
-// Rows copied ahead into shared memory, 16 bytes at a time, by the thread that will
-// read them: no barrier, no registers held by what is in flight.  A ring of S
-// stages: wait_ahead<S - 2>() leaves the newest S - 2 rows in flight.
+// Rows copied ahead into shared memory, 16 bytes at a time, without registers held by
+// what is in flight, by the thread that will read them (no barrier) or by its warp
+// (__syncwarp() between the wait and the reads, and between the reads and the copies
+// that take their place).  A ring of S stages: wait_ahead<S - 2>() leaves the newest S - 2
+// rows in flight.
 __device__ __forceinline__ void copy_ahead16(uint4* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(to)), "l"(from) : "memory");
 }
