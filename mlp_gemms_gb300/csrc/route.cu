@@ -450,7 +450,9 @@ __device__ __forceinline__ int group_rank_exact(const RouteParams& p, int64_t t,
   for (int i = 0; i < p.per_lane; i++) {
     const int e = lane * p.per_lane + i;
     const float x = load_logit(p, t, e);
-    const double c = x == minus_inf<float>() ? closed : add_alone(score_of<double, SIG>(x, s), p.bias != nullptr ? (double)*(p.bias + e) : 0.);
+    const double c = x == minus_inf<float>()
+                         ? closed
+                         : add_alone(score_of<double, SIG>(x, s), p.bias != nullptr ? (double)*(p.bias + e) : 0.);
     second = c > first ? first : (c > second ? c : second);
     first = c > first ? c : first;
   }
@@ -576,13 +578,14 @@ __device__ __forceinline__ int choose_scored(const RouteParams& p, int64_t t, co
       near = p.x_f32 && mine == up;
     } else {
       const float si = SIG ? sigmoid_near(xi) : exp_near(xi - s.top) * s.inv, ci = si + bi;
-      const float ux = __shfl_sync(0xFFFFFFFFu, xi, from), us = __shfl_sync(0xFFFFFFFFu, si, from);
-      const float uc = __shfl_sync(0xFFFFFFFFu, ci, from);
-      // units of 2^-24 of a score: 7 + 2.5 |x| (softmax: from the top), two of them; a
-      // sum with a bias 1; the slot's bits 2 V of the value; the softmax's sum 60,
-      // the same part of both scores
-      const float far = SIG ? fmaxf(fabsf(xi), fabsf(ux)) : fmaxf(fabsf(xi - s.top), fabsf(ux - s.top));
-      const float pair = (1.2e-6f + 3.2e-7f * far) * fmaxf(si, us) + (SIG ? 0.f : 4e-6f * fabsf(us - si));
+      // units of 2^-24 of a score: 7 + 2.5 |x| (softmax: from the top), here 10 + 2.7 |x|,
+      // each of its own score, so that a finite mask, far away with a score of 0, adds
+      // nothing (by the larger of both every token with a mask of -1e9 needed exact values:
+      // 32768 x 128 softmax with a bias 176 us instead of 28); a sum with a bias 1; the
+      // slot's bits 2 V of the value; the softmax's sum 60, the same part of both scores
+      const float ei = (6e-7f + 1.6e-7f * fabsf(SIG ? xi : xi - s.top)) * si;
+      const float us = __shfl_sync(0xFFFFFFFFu, si, from), uc = __shfl_sync(0xFFFFFFFFu, ci, from);
+      const float pair = ei + __shfl_sync(0xFFFFFFFFu, ei, from) + (SIG ? 0.f : 4e-6f * fabsf(us - si));
       const float tol = last ? fmaxf(pair, any_score) : pair;
       near = uc - ci <= tol + (2.5e-7f + V * 1.2e-7f) * (fabsf(uc) + fabsf(ci)) + 1e-36f;
     }
