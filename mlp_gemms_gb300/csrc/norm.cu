@@ -163,9 +163,9 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int W
 // ([65536, 2048] BF16 152 us, 137 this way; [32768, 4096] fp32 with dres 310, 279 =
 // 99 % of the copy rate; [16384, 8192] fp32 489, 275).
 // PAIR: more than 8192 columns, half of them in each block of a cluster of two,
-// which exchange their halves of a row's two sums ([10217, 13136] BF16 with dres in one block
-// with the sums of dw and db in shared memory 638 us, 344 this way; [8192, 16384]
-// without 219 and 263: two exchanges a row, 2.4 us).
+// which exchange their halves of a row's two sums ([10217, 13136] BF16 with dres in one
+// block with the sums of dw and db in shared memory 638 us, 347 this way; [8192, 16384]
+// without 219 and 264: two exchanges a row, 2.4 us).
 __host__ __device__ constexpr int bwd_half(int D) { return ((D >> 3) + 1) / 2 * 8; }
 constexpr int bwd_stages(bool f32, int C, bool res) {
   return ((f32 ? 32 : 16) * (res ? 2 : 1) + 16) * C * 512 * 3 <= 150 * 1024 ? 3 : 2;
