@@ -315,6 +315,9 @@ mx_status_t check_pair(const mx_tensor_t* a, const mx_tensor_t* b, const char* a
   return MX_OK;
 }
 
+// rows * ld below 2^40 elements, without a product that may wrap.
+bool fits(int64_t rows, int64_t ld) { return rows <= 0 || ld <= ((1ll << 40) - 1) / rows; }
+
 bool env_validate_offsets() {
   const char* v = getenv("MX_VALIDATE_OFFSETS");
   return v && v[0] == '1';
@@ -656,7 +659,8 @@ mx_status_t mx_moe_route_index_pad(const int32_t* topk_dev, int64_t T, int32_t k
   MX_CHECK(pad == 128 || pad == 256, MX_ERR_INVALID_ARG, "pad = %d; segments are padded to 128 or 256 rows", pad);
   MX_CHECK(T >= 0 && k >= 1, MX_ERR_INVALID_ARG, "T = %lld, k = %d", (long long)T, k);
   MX_CHECK(G >= 1 && G <= 1024, MX_ERR_INVALID_ARG, "G = %d is outside [1, 1024]", G);
-  MX_CHECK(T * k < (1ll << 31), MX_ERR_SHAPE, "T * k = %lld exceeds the int32 row range", (long long)(T * k));
+  MX_CHECK(T < (1ll << 31) && T * k < (1ll << 31), MX_ERR_SHAPE, "T * k exceeds the int32 row range (T = %lld)",
+           (long long)T);
   MX_CHECK(R_cap >= mx_moe_route_rows_pad(T, k, G, pad) && R_cap < (1ll << 31), MX_ERR_SHAPE,
            "R_cap = %lld; mx_moe_route_rows_pad gives %lld", (long long)R_cap,
            (long long)mx_moe_route_rows_pad(T, k, G, pad));
@@ -693,7 +697,7 @@ mx_status_t mx_permute_quantize(const void* x_bf16, int64_t T, int64_t D, int64_
   MX_CHECK(aligned16(x_bf16) && aligned16(src_dev) && aligned16(offsets_dev), MX_ERR_ALIGNMENT,
            "pointers must be 16-byte aligned");
   MX_CHECK(offsets_dev == nullptr || G >= 1, MX_ERR_INVALID_ARG, "G = %d with offsets", G);
-  MX_CHECK(T * ld < (1ll << 40), MX_ERR_SHAPE, "input too large");
+  MX_CHECK(T < (1ll << 31) && fits(T, ld), MX_ERR_SHAPE, "input too large");
   mx_status_t st;
   if (flags & MX_ROWWISE) {
     if ((st = check_tensor(out_row, "out_row", R_cap, D, fmt, 0)) != MX_OK) return st;
@@ -746,7 +750,7 @@ mx_status_t mx_moe_unpermute(const void* in_bf16, int64_t R, int64_t D, const in
            MX_ERR_INVALID_ARG, "in, row_of or out is NULL");
   MX_CHECK(aligned16(in_bf16) && aligned16(row_of_dev) && aligned16(weights_dev) && aligned16(out_bf16),
            MX_ERR_ALIGNMENT, "pointers must be 16-byte aligned");
-  MX_CHECK(R * D < (1ll << 40) && T * D < (1ll << 40) && T * k < (1ll << 31), MX_ERR_SHAPE, "input too large");
+  MX_CHECK(fits(R, D) && T < (1ll << 31) && fits(T, D) && T * k < (1ll << 31), MX_ERR_SHAPE, "input too large");
   if (T == 0) return MX_OK;
   DevInfo dev;
   mx_status_t st;
@@ -802,7 +806,7 @@ mx_status_t grouped_gemm_impl(const mx_tensor_t* a, const mx_tensor_t* b, int32_
            "out must be a 16-byte aligned pointer");
   MX_CHECK(ld_out >= N && ld_out % 8 == 0, MX_ERR_ALIGNMENT, "ld_out = %lld must be >= N and a multiple of 8",
            (long long)ld_out);
-  MX_CHECK(R * ld_out < (1ll << 40), MX_ERR_SHAPE, "output too large");
+  MX_CHECK(fits(R, ld_out), MX_ERR_SHAPE, "output too large");
   if ((st = check_offsets(offsets_dev, G, R, s)) != MX_OK) return st;
   if (R == 0) return MX_OK;
   DevInfo dev;
@@ -876,7 +880,7 @@ mx_status_t pair_gemm_impl(const mx_tensor_t* a, const mx_tensor_t* b, int32_t G
            "out must be a 16-byte aligned pointer");
   MX_CHECK(ld_out >= N && ld_out % 8 == 0, MX_ERR_ALIGNMENT, "ld_out = %lld must be >= N and a multiple of 8",
            (long long)ld_out);
-  MX_CHECK(R * ld_out < (1ll << 40), MX_ERR_SHAPE, "output too large");
+  MX_CHECK(fits(R, ld_out), MX_ERR_SHAPE, "output too large");
   if ((st = check_offsets(offsets_dev, G, R, s)) != MX_OK) return st;
   if (R == 0) return MX_OK;
   DevInfo dev;
@@ -1151,7 +1155,7 @@ mx_status_t wgrad_common(const mx_tensor_t* a_col, const mx_tensor_t* b_col, int
   MX_CHECK(N > 0 && N % 128 == 0, MX_ERR_SHAPE, "N = %lld is not a positive multiple of 128", (long long)N);
   MX_CHECK(K > 0 && K % 128 == 0, MX_ERR_SHAPE, "K = %lld is not a positive multiple of 128", (long long)K);
   MX_CHECK(out != nullptr && aligned16(out), MX_ERR_ALIGNMENT, "out must be a 16-byte aligned pointer");
-  MX_CHECK((int64_t)G * N * K < (1ll << 40), MX_ERR_SHAPE, "output too large");
+  MX_CHECK(fits((int64_t)G * N, K), MX_ERR_SHAPE, "output too large");
   if ((st = check_offsets(offsets_dev, G, R, s)) != MX_OK) return st;
   DevInfo dev;
   if ((st = device_info(&dev)) != MX_OK) return st;
